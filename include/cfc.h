@@ -405,6 +405,205 @@ int cfc_probe_l2_read(const float* buf, size_t n_floats, int passes, float* out,
  */
 int cfc_copy(const void* src, void* dst, size_t bytes, cfc_stream_t stream);
 
+/*
+ * ---- Trunk operators ----
+ *
+ * The layers around the cell that the pages name beside it (their layer norm and its parameter
+ * reducer, their selective scan): layer norm, dropout with the residual sum, a short causal
+ * convolution, and a selective state space scan, each forward, backward, and (the convolution and
+ * the scan) for single tokens.  The pages print none of their equations; they are stated below.
+ *
+ * Conventions beyond the ones at the top of this file.
+ *   - Activations are fp32 or bf16 (`dtype`: CFC_F32 or CFC_BF16, the same for every activation
+ *     of a call); parameters, their gradients, statistics and scan states are fp32.  All
+ *     arithmetic is fp32; a bf16 output is rounded once, to nearest even.
+ *   - Activations may be strided views whose innermost dimension is contiguous: rows of a matrix
+ *     are `ld` elements apart, steps and sequences of a time-major [K][B][D] tensor are `_t` and
+ *     `_b` elements apart (slices of a packed projection, or batch-first memory, are used in
+ *     place; what is read may have stride 0, what is written has ld >= n, or _t and _b >= 1).  They need their element's alignment only: aligned ones (16
+ *     bytes for bf16, 32 for fp32, strides in multiples of 8) take vector loads.  Other tensors
+ *     are contiguous; fp32 ones need 4-byte, workspaces and scan states 16-byte alignment.
+ *   - Outputs are overwritten and do not overlap inputs, but where a call says otherwise.
+ *   - `lengths` (or NULL: all sequences have K steps) holds B ints on the device, one length per
+ *     sequence; they are used clamped to 0 .. K.  Steps at or beyond a sequence's length are not
+ *     read; outputs and gradients there are 0, and a carried state is the one at the length.
+ *   - Results are bitwise reproducible: orders of summation depend on sizes alone.
+ */
+#define CFC_F32 0
+#define CFC_BF16 1
+
+/*
+ * cfc_layernorm_forward -- y = (x - mean) rstd w + b for each of `rows` rows of n columns, with
+ * mean = sum x / n and rstd = (sum (x - mean)^2 / n + eps)^-1/2.
+ *   x [rows][n] (ldx), w [n], b [n], eps >= 0
+ *   y [rows][n] (ldy) OUTPUT;  stats [rows][2] OUTPUT: mean, rstd (read by the backward pass)
+ */
+int cfc_layernorm_forward(const void* x, long long ldx, const float* w, const float* b, int rows,
+                          int n, float eps, int dtype, void* y, long long ldy, float* stats,
+                          cfc_stream_t stream);
+
+/*
+ * cfc_layernorm_workspace_bytes -- workspace of the two backward calls below.  Writes *bytes
+ * (0: none is needed and ws may be NULL).
+ */
+int cfc_layernorm_workspace_bytes(int rows, int n, size_t* bytes);
+
+/*
+ * cfc_layernorm_backward -- dx, dw = sum_rows dy (x - mean) rstd, db = sum_rows dy.
+ *   dy, x [rows][n]; w; stats from the forward pass
+ *   dx [rows][n] OUTPUT (may be dy's or x's own memory), dw [n], db [n] OUTPUT
+ */
+int cfc_layernorm_backward(const void* dy, long long lddy, const void* x, long long ldx,
+                           const float* w, const float* stats, int rows, int n, int dtype, void* dx,
+                           long long lddx, float* dw, float* db, void* ws, size_t ws_bytes,
+                           cfc_stream_t stream);
+
+/*
+ * cfc_dropout_forward -- y = residual + keep x / (1 - q) (residual NULL: no sum; where an element
+ * is dropped x is not used, whatever it holds).  q = round(65536 p) / 65536 is the drop
+ * probability held; 0 <= p <= 1 (p = 1: everything is dropped).  The mask is not stored: element
+ * (row, col) is kept when a 16-bit piece of a counter-based generator is >= 65536 q.  The
+ * generator is Philox 4x32 with ten rounds, key = the 64-bit seed, counter words = (col / 8, row,
+ * offset low, offset high), and column 8 i + j takes bits 16 j .. 16 j + 15 of the 128.  `rng`
+ * points to device memory {seed, offset} (two 64-bit integers), read when the kernel runs, so a
+ * captured graph draws new masks once the caller advances the offset.
+ * y may be x's or residual's own memory.
+ */
+int cfc_dropout_forward(const void* x, long long ldx, const void* residual, long long ldr,
+                        const void* rng, float p, int rows, int n, int dtype, void* y,
+                        long long ldy, cfc_stream_t stream);
+
+/*
+ * cfc_dropout_backward -- dx = keep dy / (1 - q) with the mask of the forward call of the same
+ * rng, p and sizes.  (The residual's gradient is dy itself.)  dx may be dy's own memory.
+ */
+int cfc_dropout_backward(const void* dy, long long lddy, const void* rng, float p, int rows, int n,
+                         int dtype, void* dx, long long lddx, cfc_stream_t stream);
+
+/*
+ * cfc_dropout_layernorm_forward -- s = cfc_dropout_forward(x, residual), y = layer norm of s, in
+ * one pass.  The norm reads s as stored (rounded to dtype), so its backward pass is exact for it.
+ *   s, y [rows][n] OUTPUT, stats [rows][2] OUTPUT
+ */
+int cfc_dropout_layernorm_forward(const void* x, long long ldx, const void* residual,
+                                  long long ldr, const void* rng, float p, const float* w,
+                                  const float* b, int rows, int n, float eps, int dtype, void* s,
+                                  long long lds, void* y, long long ldy, float* stats,
+                                  cfc_stream_t stream);
+
+/*
+ * cfc_dropout_layernorm_backward -- from dy (of y) and ds (of s as it goes on, NULL: none):
+ * dres = ds + the norm's gradient (of the residual; NULL: not wanted), dx = keep dres / (1 - q),
+ * dw, db.  Workspace: cfc_layernorm_workspace_bytes.
+ */
+int cfc_dropout_layernorm_backward(const void* dy, long long lddy, const void* ds, long long ldds,
+                                   const void* s, long long lds, const void* rng, float p,
+                                   const float* w, const float* stats, int rows, int n, int dtype,
+                                   void* dx, long long lddx, void* dres, long long lddr, float* dw,
+                                   float* db, void* ws, size_t ws_bytes, cfc_stream_t stream);
+
+/*
+ * Causal convolution: one filter of W taps (2 <= W <= 4) per channel,
+ *   p_t = bias + sum_j w[j] x_{t-(W-1)+j},   u_t = silu ? p_t sigmoid(p_t) : p_t,
+ * where x before step 0 is the history x0 (NULL: zeros).
+ */
+typedef struct cfc_conv_args {
+  int B, K, D, W;          /* sequences (<= 65535), steps (<= 2^24), channels, taps              */
+  int dtype, silu;
+  const int* lengths;      /* [B] or NULL                                                        */
+  const void* x;           /* [K][B][D]                                                          */
+  long long x_t, x_b;
+  const float* w;          /* [D][W]                                                             */
+  const float* bias;       /* [D] or NULL                                                        */
+  const void* x0;          /* [B][W-1][D], oldest first, or NULL                                 */
+} cfc_conv_args;
+
+/*
+ * cfc_conv_forward -- u [K][B][D] (strides u_t, u_b) and last [B][W-1][D] (or NULL): the last W-1
+ * inputs before each sequence's end, the next call's x0 (not in x0's own memory).
+ */
+int cfc_conv_forward(const cfc_conv_args* a, void* u, long long u_t, long long u_b, void* last,
+                     cfc_stream_t stream);
+
+/* cfc_conv_workspace_bytes -- workspace of cfc_conv_backward.  Writes *bytes (0: none). */
+int cfc_conv_workspace_bytes(int B, int K, int D, int W, int dtype, size_t* bytes);
+
+/*
+ * cfc_conv_backward -- from du (of u): dx [K][B][D], dw [D][W], dbias [D], and dx0 [B][W-1][D]
+ * (or NULL).  A gradient of `last` belongs to the inputs it was copied from; add it there.
+ */
+int cfc_conv_backward(const cfc_conv_args* a, const void* du, long long du_t, long long du_b,
+                      void* dx, long long dx_t, long long dx_b, float* dw, float* dbias, void* dx0,
+                      void* ws, size_t ws_bytes, cfc_stream_t stream);
+
+/*
+ * cfc_conv_step -- one token per sequence: x [B][D] (row stride x_b), state [B][W-1][D];
+ * u [B][D] (u_b) and new_state (which may be state's own memory) OUTPUT.
+ */
+int cfc_conv_step(const void* x, long long x_b, const float* w, const float* bias,
+                  const void* state, int B, int D, int W, int dtype, int silu, void* u,
+                  long long u_b, void* new_state, cfc_stream_t stream);
+
+/*
+ * Selective scan: per sequence, channel d and state n,
+ *   d_t = softplus ? ln(1 + exp(dt_t + dt_bias)) : dt_t + dt_bias
+ *   h_t[n] = exp(d_t A[d][n]) h_{t-1}[n] + d_t B_t[n] x_t,          h_{-1} = h0 (NULL: zeros)
+ *   y_t = (sum_n C_t[n] h_t[n] + skip x_t) (z ? z_t sigmoid(z_t) : 1)
+ * with channel d in group d / (D / G).  Strides of the step's form (cfc_scan_step) are the `_b`
+ * ones; K and lengths are not used there.
+ */
+typedef struct cfc_scan_args {
+  int B, K, D, N, G;       /* sequences (<= 65535), steps, channels, states (<= 128), groups     */
+  int dtype, softplus;     /* G divides D                                                        */
+  const int* lengths;      /* [B] or NULL                                                        */
+  const void *x, *dt, *z;  /* [K][B][D]; z may be NULL                                           */
+  long long x_t, x_b, dt_t, dt_b, z_t, z_b;
+  const void *Bm, *Cm;     /* [K][B][G][N], groups and states contiguous                         */
+  long long Bm_t, Bm_b, Cm_t, Cm_b;
+  const float* A;          /* [D][N]                                                             */
+  const float* skip;       /* [D] or NULL                                                        */
+  const float* dt_bias;    /* [D] or NULL                                                        */
+  const float* h0;         /* [B][D][N] or NULL                                                  */
+} cfc_scan_args;
+
+/*
+ * cfc_scan_workspace_bytes -- workspace of cfc_scan_forward (backward = 0) or cfc_scan_backward
+ * (backward = 1) for a's sizes and dtype.  Writes *bytes (0: none).
+ * cfc_scan_states_bytes -- bytes of the states that a training forward keeps for the backward
+ * pass: [ceil(K / 8)][B][D][N] fp32.
+ */
+int cfc_scan_workspace_bytes(const cfc_scan_args* a, int backward, size_t* bytes);
+int cfc_scan_states_bytes(const cfc_scan_args* a, size_t* bytes);
+
+/*
+ * cfc_scan_forward -- y [K][B][D] (strides y_t, y_b), h_last [B][D][N] (or NULL; not h0's own
+ * memory) and, for training, states (NULL: none kept).
+ */
+int cfc_scan_forward(const cfc_scan_args* a, void* y, long long y_t, long long y_b, float* h_last,
+                     float* states, void* ws, size_t ws_bytes, cfc_stream_t stream);
+
+/*
+ * cfc_scan_backward -- from dy (of y), dh_last (of h_last, NULL: none) and the forward pass's
+ * states: the gradients in g, each with its input's shape; strides as given, dB and dC
+ * contiguous.  NULL is allowed for dz where z is NULL, dskip, ddt_bias and dh0.
+ */
+typedef struct cfc_scan_grads {
+  void *dx, *ddt, *dz;
+  long long dx_t, dx_b, ddt_t, ddt_b, dz_t, dz_b;
+  void *dB, *dC;           /* [K][B][G][N]                                                       */
+  float *dA, *dskip, *ddt_bias, *dh0;
+} cfc_scan_grads;
+int cfc_scan_backward(const cfc_scan_args* a, const float* states, const void* dy, long long dy_t,
+                      long long dy_b, const float* dh_last, const cfc_scan_grads* g, void* ws,
+                      size_t ws_bytes, cfc_stream_t stream);
+
+/*
+ * cfc_scan_step -- one token per sequence: x, dt, z [B][D], Bm, Cm [B][G][N] (strides _b), the
+ * state a->h0 [B][D][N] (required); y [B][D] (y_b) and new_state (which may be h0's own memory).
+ */
+int cfc_scan_step(const cfc_scan_args* a, void* y, long long y_b, float* new_state,
+                  cfc_stream_t stream);
+
 /* cfc_error_string -- static English text for a status code (never NULL). */
 const char* cfc_error_string(int code);
 

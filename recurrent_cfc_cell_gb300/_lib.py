@@ -35,9 +35,41 @@ EXPORTED = ("cfc_workspace_bytes", "cfc_forward", "cfc_backward", "cfc_backward_
             "cfc_backward_recurrence_ws", "cfc_wait_self_test", "cfc_probe_fma",
             "cfc_probe_l2_read", "cfc_forward_bf16_workspace_bytes", "cfc_forward_bf16",
             "cfc_backward_bf16", "cfc_decay_forward", "cfc_decay_workspace_bytes",
-            "cfc_decay_backward", "cfc_forward_workspace_bytes", "cfc_copy")
+            "cfc_decay_backward", "cfc_forward_workspace_bytes", "cfc_copy",
+            "cfc_layernorm_forward", "cfc_layernorm_workspace_bytes", "cfc_layernorm_backward",
+            "cfc_dropout_forward", "cfc_dropout_backward", "cfc_dropout_layernorm_forward",
+            "cfc_dropout_layernorm_backward", "cfc_conv_forward", "cfc_conv_workspace_bytes",
+            "cfc_conv_backward", "cfc_conv_step", "cfc_scan_workspace_bytes",
+            "cfc_scan_states_bytes", "cfc_scan_forward", "cfc_scan_backward", "cfc_scan_step")
+CFC_F32, CFC_BF16 = 0, 1          # activation types of the trunk operators
+SCAN_PERIOD = 8                   # steps between the states a training scan keeps
 CFC_ERR_SCRATCH_LIMIT = -10
 NOALLOC_SCRATCH_BYTES = 32 << 20  # size of cfc_backward_noalloc's built-in device scratch
+
+
+class ConvArgs(ctypes.Structure):
+    """cfc_conv_args of include/cfc.h."""
+    _fields_ = [(k, ctypes.c_int) for k in ("B", "K", "D", "W", "dtype", "silu")] + [
+        ("lengths", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_t", ctypes.c_longlong),
+        ("x_b", ctypes.c_longlong), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("x0", ctypes.c_void_p)]
+
+
+class ScanArgs(ctypes.Structure):
+    """cfc_scan_args of include/cfc.h."""
+    _fields_ = [(k, ctypes.c_int) for k in ("B", "K", "D", "N", "G", "dtype", "softplus")] + [
+        (k, ctypes.c_void_p) for k in ("lengths", "x", "dt", "z")] + [
+        (k, ctypes.c_longlong) for k in ("x_t", "x_b", "dt_t", "dt_b", "z_t", "z_b")] + [
+        (k, ctypes.c_void_p) for k in ("Bm", "Cm")] + [
+        (k, ctypes.c_longlong) for k in ("Bm_t", "Bm_b", "Cm_t", "Cm_b")] + [
+        (k, ctypes.c_void_p) for k in ("A", "skip", "dt_bias", "h0")]
+
+
+class ScanGrads(ctypes.Structure):
+    """cfc_scan_grads of include/cfc.h."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "ddt", "dz")] + [
+        (k, ctypes.c_longlong) for k in ("dx_t", "dx_b", "ddt_t", "ddt_b", "dz_t", "dz_b")] + [
+        (k, ctypes.c_void_p) for k in ("dB", "dC", "dA", "dskip", "ddt_bias", "dh0")]
 
 
 class CfcError(RuntimeError):
@@ -112,6 +144,30 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.cfc_decay_backward.restype = i
     lib.cfc_copy.argtypes = [vp, vp, sz, vp]
     lib.cfc_copy.restype = i
+    ll, fl, szp = ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(sz)
+    conv, scan, grads = (ctypes.POINTER(c) for c in (ConvArgs, ScanArgs, ScanGrads))
+    for name, args in {
+        "cfc_layernorm_forward": [vp, ll, vp, vp, i, i, fl, i, vp, ll, vp, vp],
+        "cfc_layernorm_workspace_bytes": [i, i, szp],
+        "cfc_layernorm_backward": [vp, ll, vp, ll, vp, vp, i, i, i, vp, ll, vp, vp, vp, sz, vp],
+        "cfc_dropout_forward": [vp, ll, vp, ll, vp, fl, i, i, i, vp, ll, vp],
+        "cfc_dropout_backward": [vp, ll, vp, fl, i, i, i, vp, ll, vp],
+        "cfc_dropout_layernorm_forward": [vp, ll, vp, ll, vp, fl, vp, vp, i, i, fl, i, vp, ll, vp,
+                                          ll, vp, vp],
+        "cfc_dropout_layernorm_backward": [vp, ll, vp, ll, vp, ll, vp, fl, vp, vp, i, i, i, vp, ll,
+                                           vp, ll, vp, vp, vp, sz, vp],
+        "cfc_conv_forward": [conv, vp, ll, ll, vp, vp],
+        "cfc_conv_workspace_bytes": [i] * 5 + [szp],
+        "cfc_conv_backward": [conv, vp, ll, ll, vp, ll, ll, vp, vp, vp, vp, sz, vp],
+        "cfc_conv_step": [vp, ll, vp, vp, vp, i, i, i, i, i, vp, ll, vp, vp],
+        "cfc_scan_workspace_bytes": [scan, i, szp],
+        "cfc_scan_states_bytes": [scan, szp],
+        "cfc_scan_forward": [scan, vp, ll, ll, vp, vp, vp, sz, vp],
+        "cfc_scan_backward": [scan, vp, vp, ll, ll, vp, grads, vp, sz, vp],
+        "cfc_scan_step": [scan, vp, ll, vp, vp],
+    }.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
     if path is None:
         _lib = lib
     return lib
@@ -462,3 +518,333 @@ def cfc_decay_backward(dH, x, h0, W, tau, ts, H, E, dW, db, dtau, dx, dh0, ws,
         _ptr(dW, "dW", (C, n_x + C)), _ptr(db, "db", (C,)), _ptr(dtau, "dtau", (C,)),
         _ptr(dx, "dx", (K, B, n_x)), _ptr(dh0, "dh0", (B, C)), wp, wn, _stream(stream))
     _check("cfc_decay_backward", rc)
+
+
+# ---- trunk operators: layer norm, dropout, causal convolution, selective scan ----
+
+class Prepared:
+    """A checked call of an entry point on given tensors (kept by reference): calling it enqueues
+    the work on ``stream`` (default: the current stream)."""
+
+    __slots__ = ("name", "fn", "args", "kept", "device")
+
+    def __init__(self, name, fn, args, kept, device):
+        self.name, self.fn, self.args, self.kept, self.device = name, fn, args, kept, device
+
+    def __call__(self, stream=None) -> None:
+        import torch
+
+        s = (torch._C._cuda_getCurrentRawStream(self.device) if stream is None
+             else stream.cuda_stream)
+        rc = self.fn(*self.args, s)
+        if rc != CFC_OK:
+            _check(self.name, rc)
+
+
+def _entry(f):
+    """An entry point from the function that checks its tensors and marshals its arguments:
+    f(...) enqueues, f.prepare(...) returns the Prepared call."""
+    import functools
+
+    name = f.__name__
+
+    @functools.wraps(f)
+    def call(*a, stream=None, **k):
+        prepare(*a, **k)(stream)
+
+    def prepare(*a, **k) -> Prepared:
+        import torch
+
+        args, kept = f(*a, **k)
+        dev = torch.cuda.current_device()
+        for t in kept:
+            if isinstance(t, torch.Tensor) and t.device.index != dev:
+                raise ValueError(f"{name}: a tensor is not on the current device")
+        return Prepared(name, getattr(load(), name), args, kept, dev)
+
+    call.prepare = prepare
+    return call
+
+
+def _act(t, name: str, shape, dtype=None):
+    """(pointer, dtype code) of an activation: fp32 or bf16, the last dimension contiguous."""
+    import torch
+
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.float32, torch.bfloat16) or not t.is_cuda:
+        raise ValueError(f"{name} must be a float32 or bfloat16 CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has type {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
+
+
+def _code(t) -> int:
+    import torch
+
+    return CFC_BF16 if t.dtype == torch.bfloat16 else CFC_F32
+
+
+def _par(t, name: str, shape):
+    """Address of a contiguous fp32 tensor (None stays None)."""
+    p = _ptr(t, name, shape)
+    return None if p is None else p.value
+
+
+def _con(t, name: str, shape, dtype):
+    """Address of a contiguous activation-typed tensor (None stays None)."""
+    p = _act(t, name, shape, dtype)
+    if p is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def _ld(t) -> int:
+    return 0 if t is None else t.stride(0)
+
+
+def _tb(t) -> tuple[int, int]:
+    return (0, 0) if t is None else (t.stride(0), t.stride(1))
+
+
+def _rng(rng):
+    import torch
+
+    if (not isinstance(rng, torch.Tensor) or rng.dtype not in (torch.int64, torch.uint64)
+            or not rng.is_cuda or tuple(rng.shape) != (2,) or not rng.is_contiguous()):
+        raise ValueError("rng must be a contiguous 64-bit integer CUDA tensor {seed, offset}")
+    return rng.data_ptr()
+
+
+def _lengths(lengths, B):
+    import torch
+
+    if lengths is None:
+        return None
+    if (not isinstance(lengths, torch.Tensor) or lengths.dtype != torch.int32
+            or not lengths.is_cuda or tuple(lengths.shape) != (B,) or not lengths.is_contiguous()):
+        raise ValueError("lengths must be a contiguous int32 CUDA tensor, one per sequence")
+    return lengths.data_ptr()
+
+
+def _work(ws):
+    if ws is None:
+        return None, 0
+    p, n = _ws(ws)
+    return p.value, n
+
+
+def layernorm_workspace_bytes(rows: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("cfc_layernorm_workspace_bytes",
+           load().cfc_layernorm_workspace_bytes(rows, n, ctypes.byref(out)))
+    return out.value
+
+
+@_entry
+def cfc_layernorm_forward(x, w, b, y, stats, eps: float = 1e-5):
+    """y [rows, n] and stats [rows, 2] (mean, rstd) <- layer norm of x's rows."""
+    rows, n = x.shape
+    return ((_act(x, "x", (rows, n)), _ld(x), _par(w, "w", (n,)), _par(b, "b", (n,)), rows, n, eps,
+             _code(x), _act(y, "y", (rows, n), x.dtype), _ld(y), _par(stats, "stats", (rows, 2))),
+            (x, w, b, y, stats))
+
+
+@_entry
+def cfc_layernorm_backward(dy, x, w, stats, dx, dw, db, ws=None):
+    """dx [rows, n], dw [n], db [n] <- gradient of the layer norm."""
+    rows, n = x.shape
+    wp, wn = _work(ws)
+    return ((_act(dy, "dy", (rows, n), x.dtype), _ld(dy), _act(x, "x", (rows, n)), _ld(x),
+             _par(w, "w", (n,)), _par(stats, "stats", (rows, 2)), rows, n, _code(x),
+             _act(dx, "dx", (rows, n), x.dtype), _ld(dx), _par(dw, "dw", (n,)),
+             _par(db, "db", (n,)), wp, wn), (dy, x, w, stats, dx, dw, db, ws))
+
+
+@_entry
+def cfc_dropout_forward(x, residual, rng, p: float, y):
+    """y [rows, n] <- residual (or None) + dropout of x, drawn from rng = {seed, offset}."""
+    rows, n = x.shape
+    return ((_act(x, "x", (rows, n)), _ld(x), _act(residual, "residual", (rows, n), x.dtype),
+             _ld(residual), _rng(rng), p, rows, n, _code(x), _act(y, "y", (rows, n), x.dtype),
+             _ld(y)), (x, residual, rng, y))
+
+
+@_entry
+def cfc_dropout_backward(dy, rng, p: float, dx):
+    """dx [rows, n] <- dy through the mask of the forward call with the same rng and p."""
+    rows, n = dy.shape
+    return ((_act(dy, "dy", (rows, n)), _ld(dy), _rng(rng), p, rows, n, _code(dy),
+             _act(dx, "dx", (rows, n), dy.dtype), _ld(dx)), (dy, rng, dx))
+
+
+@_entry
+def cfc_dropout_layernorm_forward(x, residual, rng, p: float, w, b, s, y, stats,
+                                  eps: float = 1e-5):
+    """s <- residual (or None) + dropout of x; y, stats <- layer norm of s."""
+    rows, n = x.shape
+    return ((_act(x, "x", (rows, n)), _ld(x), _act(residual, "residual", (rows, n), x.dtype),
+             _ld(residual), _rng(rng), p, _par(w, "w", (n,)), _par(b, "b", (n,)), rows, n, eps,
+             _code(x), _act(s, "s", (rows, n), x.dtype), _ld(s),
+             _act(y, "y", (rows, n), x.dtype), _ld(y), _par(stats, "stats", (rows, 2))),
+            (x, residual, rng, w, b, s, y, stats))
+
+
+@_entry
+def cfc_dropout_layernorm_backward(dy, ds, s, rng, p: float, w, stats, dx, dres, dw, db, ws=None):
+    """dres (or None) <- ds (or None) + the norm's gradient; dx <- dres through the mask; dw, db."""
+    rows, n = s.shape
+    wp, wn = _work(ws)
+    return ((_act(dy, "dy", (rows, n), s.dtype), _ld(dy), _act(ds, "ds", (rows, n), s.dtype),
+             _ld(ds), _act(s, "s", (rows, n)), _ld(s), _rng(rng), p, _par(w, "w", (n,)),
+             _par(stats, "stats", (rows, 2)), rows, n, _code(s),
+             _act(dx, "dx", (rows, n), s.dtype), _ld(dx),
+             _act(dres, "dres", (rows, n), s.dtype), _ld(dres), _par(dw, "dw", (n,)),
+             _par(db, "db", (n,)), wp, wn), (dy, ds, s, rng, w, stats, dx, dres, dw, db, ws))
+
+
+def conv_workspace_bytes(B: int, K: int, D: int, W: int, dtype: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("cfc_conv_workspace_bytes",
+           load().cfc_conv_workspace_bytes(B, K, D, W, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def _conv_args(x, w, bias, x0, lengths, silu):
+    K, B, D = x.shape
+    W = w.shape[1]
+    return ConvArgs(B, K, D, W, _code(x), int(silu), _lengths(lengths, B), _act(x, "x", (K, B, D)),
+                    *_tb(x), _par(w, "w", (D, W)), _par(bias, "bias", (D,)),
+                    _con(x0, "x0", (B, W - 1, D), x.dtype))
+
+
+@_entry
+def cfc_conv_forward(x, w, u, bias=None, x0=None, lengths=None, last=None, silu: bool = True):
+    """u [K, B, D] and last [B, W-1, D] (or None) <- causal convolution of x [K, B, D]."""
+    K, B, D = x.shape
+    a = _conv_args(x, w, bias, x0, lengths, silu)
+    return ((ctypes.byref(a), _act(u, "u", (K, B, D), x.dtype), *_tb(u),
+             _con(last, "last", (B, w.shape[1] - 1, D), x.dtype)),
+            (x, w, u, bias, x0, lengths, last, a))
+
+
+@_entry
+def cfc_conv_backward(du, x, w, dx, dw, dbias, bias=None, x0=None, lengths=None, dx0=None, ws=None,
+                      silu: bool = True):
+    """dx, dw [D, W], dbias [D], dx0 (or None) <- gradient of the causal convolution."""
+    K, B, D = x.shape
+    W = w.shape[1]
+    a = _conv_args(x, w, bias, x0, lengths, silu)
+    wp, wn = _work(ws)
+    return ((ctypes.byref(a), _act(du, "du", (K, B, D), x.dtype), *_tb(du),
+             _act(dx, "dx", (K, B, D), x.dtype), *_tb(dx), _par(dw, "dw", (D, W)),
+             _par(dbias, "dbias", (D,)), _con(dx0, "dx0", (B, W - 1, D), x.dtype), wp, wn),
+            (du, x, w, dx, dw, dbias, bias, x0, lengths, dx0, ws, a))
+
+
+@_entry
+def cfc_conv_step(x, w, state, new_state, u, bias=None, silu: bool = True):
+    """u [B, D], new_state [B, W-1, D] (may be state) <- one token of the causal convolution."""
+    B, D = x.shape
+    W = w.shape[1]
+    return ((_act(x, "x", (B, D)), _ld(x), _par(w, "w", (D, W)), _par(bias, "bias", (D,)),
+             _con(state, "state", (B, W - 1, D), x.dtype), B, D, W, _code(x), int(silu),
+             _act(u, "u", (B, D), x.dtype), _ld(u),
+             _con(new_state, "new_state", (B, W - 1, D), x.dtype)),
+            (x, w, bias, state, new_state, u))
+
+
+def _scan_sizes(K, B, D, N, G, dtype):
+    return ScanArgs(B=B, K=K, D=D, N=N, G=G, dtype=dtype)
+
+
+def scan_workspace_bytes(K: int, B: int, D: int, N: int, G: int, dtype: int, backward: bool) -> int:
+    out, a = ctypes.c_size_t(0), _scan_sizes(K, B, D, N, G, dtype)
+    _check("cfc_scan_workspace_bytes",
+           load().cfc_scan_workspace_bytes(ctypes.byref(a), int(backward), ctypes.byref(out)))
+    return out.value
+
+
+def scan_states_bytes(K: int, B: int, D: int, N: int, G: int, dtype: int) -> int:
+    out, a = ctypes.c_size_t(0), _scan_sizes(K, B, D, N, G, dtype)
+    _check("cfc_scan_states_bytes",
+           load().cfc_scan_states_bytes(ctypes.byref(a), ctypes.byref(out)))
+    return out.value
+
+
+def _groups(t, name, shape, dtype):
+    p = _act(t, name, shape, dtype)
+    if t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+        raise ValueError(f"{name} must be contiguous in its last two dimensions")
+    return p
+
+
+def _scan_args(x, dt, A, Bm, Cm, D, dt_bias, z, h0, lengths, softplus):
+    K, B, Dn = x.shape
+    G, N = Bm.shape[-2:]
+    rows, bc = (K, B, Dn), (K, B, G, N)
+    return ScanArgs(B, K, Dn, N, G, _code(x), int(softplus), _lengths(lengths, B),
+                    _act(x, "x", rows), _act(dt, "dt", rows, x.dtype), _act(z, "z", rows, x.dtype),
+                    *_tb(x), *_tb(dt), *_tb(z), _groups(Bm, "Bm", bc, x.dtype),
+                    _groups(Cm, "Cm", bc, x.dtype), *_tb(Bm), *_tb(Cm), _par(A, "A", (Dn, N)),
+                    _par(D, "D", (Dn,)), _par(dt_bias, "dt_bias", (Dn,)),
+                    _par(h0, "h0", (B, Dn, N)))
+
+
+@_entry
+def cfc_scan_forward(x, dt, A, Bm, Cm, y, D=None, dt_bias=None, z=None, h0=None, lengths=None,
+                     h_last=None, states=None, ws=None, softplus: bool = True):
+    """y [K, B, D], h_last [B, D, N] (or None) and, for training, states (a float32 tensor of
+    scan_states_bytes() bytes, or None) <- selective scan."""
+    K, B, Dn = x.shape
+    N = A.shape[1]
+    a = _scan_args(x, dt, A, Bm, Cm, D, dt_bias, z, h0, lengths, softplus)
+    wp, wn = _work(ws)
+    kept = (-(-K // SCAN_PERIOD), B, Dn, N)
+    return ((ctypes.byref(a), _act(y, "y", (K, B, Dn), x.dtype), *_tb(y),
+             _par(h_last, "h_last", (B, Dn, N)), _par(states, "states", kept), wp, wn),
+            (x, dt, A, Bm, Cm, y, D, dt_bias, z, h0, lengths, h_last, states, ws, a))
+
+
+@_entry
+def cfc_scan_backward(dy, x, dt, A, Bm, Cm, states, dx, ddt, dA, dB, dC, D=None, dt_bias=None,
+                      z=None, h0=None, lengths=None, dh_last=None, dD=None, ddt_bias=None, dz=None,
+                      dh0=None, ws=None, softplus: bool = True):
+    """The selective scan's gradients from dy and dh_last (or None)."""
+    K, B, Dn = x.shape
+    G, N = Bm.shape[-2:]
+    a = _scan_args(x, dt, A, Bm, Cm, D, dt_bias, z, h0, lengths, softplus)
+    rows = (K, B, Dn)
+    g = ScanGrads(_act(dx, "dx", rows, x.dtype), _act(ddt, "ddt", rows, x.dtype),
+                  _act(dz, "dz", rows, x.dtype), *_tb(dx), *_tb(ddt), *_tb(dz),
+                  _con(dB, "dB", (K, B, G, N), x.dtype), _con(dC, "dC", (K, B, G, N), x.dtype),
+                  _par(dA, "dA", (Dn, N)), _par(dD, "dD", (Dn,)),
+                  _par(ddt_bias, "ddt_bias", (Dn,)), _par(dh0, "dh0", (B, Dn, N)))
+    wp, wn = _work(ws)
+    return ((ctypes.byref(a), _par(states, "states", (-(-K // SCAN_PERIOD), B, Dn, N)),
+             _act(dy, "dy", rows, x.dtype), *_tb(dy), _par(dh_last, "dh_last", (B, Dn, N)),
+             ctypes.byref(g), wp, wn),
+            (dy, x, dt, A, Bm, Cm, states, dx, ddt, dA, dB, dC, D, dt_bias, z, h0, lengths,
+             dh_last, dD, ddt_bias, dz, dh0, ws, a, g))
+
+
+@_entry
+def cfc_scan_step(x, dt, A, Bm, Cm, state, new_state, y, D=None, dt_bias=None, z=None,
+                  softplus: bool = True):
+    """y [B, D], new_state [B, D, N] (may be state) <- one token of the selective scan; x, dt, z
+    [B, D], Bm, Cm [B, G, N]."""
+    def steps(t):
+        return None if t is None else t[None]
+
+    a = _scan_args(x[None], steps(dt), A, steps(Bm), steps(Cm), D, dt_bias, steps(z), state, None,
+                   softplus)
+    B, Dn = x.shape
+    return ((ctypes.byref(a), _act(y, "y", (B, Dn), x.dtype), _ld(y),
+             _par(new_state, "new_state", (B, Dn, A.shape[1]))),
+            (x, dt, A, Bm, Cm, state, new_state, y, D, dt_bias, z, a))

@@ -271,6 +271,16 @@ BwdLayout bwd_layout(int B, int K, int C, int n_x, int mode) {
 
 }  // namespace
 
+namespace cfc {
+// CFC_OK when the current device can run the library (cfc_trunk_abi.cu's entry points, whose
+// kernels need no other per-device state).
+int device_ready() {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* st = nullptr;
+  return device_state(&st);
+}
+}  // namespace cfc
+
 extern "C" {
 
 const char* cfc_error_string(int code) {

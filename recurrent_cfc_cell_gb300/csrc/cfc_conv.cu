@@ -1,0 +1,368 @@
+// cfc_conv.cu -- the short causal convolution in front of the selective scan: one filter of W
+// taps per channel over the steps of each sequence, a bias and (optionally) SiLU.
+//
+//   forward   p_t = bias + sum_j w[j] x_{t-(W-1)+j},  u_t = p_t sigmoid(p_t)
+//   backward  g_t = du_t s (1 + p_t (1 - s)), s = sigmoid(p_t)   (p_t formed again from x)
+//             dx_t = sum_j w[j] g_{t+(W-1)-j},  dw[j] = sum_{t,b} g_t x_{t-(W-1)+j},
+//             dbias = sum_{t,b} g_t
+//
+// x before the sequence's first step comes from a carried history of W-1 inputs (zero without
+// one); a sequence of length L < K ends at L, its later outputs and gradients are 0 and its
+// last history is the one before L.
+//
+// Bound by memory: x is read and u written once (backward: x and du read, dx written), up to
+// W - 1 steps read again where two runs of steps meet.  A thread holds V neighbouring channels
+// (16 bytes) and walks a run of steps with the last W inputs in registers; runs are short where
+// there are few channels and sequences, so that the GPU is full, and long otherwise.  The
+// parameter gradients are summed in registers over the run, over the CTA's eight runs in
+// shared memory and over the CTAs by reduce_axis0.
+#include "cfc_kernels.h"
+#include "cfc_launch.cuh"
+#include "cfc_trunk.cuh"
+
+namespace cfc {
+namespace {
+
+constexpr int kLanes = 32;  // channel vectors of a CTA
+constexpr int kRuns = 8;    // runs of steps of a CTA
+
+// V neighbouring channels of 4-byte or 2-byte activations (V = 16 bytes of them, or 1).
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = to_f32(*p);
+  } else if constexpr (V == 4) {
+    const float4 r = *reinterpret_cast<const float4*>(p);
+    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+  } else {
+    load8(p, v);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = from_f32<T>(v[0]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    store8(p, v);
+  }
+}
+
+struct ConvArgs {
+  ConvCall q;
+  int run;   // steps of a run
+  float *pw, *pb;
+};
+
+template <typename T, int V, int W>
+struct Window {
+  float x[W][V];
+  __device__ __forceinline__ void shift() {
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j][v] = x[j + 1][v];
+  }
+};
+
+// x_t of sequence b (t < 0: the history), channels c .. c + V - 1.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_x(const ConvCall& q, int t, int b, int c, float (&v)[V]) {
+  if (t >= 0) {
+    load_v<T, V>(static_cast<const T*>(q.x) + t * q.x_t + b * q.x_b + c, v);
+  } else if (q.x0 != nullptr && t >= -(W - 1)) {
+    load_v<T, V>(static_cast<const T*>(q.x0) + (static_cast<long long>(b) * (W - 1) + t + W - 1) * q.D + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+  }
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs a) {
+  const ConvCall& q = a.q;
+  const int c = (blockIdx.x * kLanes + threadIdx.x % kLanes) * V;
+  if (c >= q.D) return;
+  const int b = blockIdx.y;
+  const int len = q.lengths ? min(max(q.lengths[b], 0), q.K) : q.K;
+  const int t0 = (blockIdx.z * kRuns + threadIdx.x / kLanes) * a.run;
+  const int t1 = min(q.K, t0 + a.run);
+  T* u = static_cast<T*>(q.u);
+  if (t0 == 0 && q.last != nullptr) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      float h[V];
+      load_x<T, V, W>(q, len - (W - 1) + j, b, c, h);
+      store_v<T, V>(static_cast<T*>(q.last) + (static_cast<long long>(b) * (W - 1) + j) * q.D + c, h);
+    }
+  }
+  if (t0 >= q.K) return;
+  float w[W][V], bias[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    bias[v] = q.bias ? q.bias[c + v] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][v] = q.w[static_cast<long long>(c + v) * W + j];
+  }
+  Window<T, V, W> win;
+  const int te = min(t1, len);
+  if (t0 < te) {
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) load_x<T, V, W>(q, t0 - (W - 1) + j, b, c, win.x[j]);
+  }
+  // Four steps at a time: their loads are in flight together.
+  constexpr int U = 4;
+  int t = t0;
+  for (; t < te; t += U) {
+    float nx[U][V];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (t + i < te) load_x<T, V, W>(q, t + i, b, c, nx[i]);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (t + i >= te) break;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        win.x[W - 1][v] = nx[i][v];
+        float p = bias[v];
+#pragma unroll
+        for (int j = 0; j < W; ++j) p = fmaf(w[j][v], win.x[j][v], p);
+        o[v] = q.silu ? p * sigmoid_fast(p) : p;
+      }
+      store_v<T, V>(u + (t + i) * q.u_t + b * q.u_b + c, o);
+      win.shift();
+    }
+  }
+  const float zero[V] = {};
+  for (t = max(t0, te); t < t1; ++t) store_v<T, V>(u + t * q.u_t + b * q.u_b + c, zero);
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs a) {
+  __shared__ float part[kRuns][(W + 1) * V][kLanes];
+  const ConvCall& q = a.q;
+  const int lane = threadIdx.x % kLanes, run = threadIdx.x / kLanes;
+  const int c = (blockIdx.x * kLanes + lane) * V;
+  const int b = blockIdx.y;
+  const int len = q.lengths ? min(max(q.lengths[b], 0), q.K) : q.K;
+  const int t0 = (blockIdx.z * kRuns + run) * a.run;
+  const int t1 = min(q.K, t0 + a.run);
+  float dw[W][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    db[v] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
+  }
+  if (c < q.D && (t0 < t1)) {
+    float w[W][V], bias[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      bias[v] = q.bias ? q.bias[c + v] : 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][v] = q.w[static_cast<long long>(c + v) * W + j];
+    }
+    T* dx = static_cast<T*>(q.dx);
+    T* dx0 = static_cast<T*>(q.dx0);
+    const T* du = static_cast<const T*>(q.du);
+    Window<T, V, W> win, g;  // the last W inputs, and the last W gradients of p
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) g.x[j][v] = 0.f;
+    const int te = min(t1, len);
+    if (t0 < te) {
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) load_x<T, V, W>(q, t0 - (W - 1) + j, b, c, win.x[j]);
+    }
+    // g_t for t up to W - 1 steps beyond the run: dx_t takes g_t .. g_{t+W-1}.  The step at t
+    // completes dx at t - (W - 1).
+    constexpr int U = 4;
+    const int tl = t1 + W - 1;
+    for (int t = t0; t < tl; t += U) {
+      float nx[U][V], nd[U][V];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (t + i < min(tl, len)) {
+          load_x<T, V, W>(q, t + i, b, c, nx[i]);
+          load_v<T, V>(du + (t + i) * q.du_t + b * q.du_b + c, nd[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (t + i >= tl) break;
+        g.shift();
+        const bool in = t + i < len;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float gv = 0.f;
+          if (in) {
+            win.x[W - 1][v] = nx[i][v];
+            gv = nd[i][v];
+            if (q.silu) {
+              float p = bias[v];
+#pragma unroll
+              for (int j = 0; j < W; ++j) p = fmaf(w[j][v], win.x[j][v], p);
+              const float s = sigmoid_fast(p);
+              gv *= s * fmaf(p, 1.f - s, 1.f);
+            }
+            if (t + i < te) {
+              db[v] += gv;
+#pragma unroll
+              for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gv, win.x[j][v], dw[j][v]);
+            }
+          }
+          g.x[W - 1][v] = gv;
+        }
+        if (in) win.shift();
+        const int td = t + i - (W - 1);  // g.x[k] is now g at td + k
+        if (td < t0 && (t0 > 0 || dx0 == nullptr)) continue;
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v] = 0.f;
+#pragma unroll
+          for (int k = 0; k < W; ++k) o[v] = fmaf(w[W - 1 - k][v], g.x[k][v], o[v]);
+        }
+        if (td >= 0) store_v<T, V>(dx + td * q.dx_t + b * q.dx_b + c, o);
+        else store_v<T, V>(dx0 + (static_cast<long long>(b) * (W - 1) + td + W - 1) * q.D + c, o);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[run][v * W + j][lane] = dw[j][v];
+    part[run][V * W + v][lane] = db[v];
+  }
+  __syncthreads();
+  // Sums over the CTA's runs, in run order.
+  const size_t row = static_cast<size_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+  for (int e = threadIdx.x; e < (W + 1) * V * kLanes; e += kLanes * kRuns) {
+    const int l = e % kLanes, k = e / kLanes;
+    const int ch = (blockIdx.x * kLanes + l) * V + (k < V * W ? k / W : k - V * W);
+    if (ch >= q.D) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) s += part[r][k][l];
+    if (k < V * W) a.pw[(row * q.D + ch) * W + k % W] = s;
+    else a.pb[row * q.D + ch] = s;
+  }
+}
+
+// One token: u = silu(bias + w . [state ; x]), and the state moves on by one input.  A thread
+// holds V channels of one sequence.  The state may be the new state's own memory: a thread reads
+// what it writes before it writes it.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvCall q) {
+  const int c = (blockIdx.x * 128 + threadIdx.x) * V;
+  const int b = blockIdx.y;
+  if (c >= q.D) return;
+  float x[W][V], o[V];
+  const T* st = static_cast<const T*>(q.x0) + static_cast<long long>(b) * (W - 1) * q.D + c;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) load_v<T, V>(st + static_cast<long long>(j) * q.D, x[j]);
+  load_v<T, V>(static_cast<const T*>(q.x) + b * q.x_b + c, x[W - 1]);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float p = q.bias ? q.bias[c + v] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) p = fmaf(q.w[static_cast<long long>(c + v) * W + j], x[j][v], p);
+    o[v] = q.silu ? p * sigmoid_fast(p) : p;
+  }
+  T* ns = static_cast<T*>(q.last) + static_cast<long long>(b) * (W - 1) * q.D + c;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) store_v<T, V>(ns + static_cast<long long>(j) * q.D, x[j + 1]);
+  store_v<T, V>(static_cast<T*>(q.u) + b * q.u_b + c, o);
+}
+
+// ---- host side ----
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Vector width: 16 bytes of channels where every row starts on 16 bytes, else one channel.
+bool conv_vec(const ConvCall& q) {
+  const long long v = q.bf16 ? 8 : 4;
+  return q.D % v == 0 && al16(q.x) && al16(q.u) && al16(q.x0) && al16(q.last) && al16(q.du) &&
+         al16(q.dx) && al16(q.dx0) && q.x_t % v == 0 && q.x_b % v == 0 && q.u_t % v == 0 &&
+         q.u_b % v == 0 && q.du_t % v == 0 && q.du_b % v == 0 && q.dx_t % v == 0 &&
+         q.dx_b % v == 0;
+}
+
+// Steps of a run and CTAs along the steps, from the sizes alone (so the order of the parameter
+// sums does not change with alignment).
+int conv_run(int B, int K, int D, bool bf16, int halo) {
+  const long long threads = static_cast<long long>(B) * ((D + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4));
+  int run = 64;
+  while (run > (halo ? 8 : 4) && threads * ((K + run - 1) / run) < 152LL * 1024) run /= 2;
+  return run;
+}
+int conv_ctas_t(int K, int run) { return (K + run * kRuns - 1) / (run * kRuns); }
+
+template <typename F>
+cudaError_t by_taps(int W, F&& f) {
+  switch (W) {
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    default: return f(std::integral_constant<int, 4>{});
+  }
+}
+
+template <typename T, int V>
+cudaError_t conv_fwd(const ConvArgs& a, cudaStream_t s) {
+  LaunchCfg c;
+  c.grid = dim3((a.q.D + kLanes * V - 1) / (kLanes * V), a.q.B, conv_ctas_t(a.q.K, a.run));
+  c.block = dim3(kLanes * kRuns);
+  c.stream = s;
+  return by_taps(a.q.W, [&](auto w) { return launch(c, conv_fwd_kernel<T, V, decltype(w)::value>, a); });
+}
+
+template <typename T, int V>
+cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
+  LaunchCfg c;
+  c.grid = dim3((a.q.D + kLanes * V - 1) / (kLanes * V), a.q.B, conv_ctas_t(a.q.K, a.run));
+  c.block = dim3(kLanes * kRuns);
+  c.stream = s;
+  return by_taps(a.q.W, [&](auto w) { return launch(c, conv_bwd_kernel<T, V, decltype(w)::value>, a); });
+}
+
+template <typename T, int V>
+cudaError_t conv_step(const ConvCall& q, cudaStream_t s) {
+  LaunchCfg c;
+  c.grid = dim3((q.D + 128 * V - 1) / (128 * V), q.B);
+  c.block = dim3(128);
+  c.stream = s;
+  return by_taps(q.W, [&](auto w) { return launch(c, conv_step_kernel<T, V, decltype(w)::value>, q); });
+}
+
+}  // namespace
+
+int conv_partials(int B, int K, int D, bool bf16) {
+  return B * conv_ctas_t(K, conv_run(B, K, D, bf16, 1));
+}
+
+cudaError_t conv_fwd_launch(const ConvCall& q, cudaStream_t s) {
+  const ConvArgs a{q, conv_run(q.B, q.K, q.D, q.bf16, 0), nullptr, nullptr};
+  if (q.bf16) return conv_vec(q) ? conv_fwd<__nv_bfloat16, 8>(a, s) : conv_fwd<__nv_bfloat16, 1>(a, s);
+  return conv_vec(q) ? conv_fwd<float, 4>(a, s) : conv_fwd<float, 1>(a, s);
+}
+
+cudaError_t conv_bwd_launch(const ConvCall& q, float* dw, float* db, float* ws, cudaStream_t s) {
+  ConvArgs a{q, conv_run(q.B, q.K, q.D, q.bf16, 1), nullptr, nullptr};
+  const int P = conv_partials(q.B, q.K, q.D, q.bf16);
+  a.pw = P == 1 ? dw : ws;
+  a.pb = P == 1 ? db : ws + static_cast<size_t>(P) * q.D * q.W;
+  cudaError_t e;
+  if (q.bf16) e = conv_vec(q) ? conv_bwd<__nv_bfloat16, 8>(a, s) : conv_bwd<__nv_bfloat16, 1>(a, s);
+  else e = conv_vec(q) ? conv_bwd<float, 4>(a, s) : conv_bwd<float, 1>(a, s);
+  if (e != cudaSuccess || P == 1) return e;
+  return reduce_axis0_pair_launch(a.pw, P, q.D * q.W, 0, 0, dw, nullptr, a.pb, P, q.D, db, s, true);
+}
+
+cudaError_t conv_step_launch(const ConvCall& q, cudaStream_t s) {
+  if (q.bf16) return conv_vec(q) ? conv_step<__nv_bfloat16, 8>(q, s) : conv_step<__nv_bfloat16, 1>(q, s);
+  return conv_vec(q) ? conv_step<float, 4>(q, s) : conv_step<float, 1>(q, s);
+}
+
+}  // namespace cfc

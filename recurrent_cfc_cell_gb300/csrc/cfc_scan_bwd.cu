@@ -1,0 +1,473 @@
+// cfc_scan_bwd.cu -- the selective scan's backward pass.  With a_t = exp(d_t A), q_t = a_t h_{t-1},
+// r_t = dL/d(y_t before the gate) and e_t = dL/dh_t:
+//
+//   e_t = r_t C_t + a_{t+1} e_{t+1}
+//   dC_t = sum_d r_t h_t,  dB_t = sum_d e_t d_t x_t          (over the channels of a group)
+//   dA = sum_{t,b} e_t q_t d_t
+//   dx_t = d_t sum_n e_t B_t + skip r_t,  dd_t = sum_n e_t (A q_t + x_t B_t)
+//   ddt_t = dd_t sigmoid(dt_t + dt_bias),  dskip = sum r_t x_t,  ddt_bias = sum ddt_t
+//   dz_t = dy_t (y_t before the gate) silu'(z_t),  dh0 = a_0 e_0
+//
+// The forward pass kept the state before every kScanPeriod-th step, so the pass walks chunks of
+// that many steps from the last: forwards through the chunk from its kept state (the sums with
+// h_t: y, dC), leaving q_t in shared memory, then backwards (everything with e_t).
+//
+// A lane holds four channels times four states, and a warp 32 channels times 16 states: the sums
+// over states (y, e B, e A q) then cross four lanes and the sums over channels (dB, dC) eight,
+// each by exchanging halves, so that a step of 512 state updates takes 17 shuffles; with one
+// channel's sixteen states to a lane the sums over channels alone would take 31.  What a step
+// needs per channel (d, x, r and the gate's and softplus's derivatives) is formed once per
+// chunk, a thread a value, and read back four channels at a time.  NT warps side by side hold up
+// to 16 NT states, CW warps 32 CW channels.  Sums over warps, channel tiles, sequences and
+// splits are added in a fixed order (shared memory, then a merge), without atomics.
+#include "cfc_kernels.h"
+#include "cfc_launch.cuh"
+#include "cfc_trunk.cuh"
+
+namespace cfc {
+namespace {
+
+constexpr int T8 = kScanPeriod;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int CW, int NT>
+struct Shape {
+  static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = 32 * CW, NP = 16 * NT;
+  // Shared memory, in floats.
+  static constexpr int kPer = T8 * CH;                  // one value per (step, channel)
+  static constexpr int oD = 0, oX = oD + kPer, oR = oX + kPer, oZ = oR + kPer, oS = oZ + kPer;
+  static constexpr int oY = oS + kPer, oV = oY + NT * kPer, oW = oV + NT * kPer;
+  static constexpr int oB = oW + NT * kPer, oC = oB + T8 * NP;
+  static constexpr int oDB = oC + T8 * NP, oDC = oDB + CW * T8 * NP;
+  static constexpr int oQ = oDC + CW * T8 * NP;         // [warp][step][4][lane][4]
+  static constexpr int kFloats = oQ + kWarps * T8 * 512;
+};
+
+// Sum of v[0..3] over the four state lanes (lane bits 0, 1): lane nl keeps v[nl].
+__device__ __forceinline__ float sum_states(const float (&v)[4], int lane) {
+  const bool hi = lane & 2;
+  const float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
+  const float s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
+  const float a = k0 + __shfl_xor_sync(0xffffffffu, s0, 2);
+  const float b = k1 + __shfl_xor_sync(0xffffffffu, s1, 2);
+  const bool lo = lane & 1;
+  return (lo ? b : a) + __shfl_xor_sync(0xffffffffu, lo ? a : b, 1);
+}
+
+// Sum of v[0..3] over the eight channel lanes (lane bits 2..4): the lane keeps v[lane >> 3].
+__device__ __forceinline__ float sum_channels(const float (&v)[4], int lane) {
+  const bool hi = lane & 16;
+  const float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
+  const float s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
+  const float a = k0 + __shfl_xor_sync(0xffffffffu, s0, 16);
+  const float b = k1 + __shfl_xor_sync(0xffffffffu, s1, 16);
+  const bool lo = lane & 8;
+  const float c = (lo ? b : a) + __shfl_xor_sync(0xffffffffu, lo ? a : b, 8);
+  return c + __shfl_xor_sync(0xffffffffu, c, 4);
+}
+
+struct BwdPlan {
+  int per_group, tiles_per_group, steps;
+  const float* carry;   // [splits][B][D][N] or null
+  float* params;        // [splits * B][D][N + 2]
+  float *pB, *pC;       // [tiles_per_group][K][B][G][N], or null: straight to dB / dC
+};
+
+template <typename T, int CW, int NT>
+__global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q, const BwdPlan pl) {
+  using Sh = Shape<CW, NT>;
+  extern __shared__ __align__(16) float sm[];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int nt = warp % NT, cw = warp / NT;
+  const int group = blockIdx.x / pl.tiles_per_group, tile = blockIdx.x % pl.tiles_per_group;
+  const int b = blockIdx.y, split = blockIdx.z;
+  const int len = q.lengths ? min(max(q.lengths[b], 0), q.K) : q.K;
+  const int lo = split * pl.steps, hi = min(q.K, lo + pl.steps), end = min(hi, len);
+  const size_t plane = static_cast<size_t>(q.B) * q.D * q.N;
+  const int d_base = group * pl.per_group;   // the group's first channel
+  const int t_base = tile * Sh::CH;          // the tile's first channel in its group
+
+  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...
+  const int chf = tid % Sh::CH, tf = tid / Sh::CH;
+  const bool livef = t_base + chf < pl.per_group;
+  const int df = d_base + (livef ? t_base + chf : 0);
+  const float bias = q.dt_bias ? q.dt_bias[df] : 0.f, skip = q.skip ? q.skip[df] : 0.f;
+  const T* xp = static_cast<const T*>(q.x) + b * q.x_b + df;
+  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + df;
+  const T* zp = q.z ? static_cast<const T*>(q.z) + b * q.z_b + df : nullptr;
+  const T* gp = static_cast<const T*>(q.dy) + b * q.dy_b + df;
+  T* dxp = static_cast<T*>(q.dx) + b * q.dx_b + df;
+  T* dtp = static_cast<T*>(q.ddt) + b * q.ddt_b + df;
+  T* dzp = q.dz ? static_cast<T*>(q.dz) + b * q.dz_b + df : nullptr;
+  const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N;
+  const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
+
+  // This lane's states: channels c0 .. c0 + 3 of the tile, states n0 .. n0 + 3.
+  const int c0 = cw * 32 + (lane >> 2) * 4, n0 = nt * 16 + (lane & 3) * 4;
+  float2 A2[4][2], e[4][2], dA[4][2];
+  auto in_state = [&](int c, int s) { return t_base + c0 + c < pl.per_group && n0 + s < q.N; };
+  auto state_at = [&](int c) {  // offset of state n0 of channel c in a [B][D][N] plane
+    return (static_cast<size_t>(b) * q.D + d_base + t_base + c0 + c) * q.N + n0;
+  };
+  // Four states of channel c from a plane, zero outside.
+  const bool quad = q.N % 4 == 0;
+  auto load_states = [&](const float* p, int c, float2 (&v)[2]) {
+    v[0] = v[1] = make_float2(0.f, 0.f);
+    if (!in_state(c, 0) || p == nullptr) return;
+    const float* at = p + state_at(c);
+    if (quad) {
+      const float4 r = *reinterpret_cast<const float4*>(at);
+      v[0] = make_float2(r.x, r.y);
+      v[1] = make_float2(r.z, r.w);
+    } else {
+      v[0].x = at[0];
+      if (n0 + 1 < q.N) v[0].y = at[1];
+      if (n0 + 2 < q.N) v[1].x = at[2];
+      if (n0 + 3 < q.N) v[1].y = at[3];
+    }
+  };
+  const float* c_in = pl.carry ? pl.carry + split * plane : q.dh_last;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    load_states(c_in, c, e[c]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float av = in_state(c, s)
+          ? q.A[static_cast<size_t>(d_base + t_base + c0 + c) * q.N + n0 + s] * kLog2e : 0.f;
+      (s & 1 ? A2[c][s / 2].y : A2[c][s / 2].x) = av;
+    }
+    dA[c][0] = dA[c][1] = make_float2(0.f, 0.f);
+  }
+  float dskip = 0.f, dbias = 0.f;
+  float* const hist = sm + Sh::oQ + warp * (T8 * 512) + lane * 4;
+
+  // dB / dC of this tile: partial sums, or the outputs themselves.
+  auto put_bc = [&](int t, int n, float vb, float vc) {
+    const size_t row = (static_cast<size_t>(t) * q.B + b) * q.G + group;
+    if (pl.pB) {
+      const size_t at = (static_cast<size_t>(tile) * q.K * q.B * q.G + row) * q.N + n;
+      pl.pB[at] = vb;
+      pl.pC[at] = vc;
+    } else {
+      static_cast<T*>(q.dB)[row * q.N + n] = from_f32<T>(vb);
+      static_cast<T*>(q.dC)[row * q.N + n] = from_f32<T>(vc);
+    }
+  };
+
+  const int chunks = end > lo ? (end - lo + T8 - 1) / T8 : 0;
+  // Steps after the sequence's end: zeros.
+  for (int t = lo + chunks * T8 + tf; t < hi; t += NT) {
+    if (!livef) continue;
+    dxp[t * q.dx_t] = from_f32<T>(0.f);
+    dtp[t * q.ddt_t] = from_f32<T>(0.f);
+    if (dzp) dzp[t * q.dz_t] = from_f32<T>(0.f);
+  }
+  for (int t = lo + chunks * T8; t < hi; ++t)
+    for (int n = tid; n < q.N; n += Sh::kThreads) put_bc(t, n, 0.f, 0.f);
+
+  for (int ck = chunks - 1; ck >= 0; --ck) {
+    const int t0 = lo + ck * T8;
+    // ---- per channel and step: d, x, r, dy silu'(z), sigmoid(dt + bias)
+#pragma unroll
+    for (int i = 0; i < (T8 + NT - 1) / NT; ++i) {
+      const int k = tf + i * NT, t = t0 + k;
+      if (k >= T8) break;
+      float dv = 0.f, xv = 0.f, rv = 0.f, zf = 0.f, sg = 0.f;
+      if (livef && t < end) {
+        const float raw = to_f32(tp[t * q.dt_t]) + bias;
+        xv = to_f32(xp[t * q.x_t]);
+        const float g = to_f32(gp[t * q.dy_t]);
+        dv = q.softplus ? softplus_f(raw) : raw;
+        sg = q.softplus ? sigmoid_fast(raw) : 1.f;
+        rv = g;
+        if (zp) {
+          const float z = to_f32(zp[t * q.z_t]);
+          const float s = sigmoid_fast(z);
+          rv = g * z * s;
+          zf = g * s * fmaf(z, 1.f - s, 1.f);
+        }
+      }
+      const int at = k * Sh::CH + chf;
+      sm[Sh::oD + at] = dv;
+      sm[Sh::oX + at] = xv;
+      sm[Sh::oR + at] = rv;
+      sm[Sh::oZ + at] = zf;
+      sm[Sh::oS + at] = sg;
+    }
+    for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
+      const int k = i / Sh::NP, n = i % Sh::NP;
+      const bool in = t0 + k < end && n < q.N;
+      sm[Sh::oB + i] = in ? to_f32(Bp[(t0 + k) * q.Bm_t + n]) : 0.f;
+      sm[Sh::oC + i] = in ? to_f32(Cp[(t0 + k) * q.Cm_t + n]) : 0.f;
+    }
+    float2 h[4][2];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) load_states(q.states + (t0 / T8) * plane, c, h[c]);
+    __syncthreads();
+
+    // ---- forwards through the chunk
+#pragma unroll 2
+    for (int k = 0; k < T8; ++k) {
+      const float4 d4 = *reinterpret_cast<const float4*>(&sm[Sh::oD + k * Sh::CH + c0]);
+      const float4 x4 = *reinterpret_cast<const float4*>(&sm[Sh::oX + k * Sh::CH + c0]);
+      const float4 r4 = *reinterpret_cast<const float4*>(&sm[Sh::oR + k * Sh::CH + c0]);
+      const float4 B4 = *reinterpret_cast<const float4*>(&sm[Sh::oB + k * Sh::NP + n0]);
+      const float4 C4 = *reinterpret_cast<const float4*>(&sm[Sh::oC + k * Sh::NP + n0]);
+      const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+      const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
+      const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
+      const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
+      float y[4];
+      float2 dc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 d2 = make_float2(dv[c], dv[c]);
+        const float2 u2 = make_float2(dv[c] * xv[c], dv[c] * xv[c]);
+        const float2 r2 = make_float2(rv[c], rv[c]);
+        float2 y2 = make_float2(0.f, 0.f), qq[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const float2 m = __fmul2_rn(d2, A2[c][s]);
+          qq[s] = __fmul2_rn(make_float2(exp2_f(m.x), exp2_f(m.y)), h[c][s]);
+          h[c][s] = fma2(u2, Bv[s], qq[s]);
+          y2 = fma2(h[c][s], Cv[s], y2);
+          dc[s] = fma2(r2, h[c][s], dc[s]);
+        }
+        y[c] = y2.x + y2.y;
+        *reinterpret_cast<float4*>(hist + (k * 4 + c) * 128) =
+            make_float4(qq[0].x, qq[0].y, qq[1].x, qq[1].y);
+      }
+      sm[Sh::oY + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(y, lane);
+      const float dcs[4] = {dc[0].x, dc[0].y, dc[1].x, dc[1].y};
+      const float sc = sum_channels(dcs, lane);
+      if (!(lane & 4)) sm[Sh::oDC + (cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sc;
+    }
+    // ---- and back
+#pragma unroll 2
+    for (int k = T8 - 1; k >= 0; --k) {
+      const float4 d4 = *reinterpret_cast<const float4*>(&sm[Sh::oD + k * Sh::CH + c0]);
+      const float4 x4 = *reinterpret_cast<const float4*>(&sm[Sh::oX + k * Sh::CH + c0]);
+      const float4 r4 = *reinterpret_cast<const float4*>(&sm[Sh::oR + k * Sh::CH + c0]);
+      const float4 B4 = *reinterpret_cast<const float4*>(&sm[Sh::oB + k * Sh::NP + n0]);
+      const float4 C4 = *reinterpret_cast<const float4*>(&sm[Sh::oC + k * Sh::NP + n0]);
+      const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+      const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
+      const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
+      const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
+      float v[4], w[4];
+      float2 db[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 d2 = make_float2(dv[c], dv[c]);
+        const float2 u2 = make_float2(dv[c] * xv[c], dv[c] * xv[c]);
+        const float2 r2 = make_float2(rv[c], rv[c]);
+        const float4 q4 = *reinterpret_cast<const float4*>(hist + (k * 4 + c) * 128);
+        const float2 qq[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
+        float2 v2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const float2 m = __fmul2_rn(d2, A2[c][s]);
+          const float2 a = make_float2(exp2_f(m.x), exp2_f(m.y));
+          const float2 et = fma2(r2, Cv[s], e[c][s]);
+          const float2 p = __fmul2_rn(et, qq[s]);
+          dA[c][s] = fma2(p, d2, dA[c][s]);
+          w2 = fma2(p, A2[c][s], w2);
+          v2 = fma2(et, Bv[s], v2);
+          db[s] = fma2(et, u2, db[s]);
+          e[c][s] = __fmul2_rn(a, et);
+        }
+        v[c] = v2.x + v2.y;
+        w[c] = w2.x + w2.y;
+      }
+      sm[Sh::oV + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(v, lane);
+      sm[Sh::oW + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(w, lane);
+      const float dbs[4] = {db[0].x, db[0].y, db[1].x, db[1].y};
+      const float sb = sum_channels(dbs, lane);
+      if (!(lane & 4)) sm[Sh::oDB + (cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sb;
+    }
+    __syncthreads();
+
+    // ---- per channel and step: the gradients of the inputs
+#pragma unroll
+    for (int i = 0; i < (T8 + NT - 1) / NT; ++i) {
+      const int k = tf + i * NT, t = t0 + k;
+      if (k >= T8 || t >= hi) break;
+      const int at = k * Sh::CH + chf;
+      float y = 0.f, v = 0.f, w = 0.f;
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        y += sm[Sh::oY + m * Sh::kPer + at];
+        v += sm[Sh::oV + m * Sh::kPer + at];
+        w += sm[Sh::oW + m * Sh::kPer + at];
+      }
+      const float xv = sm[Sh::oX + at], rv = sm[Sh::oR + at];
+      const float ddt = sm[Sh::oS + at] * fmaf(w, kLn2, xv * v);
+      dskip = fmaf(rv, xv, dskip);
+      dbias += ddt;
+      if (livef) {
+        dxp[t * q.dx_t] = from_f32<T>(fmaf(sm[Sh::oD + at], v, skip * rv));
+        dtp[t * q.ddt_t] = from_f32<T>(ddt);
+        if (dzp) dzp[t * q.dz_t] = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
+      }
+    }
+    for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
+      const int k = i / Sh::NP, n = i % Sh::NP;
+      if (t0 + k >= hi || n >= q.N) continue;
+      float vb = 0.f, vc = 0.f;
+#pragma unroll
+      for (int m = 0; m < CW; ++m) {
+        vb += sm[Sh::oDB + m * T8 * Sh::NP + i];
+        vc += sm[Sh::oDC + m * T8 * Sh::NP + i];
+      }
+      put_bc(t0 + k, n, vb, vc);
+    }
+    __syncthreads();
+  }
+
+  // ---- what leaves the split
+  float* params = pl.params + (static_cast<size_t>(split) * q.B + b) * q.D * (q.N + 2);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (!in_state(c, s)) continue;
+      if (split == 0 && q.dh0) q.dh0[state_at(c) + s] = s & 1 ? e[c][s / 2].y : e[c][s / 2].x;
+      params[static_cast<size_t>(d_base + t_base + c0 + c) * (q.N + 2) + n0 + s] =
+          s & 1 ? dA[c][s / 2].y : dA[c][s / 2].x;
+    }
+  }
+  // The NT threads of a channel, in order (the chunk loop ended with a barrier; the region of
+  // the first per-channel values is free).
+  sm[tid] = dskip;
+  sm[Sh::kThreads + tid] = dbias;
+  __syncthreads();
+  if (tid < Sh::CH && livef) {
+    float sk = 0.f, bi = 0.f;
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      sk += sm[tid + m * Sh::CH];
+      bi += sm[Sh::kThreads + tid + m * Sh::CH];
+    }
+    params[static_cast<size_t>(df) * (q.N + 2) + q.N] = sk;
+    params[static_cast<size_t>(df) * (q.N + 2) + q.N + 1] = bi;
+  }
+}
+
+// dB and dC: the channel tiles' partial sums added in tile order, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) scan_bc_kernel(const float* pB, const float* pC, int tiles,
+                                                      size_t count, T* dB, T* dC) {
+  grid_dep_wait();
+  const float* p = blockIdx.y ? pC : pB;
+  T* out = blockIdx.y ? dC : dB;
+  for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < count;
+       i += static_cast<size_t>(gridDim.x) * 256) {
+    float s = p[i];
+    for (int k = 1; k < tiles; ++k) s += p[k * count + i];
+    out[i] = from_f32<T>(s);
+  }
+}
+
+// ---- host side ----
+
+template <typename F>
+cudaError_t by_tiles(int N, F&& f) {
+  using std::integral_constant;
+  if (N <= 16) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  if (N <= 32) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+  if (N <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+  return f(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+}
+
+struct BwdLayout {
+  ScanSplit sp;
+  int tiles;          // channel tiles per group
+  size_t params, bc, carry, total;  // offsets in floats
+};
+
+BwdLayout bwd_layout(const ScanCall& q) {
+  BwdLayout L{};
+  int ch = 32, warps = 4;
+  (void)by_tiles(q.N, [&](auto CW, auto NT) {
+    ch = Shape<decltype(CW)::value, decltype(NT)::value>::CH;
+    warps = Shape<decltype(CW)::value, decltype(NT)::value>::kWarps;
+    return cudaSuccess;
+  });
+  // One CTA covers `ch` channels with `warps` warps; eight warps an SM fill it.
+  L.sp = scan_split(q, ch, 152 * 8 / warps);
+  L.tiles = (q.D / q.G + ch - 1) / ch;
+  auto up = [](size_t v) { return (v + 3) & ~static_cast<size_t>(3); };
+  L.params = 0;
+  L.bc = up(static_cast<size_t>(L.sp.splits) * q.B * q.D * (q.N + 2));
+  const size_t bc = static_cast<size_t>(L.tiles) * q.K * q.B * q.G * q.N;
+  L.carry = L.bc + (L.tiles > 1 ? 2 * up(bc) : 0);
+  L.total = L.carry + scan_carry_floats(q, L.sp);
+  return L;
+}
+
+template <typename T, int CW, int NT>
+cudaError_t run_bwd(const ScanCall& q, const BwdLayout& L, cudaStream_t s) {
+  using Sh = Shape<CW, NT>;
+  static_assert(2 * Sh::kThreads <= 5 * Sh::kPer, "the last sums fit the per-channel values");
+  constexpr size_t smem = Sh::kFloats * sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, CW, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  BwdPlan pl{};
+  pl.per_group = q.D / q.G;
+  pl.tiles_per_group = L.tiles;
+  pl.steps = L.sp.steps;
+  pl.carry = L.sp.splits > 1 ? q.ws + L.carry : nullptr;
+  pl.params = q.ws + L.params;
+  const size_t bc = static_cast<size_t>(L.tiles) * q.K * q.B * q.G * q.N;
+  if (L.tiles > 1) {
+    pl.pB = q.ws + L.bc;
+    pl.pC = pl.pB + ((bc + 3) & ~static_cast<size_t>(3));
+  }
+  LaunchCfg c;
+  c.grid = dim3(L.tiles * q.G, q.B, L.sp.splits);
+  c.block = dim3(Sh::kThreads);
+  c.smem = smem;
+  c.stream = s;
+  return launch(c, scan_bwd_kernel<T, CW, NT>, q, pl);
+}
+
+template <typename T>
+cudaError_t bwd_all(const ScanCall& q, cudaStream_t s) {
+  const BwdLayout L = bwd_layout(q);
+  cudaError_t e = cudaSuccess;
+  if (L.sp.splits > 1) e = scan_carry_launch(q, L.sp, true, q.ws + L.carry, s);
+  if (e == cudaSuccess)
+    e = by_tiles(q.N, [&](auto CW, auto NT) {
+      return run_bwd<T, decltype(CW)::value, decltype(NT)::value>(q, L, s);
+    });
+  if (e == cudaSuccess && L.tiles > 1) {
+    const size_t count = static_cast<size_t>(q.K) * q.B * q.G * q.N;
+    const size_t bc = static_cast<size_t>(L.tiles) * count;
+    const float* pB = q.ws + L.bc;
+    const float* pC = pB + ((bc + 3) & ~static_cast<size_t>(3));
+    LaunchCfg c;
+    const size_t blocks = (count + 255) / 256;
+    c.grid = dim3(static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16), 2);
+    c.block = dim3(256);
+    c.stream = s;
+    c.pdl = true;
+    e = launch(c, scan_bc_kernel<T>, pB, pC, L.tiles, count, static_cast<T*>(q.dB),
+               static_cast<T*>(q.dC));
+  }
+  if (e == cudaSuccess)
+    e = reduce_axis0_rows_launch(q.ws + L.params, L.sp.splits * q.B, q.D * (q.N + 2), q.N + 2, q.N,
+                                 q.dA, q.dskip, s, true, q.ddt_bias);
+  return e;
+}
+
+}  // namespace
+
+size_t scan_bwd_ws_floats(const ScanCall& q) { return bwd_layout(q).total; }
+
+cudaError_t scan_bwd_launch(const ScanCall& q, cudaStream_t s) {
+  return q.bf16 ? bwd_all<__nv_bfloat16>(q, s) : bwd_all<float>(q, s);
+}
+
+}  // namespace cfc

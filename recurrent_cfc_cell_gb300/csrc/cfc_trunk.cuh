@@ -1,0 +1,125 @@
+// cfc_trunk.cuh -- device helpers of the trunk operators (layer norm, dropout, causal
+// convolution, selective scan): 8-column loads and stores of fp32 or bf16 activations, the
+// activations' functions, and the counter-based generator.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cfc_ptx.cuh"
+
+namespace cfc {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Eight consecutive activations as fp32: 32 bytes of fp32 or 16 bytes of bf16 in one load
+// (p aligned to that size).
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint4 r;
+  r.x = bf16x2_rn(v[0], v[1]);
+  r.y = bf16x2_rn(v[2], v[3]);
+  r.z = bf16x2_rn(v[4], v[5]);
+  r.w = bf16x2_rn(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = r;
+}
+
+// 2^v, a few ulp, 0 for v below the normal range.
+__device__ __forceinline__ float exp2_f(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// ln(1 + e^v) = max(v, 0) + ln(1 + t), t = e^-|v| in (0, 1].  ln(1 + t) = 2 artanh(s) with
+// s = t / (2 + t) <= 1/3: the odd series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14 leaves
+// 2 s^17 / 17 < 2^-26 of the sum at s = 1/3, and keeps full relative precision for small t,
+// where 1 + t would lose it.
+__device__ __forceinline__ float softplus_f(float v) {
+  const float t = __expf(-fabsf(v));
+  const float s = __fdividef(t, 2.f + t);
+  const float q = s * s;
+  float p = 1.f / 15.f;
+  p = fmaf(p, q, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  return fmaxf(v, 0.f) + 2.f * s * p;
+}
+
+// Philox 4x32, ten rounds (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as
+// 1, 2, 3", 2011): 128 random bits from a 128-bit counter and a 64-bit key.
+__device__ __forceinline__ uint4 philox4x32(uint4 c, uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint32_t h0 = __umulhi(c.x, 0xD2511F53u), l0 = c.x * 0xD2511F53u;
+    const uint32_t h1 = __umulhi(c.z, 0xCD9E8D57u), l1 = c.z * 0xCD9E8D57u;
+    c = make_uint4(h1 ^ c.y ^ k0, l1, h0 ^ c.w ^ k1, l0);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return c;
+}
+
+// Key and offset of a dropout call, read from its device-side {seed, offset} pair.
+struct DropKey {
+  uint32_t k0, k1, o0, o1;
+};
+__device__ __forceinline__ DropKey drop_key(const unsigned long long* rng) {
+  const unsigned long long s = rng[0], o = rng[1];
+  return {static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32), static_cast<uint32_t>(o),
+          static_cast<uint32_t>(o >> 32)};
+}
+
+// Which of the eight columns 8 * group .. 8 * group + 7 of `row` are kept (bit j: column
+// 8 * group + j): its 16-bit piece of the generator's output, lowest first, is >= cut.
+// Sixteen bits an element hold the drop probability to 2^-17 and cost one generator call for
+// eight elements; the scale uses the held probability, so the expectation is exact.
+__device__ __forceinline__ uint32_t keep_mask8(const DropKey& k, uint32_t row, uint32_t group,
+                                               uint32_t cut) {
+  const uint4 r = philox4x32(make_uint4(group, row, k.o0, k.o1), k.k0, k.k1);
+  uint32_t m = 0;
+  m |= ((r.x & 0xffffu) >= cut) ? 1u : 0u;
+  m |= ((r.x >> 16) >= cut) ? 2u : 0u;
+  m |= ((r.y & 0xffffu) >= cut) ? 4u : 0u;
+  m |= ((r.y >> 16) >= cut) ? 8u : 0u;
+  m |= ((r.z & 0xffffu) >= cut) ? 16u : 0u;
+  m |= ((r.z >> 16) >= cut) ? 32u : 0u;
+  m |= ((r.w & 0xffffu) >= cut) ? 64u : 0u;
+  m |= ((r.w >> 16) >= cut) ? 128u : 0u;
+  return m;
+}
+
+}  // namespace cfc
