@@ -291,13 +291,13 @@ size_t scan_bwd_ws_floats(const ScanCall& q);
 cudaError_t scan_fwd_launch(const ScanCall& q, cudaStream_t s);
 cudaError_t scan_bwd_launch(const ScanCall& q, cudaStream_t s);
 cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s);
-// Splits of the steps over CTAs (1: none) for the forward and the backward recurrence, and the
-// pass that carries the state (or its gradient) over the splits: on return carry
+// Splits of the steps over CTAs (1: none) so that there are about `warps_wanted` warps of 32
+// channels and 16 states, for the forward and the backward recurrence, and the pass that carries the state (or its gradient) over the splits: on return carry
 // [splits][B][D][N] holds what enters each split.
 struct ScanSplit {
   int splits, steps;               // steps per split, a multiple of 2 kScanPeriod
 };
-ScanSplit scan_split(const ScanCall& q, int channels_per_warp, int warps_wanted);
+ScanSplit scan_split(const ScanCall& q, int warps_wanted);
 size_t scan_carry_floats(const ScanCall& q, const ScanSplit& sp);
 cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool reverse, float* carry,
                               cudaStream_t s);

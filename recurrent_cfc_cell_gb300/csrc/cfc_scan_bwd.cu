@@ -12,10 +12,11 @@
 // that many steps from the last: forwards through the chunk from its kept state (the sums with
 // h_t: y, dC), leaving q_t in shared memory, then backwards (everything with e_t).
 //
-// A lane holds four channels times four states, and a warp 32 channels times 16 states: the sums
-// over states (y, e B, e A q) then cross four lanes and the sums over channels (dB, dC) eight,
-// each by exchanging halves, so that a step of 512 state updates takes 17 shuffles; with one
-// channel's sixteen states to a lane the sums over channels alone would take 31.  What a step
+// A lane holds four channels times four states (its arithmetic in packed pairs of channels), and a
+// warp 32 channels times 16 states: the sums over states (y, e B, e A q) then cross four lanes and
+// the sums over channels (dB, dC) eight, each by exchanging halves, so that a step of 512 state
+// updates takes 17 shuffles; with one channel's sixteen states to a lane the sums over channels
+// alone would take 31.  What a step
 // needs per channel (d, x, r and the gate's and softplus's derivatives) is formed once per
 // chunk, a thread a value, and read back four channels at a time.  NT warps side by side hold up
 // to 16 NT states, CW warps 32 CW channels.  Sums over warps, channel tiles, sequences and
@@ -35,10 +36,11 @@ struct Shape {
   static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = 32 * CW, NP = 16 * NT;
   // Shared memory, in floats.
   static constexpr int kPer = T8 * CH;                  // one value per (step, channel)
-  static constexpr int oD = 0, oX = oD + kPer, oR = oX + kPer, oZ = oR + kPer, oS = oZ + kPer;
+  static constexpr int oD = 0, oU = oD + kPer, oR = oU + kPer;  // d, d x, r
+  static constexpr int oX = oR + kPer, oZ = oX + kPer, oS = oZ + kPer;
   static constexpr int oY = oS + kPer, oV = oY + NT * kPer, oW = oV + NT * kPer;
-  static constexpr int oB = oW + NT * kPer, oC = oB + T8 * NP;
-  static constexpr int oDB = oC + T8 * NP, oDC = oDB + CW * T8 * NP;
+  static constexpr int oB = oW + NT * kPer, oC = oB + 2 * T8 * NP;  // every value twice
+  static constexpr int oDB = oC + 2 * T8 * NP, oDC = oDB + CW * T8 * NP;
   static constexpr int oQ = oDC + CW * T8 * NP;         // [warp][step][4][lane][4]
   static constexpr int kFloats = oQ + kWarps * T8 * 512;
 };
@@ -102,42 +104,45 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N;
   const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
 
-  // This lane's states: channels c0 .. c0 + 3 of the tile, states n0 .. n0 + 3.
+  // This lane's states: channels c0 .. c0 + 3 of the tile, states n0 .. n0 + 3, in pairs of
+  // channels: v[s][p] holds channels c0 + 2 p and c0 + 2 p + 1 of state n0 + s.
   const int c0 = cw * 32 + (lane >> 2) * 4, n0 = nt * 16 + (lane & 3) * 4;
-  float2 A2[4][2], e[4][2], dA[4][2];
+  float2 A2[4][2], e[4][2], dA[4][2], h[4][2];
   auto in_state = [&](int c, int s) { return t_base + c0 + c < pl.per_group && n0 + s < q.N; };
   auto state_at = [&](int c) {  // offset of state n0 of channel c in a [B][D][N] plane
     return (static_cast<size_t>(b) * q.D + d_base + t_base + c0 + c) * q.N + n0;
   };
-  // Four states of channel c from a plane, zero outside.
+  // The lane's states of a plane, zero outside.
   const bool quad = q.N % 4 == 0;
-  auto load_states = [&](const float* p, int c, float2 (&v)[2]) {
-    v[0] = v[1] = make_float2(0.f, 0.f);
-    if (!in_state(c, 0) || p == nullptr) return;
-    const float* at = p + state_at(c);
-    if (quad) {
-      const float4 r = *reinterpret_cast<const float4*>(at);
-      v[0] = make_float2(r.x, r.y);
-      v[1] = make_float2(r.z, r.w);
-    } else {
-      v[0].x = at[0];
-      if (n0 + 1 < q.N) v[0].y = at[1];
-      if (n0 + 2 < q.N) v[1].x = at[2];
-      if (n0 + 3 < q.N) v[1].y = at[3];
+  auto load_states = [&](const float* p, float2 (&v)[4][2]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float r[4] = {0.f, 0.f, 0.f, 0.f};
+      if (p != nullptr && in_state(c, 0)) {
+        const float* at = p + state_at(c);
+        if (quad) {
+          const float4 f = *reinterpret_cast<const float4*>(at);
+          r[0] = f.x; r[1] = f.y; r[2] = f.z; r[3] = f.w;
+        } else {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (n0 + s < q.N) r[s] = at[s];
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) (c & 1 ? v[s][c / 2].y : v[s][c / 2].x) = r[s];
     }
   };
-  const float* c_in = pl.carry ? pl.carry + split * plane : q.dh_last;
+  load_states(pl.carry ? pl.carry + split * plane : q.dh_last, e);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    load_states(c_in, c, e[c]);
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const float av = in_state(c, s)
           ? q.A[static_cast<size_t>(d_base + t_base + c0 + c) * q.N + n0 + s] * kLog2e : 0.f;
-      (s & 1 ? A2[c][s / 2].y : A2[c][s / 2].x) = av;
+      (c & 1 ? A2[s][c / 2].y : A2[s][c / 2].x) = av;
+      (c & 1 ? dA[s][c / 2].y : dA[s][c / 2].x) = 0.f;
     }
-    dA[c][0] = dA[c][1] = make_float2(0.f, 0.f);
-  }
   float dskip = 0.f, dbias = 0.f;
   float* const hist = sm + Sh::oQ + warp * (T8 * 512) + lane * 4;
 
@@ -165,133 +170,167 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   for (int t = lo + chunks * T8; t < hi; ++t)
     for (int n = tid; n < q.N; n += Sh::kThreads) put_bc(t, n, 0.f, 0.f);
 
+  // The next chunk's inputs, as they are stored.
+  constexpr int kEl = (T8 + NT - 1) / NT, kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
+  T rx[kEl], rt[kEl], rz[kEl], rg[kEl], rB[kBC], rC[kBC];
+  const T none = from_f32<T>(0.f);
+  auto fetch = [&](int t0) {
+    const T* x0 = xp + t0 * q.x_t;
+    const T* d0 = tp + t0 * q.dt_t;
+    const T* g0 = gp + t0 * q.dy_t;
+    const T* z0 = zp ? zp + t0 * q.z_t : nullptr;
+#pragma unroll
+    for (int i = 0; i < kEl; ++i) {
+      const int k = tf + i * NT;
+      const bool in = livef && k < T8 && t0 + k < end;
+      rx[i] = in ? x0[k * q.x_t] : none;
+      rt[i] = in ? d0[k * q.dt_t] : none;
+      rg[i] = in ? g0[k * q.dy_t] : none;
+      rz[i] = (in && zp) ? z0[k * q.z_t] : none;
+    }
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+      const int at = tid + i * Sh::kThreads, k = at / Sh::NP, n = at % Sh::NP;
+      const bool in = k < T8 && t0 + k < end && n < q.N;
+      rB[i] = in ? Bp[(t0 + k) * q.Bm_t + n] : none;
+      rC[i] = in ? Cp[(t0 + k) * q.Cm_t + n] : none;
+    }
+  };
+  if (chunks > 0) {
+    fetch(lo + (chunks - 1) * T8);
+    load_states(q.states + ((lo + (chunks - 1) * T8) / T8) * plane, h);
+  }
+
   for (int ck = chunks - 1; ck >= 0; --ck) {
     const int t0 = lo + ck * T8;
-    // ---- per channel and step: d, x, r, dy silu'(z), sigmoid(dt + bias)
+    // ---- per channel and step: d, d x, r, and for the end x, dy silu'(z), sigmoid(dt + bias)
 #pragma unroll
-    for (int i = 0; i < (T8 + NT - 1) / NT; ++i) {
-      const int k = tf + i * NT, t = t0 + k;
-      if (k >= T8) break;
-      float dv = 0.f, xv = 0.f, rv = 0.f, zf = 0.f, sg = 0.f;
-      if (livef && t < end) {
-        const float raw = to_f32(tp[t * q.dt_t]) + bias;
-        xv = to_f32(xp[t * q.x_t]);
-        const float g = to_f32(gp[t * q.dy_t]);
-        dv = q.softplus ? softplus_f(raw) : raw;
-        sg = q.softplus ? sigmoid_fast(raw) : 1.f;
-        rv = g;
-        if (zp) {
-          const float z = to_f32(zp[t * q.z_t]);
-          const float s = sigmoid_fast(z);
-          rv = g * z * s;
-          zf = g * s * fmaf(z, 1.f - s, 1.f);
+    for (int j = 0; j < (kEl + 1) / 2; ++j) {
+      const int i1 = 2 * j + 1 < kEl ? 2 * j + 1 : 2 * j;
+      const float2 raw = make_float2(to_f32(rt[2 * j]) + bias, to_f32(rt[i1]) + bias);
+      const float2 d2 = q.softplus ? softplus2_f(raw) : raw;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int i = 2 * j + m, k = tf + i * NT;
+        if (i < kEl && k < T8) {
+          // Steps past the end leave the state and its gradient alone: d = 0, r = 0.
+          const bool in = t0 + k < end;
+          const float dv = in ? (m ? d2.y : d2.x) : 0.f, xv = to_f32(rx[i]);
+          float rv = to_f32(rg[i]), zf = 0.f;
+          if (zp) {
+            const float z = to_f32(rz[i]), s = sigmoid_fast(z), gs = rv * s;
+            rv = gs * z;
+            zf = gs * fmaf(z, 1.f - s, 1.f);
+          }
+          const int at = k * Sh::CH + chf;
+          sm[Sh::oD + at] = dv;
+          sm[Sh::oU + at] = dv * xv;
+          sm[Sh::oR + at] = rv;
+          sm[Sh::oX + at] = xv;
+          sm[Sh::oZ + at] = zf;
+          sm[Sh::oS + at] = !in ? 0.f : q.softplus ? sigmoid_fast(m ? raw.y : raw.x) : 1.f;
         }
       }
-      const int at = k * Sh::CH + chf;
-      sm[Sh::oD + at] = dv;
-      sm[Sh::oX + at] = xv;
-      sm[Sh::oR + at] = rv;
-      sm[Sh::oZ + at] = zf;
-      sm[Sh::oS + at] = sg;
     }
-    for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
-      const int k = i / Sh::NP, n = i % Sh::NP;
-      const bool in = t0 + k < end && n < q.N;
-      sm[Sh::oB + i] = in ? to_f32(Bp[(t0 + k) * q.Bm_t + n]) : 0.f;
-      sm[Sh::oC + i] = in ? to_f32(Cp[(t0 + k) * q.Cm_t + n]) : 0.f;
-    }
-    float2 h[4][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) load_states(q.states + (t0 / T8) * plane, c, h[c]);
+    for (int i = 0; i < kBC; ++i) {
+      const int at = tid + i * Sh::kThreads;
+      if (at < T8 * Sh::NP) {
+        const float bv = to_f32(rB[i]), cv = to_f32(rC[i]);
+        reinterpret_cast<float2*>(sm + Sh::oB)[at] = make_float2(bv, bv);
+        reinterpret_cast<float2*>(sm + Sh::oC)[at] = make_float2(cv, cv);
+      }
+    }
     __syncthreads();
+    if (ck > 0) fetch(t0 - T8);
+
+    // What both directions read of a step: d, d x and r of the lane's four channels in pairs, B
+    // and C of its four states, each twice.
+    float2 d2[2], u2[2], r2[2], B2[4], C2[4];
+    auto read = [&](int k) {
+      const float4 dv = *reinterpret_cast<const float4*>(&sm[Sh::oD + k * Sh::CH + c0]);
+      const float4 uv = *reinterpret_cast<const float4*>(&sm[Sh::oU + k * Sh::CH + c0]);
+      const float4 rv = *reinterpret_cast<const float4*>(&sm[Sh::oR + k * Sh::CH + c0]);
+      d2[0] = make_float2(dv.x, dv.y); d2[1] = make_float2(dv.z, dv.w);
+      u2[0] = make_float2(uv.x, uv.y); u2[1] = make_float2(uv.z, uv.w);
+      r2[0] = make_float2(rv.x, rv.y); r2[1] = make_float2(rv.z, rv.w);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 bv = *reinterpret_cast<const float4*>(&sm[Sh::oB + 2 * (k * Sh::NP + n0) + 4 * i]);
+        const float4 cv = *reinterpret_cast<const float4*>(&sm[Sh::oC + 2 * (k * Sh::NP + n0) + 4 * i]);
+        B2[2 * i] = make_float2(bv.x, bv.y); B2[2 * i + 1] = make_float2(bv.z, bv.w);
+        C2[2 * i] = make_float2(cv.x, cv.y); C2[2 * i + 1] = make_float2(cv.z, cv.w);
+      }
+    };
+    const float2 zero2 = make_float2(0.f, 0.f);
 
     // ---- forwards through the chunk
 #pragma unroll 2
     for (int k = 0; k < T8; ++k) {
-      const float4 d4 = *reinterpret_cast<const float4*>(&sm[Sh::oD + k * Sh::CH + c0]);
-      const float4 x4 = *reinterpret_cast<const float4*>(&sm[Sh::oX + k * Sh::CH + c0]);
-      const float4 r4 = *reinterpret_cast<const float4*>(&sm[Sh::oR + k * Sh::CH + c0]);
-      const float4 B4 = *reinterpret_cast<const float4*>(&sm[Sh::oB + k * Sh::NP + n0]);
-      const float4 C4 = *reinterpret_cast<const float4*>(&sm[Sh::oC + k * Sh::NP + n0]);
-      const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
-      const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
-      const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-      const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-      float y[4];
-      float2 dc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      read(k);
+      float2 y2[2] = {zero2, zero2}, dc[4], qq[4][2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 d2 = make_float2(dv[c], dv[c]);
-        const float2 u2 = make_float2(dv[c] * xv[c], dv[c] * xv[c]);
-        const float2 r2 = make_float2(rv[c], rv[c]);
-        float2 y2 = make_float2(0.f, 0.f), qq[2];
+      for (int s = 0; s < 4; ++s) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float2 m = __fmul2_rn(d2, A2[c][s]);
-          qq[s] = __fmul2_rn(make_float2(exp2_f(m.x), exp2_f(m.y)), h[c][s]);
-          h[c][s] = fma2(u2, Bv[s], qq[s]);
-          y2 = fma2(h[c][s], Cv[s], y2);
-          dc[s] = fma2(r2, h[c][s], dc[s]);
+        for (int p = 0; p < 2; ++p) {
+          const float2 m = __fmul2_rn(d2[p], A2[s][p]);
+          qq[s][p] = __fmul2_rn(make_float2(exp2_f(m.x), exp2_f(m.y)), h[s][p]);
+          h[s][p] = fma2(u2[p], B2[s], qq[s][p]);
+          y2[p] = fma2(h[s][p], C2[s], y2[p]);
         }
-        y[c] = y2.x + y2.y;
-        *reinterpret_cast<float4*>(hist + (k * 4 + c) * 128) =
-            make_float4(qq[0].x, qq[0].y, qq[1].x, qq[1].y);
+        dc[s] = fma2(r2[1], h[s][1], __fmul2_rn(r2[0], h[s][0]));
+        *reinterpret_cast<float4*>(hist + (k * 4 + s) * 128) =
+            make_float4(qq[s][0].x, qq[s][0].y, qq[s][1].x, qq[s][1].y);
       }
+      const float y[4] = {y2[0].x, y2[0].y, y2[1].x, y2[1].y};
       sm[Sh::oY + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(y, lane);
-      const float dcs[4] = {dc[0].x, dc[0].y, dc[1].x, dc[1].y};
+      const float dcs[4] = {dc[0].x + dc[0].y, dc[1].x + dc[1].y, dc[2].x + dc[2].y, dc[3].x + dc[3].y};
       const float sc = sum_channels(dcs, lane);
       if (!(lane & 4)) sm[Sh::oDC + (cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sc;
     }
+    // The next chunk's kept state, on its way during the walk back.
+    if (ck > 0) load_states(q.states + (t0 / T8 - 1) * plane, h);
     // ---- and back
 #pragma unroll 2
     for (int k = T8 - 1; k >= 0; --k) {
-      const float4 d4 = *reinterpret_cast<const float4*>(&sm[Sh::oD + k * Sh::CH + c0]);
-      const float4 x4 = *reinterpret_cast<const float4*>(&sm[Sh::oX + k * Sh::CH + c0]);
-      const float4 r4 = *reinterpret_cast<const float4*>(&sm[Sh::oR + k * Sh::CH + c0]);
-      const float4 B4 = *reinterpret_cast<const float4*>(&sm[Sh::oB + k * Sh::NP + n0]);
-      const float4 C4 = *reinterpret_cast<const float4*>(&sm[Sh::oC + k * Sh::NP + n0]);
-      const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
-      const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
-      const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-      const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-      float v[4], w[4];
-      float2 db[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      read(k);
+      float2 v2[2] = {zero2, zero2}, w2[2] = {zero2, zero2}, db[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 d2 = make_float2(dv[c], dv[c]);
-        const float2 u2 = make_float2(dv[c] * xv[c], dv[c] * xv[c]);
-        const float2 r2 = make_float2(rv[c], rv[c]);
-        const float4 q4 = *reinterpret_cast<const float4*>(hist + (k * 4 + c) * 128);
+      for (int s = 0; s < 4; ++s) {
+        const float4 q4 = *reinterpret_cast<const float4*>(hist + (k * 4 + s) * 128);
         const float2 qq[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
-        float2 v2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
+        float2 et[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float2 m = __fmul2_rn(d2, A2[c][s]);
+        for (int p = 0; p < 2; ++p) {
+          const float2 m = __fmul2_rn(d2[p], A2[s][p]);
           const float2 a = make_float2(exp2_f(m.x), exp2_f(m.y));
-          const float2 et = fma2(r2, Cv[s], e[c][s]);
-          const float2 p = __fmul2_rn(et, qq[s]);
-          dA[c][s] = fma2(p, d2, dA[c][s]);
-          w2 = fma2(p, A2[c][s], w2);
-          v2 = fma2(et, Bv[s], v2);
-          db[s] = fma2(et, u2, db[s]);
-          e[c][s] = __fmul2_rn(a, et);
+          et[p] = fma2(r2[p], C2[s], e[s][p]);
+          const float2 eq = __fmul2_rn(et[p], qq[p]);
+          dA[s][p] = fma2(eq, d2[p], dA[s][p]);
+          w2[p] = fma2(eq, A2[s][p], w2[p]);
+          v2[p] = fma2(et[p], B2[s], v2[p]);
+          e[s][p] = __fmul2_rn(a, et[p]);
         }
-        v[c] = v2.x + v2.y;
-        w[c] = w2.x + w2.y;
+        db[s] = fma2(et[1], u2[1], __fmul2_rn(et[0], u2[0]));
       }
+      const float v[4] = {v2[0].x, v2[0].y, v2[1].x, v2[1].y};
+      const float w[4] = {w2[0].x, w2[0].y, w2[1].x, w2[1].y};
       sm[Sh::oV + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(v, lane);
       sm[Sh::oW + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(w, lane);
-      const float dbs[4] = {db[0].x, db[0].y, db[1].x, db[1].y};
+      const float dbs[4] = {db[0].x + db[0].y, db[1].x + db[1].y, db[2].x + db[2].y, db[3].x + db[3].y};
       const float sb = sum_channels(dbs, lane);
       if (!(lane & 4)) sm[Sh::oDB + (cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sb;
     }
     __syncthreads();
 
     // ---- per channel and step: the gradients of the inputs
+    T* const dx0 = dxp + t0 * q.dx_t;
+    T* const dt0 = dtp + t0 * q.ddt_t;
+    T* const dz0 = dzp ? dzp + t0 * q.dz_t : nullptr;
 #pragma unroll
-    for (int i = 0; i < (T8 + NT - 1) / NT; ++i) {
-      const int k = tf + i * NT, t = t0 + k;
-      if (k >= T8 || t >= hi) break;
+    for (int i = 0; i < kEl; ++i) {
+      const int k = tf + i * NT;
+      if (k >= T8 || t0 + k >= hi) break;
       const int at = k * Sh::CH + chf;
       float y = 0.f, v = 0.f, w = 0.f;
 #pragma unroll
@@ -305,9 +344,9 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       dskip = fmaf(rv, xv, dskip);
       dbias += ddt;
       if (livef) {
-        dxp[t * q.dx_t] = from_f32<T>(fmaf(sm[Sh::oD + at], v, skip * rv));
-        dtp[t * q.ddt_t] = from_f32<T>(ddt);
-        if (dzp) dzp[t * q.dz_t] = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
+        dx0[k * q.dx_t] = from_f32<T>(fmaf(sm[Sh::oD + at], v, skip * rv));
+        dt0[k * q.ddt_t] = from_f32<T>(ddt);
+        if (dzp) dz0[k * q.dz_t] = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
       }
     }
     for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
@@ -331,9 +370,9 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (!in_state(c, s)) continue;
-      if (split == 0 && q.dh0) q.dh0[state_at(c) + s] = s & 1 ? e[c][s / 2].y : e[c][s / 2].x;
+      if (split == 0 && q.dh0) q.dh0[state_at(c) + s] = c & 1 ? e[s][c / 2].y : e[s][c / 2].x;
       params[static_cast<size_t>(d_base + t_base + c0 + c) * (q.N + 2) + n0 + s] =
-          s & 1 ? dA[c][s / 2].y : dA[c][s / 2].x;
+          c & 1 ? dA[s][c / 2].y : dA[s][c / 2].x;
     }
   }
   // The NT threads of a channel, in order (the chunk loop ended with a barrier; the region of
@@ -387,14 +426,12 @@ struct BwdLayout {
 
 BwdLayout bwd_layout(const ScanCall& q) {
   BwdLayout L{};
-  int ch = 32, warps = 4;
+  int ch = 32;
   (void)by_tiles(q.N, [&](auto CW, auto NT) {
     ch = Shape<decltype(CW)::value, decltype(NT)::value>::CH;
-    warps = Shape<decltype(CW)::value, decltype(NT)::value>::kWarps;
     return cudaSuccess;
   });
-  // One CTA covers `ch` channels with `warps` warps; eight warps an SM fill it.
-  L.sp = scan_split(q, ch, 152 * 8 / warps);
+  L.sp = scan_split(q, 152 * 8);  // eight warps an SM fill it
   L.tiles = (q.D / q.G + ch - 1) / ch;
   auto up = [](size_t v) { return (v + 3) & ~static_cast<size_t>(3); };
   L.params = 0;

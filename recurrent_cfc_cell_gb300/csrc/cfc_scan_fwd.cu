@@ -8,13 +8,20 @@
 // per channel, with N states; B and C are shared by the channels of a group.  A sequence of
 // length L < K ends at L: its state stays and its later outputs are 0.
 //
-// A lane holds S states of one channel in registers and LPC lanes share a channel, so a warp
-// covers 32 / LPC neighbouring channels and its loads of x, dt and z are consecutive.  exp is
-// 2^(d A log2 e), and the state arithmetic runs in pairs of states (packed FMA).  B and C of a
-// chunk of steps sit in shared memory as fp32 and are read by broadcast; the next chunk's
-// inputs are in registers while this one is computed.  With few channels and many steps the
-// steps are split over CTAs: a first pass runs every split from a zero state, the splits'
-// end states are folded in order, and the second pass starts each split from its true state.
+// A warp holds 32 neighbouring channels times S (4, 8 or 16) states, a channel to a lane, its
+// states in registers; NT warps side by side hold up to 16 NT states, CW warps 32 CW channels.
+// exp is 2^(d A log2 e), and the state arithmetic runs in pairs of states (packed FMA).  The steps
+// go in chunks: what a step needs per channel (d and d x) is formed once, a thread a value, and
+// put in shared memory with the chunk's B and C as fp32 (read by broadcast); the warps then run
+// the recurrence over the chunk, and the sums over states come back through shared memory to the
+// threads that formed the values, which hold x and z for the skip and the gate.  The next
+// chunk's inputs are loaded meanwhile.
+//
+// Bound by arithmetic at 16 states: a state's step takes one exponential, two multiplications
+// and two multiply-adds, so both the exponential unit (32 a clock and SM) and the FMA pipe (128)
+// allow 32 states a clock and SM.  With few channels and many steps the steps are split over
+// CTAs: a first pass runs every split from a zero state, the splits' end states are folded in
+// order, and the second pass starts each split from its true state.
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
@@ -22,41 +29,45 @@
 namespace cfc {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kTC = 8;  // steps of a chunk
-static_assert(kScanPeriod % kTC == 0 || kTC % kScanPeriod == 0, "chunks and kept states line up");
+constexpr int kT = kScanPeriod;  // steps of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 
-// What a lane group's tile is: channels of one group of B / C.
 struct Tile {
-  int tiles_per_group, per_group;  // per_group: channels D / G
+  int tiles_per_group, per_group;  // channel tiles and channels of a group of B / C
 };
 
-// MODE 0: outputs.  MODE 1: the end state of each split from a zero state (forward), and the sum
-// of its steps.  MODE 2: the same for the gradient, running the steps backwards.
-template <typename T, int S, int LPC, int MODE>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanCall q, const Tile tl,
-                                                            const int steps, float* carry,
-                                                            float* dsum) {
-  constexpr int NP = S * LPC;            // padded states
-  constexpr int CH = kThreads / LPC;     // channels of a CTA
-  constexpr int kPer = (kTC * NP + kThreads - 1) / kThreads;  // staged values per thread and array
-  __shared__ __align__(16) float sB[kTC][NP];
-  __shared__ __align__(16) float sC[MODE == 1 ? 1 : kTC][MODE == 1 ? 4 : NP];
-  const int tid = threadIdx.x;
+// MODE 0: outputs.  MODE 1: the end state of each split from a zero state, and the sum of its
+// steps.  MODE 2: the same for the gradient carried backwards, c <- a_t (c + C_t r_t) with r_t the
+// gradient of y_t before the gate (it reads dy in the place of x).
+template <typename T, int S, int CW, int NT, int MODE>
+__global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q, const Tile tl,
+                                                                const int steps, float* carry,
+                                                                float* dsum) {
+  constexpr int kThreads = 32 * CW * NT, CH = 32 * CW, NP = S * NT;
+  constexpr int kEl = (kT + NT - 1) / NT;                      // per-channel values of a thread
+  constexpr int kEl2 = (kEl + 1) / 2;
+  constexpr int kBC = (kT * NP + kThreads - 1) / kThreads;     // B (or C) values of a thread
+  constexpr bool kGate = MODE != 1;
+  __shared__ __align__(16) float2 sDU[kT][CH];
+  __shared__ __align__(16) float sB[kT][NP];
+  __shared__ __align__(16) float sC[MODE == 0 ? kT : 1][NP];
+  __shared__ float sY[MODE == 0 ? NT : 1][MODE == 0 ? kT : 1][CH];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int nt = warp % NT, cw = warp / NT;
   const int group = blockIdx.x / tl.tiles_per_group;
-  const int in_group = (blockIdx.x % tl.tiles_per_group) * CH + tid / LPC;
-  const bool live = in_group < tl.per_group;
-  const int d = group * tl.per_group + (live ? in_group : 0);
+  const int t_base = (blockIdx.x % tl.tiles_per_group) * CH;
   const int b = blockIdx.y, split = blockIdx.z;
-  const int n0 = (tid % LPC) * S;
   const int len = q.lengths ? min(max(q.lengths[b], 0), q.K) : q.K;
   const int lo = split * steps;
   const int hi = min(q.K, lo + steps);
   const int end = min(hi, len);  // steps [lo, end) count
-  const size_t cn = (static_cast<size_t>(b) * q.D + d) * q.N + n0;  // this lane's states
   const size_t plane = static_cast<size_t>(q.B) * q.D * q.N;
 
+  // This lane's channel and states in the recurrence.
+  const int ch = cw * 32 + lane, n0 = nt * S;
+  const bool live = t_base + ch < tl.per_group;
+  const int d = group * tl.per_group + (live ? t_base + ch : 0);
+  const size_t cn = (static_cast<size_t>(b) * q.D + d) * q.N + n0;
   float2 A2[S / 2], h[S / 2];
 #pragma unroll
   for (int i = 0; i < S; ++i) {
@@ -67,142 +78,189 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanCall q, co
       if (carry) hv = carry[split * plane + cn + i];
       else if (q.h0) hv = q.h0[cn + i];
     }
-    if (i & 1) {
-      A2[i / 2].y = av;
-      h[i / 2].y = hv;
-    } else {
-      A2[i / 2].x = av;
-      h[i / 2].x = hv;
-    }
+    (i & 1 ? A2[i / 2].y : A2[i / 2].x) = av;
+    (i & 1 ? h[i / 2].y : h[i / 2].x) = hv;
   }
-  const float bias = q.dt_bias ? q.dt_bias[d] : 0.f;
-  const float skip = q.skip ? q.skip[d] : 0.f;
-  const T* xp = static_cast<const T*>(MODE == 2 ? q.dy : q.x) + (MODE == 2 ? b * q.dy_b : b * q.x_b) + d;
-  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + d;
-  const T* zp = (q.z && MODE != 1) ? static_cast<const T*>(q.z) + b * q.z_b + d : nullptr;
-  const long long x_t = MODE == 2 ? q.dy_t : q.x_t;
-  const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N;
-  const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
-  T* yp = static_cast<T*>(q.y) + b * q.y_b + d;
-
-  // Chunks of kTC steps, forwards or backwards; chunk c covers steps lo + c kTC ...
-  const int chunks = end > lo ? (end - lo + kTC - 1) / kTC : 0;
-  // The next chunk's inputs, as they are stored (converted when their chunk begins, so that
-  // nothing waits for the loads before that).
-  T rx[kTC], rt[kTC], rz[kTC], rB[kPer], rC[kPer];
-  const T none = from_f32<T>(0.f);
-  auto fetch = [&](int c) {
-    const int t0 = lo + c * kTC;
+  const bool octet = q.N % 8 == 0;
+  auto put_state = [&](float* p) {
+    if (!live) return;
+    if (S >= 8 && octet && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
 #pragma unroll
-    for (int i = 0; i < kTC; ++i) {
-      const bool in = t0 + i < end;
-      rx[i] = in ? xp[(t0 + i) * x_t] : none;
-      rt[i] = in ? tp[(t0 + i) * q.dt_t] : none;
-      rz[i] = (in && zp) ? zp[(t0 + i) * q.z_t] : none;
-    }
+      for (int i = 0; i < S / 8; ++i)
+        if (n0 + 8 * i < q.N) {
+          const float v[8] = {h[4 * i].x, h[4 * i].y, h[4 * i + 1].x, h[4 * i + 1].y,
+                              h[4 * i + 2].x, h[4 * i + 2].y, h[4 * i + 3].x, h[4 * i + 3].y};
+          store8(p + 8 * i, v);
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kThreads, t = e / NP, n = e % NP;
-      const bool in = t < kTC && t0 + t < end && n < q.N;
-      if (MODE != 2) rB[i] = in ? Bp[(t0 + t) * q.Bm_t + n] : none;
-      if (MODE != 1) rC[i] = in ? Cp[(t0 + t) * q.Cm_t + n] : none;
+      for (int i = 0; i < S; ++i)
+        if (n0 + i < q.N) p[i] = (i & 1) ? h[i / 2].y : h[i / 2].x;
     }
   };
-  float total = 0.f;  // sum of the split's steps
-  if (chunks > 0) fetch(MODE == 2 ? chunks - 1 : 0);
-  for (int cc = 0; cc < chunks; ++cc) {
-    const int c = MODE == 2 ? chunks - 1 - cc : cc;
-    const int t0 = lo + c * kTC;
-    float x[kTC], dt[kTC], z[kTC];
+
+  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...
+  const int chf = tid % CH, tf = tid / CH;
+  const bool livef = t_base + chf < tl.per_group;
+  const int df = group * tl.per_group + (livef ? t_base + chf : 0);
+  const float bias = q.dt_bias ? q.dt_bias[df] : 0.f;
+  const float skip = q.skip ? q.skip[df] : 0.f;
+  const bool gated = kGate && q.z != nullptr;
+  const long long x_t = MODE == 2 ? q.dy_t : q.x_t;
+  const T* xp = (MODE == 2 ? static_cast<const T*>(q.dy) + b * q.dy_b
+                           : static_cast<const T*>(q.x) + b * q.x_b) + df;
+  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + df;
+  const T* zp = gated ? static_cast<const T*>(q.z) + b * q.z_b + df : nullptr;
+  // MODE 2 reads C in the place of B.
+  const long long B_t = MODE == 2 ? q.Cm_t : q.Bm_t;
+  const T* Bp = (MODE == 2 ? static_cast<const T*>(q.Cm) + b * q.Cm_b
+                           : static_cast<const T*>(q.Bm) + b * q.Bm_b) +
+                static_cast<long long>(group) * q.N;
+  const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
+  T* yp = static_cast<T*>(q.y) + b * q.y_b + df;
+
+  // The next chunk's inputs, as they are stored (converted when their chunk begins, so that
+  // nothing waits for the loads before that).
+  T rx[kEl], rt[kEl], rz[kEl], rB[kBC], rC[kBC];
+  const T none = from_f32<T>(0.f);
+  auto fetch = [&](int t0) {
+    const T* x0 = xp + t0 * x_t;
+    const T* d0 = tp + t0 * q.dt_t;
+    const T* z0 = gated ? zp + t0 * q.z_t : nullptr;
 #pragma unroll
-    for (int i = 0; i < kTC; ++i) {
+    for (int i = 0; i < kEl; ++i) {
+      const int k = tf + i * NT;
+      const bool in = livef && k < kT && t0 + k < end;
+      rx[i] = in ? x0[k * x_t] : none;
+      rt[i] = in ? d0[k * q.dt_t] : none;
+      rz[i] = (in && gated) ? z0[k * q.z_t] : none;
+    }
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+      const int e = tid + i * kThreads, k = e / NP, n = e % NP;
+      const bool in = k < kT && t0 + k < end && n < q.N;
+      rB[i] = in ? Bp[(t0 + k) * B_t + n] : none;
+      if (MODE == 0) rC[i] = in ? Cp[(t0 + k) * q.Cm_t + n] : none;
+    }
+  };
+
+  float total = 0.f;  // sum of this thread's steps d
+  const int chunks = end > lo ? (end - lo + kT - 1) / kT : 0;
+  if (chunks > 0) fetch(lo + (MODE == 2 ? chunks - 1 : 0) * kT);
+  for (int cc = 0; cc < chunks; ++cc) {
+    const int t0 = lo + (MODE == 2 ? chunks - 1 - cc : cc) * kT;
+    // ---- per channel and step: d and d x (MODE 2: d and r)
+    float x[kEl], z[kEl];
+#pragma unroll
+    for (int i = 0; i < kEl; ++i) {
       x[i] = to_f32(rx[i]);
-      dt[i] = to_f32(rt[i]) + bias;
       z[i] = to_f32(rz[i]);
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kThreads;
-      if (e < kTC * NP) {
-        if (MODE != 2) (&sB[0][0])[e] = to_f32(rB[i]);
-        if (MODE != 1) (&sC[0][0])[e] = to_f32(rC[i]);
-      }
-    }
-    __syncthreads();
-    if (cc + 1 < chunks) fetch(MODE == 2 ? c - 1 : c + 1);
-    if (MODE == 0 && q.states != nullptr && t0 % kScanPeriod == 0 && live) {
-      float* st = q.states + (t0 / kScanPeriod) * plane + cn;
-      if (q.N % 4 == 0) {
+    for (int j = 0; j < kEl2; ++j) {
+      const int i0 = 2 * j, i1 = 2 * j + 1 < kEl ? 2 * j + 1 : 2 * j;
+      const float2 raw = make_float2(to_f32(rt[i0]) + bias, to_f32(rt[i1]) + bias);
+      const float2 dv = q.softplus ? softplus2_f(raw) : raw;
 #pragma unroll
-        for (int i = 0; i < S / 4; ++i)
-          if (n0 + 4 * i < q.N)
-            reinterpret_cast<float4*>(st)[i] =
-                make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
-      } else {
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-          if (n0 + i < q.N) st[i] = (i & 1) ? h[i / 2].y : h[i / 2].x;
-      }
-    }
-#pragma unroll
-    for (int ii = 0; ii < kTC; ++ii) {
-      const int i = MODE == 2 ? kTC - 1 - ii : ii;
-      if (t0 + i < end) {
-        const float dv = q.softplus ? softplus_f(dt[i]) : dt[i];
-        if (MODE != 0) total += dv;
-        const float2 d2 = make_float2(dv, dv);
-        if constexpr (MODE != 2) {
-          const float2 dx2 = make_float2(dv * x[i], dv * x[i]);
-          float2 y2 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int s = 0; s < S / 2; ++s) {
-            const float2 e = __fmul2_rn(d2, A2[s]);
-            const float2 a = make_float2(exp2_f(e.x), exp2_f(e.y));
-            const float2 Bv = reinterpret_cast<const float2*>(&sB[i][n0])[s];
-            h[s] = fma2(a, h[s], __fmul2_rn(dx2, Bv));
-            if constexpr (MODE == 0)
-              y2 = fma2(h[s], reinterpret_cast<const float2*>(&sC[i][n0])[s], y2);
+      for (int m = 0; m < 2; ++m) {
+        const int i = 2 * j + m;
+        const int k = tf + i * NT;
+        if (i < kEl && k < kT) {
+          // Steps past the end leave the state alone: d = 0, so a = 1 and nothing is added.
+          const float dd = t0 + k < end ? (m ? dv.y : dv.x) : 0.f;
+          float u = dd * x[i];
+          if (MODE == 2) {
+            u = x[i];
+            if (gated) u *= z[i] * sigmoid_fast(z[i]);
           }
-          if constexpr (MODE == 0) {
-            float y = y2.x + y2.y;
-#pragma unroll
-            for (int m = LPC / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-            y = fmaf(skip, x[i], y);
-            if (zp) y *= z[i] * sigmoid_fast(z[i]);
-            if (live && tid % LPC == 0) yp[(t0 + i) * q.y_t] = from_f32<T>(y);
-          }
-        } else {
-          // c <- a_t (c + C_t g_t), g_t the gradient of y_t before the gate
-          float g = x[i];
-          if (zp) g *= z[i] * sigmoid_fast(z[i]);
-          const float2 g2 = make_float2(g, g);
-#pragma unroll
-          for (int s = 0; s < S / 2; ++s) {
-            const float2 e = __fmul2_rn(d2, A2[s]);
-            const float2 a = make_float2(exp2_f(e.x), exp2_f(e.y));
-            h[s] = __fmul2_rn(a, fma2(g2, reinterpret_cast<const float2*>(&sC[i][n0])[s], h[s]));
-          }
+          sDU[k][chf] = make_float2(dd, u);
+          if (MODE != 0) total += dd;
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+      const int e = tid + i * kThreads;
+      if (e < kT * NP) {
+        (&sB[0][0])[e] = to_f32(rB[i]);
+        if (MODE == 0) (&sC[0][0])[e] = to_f32(rC[i]);
+      }
+    }
+    __syncthreads();
+    if (cc + 1 < chunks) fetch(MODE == 2 ? t0 - kT : t0 + kT);
+
+    // ---- the recurrence
+    if (MODE == 0 && q.states != nullptr) put_state(q.states + (t0 / kT) * plane + cn);
+#pragma unroll 4
+    for (int kk = 0; kk < kT; ++kk) {
+      const int k = MODE == 2 ? kT - 1 - kk : kk;
+      const float2 du = sDU[k][ch];
+      const float2 d2 = make_float2(du.x, du.x), u2 = make_float2(du.y, du.y);
+      const float4* B4 = reinterpret_cast<const float4*>(&sB[k][n0]);
+      const float4* C4 = reinterpret_cast<const float4*>(&sC[MODE == 0 ? k : 0][n0]);
+      float2 y2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < S / 4; ++s) {
+        const float4 bv = B4[s];
+        const float2 B2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
+        float2 C2[2] = {};
+        if constexpr (MODE == 0) {
+          const float4 cv = C4[s];
+          C2[0] = make_float2(cv.x, cv.y);
+          C2[1] = make_float2(cv.z, cv.w);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float2& hs = h[2 * s + m];
+          const float2 e = __fmul2_rn(d2, A2[2 * s + m]);
+          const float2 a = make_float2(exp2_f(e.x), exp2_f(e.y));
+          if constexpr (MODE == 2) {
+            hs = __fmul2_rn(a, fma2(u2, B2[m], hs));
+          } else {
+            hs = fma2(a, hs, __fmul2_rn(u2, B2[m]));
+            if constexpr (MODE == 0) y2 = fma2(hs, C2[m], y2);
+          }
+        }
+      }
+      if constexpr (MODE == 0) sY[nt][k][ch] = y2.x + y2.y;
+    }
+    __syncthreads();
+
+    // ---- per channel and step: the skip, the gate, the output
+    if constexpr (MODE == 0) {
+      T* y0 = yp + t0 * q.y_t;
+#pragma unroll
+      for (int i = 0; i < kEl; ++i) {
+        const int k = tf + i * NT;
+        if (!livef || k >= kT || t0 + k >= hi) continue;
+        float y = sY[0][k][chf];
+#pragma unroll
+        for (int m = 1; m < NT; ++m) y += sY[m][k][chf];
+        y = fmaf(skip, x[i], y);
+        if (gated) y *= z[i] * sigmoid_fast(z[i]);
+        y0[k * q.y_t] = t0 + k < end ? from_f32<T>(y) : none;
+      }
+    }
   }
-  if (!live) return;
+
   if constexpr (MODE == 0) {
+    if (livef)
+      for (int t = lo + chunks * kT + tf; t < hi; t += NT) yp[t * q.y_t] = none;
     // The end of the sequence, where this split holds it.
     const bool last = (len > lo && len <= hi) || (len == 0 && split == 0);
-    if (q.h_last != nullptr && last) {
-#pragma unroll
-      for (int i = 0; i < S; ++i)
-        if (n0 + i < q.N) q.h_last[cn + i] = (i & 1) ? h[i / 2].y : h[i / 2].x;
-    }
-    if (tid % LPC == 0)
-      for (int t = max(lo, end); t < hi; ++t) yp[t * q.y_t] = from_f32<T>(0.f);
+    if (q.h_last != nullptr && last) put_state(q.h_last + cn);
   } else {
+    put_state(carry + split * plane + cn);
+    // The NT threads of a channel, in order.
+    float* sum = reinterpret_cast<float*>(&sDU[0][0]);
+    static_assert(kThreads <= 2 * kT * CH, "the sums fit the staged values");
+    sum[tid] = total;
+    __syncthreads();
+    if (tid < CH && livef) {
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (n0 + i < q.N) carry[split * plane + cn + i] = (i & 1) ? h[i / 2].y : h[i / 2].x;
-    if (tid % LPC == 0) dsum[(static_cast<size_t>(split) * q.B + b) * q.D + d] = total;
+      for (int m = 1; m < NT; ++m) total += sum[tid + m * CH];
+      dsum[(static_cast<size_t>(split) * q.B + b) * q.D + df] = total;
+    }
   }
 }
 
@@ -306,64 +364,43 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
 
 // ---- host side ----
 
-// States per lane and lanes per channel: f(S, LPC).  `few`: there are few channels, so that the
-// step's latency counts and the states are spread over more lanes.
+// States of a warp and warps side by side: f(S, CW, NT).
 template <typename F>
-cudaError_t by_states(int N, bool few, F&& f) {
+cudaError_t by_states(int N, F&& f) {
   using std::integral_constant;
-#define CFC_SCAN_CASE(S, L) return f(integral_constant<int, S>{}, integral_constant<int, L>{})
-  if (N <= 4) CFC_SCAN_CASE(4, 1);
-  if (few) {
-    if (N <= 8) CFC_SCAN_CASE(4, 2);
-    if (N <= 16) CFC_SCAN_CASE(4, 4);
-    if (N <= 32) CFC_SCAN_CASE(4, 8);
-    if (N <= 64) CFC_SCAN_CASE(4, 16);
-  }
-  if (N <= 8) CFC_SCAN_CASE(8, 1);
-  if (N <= 16) CFC_SCAN_CASE(16, 1);
-  if (N <= 32) CFC_SCAN_CASE(16, 2);
-  if (N <= 64) CFC_SCAN_CASE(16, 4);
-  CFC_SCAN_CASE(16, 8);
+#define CFC_SCAN_CASE(S, C, L) \
+  return f(integral_constant<int, S>{}, integral_constant<int, C>{}, integral_constant<int, L>{})
+  if (N <= 4) CFC_SCAN_CASE(4, 2, 1);
+  if (N <= 8) CFC_SCAN_CASE(8, 2, 1);
+  if (N <= 16) CFC_SCAN_CASE(16, 2, 1);
+  if (N <= 32) CFC_SCAN_CASE(16, 1, 2);
+  if (N <= 64) CFC_SCAN_CASE(16, 1, 4);
+  CFC_SCAN_CASE(16, 1, 8);
 #undef CFC_SCAN_CASE
 }
 
-// Fewer channels than this leave SMs without a warp when a lane holds sixteen states.
-bool scan_few(const ScanCall& q) {
-  return static_cast<long long>(q.B) * q.D * ((q.N + 15) / 16) < 152LL * 4 * 32 * 2;
-}
-
-int lanes_for(const ScanCall& q) {
-  int l = 1;
-  (void)by_states(q.N, scan_few(q), [&](auto, auto L) {
-    l = decltype(L)::value;
-    return cudaSuccess;
-  });
-  return l;
-}
-
 template <typename T, int MODE>
-cudaError_t run_scan(const ScanCall& q, const ScanSplit& sp, float* carry, float* dsum, bool pdl,
+cudaError_t run_scan(const ScanCall& q, const ScanSplit& sp, float* carry, float* dsum,
                      cudaStream_t s) {
-  (void)pdl;
-  return by_states(q.N, scan_few(q), [&](auto S, auto L) {
-    constexpr int CH = kThreads / decltype(L)::value;
+  return by_states(q.N, [&](auto S, auto C, auto L) {
+    constexpr int CW = decltype(C)::value, NT = decltype(L)::value;
     Tile tl;
     tl.per_group = q.D / q.G;
-    tl.tiles_per_group = (tl.per_group + CH - 1) / CH;
+    tl.tiles_per_group = (tl.per_group + 32 * CW - 1) / (32 * CW);
     LaunchCfg c;
     c.grid = dim3(tl.tiles_per_group * q.G, q.B, sp.splits);
-    c.block = dim3(kThreads);
+    c.block = dim3(32 * CW * NT);
     c.stream = s;
-    return launch(c, scan_fwd_kernel<T, decltype(S)::value, decltype(L)::value, MODE>, q, tl,
-                  sp.steps, carry, dsum);
+    return launch(c, scan_fwd_kernel<T, decltype(S)::value, CW, NT, MODE>, q, tl, sp.steps, carry,
+                  dsum);
   });
 }
 
 }  // namespace
 
-ScanSplit scan_split(const ScanCall& q, int channels_per_warp, int warps_wanted) {
-  const long long warps =
-      static_cast<long long>(q.B) * q.G * ((q.D / q.G + channels_per_warp - 1) / channels_per_warp);
+ScanSplit scan_split(const ScanCall& q, int warps_wanted) {
+  const long long tiles = static_cast<long long>(q.B) * q.G * ((q.D / q.G + 31) / 32);
+  const long long warps = tiles * ((q.N + 15) / 16);  // of 32 channels and 16 states
   const int unit = 2 * kScanPeriod;
   ScanSplit sp{1, q.K};
   if (warps * 2 > warps_wanted || q.K < 16 * unit) return sp;
@@ -386,11 +423,11 @@ cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool rever
   float* dsum = carry + sp.splits * plane;
   cudaError_t e;
   if (q.bf16)
-    e = reverse ? run_scan<__nv_bfloat16, 2>(q, sp, carry, dsum, false, s)
-                : run_scan<__nv_bfloat16, 1>(q, sp, carry, dsum, false, s);
+    e = reverse ? run_scan<__nv_bfloat16, 2>(q, sp, carry, dsum, s)
+                : run_scan<__nv_bfloat16, 1>(q, sp, carry, dsum, s);
   else
-    e = reverse ? run_scan<float, 2>(q, sp, carry, dsum, false, s)
-                : run_scan<float, 1>(q, sp, carry, dsum, false, s);
+    e = reverse ? run_scan<float, 2>(q, sp, carry, dsum, s)
+                : run_scan<float, 1>(q, sp, carry, dsum, s);
   if (e != cudaSuccess) return e;
   LaunchCfg c;
   c.grid = dim3(static_cast<unsigned>((plane + 255) / 256));
@@ -401,7 +438,7 @@ cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool rever
 }
 
 namespace {
-ScanSplit fwd_split(const ScanCall& q) { return scan_split(q, 32 / lanes_for(q), 152 * 12); }
+ScanSplit fwd_split(const ScanCall& q) { return scan_split(q, 152 * 12); }
 }  // namespace
 
 size_t scan_fwd_ws_floats(const ScanCall& q) { return scan_carry_floats(q, fwd_split(q)); }
@@ -414,8 +451,8 @@ cudaError_t scan_fwd_launch(const ScanCall& q, cudaStream_t s) {
     const cudaError_t e = scan_carry_launch(q, sp, false, carry, s);
     if (e != cudaSuccess) return e;
   }
-  return q.bf16 ? run_scan<__nv_bfloat16, 0>(q, sp, carry, nullptr, false, s)
-                : run_scan<float, 0>(q, sp, carry, nullptr, false, s);
+  return q.bf16 ? run_scan<__nv_bfloat16, 0>(q, sp, carry, nullptr, s)
+                : run_scan<float, 0>(q, sp, carry, nullptr, s);
 }
 
 cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s) {

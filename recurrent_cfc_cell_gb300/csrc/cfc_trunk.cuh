@@ -61,23 +61,22 @@ __device__ __forceinline__ float exp2_f(float v) {
 }
 
 // ln(1 + e^v) = max(v, 0) + ln(1 + t), t = e^-|v| in (0, 1].  ln(1 + t) = 2 artanh(s) with
-// s = t / (2 + t) <= 1/3: the odd series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14 leaves
-// 2 s^17 / 17 < 2^-26 of the sum at s = 1/3, and keeps full relative precision for small t,
-// where 1 + t would lose it.
-__device__ __forceinline__ float softplus_f(float v) {
-  const float t = __expf(-fabsf(v));
-  const float s = __fdividef(t, 2.f + t);
-  const float q = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  p = fmaf(p, q, 1.f);
-  return fmaxf(v, 0.f) + 2.f * s * p;
+// s = t / (2 + t) <= 1/3, which keeps full relative precision for small t, where 1 + t would lose
+// it.  artanh(s) / s is a polynomial in s^2 of degree 4, interpolated at the Chebyshev nodes of
+// [0, 1/9] (relative error 8e-9, below fp32's rounding; the power series would take degree 7).
+// Two values at a time: the polynomial runs in packed pairs.
+__device__ __forceinline__ float2 softplus2_f(float2 v) {
+  const float2 t = make_float2(__expf(-fabsf(v.x)), __expf(-fabsf(v.y)));
+  const float2 s = make_float2(__fdividef(t.x, 2.f + t.x), __fdividef(t.y, 2.f + t.y));
+  const float2 q = __fmul2_rn(s, s);
+  float2 p = make_float2(0.14078889787197113f, 0.14078889787197113f);
+  p = fma2(p, q, make_float2(0.13982579112052917f, 0.13982579112052917f));
+  p = fma2(p, q, make_float2(0.20012298226356506f, 0.20012298226356506f));
+  p = fma2(p, q, make_float2(0.3333316147327423f, 0.3333316147327423f));
+  p = fma2(p, q, make_float2(1.f, 1.f));
+  return fma2(__fmul2_rn(s, p), make_float2(2.f, 2.f), make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
+__device__ __forceinline__ float softplus_f(float v) { return softplus2_f(make_float2(v, v)).x; }
 
 // Philox 4x32, ten rounds (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as
 // 1, 2, 3", 2011): 128 random bits from a 128-bit counter and a 64-bit key.
