@@ -89,18 +89,25 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   const int d_base = group * pl.per_group;   // the group's first channel
   const int t_base = tile * Sh::CH;          // the tile's first channel in its group
 
-  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...
-  const int chf = tid % Sh::CH, tf = tid / Sh::CH;
+  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...  Addresses
+  // are a uniform base (sequence, tile, step) plus the thread's own offset.
+  const int chf = NT == 1 ? tid : tid % Sh::CH, tf = NT == 1 ? 0 : tid / Sh::CH;
   const bool livef = t_base + chf < pl.per_group;
-  const int df = d_base + (livef ? t_base + chf : 0);
-  const float bias = q.dt_bias ? q.dt_bias[df] : 0.f, skip = q.skip ? q.skip[df] : 0.f;
-  const T* xp = static_cast<const T*>(q.x) + b * q.x_b + df;
-  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + df;
-  const T* zp = q.z ? static_cast<const T*>(q.z) + b * q.z_b + df : nullptr;
-  const T* gp = static_cast<const T*>(q.dy) + b * q.dy_b + df;
-  T* dxp = static_cast<T*>(q.dx) + b * q.dx_b + df;
-  T* dtp = static_cast<T*>(q.ddt) + b * q.ddt_b + df;
-  T* dzp = q.dz ? static_cast<T*>(q.dz) + b * q.dz_b + df : nullptr;
+  const unsigned own = livef ? chf : 0;
+  const int d0 = d_base + t_base;
+  const float bias = q.dt_bias ? q.dt_bias[d0 + own] : 0.f, skip = q.skip ? q.skip[d0 + own] : 0.f;
+  const T* xp = static_cast<const T*>(q.x) + b * q.x_b + d0;
+  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + d0;
+  const T* zp = q.z ? static_cast<const T*>(q.z) + b * q.z_b + d0 : nullptr;
+  const T* gp = static_cast<const T*>(q.dy) + b * q.dy_b + d0;
+  T* dxp = static_cast<T*>(q.dx) + b * q.dx_b + d0;
+  T* dtp = static_cast<T*>(q.ddt) + b * q.ddt_b + d0;
+  T* dzp = q.dz ? static_cast<T*>(q.dz) + b * q.dz_b + d0 : nullptr;
+  // The thread's element of row `base`, NT rows apart from the thread's first.
+  auto pick = [&](auto* base, long long stride) {
+    if constexpr (NT == 1) return base + own;
+    return base + (own + tf * stride);
+  };
   const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N;
   const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
 
@@ -163,38 +170,47 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   // Steps after the sequence's end: zeros.
   for (int t = lo + chunks * T8 + tf; t < hi; t += NT) {
     if (!livef) continue;
-    dxp[t * q.dx_t] = from_f32<T>(0.f);
-    dtp[t * q.ddt_t] = from_f32<T>(0.f);
-    if (dzp) dzp[t * q.dz_t] = from_f32<T>(0.f);
+    dxp[t * q.dx_t + own] = from_f32<T>(0.f);
+    dtp[t * q.ddt_t + own] = from_f32<T>(0.f);
+    if (dzp) dzp[t * q.dz_t + own] = from_f32<T>(0.f);
   }
   for (int t = lo + chunks * T8; t < hi; ++t)
     for (int n = tid; n < q.N; n += Sh::kThreads) put_bc(t, n, 0.f, 0.f);
 
   // The next chunk's inputs, as they are stored.
-  constexpr int kEl = (T8 + NT - 1) / NT, kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
+  constexpr int kEl = T8 / NT, kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
+  static_assert(T8 % NT == 0, "every thread has the same number of steps");
   T rx[kEl], rt[kEl], rz[kEl], rg[kEl], rB[kBC], rC[kBC];
   const T none = from_f32<T>(0.f);
-  auto fetch = [&](int t0) {
+  auto fetch_as = [&](int t0, auto all) {
+    constexpr bool kAll = decltype(all)::value;  // every step of the chunk counts
     const T* x0 = xp + t0 * q.x_t;
-    const T* d0 = tp + t0 * q.dt_t;
+    const T* dt0 = tp + t0 * q.dt_t;
     const T* g0 = gp + t0 * q.dy_t;
     const T* z0 = zp ? zp + t0 * q.z_t : nullptr;
 #pragma unroll
     for (int i = 0; i < kEl; ++i) {
-      const int k = tf + i * NT;
-      const bool in = livef && k < T8 && t0 + k < end;
-      rx[i] = in ? x0[k * q.x_t] : none;
-      rt[i] = in ? d0[k * q.dt_t] : none;
-      rg[i] = in ? g0[k * q.dy_t] : none;
-      rz[i] = (in && zp) ? z0[k * q.z_t] : none;
+      const bool in = kAll || t0 + tf + i * NT < end;
+      rx[i] = in ? *pick(x0 + i * NT * q.x_t, q.x_t) : none;
+      rt[i] = in ? *pick(dt0 + i * NT * q.dt_t, q.dt_t) : none;
+      rg[i] = in ? *pick(g0 + i * NT * q.dy_t, q.dy_t) : none;
+    }
+    if (zp) {
+#pragma unroll
+      for (int i = 0; i < kEl; ++i)
+        rz[i] = kAll || t0 + tf + i * NT < end ? *pick(z0 + i * NT * q.z_t, q.z_t) : none;
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
       const int at = tid + i * Sh::kThreads, k = at / Sh::NP, n = at % Sh::NP;
-      const bool in = k < T8 && t0 + k < end && n < q.N;
+      const bool in = k < T8 && (kAll || t0 + k < end) && n < q.N;
       rB[i] = in ? Bp[(t0 + k) * q.Bm_t + n] : none;
       rC[i] = in ? Cp[(t0 + k) * q.Cm_t + n] : none;
     }
+  };
+  auto fetch = [&](int t0) {
+    if (t0 + T8 <= end) fetch_as(t0, std::true_type{});
+    else fetch_as(t0, std::false_type{});
   };
   if (chunks > 0) {
     fetch(lo + (chunks - 1) * T8);
@@ -212,13 +228,14 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int i = 2 * j + m, k = tf + i * NT;
-        if (i < kEl && k < T8) {
-          // Steps past the end leave the state and its gradient alone: d = 0, r = 0.
-          const bool in = t0 + k < end;
-          const float dv = in ? (m ? d2.y : d2.x) : 0.f, xv = to_f32(rx[i]);
-          float rv = to_f32(rg[i]), zf = 0.f;
+        if (i < kEl) {
+          // Steps past the end and channels past the group's leave the state, its gradient and the
+          // sums over channels alone: d = 0, x = 0, r = 0.
+          const bool in = livef && t0 + k < end;
+          const float dv = in ? (m ? d2.y : d2.x) : 0.f, xv = in ? to_f32(rx[i]) : 0.f;
+          float rv = in ? to_f32(rg[i]) : 0.f, zf = 0.f;
           if (zp) {
-            const float z = to_f32(rz[i]), s = sigmoid_fast(z), gs = rv * s;
+            const float z = in ? to_f32(rz[i]) : 0.f, s = sigmoid_fast(z), gs = rv * s;
             rv = gs * z;
             zf = gs * fmaf(z, 1.f - s, 1.f);
           }
@@ -327,14 +344,15 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     T* const dx0 = dxp + t0 * q.dx_t;
     T* const dt0 = dtp + t0 * q.ddt_t;
     T* const dz0 = dzp ? dzp + t0 * q.dz_t : nullptr;
+    const bool all = t0 + T8 <= hi;
 #pragma unroll
     for (int i = 0; i < kEl; ++i) {
       const int k = tf + i * NT;
-      if (k >= T8 || t0 + k >= hi) break;
+      if (!all && t0 + k >= hi) break;
       const int at = k * Sh::CH + chf;
-      float y = 0.f, v = 0.f, w = 0.f;
+      float y = sm[Sh::oY + at], v = sm[Sh::oV + at], w = sm[Sh::oW + at];
 #pragma unroll
-      for (int m = 0; m < NT; ++m) {
+      for (int m = 1; m < NT; ++m) {
         y += sm[Sh::oY + m * Sh::kPer + at];
         v += sm[Sh::oV + m * Sh::kPer + at];
         w += sm[Sh::oW + m * Sh::kPer + at];
@@ -344,9 +362,9 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       dskip = fmaf(rv, xv, dskip);
       dbias += ddt;
       if (livef) {
-        dx0[k * q.dx_t] = from_f32<T>(fmaf(sm[Sh::oD + at], v, skip * rv));
-        dt0[k * q.ddt_t] = from_f32<T>(ddt);
-        if (dzp) dz0[k * q.dz_t] = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
+        *pick(dx0 + i * NT * q.dx_t, q.dx_t) = from_f32<T>(fmaf(sm[Sh::oD + at], v, skip * rv));
+        *pick(dt0 + i * NT * q.ddt_t, q.ddt_t) = from_f32<T>(ddt);
+        if (dzp) *pick(dz0 + i * NT * q.dz_t, q.dz_t) = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
       }
     }
     for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
@@ -387,8 +405,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       sk += sm[tid + m * Sh::CH];
       bi += sm[Sh::kThreads + tid + m * Sh::CH];
     }
-    params[static_cast<size_t>(df) * (q.N + 2) + q.N] = sk;
-    params[static_cast<size_t>(df) * (q.N + 2) + q.N + 1] = bi;
+    params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N] = sk;
+    params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N + 1] = bi;
   }
 }
 

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
                                                                 const int steps, float* carry,
                                                                 float* dsum) {
   constexpr int kThreads = 32 * CW * NT, CH = 32 * CW, NP = S * NT;
-  constexpr int kEl = (kT + NT - 1) / NT;                      // per-channel values of a thread
+  constexpr int kEl = kT / NT;                                 // per-channel values of a thread
   constexpr int kEl2 = (kEl + 1) / 2;
   constexpr int kBC = (kT * NP + kThreads - 1) / kThreads;     // B (or C) values of a thread
   constexpr bool kGate = MODE != 1;
@@ -99,50 +99,69 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
     }
   };
 
-  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...
-  const int chf = tid % CH, tf = tid / CH;
+  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...  Addresses
+  // are a uniform base (sequence, tile, step) plus the thread's own offset, so that a load costs
+  // no address arithmetic of the thread's.
+  const int chf = NT == 1 ? tid : tid % CH, tf = NT == 1 ? 0 : tid / CH;
   const bool livef = t_base + chf < tl.per_group;
-  const int df = group * tl.per_group + (livef ? t_base + chf : 0);
-  const float bias = q.dt_bias ? q.dt_bias[df] : 0.f;
-  const float skip = q.skip ? q.skip[df] : 0.f;
+  const unsigned at = livef ? chf : 0;
+  const int d0 = group * tl.per_group + t_base;
+  const float bias = q.dt_bias ? q.dt_bias[d0 + at] : 0.f;
+  const float skip = q.skip ? q.skip[d0 + at] : 0.f;
   const bool gated = kGate && q.z != nullptr;
   const long long x_t = MODE == 2 ? q.dy_t : q.x_t;
   const T* xp = (MODE == 2 ? static_cast<const T*>(q.dy) + b * q.dy_b
-                           : static_cast<const T*>(q.x) + b * q.x_b) + df;
-  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + df;
-  const T* zp = gated ? static_cast<const T*>(q.z) + b * q.z_b + df : nullptr;
+                           : static_cast<const T*>(q.x) + b * q.x_b) + d0;
+  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + d0;
+  const T* zp = gated ? static_cast<const T*>(q.z) + b * q.z_b + d0 : nullptr;
+  const size_t xo = at + tf * x_t, to = at + tf * q.dt_t, zo = at + tf * q.z_t;
   // MODE 2 reads C in the place of B.
   const long long B_t = MODE == 2 ? q.Cm_t : q.Bm_t;
   const T* Bp = (MODE == 2 ? static_cast<const T*>(q.Cm) + b * q.Cm_b
                            : static_cast<const T*>(q.Bm) + b * q.Bm_b) +
                 static_cast<long long>(group) * q.N;
   const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
-  T* yp = static_cast<T*>(q.y) + b * q.y_b + df;
+  T* yp = static_cast<T*>(q.y) + b * q.y_b + d0;
+  const size_t yo = at + tf * q.y_t;
+  // Offset of thread-dependent steps: at NT == 1 there are none and it stays 32 bits wide.
+  auto pick = [&](const T* base, size_t off) -> const T* {
+    if constexpr (NT == 1) return base + at;
+    return base + off;
+  };
 
   // The next chunk's inputs, as they are stored (converted when their chunk begins, so that
   // nothing waits for the loads before that).
   T rx[kEl], rt[kEl], rz[kEl], rB[kBC], rC[kBC];
   const T none = from_f32<T>(0.f);
-  auto fetch = [&](int t0) {
+  auto fetch_as = [&](int t0, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;  // every step of the chunk counts
     const T* x0 = xp + t0 * x_t;
-    const T* d0 = tp + t0 * q.dt_t;
+    const T* dt0 = tp + t0 * q.dt_t;
     const T* z0 = gated ? zp + t0 * q.z_t : nullptr;
 #pragma unroll
     for (int i = 0; i < kEl; ++i) {
-      const int k = tf + i * NT;
-      const bool in = livef && k < kT && t0 + k < end;
-      rx[i] = in ? x0[k * x_t] : none;
-      rt[i] = in ? d0[k * q.dt_t] : none;
-      rz[i] = (in && gated) ? z0[k * q.z_t] : none;
+      const bool in = kWhole || t0 + tf + i * NT < end;
+      rx[i] = in ? *pick(x0 + i * NT * x_t, xo) : none;
+      rt[i] = in ? *pick(dt0 + i * NT * q.dt_t, to) : none;
+    }
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < kEl; ++i)
+        rz[i] = kWhole || t0 + tf + i * NT < end ? *pick(z0 + i * NT * q.z_t, zo) : none;
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
       const int e = tid + i * kThreads, k = e / NP, n = e % NP;
-      const bool in = k < kT && t0 + k < end && n < q.N;
+      const bool in = k < kT && (kWhole || t0 + k < end) && n < q.N;
       rB[i] = in ? Bp[(t0 + k) * B_t + n] : none;
       if (MODE == 0) rC[i] = in ? Cp[(t0 + k) * q.Cm_t + n] : none;
     }
   };
+  auto fetch = [&](int t0) {
+    if (t0 + kT <= end) fetch_as(t0, std::true_type{});
+    else fetch_as(t0, std::false_type{});
+  };
+  static_assert(kT % NT == 0, "every thread has the same number of steps");
 
   float total = 0.f;  // sum of this thread's steps d
   const int chunks = end > lo ? (end - lo + kT - 1) / kT : 0;
@@ -154,7 +173,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
 #pragma unroll
     for (int i = 0; i < kEl; ++i) {
       x[i] = to_f32(rx[i]);
-      z[i] = to_f32(rz[i]);
+      z[i] = gated ? to_f32(rz[i]) : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < kEl2; ++j) {
@@ -165,7 +184,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
       for (int m = 0; m < 2; ++m) {
         const int i = 2 * j + m;
         const int k = tf + i * NT;
-        if (i < kEl && k < kT) {
+        if (i < kEl) {
           // Steps past the end leave the state alone: d = 0, so a = 1 and nothing is added.
           const float dd = t0 + k < end ? (m ? dv.y : dv.x) : 0.f;
           float u = dd * x[i];
@@ -229,23 +248,25 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
     // ---- per channel and step: the skip, the gate, the output
     if constexpr (MODE == 0) {
       T* y0 = yp + t0 * q.y_t;
+      const bool whole = t0 + kT <= end;
 #pragma unroll
       for (int i = 0; i < kEl; ++i) {
         const int k = tf + i * NT;
-        if (!livef || k >= kT || t0 + k >= hi) continue;
+        if (!livef || (!whole && t0 + k >= hi)) continue;
         float y = sY[0][k][chf];
 #pragma unroll
         for (int m = 1; m < NT; ++m) y += sY[m][k][chf];
         y = fmaf(skip, x[i], y);
         if (gated) y *= z[i] * sigmoid_fast(z[i]);
-        y0[k * q.y_t] = t0 + k < end ? from_f32<T>(y) : none;
+        *const_cast<T*>(pick(y0 + i * NT * q.y_t, yo)) =
+            whole || t0 + k < end ? from_f32<T>(y) : none;
       }
     }
   }
 
   if constexpr (MODE == 0) {
     if (livef)
-      for (int t = lo + chunks * kT + tf; t < hi; t += NT) yp[t * q.y_t] = none;
+      for (int t = lo + chunks * kT + tf; t < hi; t += NT) yp[t * q.y_t + at] = none;
     // The end of the sequence, where this split holds it.
     const bool last = (len > lo && len <= hi) || (len == 0 && split == 0);
     if (q.h_last != nullptr && last) put_state(q.h_last + cn);
@@ -259,7 +280,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
     if (tid < CH && livef) {
 #pragma unroll
       for (int m = 1; m < NT; ++m) total += sum[tid + m * CH];
-      dsum[(static_cast<size_t>(split) * q.B + b) * q.D + df] = total;
+      dsum[(static_cast<size_t>(split) * q.B + b) * q.D + d0 + chf] = total;
     }
   }
 }
@@ -275,12 +296,23 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(const ScanCall q, int sp
   const float A2 = q.A[(bd % q.D) * q.N + e % q.N] * kLog2e;
   const float* start = reverse ? q.dh_last : q.h0;
   float h = start ? start[e] : 0.f;
-  for (int i = 0; i < splits; ++i) {
-    const int s = reverse ? splits - 1 - i : i;
-    const float own = carry[s * plane + e];
-    const float a = exp2_f(A2 * dsum[s * (plane / q.N) + bd]);
-    carry[s * plane + e] = h;
-    h = fmaf(a, h, own);
+  // Eight splits at a time: their loads are in flight together.
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < splits; i0 += U) {
+    float own[U], a[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = min(i0 + j, splits - 1), s = reverse ? splits - 1 - i : i;
+      own[j] = carry[s * plane + e];
+      a[j] = dsum[s * (plane / q.N) + bd];
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j, s = reverse ? splits - 1 - i : i;
+      if (i >= splits) break;
+      carry[s * plane + e] = h;
+      h = fmaf(exp2_f(A2 * a[j]), h, own[j]);
+    }
   }
 }
 
@@ -372,9 +404,9 @@ cudaError_t by_states(int N, F&& f) {
   return f(integral_constant<int, S>{}, integral_constant<int, C>{}, integral_constant<int, L>{})
   if (N <= 4) CFC_SCAN_CASE(4, 2, 1);
   if (N <= 8) CFC_SCAN_CASE(8, 2, 1);
-  if (N <= 16) CFC_SCAN_CASE(16, 2, 1);
-  if (N <= 32) CFC_SCAN_CASE(16, 1, 2);
-  if (N <= 64) CFC_SCAN_CASE(16, 1, 4);
+  if (N <= 16) CFC_SCAN_CASE(8, 2, 2);
+  if (N <= 32) CFC_SCAN_CASE(8, 1, 4);
+  if (N <= 64) CFC_SCAN_CASE(8, 1, 8);
   CFC_SCAN_CASE(16, 1, 8);
 #undef CFC_SCAN_CASE
 }
