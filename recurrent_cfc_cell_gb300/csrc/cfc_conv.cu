@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs
         float p = bias[v];
 #pragma unroll
         for (int j = 0; j < W; ++j) p = fmaf(w[j][v], win.x[j][v], p);
-        o[v] = q.silu ? p * sigmoid_fast(p) : p;
+        o[v] = q.silu ? p * sigmoid_f(p) : p;
       }
       store_v<T, V>(u + (t + i) * q.u_t + b * q.u_b + c, o);
       win.shift();
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs
               float p = bias[v];
 #pragma unroll
               for (int j = 0; j < W; ++j) p = fmaf(w[j][v], win.x[j][v], p);
-              const float s = sigmoid_fast(p);
+              const float s = sigmoid_f(p);
               gv *= s * fmaf(p, 1.f - s, 1.f);
             }
             if (t + i < te) {
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvCall q) {
     float p = q.bias ? q.bias[c + v] : 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) p = fmaf(q.w[static_cast<long long>(c + v) * W + j], x[j][v], p);
-    o[v] = q.silu ? p * sigmoid_fast(p) : p;
+    o[v] = q.silu ? p * sigmoid_f(p) : p;
   }
   T* ns = static_cast<T*>(q.last) + static_cast<long long>(b) * (W - 1) * q.D + c;
 #pragma unroll

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
           const float dv = in ? (m ? d2.y : d2.x) : 0.f, xv = in ? to_f32(rx[i]) : 0.f;
           float rv = in ? to_f32(rg[i]) : 0.f, zf = 0.f;
           if (zp) {
-            const float z = in ? to_f32(rz[i]) : 0.f, s = sigmoid_fast(z), gs = rv * s;
+            const float z = in ? to_f32(rz[i]) : 0.f, s = sigmoid_f(z), gs = rv * s;
             rv = gs * z;
             zf = gs * fmaf(z, 1.f - s, 1.f);
           }
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
           sm[Sh::oR + at] = rv;
           sm[Sh::oX + at] = xv;
           sm[Sh::oZ + at] = zf;
-          sm[Sh::oS + at] = !in ? 0.f : q.softplus ? sigmoid_fast(m ? raw.y : raw.x) : 1.f;
+          sm[Sh::oS + at] = !in ? 0.f : q.softplus ? sigmoid_f(m ? raw.y : raw.x) : 1.f;
         }
       }
     }

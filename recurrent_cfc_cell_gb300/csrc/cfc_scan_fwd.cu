@@ -29,7 +29,7 @@
 namespace cfc {
 namespace {
 
-constexpr int kT = kScanPeriod;  // steps of a chunk
+constexpr int kT = 2 * kScanPeriod;  // steps of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Tile {
@@ -129,6 +129,16 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
     return base + off;
   };
 
+  // This thread's values of a chunk's B and C: step kb + i kStepBC, state nb (NP divides the
+  // threads, or the threads NP).
+  constexpr int kPerStep = NP < kThreads ? NP : kThreads;      // threads on one step
+  constexpr int kStepBC = kThreads / kPerStep;                 // steps apart
+  constexpr int kWide = NP / kPerStep;                         // values of one step
+  constexpr int kStepsBC = kT / kStepBC;
+  static_assert(kBC == kStepsBC * kWide && kT % kStepBC == 0, "B and C spread evenly");
+  const int nb = tid % kPerStep, kb0 = tid / kPerStep;
+  const size_t bo = nb + kb0 * B_t, co = nb + kb0 * q.Cm_t;
+
   // The next chunk's inputs, as they are stored (converted when their chunk begins, so that
   // nothing waits for the loads before that).
   T rx[kEl], rt[kEl], rz[kEl], rB[kBC], rC[kBC];
@@ -149,13 +159,17 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
       for (int i = 0; i < kEl; ++i)
         rz[i] = kWhole || t0 + tf + i * NT < end ? *pick(z0 + i * NT * q.z_t, zo) : none;
     }
+    const T* b0 = Bp + t0 * B_t;
+    const T* c0 = Cp + t0 * q.Cm_t;
 #pragma unroll
-    for (int i = 0; i < kBC; ++i) {
-      const int e = tid + i * kThreads, k = e / NP, n = e % NP;
-      const bool in = k < kT && (kWhole || t0 + k < end) && n < q.N;
-      rB[i] = in ? Bp[(t0 + k) * B_t + n] : none;
-      if (MODE == 0) rC[i] = in ? Cp[(t0 + k) * q.Cm_t + n] : none;
-    }
+    for (int i = 0; i < kStepsBC; ++i)
+#pragma unroll
+      for (int w = 0; w < kWide; ++w) {
+        const bool in = (kWhole || t0 + kb0 + i * kStepBC < end) && nb + w * kPerStep < q.N;
+        rB[i * kWide + w] = in ? (b0 + i * kStepBC * B_t)[bo + w * kPerStep] : none;
+        if (MODE == 0)
+          rC[i * kWide + w] = in ? (c0 + i * kStepBC * q.Cm_t)[co + w * kPerStep] : none;
+      }
   };
   auto fetch = [&](int t0) {
     if (t0 + kT <= end) fetch_as(t0, std::true_type{});
@@ -168,6 +182,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
   if (chunks > 0) fetch(lo + (MODE == 2 ? chunks - 1 : 0) * kT);
   for (int cc = 0; cc < chunks; ++cc) {
     const int t0 = lo + (MODE == 2 ? chunks - 1 - cc : cc) * kT;
+    const bool whole = t0 + kT <= end;
     // ---- per channel and step: d and d x (MODE 2: d and r)
     float x[kEl], z[kEl];
 #pragma unroll
@@ -186,11 +201,11 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
         const int k = tf + i * NT;
         if (i < kEl) {
           // Steps past the end leave the state alone: d = 0, so a = 1 and nothing is added.
-          const float dd = t0 + k < end ? (m ? dv.y : dv.x) : 0.f;
+          const float dd = whole || t0 + k < end ? (m ? dv.y : dv.x) : 0.f;
           float u = dd * x[i];
           if (MODE == 2) {
             u = x[i];
-            if (gated) u *= z[i] * sigmoid_fast(z[i]);
+            if (gated) u *= z[i] * sigmoid_f(z[i]);
           }
           sDU[k][chf] = make_float2(dd, u);
           if (MODE != 0) total += dd;
@@ -198,57 +213,70 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBC; ++i) {
-      const int e = tid + i * kThreads;
-      if (e < kT * NP) {
-        (&sB[0][0])[e] = to_f32(rB[i]);
-        if (MODE == 0) (&sC[0][0])[e] = to_f32(rC[i]);
+    for (int i = 0; i < kStepsBC; ++i)
+#pragma unroll
+      for (int w = 0; w < kWide; ++w) {
+        sB[kb0 + i * kStepBC][nb + w * kPerStep] = to_f32(rB[i * kWide + w]);
+        if (MODE == 0) sC[kb0 + i * kStepBC][nb + w * kPerStep] = to_f32(rC[i * kWide + w]);
       }
-    }
     __syncthreads();
     if (cc + 1 < chunks) fetch(MODE == 2 ? t0 - kT : t0 + kT);
 
     // ---- the recurrence
-    if (MODE == 0 && q.states != nullptr) put_state(q.states + (t0 / kT) * plane + cn);
-#pragma unroll 4
-    for (int kk = 0; kk < kT; ++kk) {
-      const int k = MODE == 2 ? kT - 1 - kk : kk;
-      const float2 du = sDU[k][ch];
-      const float2 d2 = make_float2(du.x, du.x), u2 = make_float2(du.y, du.y);
-      const float4* B4 = reinterpret_cast<const float4*>(&sB[k][n0]);
-      const float4* C4 = reinterpret_cast<const float4*>(&sC[MODE == 0 ? k : 0][n0]);
-      float2 y2 = make_float2(0.f, 0.f);
+    float* const kept = MODE == 0 && q.states != nullptr
+                            ? q.states + (t0 / kScanPeriod) * plane + cn : nullptr;
+    // Blocks of kU steps: their decays do not depend on the state, so all of a block's
+    // exponentials are on their way before its first update.
+    constexpr int kU = S > 8 ? 2 : 4;
 #pragma unroll
-      for (int s = 0; s < S / 4; ++s) {
-        const float4 bv = B4[s];
-        const float2 B2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
-        float2 C2[2] = {};
-        if constexpr (MODE == 0) {
-          const float4 cv = C4[s];
-          C2[0] = make_float2(cv.x, cv.y);
-          C2[1] = make_float2(cv.z, cv.w);
-        }
+    for (int kb = 0; kb < kT; kb += kU) {
+      if (MODE == 0 && kept && kb % kScanPeriod == 0 && (kb == 0 || t0 + kb < end))
+        put_state(kept + (kb / kScanPeriod) * plane);
+      float2 a[kU][S / 2], u2[kU];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float2& hs = h[2 * s + m];
-          const float2 e = __fmul2_rn(d2, A2[2 * s + m]);
-          const float2 a = make_float2(exp2_f(e.x), exp2_f(e.y));
-          if constexpr (MODE == 2) {
-            hs = __fmul2_rn(a, fma2(u2, B2[m], hs));
-          } else {
-            hs = fma2(a, hs, __fmul2_rn(u2, B2[m]));
-            if constexpr (MODE == 0) y2 = fma2(hs, C2[m], y2);
-          }
+      for (int j = 0; j < kU; ++j) {
+        const float2 du = sDU[MODE == 2 ? kT - 1 - kb - j : kb + j][ch];
+        u2[j] = make_float2(du.y, du.y);
+#pragma unroll
+        for (int s = 0; s < S / 2; ++s) {
+          const float2 e = __fmul2_rn(make_float2(du.x, du.x), A2[s]);
+          a[j][s] = make_float2(exp2_f(e.x), exp2_f(e.y));
         }
       }
-      if constexpr (MODE == 0) sY[nt][k][ch] = y2.x + y2.y;
+#pragma unroll
+      for (int j = 0; j < kU; ++j) {
+        const int k = MODE == 2 ? kT - 1 - kb - j : kb + j;
+        float2 y2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < S / 4; ++s) {
+          const float4 bv = reinterpret_cast<const float4*>(&sB[k][n0])[s];
+          const float2 B2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
+          float2 C2[2] = {};
+          if constexpr (MODE == 0) {
+            const float4 cv = reinterpret_cast<const float4*>(&sC[k][n0])[s];
+            C2[0] = make_float2(cv.x, cv.y);
+            C2[1] = make_float2(cv.z, cv.w);
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            float2& hs = h[2 * s + m];
+            const float2 am = a[j][2 * s + m];
+            if constexpr (MODE == 2) {
+              hs = __fmul2_rn(am, fma2(u2[j], B2[m], hs));
+            } else {
+              hs = fma2(am, hs, __fmul2_rn(u2[j], B2[m]));
+              if constexpr (MODE == 0) y2 = fma2(hs, C2[m], y2);
+            }
+          }
+        }
+        if constexpr (MODE == 0) sY[nt][k][ch] = y2.x + y2.y;
+      }
     }
     __syncthreads();
 
     // ---- per channel and step: the skip, the gate, the output
     if constexpr (MODE == 0) {
       T* y0 = yp + t0 * q.y_t;
-      const bool whole = t0 + kT <= end;
 #pragma unroll
       for (int i = 0; i < kEl; ++i) {
         const int k = tf + i * NT;
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
 #pragma unroll
         for (int m = 1; m < NT; ++m) y += sY[m][k][chf];
         y = fmaf(skip, x[i], y);
-        if (gated) y *= z[i] * sigmoid_fast(z[i]);
+        if (gated) y *= z[i] * sigmoid_f(z[i]);
         *const_cast<T*>(pick(y0 + i * NT * q.y_t, yo)) =
             whole || t0 + k < end ? from_f32<T>(y) : none;
       }
@@ -387,7 +415,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
       float y = fmaf(skip, xv[k], yv[k]);
       if (q.z) {
         const float z = to_f32(static_cast<const T*>(q.z)[b * q.z_b + d]);
-        y *= z * sigmoid_fast(z);
+        y *= z * sigmoid_f(z);
       }
       static_cast<T*>(q.y)[b * q.y_b + d] = from_f32<T>(y);
     }

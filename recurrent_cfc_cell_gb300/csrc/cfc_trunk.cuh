@@ -60,14 +60,27 @@ __device__ __forceinline__ float exp2_f(float v) {
   return r;
 }
 
+// 1 / v, one ulp, and the logistic function from it.  The flush-to-zero forms of the hardware's
+// exponential and reciprocal: their subnormal results and arguments (here below 2^-126 of 1)
+// would take three more instructions each.
+__device__ __forceinline__ float rcp_f(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float sigmoid_f(float v) {
+  return rcp_f(1.f + exp2_f(-1.4426950408889634f * v));
+}
+
 // ln(1 + e^v) = max(v, 0) + ln(1 + t), t = e^-|v| in (0, 1].  ln(1 + t) = 2 artanh(s) with
 // s = t / (2 + t) <= 1/3, which keeps full relative precision for small t, where 1 + t would lose
 // it.  artanh(s) / s is a polynomial in s^2 of degree 4, interpolated at the Chebyshev nodes of
 // [0, 1/9] (relative error 8e-9, below fp32's rounding; the power series would take degree 7).
 // Two values at a time: the polynomial runs in packed pairs.
 __device__ __forceinline__ float2 softplus2_f(float2 v) {
-  const float2 t = make_float2(__expf(-fabsf(v.x)), __expf(-fabsf(v.y)));
-  const float2 s = make_float2(__fdividef(t.x, 2.f + t.x), __fdividef(t.y, 2.f + t.y));
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float2 t = make_float2(exp2_f(-kLog2e * fabsf(v.x)), exp2_f(-kLog2e * fabsf(v.y)));
+  const float2 s = __fmul2_rn(t, make_float2(rcp_f(2.f + t.x), rcp_f(2.f + t.y)));
   const float2 q = __fmul2_rn(s, s);
   float2 p = make_float2(0.14078889787197113f, 0.14078889787197113f);
   p = fma2(p, q, make_float2(0.13982579112052917f, 0.13982579112052917f));
