@@ -11,8 +11,8 @@
 // last history is the one before L.
 //
 // Bound by memory: x is read and u written once (backward: x and du read, dx written), up to
-// W - 1 steps read again where two runs of steps meet.  A thread holds V neighbouring channels
-// (16 bytes) and walks a run of steps with the last W inputs in registers; runs are short where
+// W - 1 steps read again where two runs of steps meet.  A thread holds neighbouring channels
+// (8 bytes of them; with 16 the backward pass's windows and sums would not fit in registers) and walks a run of steps with the last W inputs in registers; runs are short where
 // there are few channels and sequences, so that the GPU is full, and long otherwise.  The
 // parameter gradients are summed in registers over the run, over the CTA's eight runs in
 // shared memory and over the CTAs by reduce_axis0.
@@ -25,27 +25,37 @@ namespace {
 
 constexpr int kLanes = 32;  // channel vectors of a CTA
 constexpr int kRuns = 8;    // runs of steps of a CTA
+constexpr int kTokens = 4;  // sequences of a thread in the single-token form
 
-// V neighbouring channels of 4-byte or 2-byte activations (V = 16 bytes of them, or 1).
+// V neighbouring channels: 8 bytes of them (bf16 V = 4, fp32 V = 2), or one.
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = to_f32(*p);
-  } else if constexpr (V == 4) {
-    const float4 r = *reinterpret_cast<const float4*>(p);
-    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
-  } else {
-    load8(p, v);
+struct Raw;
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(v); }
+};
+template <>
+struct Raw<float, 2> {
+  float2 v;
+  __device__ __forceinline__ void get(float (&f)[2]) const { f[0] = v.x; f[1] = v.y; }
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = bf16_lo_f32(v.x); f[1] = bf16_hi_f32(v.x);
+    f[2] = bf16_lo_f32(v.y); f[3] = bf16_hi_f32(v.y);
   }
-}
+};
 template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
   if constexpr (V == 1) {
     *p = from_f32<T>(v[0]);
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
   } else {
-    store8(p, v);
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]));
   }
 }
 
@@ -55,29 +65,47 @@ struct ConvArgs {
   float *pw, *pb;
 };
 
-template <typename T, int V, int W>
-struct Window {
-  float x[W][V];
-  __device__ __forceinline__ void shift() {
+// The taps and bias of channels c .. c + V - 1.
+template <int V, int W>
+struct Taps {
+  float w[W][V], bias[V];
+  __device__ __forceinline__ Taps(const ConvCall& q, int c) {
 #pragma unroll
-    for (int j = 0; j + 1 < W; ++j)
+    for (int v = 0; v < V; ++v) {
+      bias[v] = q.bias ? q.bias[c + v] : 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[j][v] = x[j + 1][v];
+      for (int j = 0; j < W; ++j) w[j][v] = q.w[static_cast<long long>(c + v) * W + j];
+    }
+  }
+  __device__ __forceinline__ float pre(const float (&x)[W][V], int v) const {
+    float p = bias[v];
+#pragma unroll
+    for (int j = 0; j < W; ++j) p = fmaf(w[j][v], x[j][v], p);
+    return p;
   }
 };
 
-// x_t of sequence b (t < 0: the history), channels c .. c + V - 1.
+template <int V, int W>
+__device__ __forceinline__ void shift(float (&x)[W][V]) {
+#pragma unroll
+  for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[j][v] = x[j + 1][v];
+}
+
+// x_t of sequence b before step 0 (the history), channels c .. c + V - 1, or of step t.
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_x(const ConvCall& q, int t, int b, int c, float (&v)[V]) {
-  if (t >= 0) {
-    load_v<T, V>(static_cast<const T*>(q.x) + t * q.x_t + b * q.x_b + c, v);
-  } else if (q.x0 != nullptr && t >= -(W - 1)) {
-    load_v<T, V>(static_cast<const T*>(q.x0) + (static_cast<long long>(b) * (W - 1) + t + W - 1) * q.D + c, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.f;
-  }
+  Raw<T, V> r{};
+  if (t >= 0)
+    r = *reinterpret_cast<const Raw<T, V>*>(static_cast<const T*>(q.x) + t * q.x_t + b * q.x_b + c);
+  else if (q.x0 != nullptr && t >= -(W - 1))
+    r = *reinterpret_cast<const Raw<T, V>*>(
+        static_cast<const T*>(q.x0) + (static_cast<long long>(b) * (W - 1) + t + W - 1) * q.D + c);
+  r.get(v);
 }
+
+constexpr int kU = 8;  // steps whose loads are in flight together
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs a) {
@@ -88,7 +116,6 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs
   const int len = q.lengths ? min(max(q.lengths[b], 0), q.K) : q.K;
   const int t0 = (blockIdx.z * kRuns + threadIdx.x / kLanes) * a.run;
   const int t1 = min(q.K, t0 + a.run);
-  T* u = static_cast<T*>(q.u);
   if (t0 == 0 && q.last != nullptr) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
@@ -98,50 +125,50 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs
     }
   }
   if (t0 >= q.K) return;
-  float w[W][V], bias[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = q.bias ? q.bias[c + v] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][v] = q.w[static_cast<long long>(c + v) * W + j];
-  }
-  Window<T, V, W> win;
+  T* u = static_cast<T*>(q.u) + b * q.u_b + c;
   const int te = min(t1, len);
   if (t0 < te) {
+    const T* x = static_cast<const T*>(q.x) + b * q.x_b + c;
+    const Taps<V, W> taps(q, c);
+    float win[W][V];  // the last W inputs
 #pragma unroll
-    for (int j = 0; j + 1 < W; ++j) load_x<T, V, W>(q, t0 - (W - 1) + j, b, c, win.x[j]);
-  }
-  // Four steps at a time: their loads are in flight together.
-  constexpr int U = 4;
-  int t = t0;
-  for (; t < te; t += U) {
-    float nx[U][V];
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (t + i < te) load_x<T, V, W>(q, t + i, b, c, nx[i]);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (t + i >= te) break;
+    for (int j = 0; j + 1 < W; ++j) load_x<T, V, W>(q, t0 - (W - 1) + j, b, c, win[j]);
+    auto step = [&](int t, const Raw<T, V>& r) {
       float o[V];
+      r.get(win[W - 1]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        win.x[W - 1][v] = nx[i][v];
-        float p = bias[v];
-#pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(w[j][v], win.x[j][v], p);
+        const float p = taps.pre(win, v);
         o[v] = q.silu ? p * sigmoid_f(p) : p;
       }
-      store_v<T, V>(u + (t + i) * q.u_t + b * q.u_b + c, o);
-      win.shift();
+      store_v<T, V>(u + t * q.u_t, o);
+      shift(win);
+    };
+    Raw<T, V> nx[kU];
+    int t = t0;
+    for (; t + kU <= te; t += kU) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i) nx[i] = *reinterpret_cast<const Raw<T, V>*>(x + (t + i) * q.x_t);
+#pragma unroll
+      for (int i = 0; i < kU; ++i) step(t + i, nx[i]);
+    }
+    if (t < te) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        if (t + i < te) nx[i] = *reinterpret_cast<const Raw<T, V>*>(x + (t + i) * q.x_t);
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        if (t + i < te) step(t + i, nx[i]);
     }
   }
   const float zero[V] = {};
-  for (t = max(t0, te); t < t1; ++t) store_v<T, V>(u + t * q.u_t + b * q.u_b + c, zero);
+  for (int t = max(t0, te); t < t1; ++t) store_v<T, V>(u + t * q.u_t, zero);
 }
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs a) {
   __shared__ float part[kRuns][(W + 1) * V][kLanes];
+  grid_dep_launch_dependents();
   const ConvCall& q = a.q;
   const int lane = threadIdx.x % kLanes, run = threadIdx.x / kLanes;
   const int c = (blockIdx.x * kLanes + lane) * V;
@@ -156,78 +183,83 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
   }
-  if (c < q.D && (t0 < t1)) {
-    float w[W][V], bias[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      bias[v] = q.bias ? q.bias[c + v] : 0.f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[j][v] = q.w[static_cast<long long>(c + v) * W + j];
-    }
-    T* dx = static_cast<T*>(q.dx);
-    T* dx0 = static_cast<T*>(q.dx0);
-    const T* du = static_cast<const T*>(q.du);
-    Window<T, V, W> win, g;  // the last W inputs, and the last W gradients of p
+  if (c < q.D && t0 < t1) {
+    const Taps<V, W> taps(q, c);
+    const T* x = static_cast<const T*>(q.x) + b * q.x_b + c;
+    const T* du = static_cast<const T*>(q.du) + b * q.du_b + c;
+    T* dx = static_cast<T*>(q.dx) + b * q.dx_b + c;
+    T* dx0 = q.dx0 ? static_cast<T*>(q.dx0) + static_cast<long long>(b) * (W - 1) * q.D + c : nullptr;
+    float win[W][V], g[W][V];  // the last W inputs, and the last W gradients of p
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) g.x[j][v] = 0.f;
+      for (int v = 0; v < V; ++v) g[j][v] = 0.f;
     const int te = min(t1, len);
     if (t0 < te) {
 #pragma unroll
-      for (int j = 0; j + 1 < W; ++j) load_x<T, V, W>(q, t0 - (W - 1) + j, b, c, win.x[j]);
+      for (int j = 0; j + 1 < W; ++j) load_x<T, V, W>(q, t0 - (W - 1) + j, b, c, win[j]);
     }
-    // g_t for t up to W - 1 steps beyond the run: dx_t takes g_t .. g_{t+W-1}.  The step at t
-    // completes dx at t - (W - 1).
-    constexpr int U = 4;
-    const int tl = t1 + W - 1;
-    for (int t = t0; t < tl; t += U) {
-      float nx[U][V], nd[U][V];
+    // Step t forms g_t and with it completes dx at t - (W - 1), which takes g there .. g_t.
+    // `own`: the step is the run's own and counts in the parameters' sums (the W - 1 steps after
+    // the run only complete its dx).
+    auto gradient = [&](const Raw<T, V>& rx, const Raw<T, V>& rd, bool own) {
+      float d[V];
+      rx.get(win[W - 1]);
+      rd.get(d);
+      shift(g);
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (t + i < min(tl, len)) {
-          load_x<T, V, W>(q, t + i, b, c, nx[i]);
-          load_v<T, V>(du + (t + i) * q.du_t + b * q.du_b + c, nd[i]);
+      for (int v = 0; v < V; ++v) {
+        float gv = d[v];
+        if (q.silu) {
+          const float p = taps.pre(win, v), s = sigmoid_f(p);
+          gv *= s * fmaf(p, 1.f - s, 1.f);
         }
+        g[W - 1][v] = gv;
+        if (own) {
+          db[v] += gv;
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (t + i >= tl) break;
-        g.shift();
-        const bool in = t + i < len;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float gv = 0.f;
-          if (in) {
-            win.x[W - 1][v] = nx[i][v];
-            gv = nd[i][v];
-            if (q.silu) {
-              float p = bias[v];
-#pragma unroll
-              for (int j = 0; j < W; ++j) p = fmaf(w[j][v], win.x[j][v], p);
-              const float s = sigmoid_f(p);
-              gv *= s * fmaf(p, 1.f - s, 1.f);
-            }
-            if (t + i < te) {
-              db[v] += gv;
-#pragma unroll
-              for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gv, win.x[j][v], dw[j][v]);
-            }
-          }
-          g.x[W - 1][v] = gv;
+          for (int j = 0; j < W; ++j) dw[j][v] = fmaf(gv, win[j][v], dw[j][v]);
         }
-        if (in) win.shift();
-        const int td = t + i - (W - 1);  // g.x[k] is now g at td + k
-        if (td < t0 && (t0 > 0 || dx0 == nullptr)) continue;
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          o[v] = 0.f;
-#pragma unroll
-          for (int k = 0; k < W; ++k) o[v] = fmaf(w[W - 1 - k][v], g.x[k][v], o[v]);
-        }
-        if (td >= 0) store_v<T, V>(dx + td * q.dx_t + b * q.dx_b + c, o);
-        else store_v<T, V>(dx0 + (static_cast<long long>(b) * (W - 1) + td + W - 1) * q.D + c, o);
       }
+      shift(win);
+    };
+    auto finish = [&](int td) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        o[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) o[v] = fmaf(taps.w[W - 1 - k][v], g[k][v], o[v]);
+      }
+      if (td >= t0) store_v<T, V>(dx + td * q.dx_t, o);
+      else if (td < 0 && dx0) store_v<T, V>(dx0 + static_cast<long long>(td + W - 1) * q.D, o);
+    };
+    const int tl = min(t1 + W - 1, len);  // steps with a gradient that the run needs
+    Raw<T, V> nx[kU / 2], nd[kU / 2];
+    int t = t0;
+    for (; t + kU / 2 <= te; t += kU / 2) {
+#pragma unroll
+      for (int i = 0; i < kU / 2; ++i) {
+        nx[i] = *reinterpret_cast<const Raw<T, V>*>(x + (t + i) * q.x_t);
+        nd[i] = *reinterpret_cast<const Raw<T, V>*>(du + (t + i) * q.du_t);
+      }
+#pragma unroll
+      for (int i = 0; i < kU / 2; ++i) {
+        gradient(nx[i], nd[i], true);
+        finish(t + i - (W - 1));
+      }
+    }
+    for (; t < tl; ++t) {
+      gradient(*reinterpret_cast<const Raw<T, V>*>(x + t * q.x_t),
+               *reinterpret_cast<const Raw<T, V>*>(du + t * q.du_t), t < te);
+      finish(t - (W - 1));
+    }
+    // Past the sequence's end the gradients are zero, and so is dx.
+    for (; t < t1 + W - 1; ++t) {
+      shift(g);
+#pragma unroll
+      for (int v = 0; v < V; ++v) g[W - 1][v] = 0.f;
+      finish(t - (W - 1));
     }
   }
 #pragma unroll
@@ -252,40 +284,52 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs
 }
 
 // One token: u = silu(bias + w . [state ; x]), and the state moves on by one input.  A thread
-// holds V channels of one sequence.  The state may be the new state's own memory: a thread reads
-// what it writes before it writes it.
+// holds V channels of kTokens sequences, so their taps are read once for them.  The state may be
+// the new state's own memory: a thread reads what it writes before it writes it.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvCall q) {
   const int c = (blockIdx.x * 128 + threadIdx.x) * V;
-  const int b = blockIdx.y;
   if (c >= q.D) return;
-  float x[W][V], o[V];
-  const T* st = static_cast<const T*>(q.x0) + static_cast<long long>(b) * (W - 1) * q.D + c;
+  const int b0 = blockIdx.y * kTokens;
+  using R = Raw<T, V>;
+  R r[kTokens][W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_v<T, V>(st + static_cast<long long>(j) * q.D, x[j]);
-  load_v<T, V>(static_cast<const T*>(q.x) + b * q.x_b + c, x[W - 1]);
+  for (int k = 0; k < kTokens; ++k) {
+    const int b = min(b0 + k, q.B - 1);
+    const T* st = static_cast<const T*>(q.x0) + static_cast<long long>(b) * (W - 1) * q.D + c;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float p = q.bias ? q.bias[c + v] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) p = fmaf(q.w[static_cast<long long>(c + v) * W + j], x[j][v], p);
-    o[v] = q.silu ? p * sigmoid_f(p) : p;
+    for (int j = 0; j < W - 1; ++j) r[k][j] = *reinterpret_cast<const R*>(st + static_cast<long long>(j) * q.D);
+    r[k][W - 1] = *reinterpret_cast<const R*>(static_cast<const T*>(q.x) + b * q.x_b + c);
   }
-  T* ns = static_cast<T*>(q.last) + static_cast<long long>(b) * (W - 1) * q.D + c;
+  const Taps<V, W> taps(q, c);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_v<T, V>(ns + static_cast<long long>(j) * q.D, x[j + 1]);
-  store_v<T, V>(static_cast<T*>(q.u) + b * q.u_b + c, o);
+  for (int k = 0; k < kTokens; ++k) {
+    const int b = b0 + k;
+    if (b >= q.B) break;
+    float x[W][V], o[V];
+#pragma unroll
+    for (int j = 0; j < W; ++j) r[k][j].get(x[j]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float p = taps.pre(x, v);
+      o[v] = q.silu ? p * sigmoid_f(p) : p;
+    }
+    T* ns = static_cast<T*>(q.last) + static_cast<long long>(b) * (W - 1) * q.D + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<R*>(ns + static_cast<long long>(j) * q.D) = r[k][j + 1];
+    store_v<T, V>(static_cast<T*>(q.u) + b * q.u_b + c, o);
+  }
 }
 
 // ---- host side ----
 
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
-// Vector width: 16 bytes of channels where every row starts on 16 bytes, else one channel.
+// Vector width: 8 bytes of channels where every row starts on 8 bytes, else one channel.
 bool conv_vec(const ConvCall& q) {
-  const long long v = q.bf16 ? 8 : 4;
-  return q.D % v == 0 && al16(q.x) && al16(q.u) && al16(q.x0) && al16(q.last) && al16(q.du) &&
-         al16(q.dx) && al16(q.dx0) && q.x_t % v == 0 && q.x_b % v == 0 && q.u_t % v == 0 &&
+  const long long v = q.bf16 ? 4 : 2;
+  return q.D % v == 0 && al8(q.x) && al8(q.u) && al8(q.x0) && al8(q.last) && al8(q.du) &&
+         al8(q.dx) && al8(q.dx0) && q.x_t % v == 0 && q.x_b % v == 0 && q.u_t % v == 0 &&
          q.u_b % v == 0 && q.du_t % v == 0 && q.du_b % v == 0 && q.dx_t % v == 0 &&
          q.dx_b % v == 0;
 }
@@ -293,7 +337,8 @@ bool conv_vec(const ConvCall& q) {
 // Steps of a run and CTAs along the steps, from the sizes alone (so the order of the parameter
 // sums does not change with alignment).
 int conv_run(int B, int K, int D, bool bf16, int halo) {
-  const long long threads = static_cast<long long>(B) * ((D + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4));
+  const int v = bf16 ? 4 : 2;
+  const long long threads = static_cast<long long>(B) * ((D + v - 1) / v);
   int run = 64;
   while (run > (halo ? 8 : 4) && threads * ((K + run - 1) / run) < 152LL * 1024) run /= 2;
   return run;
@@ -330,7 +375,7 @@ cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
 template <typename T, int V>
 cudaError_t conv_step(const ConvCall& q, cudaStream_t s) {
   LaunchCfg c;
-  c.grid = dim3((q.D + 128 * V - 1) / (128 * V), q.B);
+  c.grid = dim3((q.D + 128 * V - 1) / (128 * V), (q.B + kTokens - 1) / kTokens);
   c.block = dim3(128);
   c.stream = s;
   return by_taps(q.W, [&](auto w) { return launch(c, conv_step_kernel<T, V, decltype(w)::value>, q); });
@@ -344,8 +389,8 @@ int conv_partials(int B, int K, int D, bool bf16) {
 
 cudaError_t conv_fwd_launch(const ConvCall& q, cudaStream_t s) {
   const ConvArgs a{q, conv_run(q.B, q.K, q.D, q.bf16, 0), nullptr, nullptr};
-  if (q.bf16) return conv_vec(q) ? conv_fwd<__nv_bfloat16, 8>(a, s) : conv_fwd<__nv_bfloat16, 1>(a, s);
-  return conv_vec(q) ? conv_fwd<float, 4>(a, s) : conv_fwd<float, 1>(a, s);
+  if (q.bf16) return conv_vec(q) ? conv_fwd<__nv_bfloat16, 4>(a, s) : conv_fwd<__nv_bfloat16, 1>(a, s);
+  return conv_vec(q) ? conv_fwd<float, 2>(a, s) : conv_fwd<float, 1>(a, s);
 }
 
 cudaError_t conv_bwd_launch(const ConvCall& q, float* dw, float* db, float* ws, cudaStream_t s) {
@@ -354,15 +399,15 @@ cudaError_t conv_bwd_launch(const ConvCall& q, float* dw, float* db, float* ws, 
   a.pw = P == 1 ? dw : ws;
   a.pb = P == 1 ? db : ws + static_cast<size_t>(P) * q.D * q.W;
   cudaError_t e;
-  if (q.bf16) e = conv_vec(q) ? conv_bwd<__nv_bfloat16, 8>(a, s) : conv_bwd<__nv_bfloat16, 1>(a, s);
-  else e = conv_vec(q) ? conv_bwd<float, 4>(a, s) : conv_bwd<float, 1>(a, s);
+  if (q.bf16) e = conv_vec(q) ? conv_bwd<__nv_bfloat16, 4>(a, s) : conv_bwd<__nv_bfloat16, 1>(a, s);
+  else e = conv_vec(q) ? conv_bwd<float, 2>(a, s) : conv_bwd<float, 1>(a, s);
   if (e != cudaSuccess || P == 1) return e;
   return reduce_axis0_pair_launch(a.pw, P, q.D * q.W, 0, 0, dw, nullptr, a.pb, P, q.D, db, s, true);
 }
 
 cudaError_t conv_step_launch(const ConvCall& q, cudaStream_t s) {
-  if (q.bf16) return conv_vec(q) ? conv_step<__nv_bfloat16, 8>(q, s) : conv_step<__nv_bfloat16, 1>(q, s);
-  return conv_vec(q) ? conv_step<float, 4>(q, s) : conv_step<float, 1>(q, s);
+  if (q.bf16) return conv_vec(q) ? conv_step<__nv_bfloat16, 4>(q, s) : conv_step<__nv_bfloat16, 1>(q, s);
+  return conv_vec(q) ? conv_step<float, 2>(q, s) : conv_step<float, 1>(q, s);
 }
 
 }  // namespace cfc

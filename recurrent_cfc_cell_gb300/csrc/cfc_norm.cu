@@ -220,6 +220,7 @@ template <typename T, typename TM, bool ALIGNED, bool DROP>
 __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a) {
   __shared__ float2 slot[2][kWarps];
   __shared__ float part[2][kWarps][256];
+  grid_dep_launch_dependents();
   const Lane<TM, ALIGNED> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);

@@ -79,6 +79,7 @@ template <typename T, int CW, int NT>
 __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q, const BwdPlan pl) {
   using Sh = Shape<CW, NT>;
   extern __shared__ __align__(16) float sm[];
+  grid_dep_launch_dependents();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int nt = warp % NT, cw = warp / NT;
   const int group = blockIdx.x / pl.tiles_per_group, tile = blockIdx.x % pl.tiles_per_group;
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 template <typename T>
 __global__ void __launch_bounds__(256) scan_bc_kernel(const float* pB, const float* pC, int tiles,
                                                       size_t count, T* dB, T* dC) {
+  grid_dep_launch_dependents();
   grid_dep_wait();
   const float* p = blockIdx.y ? pC : pB;
   T* out = blockIdx.y ? dC : dB;

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
   __shared__ __align__(16) float sB[kT][NP];
   __shared__ __align__(16) float sC[MODE == 0 ? kT : 1][NP];
   __shared__ float sY[MODE == 0 ? NT : 1][MODE == 0 ? kT : 1][CH];
+  if (MODE != 0) grid_dep_launch_dependents();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int nt = warp % NT, cw = warp / NT;
   const int group = blockIdx.x / tl.tiles_per_group;
@@ -344,11 +345,26 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(const ScanCall q, int sp
   }
 }
 
-// One token: a lane holds four states of a channel and walks over kSeqs sequences, so A and the
-// channel's parameters are read once for them.  The state may be the new state's own memory.
+// One token: a lane holds four states of a channel, LPC lanes a channel, for kSeqs sequences, so
+// that A is read once for them.  What a sequence needs per channel (d and d x, later the gate) is
+// formed by one lane of the channel and handed round.  The state may be the new state's own
+// memory: a thread reads what it writes before it writes it.
 constexpr int kSeqs = 4;
+
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 r = *reinterpret_cast<const float4*>(p);
+  v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  v[0] = bf16_lo_f32(r.x); v[1] = bf16_hi_f32(r.x);
+  v[2] = bf16_lo_f32(r.y); v[3] = bf16_hi_f32(r.y);
+}
+
+// VEC: rows of four states are aligned, in the states (16 bytes) and in B and C.
 template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
+  constexpr int kOwn = LPC >= kSeqs ? 1 : kSeqs / LPC;  // sequences whose values a lane forms
   const int lane = threadIdx.x % LPC;
   const int d_raw = blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
   const bool live = d_raw < q.D;
@@ -356,46 +372,55 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
   const int group = d / (q.D / q.G);
   const float bias = q.dt_bias ? q.dt_bias[d] : 0.f, skip = q.skip ? q.skip[d] : 0.f;
   const int b0 = blockIdx.y * kSeqs;
-  float yv[kSeqs] = {};
-  float dv[kSeqs], xv[kSeqs];
+  float own_d[kOwn], own_x[kOwn], own_z[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int k = lane % kSeqs + i * LPC, b = min(b0 + k, q.B - 1);
+    own_x[i] = to_f32(static_cast<const T*>(q.x)[b * q.x_b + d]);
+    own_z[i] = q.z ? to_f32(static_cast<const T*>(q.z)[b * q.z_b + d]) : 0.f;
+    const float raw = to_f32(static_cast<const T*>(q.dt)[b * q.dt_b + d]) + bias;
+    own_d[i] = q.softplus ? softplus_f(raw) : raw;
+  }
+  float dv[kSeqs], uv[kSeqs], yv[kSeqs] = {};
 #pragma unroll
   for (int k = 0; k < kSeqs; ++k) {
-    const int b = min(b0 + k, q.B - 1);
-    xv[k] = to_f32(static_cast<const T*>(q.x)[b * q.x_b + d]);
-    const float raw = to_f32(static_cast<const T*>(q.dt)[b * q.dt_b + d]) + bias;
-    dv[k] = q.softplus ? softplus_f(raw) : raw;
+    dv[k] = __shfl_sync(0xffffffffu, own_d[k / LPC % kOwn], k % LPC, LPC);
+    uv[k] = dv[k] * __shfl_sync(0xffffffffu, own_x[k / LPC % kOwn], k % LPC, LPC);
   }
   for (int n = lane * 4; n < q.N; n += LPC * 4) {
-    float A2[4];
+    float A2[4], h[kSeqs][4], Bv[kSeqs][4], Cv[kSeqs][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      A2[i] = n + i < q.N ? q.A[static_cast<size_t>(d) * q.N + n + i] * kLog2e : 0.f;
-    float h[kSeqs][4];
+      A2[i] = VEC || n + i < q.N ? q.A[static_cast<size_t>(d) * q.N + n + i] * kLog2e : 0.f;
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
-      const float* hp = q.h0 + (static_cast<size_t>(min(b0 + k, q.B - 1)) * q.D + d) * q.N + n;
+      const int b = min(b0 + k, q.B - 1);
+      const float* hp = q.h0 + (static_cast<size_t>(b) * q.D + d) * q.N + n;
+      const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N + n;
+      const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N + n;
       if constexpr (VEC) {
-        const float4 r = *reinterpret_cast<const float4*>(hp);
-        h[k][0] = r.x; h[k][1] = r.y; h[k][2] = r.z; h[k][3] = r.w;
+        load4(hp, h[k]);
+        load4(Bp, Bv[k]);
+        load4(Cp, Cv[k]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[k][i] = n + i < q.N ? hp[i] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const bool in = n + i < q.N;
+          h[k][i] = in ? hp[i] : 0.f;
+          Bv[k][i] = in ? to_f32(Bp[i]) : 0.f;
+          Cv[k][i] = in ? to_f32(Cp[i]) : 0.f;
+        }
       }
     }
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
-      const int b = min(b0 + k, q.B - 1);
-      const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N + n;
-      const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N + n;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool in = VEC || n + i < q.N;
-        const float bv = in ? to_f32(Bp[i]) : 0.f, cv = in ? to_f32(Cp[i]) : 0.f;
-        h[k][i] = fmaf(exp2_f(dv[k] * A2[i]), h[k][i], dv[k] * xv[k] * bv);
-        yv[k] = fmaf(h[k][i], cv, yv[k]);
+        h[k][i] = fmaf(exp2_f(dv[k] * A2[i]), h[k][i], uv[k] * Bv[k][i]);
+        yv[k] = fmaf(h[k][i], Cv[k][i], yv[k]);
       }
       if (live && b0 + k < q.B) {
-        float* np = q.h_last + (static_cast<size_t>(b) * q.D + d) * q.N + n;
+        float* np = q.h_last + (static_cast<size_t>(b0 + k) * q.D + d) * q.N + n;
         if constexpr (VEC) {
           *reinterpret_cast<float4*>(np) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
         } else {
@@ -410,15 +435,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
   for (int k = 0; k < kSeqs; ++k) {
 #pragma unroll
     for (int m = LPC / 2; m > 0; m >>= 1) yv[k] += __shfl_xor_sync(0xffffffffu, yv[k], m);
-    if (live && lane == 0 && b0 + k < q.B) {
-      const int b = b0 + k;
-      float y = fmaf(skip, xv[k], yv[k]);
-      if (q.z) {
-        const float z = to_f32(static_cast<const T*>(q.z)[b * q.z_b + d]);
-        y *= z * sigmoid_f(z);
-      }
-      static_cast<T*>(q.y)[b * q.y_b + d] = from_f32<T>(y);
-    }
+  }
+#pragma unroll
+  for (int k = 0; k < kSeqs; ++k) {
+    if (!live || lane != k % LPC || b0 + k >= q.B) continue;
+    float y = fmaf(skip, own_x[k / LPC % kOwn], yv[k]);
+    if (q.z) y *= own_z[k / LPC % kOwn] * sigmoid_f(own_z[k / LPC % kOwn]);
+    static_cast<T*>(q.y)[(b0 + k) * q.y_b + d] = from_f32<T>(y);
   }
 }
 
@@ -516,8 +539,11 @@ cudaError_t scan_fwd_launch(const ScanCall& q, cudaStream_t s) {
 }
 
 cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s) {
-  const bool vec = q.N % 4 == 0 && (reinterpret_cast<uintptr_t>(q.h0) & 15u) == 0 &&
-                   (reinterpret_cast<uintptr_t>(q.h_last) & 15u) == 0;
+  const uintptr_t e = q.bf16 ? 8 : 16;  // bytes of four values of B or C
+  const bool vec = q.N % 4 == 0 && reinterpret_cast<uintptr_t>(q.h0) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(q.h_last) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(q.Bm) % e == 0 && q.Bm_b % 4 == 0 &&
+                   reinterpret_cast<uintptr_t>(q.Cm) % e == 0 && q.Cm_b % 4 == 0;
   int lpc = 1;
   while (lpc * 4 < q.N && lpc < 32) lpc *= 2;
   LaunchCfg c;
