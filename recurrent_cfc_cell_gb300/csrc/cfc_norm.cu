@@ -11,13 +11,21 @@
 //
 // Every pass is bound by memory: each element is read once and written once, so a row stays in
 // registers between its sums and its results (two sums: the mean, then the squares of what is
-// left, so that a large mean costs no precision).  A row belongs to a team of lanes, eight
-// columns to a lane: 4 to 32 lanes of one warp up to 256 columns, 2 to 8 warps beyond, with two
-// or four pieces of 2048 columns up to 8192.  Longer rows are read again for each sum (they stay
-// in L2).  The parameter gradients stay in each lane's registers over all rows of its CTA, are
-// added over the CTA's teams in shared memory and over the CTAs by reduce_axis0: no atomics, and
-// an order that depends on the sizes alone.  The dropout mask is never stored: both passes draw
-// it again from the counter-based generator, whose counter is the element's place.
+// left, so that a large mean costs no precision), and the next row's loads are on their way
+// meanwhile.  A row belongs to a team of lanes, eight columns to a lane and piece: 4 to 32 lanes
+// of one warp up to 256 columns, 2 or 4 warps up to 1024, a whole CTA of just enough warps up to
+// 8192, two pieces a lane.  Longer rows are read again for each sum (they stay in L2).
+//
+// Lanes load and store eight columns at once.  Where rows start anywhere (an odd width), the
+// lanes' groups of eight follow the memory's alignment instead of the row's start, and the row's
+// two ends are done element by element; a team's rows are a multiple of eight apart, so their
+// starts are aligned alike and its parameters and sums stay in registers.  Tensors that are
+// aligned differently from one another are done element by element throughout.
+//
+// The parameter gradients stay in each lane's registers over all rows of its team, are added over
+// the CTA's teams in shared memory and over the CTAs by reduce_axis0: no atomics, and an order
+// that depends on the sizes and the alignment alone.  The dropout mask is never stored: both
+// passes draw it again from the counter-based generator, whose counter is the element's place.
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
@@ -26,27 +34,42 @@ namespace cfc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 16;
+constexpr int kWholeCta = 99;
 
-// How a team of lanes covers a row: WPR > 0: WPR warps and I pieces of 256 * WPR columns;
-// WPR == 0: L lanes of a warp (32 / L rows per warp), one piece.
+// How a team of lanes covers a row.  WPR 0: L lanes of a warp (32 / L rows per warp); WPR 1, 2, 4:
+// that many warps of a 256-thread CTA; kWholeCta: all warps of the CTA (as many as the row needs).
+// I pieces of 8 columns a lane.
 template <int WPR_, int L_, int I_>
 struct Team {
   static constexpr int WPR = WPR_, L = L_, I = I_;
-  static constexpr int kLanes = WPR > 0 ? 32 : L;                    // lanes of one warp's tile
-  static constexpr int kTeams = WPR > 0 ? kWarps / WPR : kThreads / L;  // teams per CTA
-  static constexpr int kCols = 8 * kLanes * (WPR > 0 ? WPR : 1);     // columns per piece
+  static constexpr bool kWhole = WPR == kWholeCta;
+  static constexpr int kLanes = WPR > 0 ? 32 : L;  // lanes of one warp's tile
+  static constexpr int kTeams = kWhole ? 1 : WPR > 0 ? kThreads / 32 / WPR : kThreads / L;
+  static constexpr int kMaxThreads = kWhole ? 32 * kMaxWarps : kThreads;
+  // Columns of a piece.
+  static __device__ __forceinline__ int cols() {
+    return kWhole ? 8 * static_cast<int>(blockDim.x) : 8 * kLanes * (WPR > 0 ? WPR : 1);
+  }
 };
 
-// A lane's place: which team of the CTA, and its first column and column stride in a piece.
-// Aligned rows: eight consecutive columns.  Others: columns kLanes apart, so that a warp's
-// scalar loads are consecutive.
-template <typename TM, bool ALIGNED>
+// How rows are laid out.  kScalar: anyhow; a lane's columns are kLanes apart, so that a warp's
+// element loads are consecutive.  kAligned: every row starts on a group of eight.  kShifted:
+// every tensor's row r starts at the same place within a group of eight.
+enum Layout { kScalar, kAligned, kShifted };
+
+// A lane's place: which team of the CTA, and its columns.
+template <typename TM, Layout LY>
 struct Lane {
   int team, lane, base;  // base: first column of this warp's tile in a piece
+  int shift = 0;         // kShifted: the row's start within its group of eight
   __device__ __forceinline__ Lane() {
-    if constexpr (TM::WPR > 0) {
-      const int w = threadIdx.x / 32;
+    const int w = threadIdx.x / 32;
+    if constexpr (TM::kWhole) {
+      team = 0;
+      lane = threadIdx.x % 32;
+      base = w * 256;
+    } else if constexpr (TM::WPR > 0) {
       team = w / TM::WPR;
       lane = threadIdx.x % 32;
       base = (w % TM::WPR) * 256;
@@ -56,77 +79,158 @@ struct Lane {
       base = 0;
     }
   }
-  __device__ __forceinline__ int col(int piece, int j) const {
-    return piece * TM::kCols + base + (ALIGNED ? lane * 8 + j : j * TM::kLanes + lane);
-  }
-  // The lane's eight columns of a row piece, `fill` beyond the row's end.
   template <typename T>
-  __device__ __forceinline__ void load(const T* row, int piece, int n, float fill,
-                                       float (&v)[8]) const {
-    if constexpr (ALIGNED) {
-      if (col(piece, 0) < n) {
-        load8(row + col(piece, 0), v);
-        return;
-      }
+  __device__ __forceinline__ void set_row(const T* row) {
+    if constexpr (LY == kShifted)
+      shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % 8);
+  }
+  __device__ __forceinline__ int col(int piece, int j) const {
+    const int c = piece * TM::cols() + base;
+    return LY == kScalar ? c + j * TM::kLanes + lane : c + lane * 8 + j - shift;
+  }
+  __device__ __forceinline__ bool in(int piece, int j, int n) const {
+    return static_cast<unsigned>(col(piece, j)) < static_cast<unsigned>(n);
+  }
+  // All eight columns of the lane are in the row, and aligned.
+  __device__ __forceinline__ bool whole(int piece, int n) const {
+    if constexpr (LY == kScalar) return false;
+    if constexpr (LY == kAligned) return col(piece, 0) < n;
+    return col(piece, 0) >= 0 && col(piece, 7) < n;
+  }
+  // The lane's eight columns of piece `piece` of row `row` of a tensor of `rows` rows, as they are
+  // stored.  At the row's ends a group reaches into the rows before and after, which is the
+  // tensor's own memory but for its first and last row (and for rows that lie on one another,
+  // ld < n); those ends are read element by element.  clean() drops what is not the row's.
+  template <typename T>
+  __device__ __forceinline__ void load(const T* p, long long ld, long long row, int rows, int piece,
+                                       int n, Raw8<T>& r) const {
+    const T* at = p + row * ld;
+    bool vec = whole(piece, n);
+    if constexpr (LY == kShifted)
+      vec = vec || (ld >= n && col(piece, 7) >= 0 && col(piece, 0) < n &&
+                    (col(piece, 0) >= 0 || row > 0) && (col(piece, 7) < n || row < rows - 1));
+    if (vec) {
+      r.load(at + col(piece, 0));
+      return;
+    }
+    r.clear();
+    if constexpr (LY == kAligned) return;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fill;
+    for (int j = 0; j < 8; ++j)
+      if (in(piece, j, n)) r.set(j, at[col(piece, j)]);
+  }
+  template <typename T>
+  __device__ __forceinline__ void clean(const Raw8<T>& r, int piece, int n, float (&v)[8]) const {
+    r.get(v);
+    if constexpr (LY == kShifted)
+      if (!whole(piece, n)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!in(piece, j, n)) v[j] = 0.f;
+      }
+  }
+  // The same of the parameters (in no particular alignment to the rows).
+  __device__ __forceinline__ void params(const float* p, int piece, int n, float (&v)[8]) const {
+    if constexpr (LY == kAligned) {
+      Raw8<float> r;
+      load(p, 0, 0, 1, piece, n, r);
+      r.get(v);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col(piece, j) < n ? to_f32(row[col(piece, j)]) : fill;
+      for (int j = 0; j < 8; ++j) v[j] = in(piece, j, n) ? p[col(piece, j)] : 0.f;
     }
   }
   template <typename T>
   __device__ __forceinline__ void store(T* row, int piece, int n, const float (&v)[8]) const {
-    if constexpr (ALIGNED) {
-      if (col(piece, 0) < n) store8(row + col(piece, 0), v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col(piece, j) < n) row[col(piece, j)] = from_f32<T>(v[j]);
+    if (whole(piece, n)) {
+      store8(row + col(piece, 0), v);
+      return;
     }
+    if constexpr (LY == kAligned) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (in(piece, j, n)) row[col(piece, j)] = from_f32<T>(v[j]);
   }
-  // Keep bits of the lane's eight columns.  The generator serves eight consecutive columns; where
-  // a lane's columns are not consecutive, each lane draws for its eight consecutive ones and the
-  // bits change hands inside the warp's tile.  Every lane of the warp takes part.
-  __device__ __forceinline__ uint32_t keep(const DropKey& k, uint32_t row, int piece,
-                                           uint32_t cut) const {
-    const uint32_t group = static_cast<uint32_t>((piece * TM::kCols + base) / 8 + lane);
-    const uint32_t own = keep_mask8(k, row, group, cut);
-    if constexpr (ALIGNED) return own;
-    uint32_t m = 0;
+  // Which of the lane's eight columns are kept.  The generator serves eight consecutive columns
+  // from a multiple of eight; where a lane's columns are others, each lane draws for its eight of
+  // those and the bits change hands inside the warp's tile.  Every lane of the warp takes part.
+  __device__ __forceinline__ void keep(const DropKey& key, uint32_t row, int piece, uint32_t cut,
+                                       bool (&k)[8]) const {
+    const int group = (piece * TM::cols() + base) / 8 + lane;
+    keep8(key, row, static_cast<uint32_t>(group), cut, k);
+    if constexpr (LY == kAligned) return;
+    uint32_t own = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int at = j * TM::kLanes + lane;
-      const uint32_t from = __shfl_sync(0xffffffffu, own, at >> 3, TM::kLanes);
-      m |= ((from >> (at & 7)) & 1u) << j;
+    for (int j = 0; j < 8; ++j) own |= k[j] ? 1u << j : 0u;
+    if constexpr (LY == kScalar) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = j * TM::kLanes + lane;
+        k[j] = __shfl_sync(0xffffffffu, own, at >> 3, TM::kLanes) >> (at & 7) & 1u;
+      }
+    } else {
+      // Columns 8 group - shift ..: the last `shift` bits of the group before, then the first of
+      // this one.
+      uint32_t before = __shfl_up_sync(0xffffffffu, own, 1, TM::kLanes);
+      if (lane == 0 && group > 0) {
+        bool p[8];
+        keep8(key, row, static_cast<uint32_t>(group - 1), cut, p);
+        before = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) before |= p[j] ? 1u << j : 0u;
+      }
+      const uint32_t both = (before & 0xffu) | own << 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k[j] = both >> (8 - shift + j) & 1u;
     }
-    return m;
   }
 };
 
-// Sum of (a, b) over the team.  Teams of several warps go through shared memory: `slot` holds
-// two sets of two floats per warp, used in turn, so one barrier a sum is enough.
-template <typename TM>
-__device__ __forceinline__ float2 team_sum(float2 v, float2 (*slot)[kWarps], int turn, int team) {
+// Sums of N values over the team.  Teams of several warps go through shared memory: `slot` holds
+// two sets of a value per warp, used in turn, so one barrier a sum is enough.  (A whole CTA's set
+// is added by every warp for itself, a slot a lane; slots without a warp hold zero.)
+template <int N>
+struct Slots {
+  float v[2][N][kMaxWarps];
+};
+template <typename TM, int N>
+__device__ __forceinline__ void clear_slots(Slots<N>& s) {
+  if constexpr (TM::kWhole) {
+    for (int i = threadIdx.x; i < 2 * N * kMaxWarps; i += blockDim.x) (&s.v[0][0][0])[i] = 0.f;
+    __syncthreads();
+  }
+}
+template <typename TM, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& slot, int turn, int team) {
   constexpr int kSpan = TM::WPR > 0 ? 32 : TM::L;
 #pragma unroll
-  for (int d = kSpan / 2; d > 0; d >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
-  }
+  for (int d = kSpan / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
   if constexpr (TM::WPR > 1) {
     const int w = threadIdx.x / 32;
-    if (threadIdx.x % 32 == 0) slot[turn][w] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TM::WPR * 32) : "memory");
-    v = slot[turn][team * TM::WPR];
+    if (threadIdx.x % 32 == 0) {
 #pragma unroll
-    for (int i = 1; i < TM::WPR; ++i) {
-      const float2 o = slot[turn][team * TM::WPR + i];
-      v.x += o.x;
-      v.y += o.y;
+      for (int i = 0; i < N; ++i) slot.v[turn][i][w] = v[i];
+    }
+    if constexpr (TM::kWhole) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = slot.v[turn][i][threadIdx.x % kMaxWarps];
+#pragma unroll
+      for (int d = kMaxWarps / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    } else {
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TM::WPR * 32) : "memory");
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = slot.v[turn][i][team * TM::WPR];
+#pragma unroll
+        for (int j = 1; j < TM::WPR; ++j) v[i] += slot.v[turn][i][team * TM::WPR + j];
+      }
     }
   }
-  return v;
 }
 
 struct NormArgs {
@@ -143,40 +247,73 @@ struct NormArgs {
   float *pw, *pb;  // [gridDim.x][n] sums of dw and db
 };
 
-template <typename T, typename TM, bool ALIGNED, bool DROP>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float2 slot[2][kWarps];
-  const Lane<TM, ALIGNED> at;
+// The rows of a team: the first, the distance to the next, and how many turns every team takes
+// (teams of one warp share its shuffles, so they take the same number).
+struct Turns {
+  long long first, step;
+  int count;
+};
+template <typename TM>
+__device__ __forceinline__ Turns turns_of(int rows, int team) {
+  const long long step = static_cast<long long>(gridDim.x) * TM::kTeams;
+  return {static_cast<long long>(blockIdx.x) * TM::kTeams + team, step,
+          static_cast<int>((rows + step - 1) / step)};
+}
+
+template <typename T, typename TM, Layout LY, bool DROP>
+__global__ void __launch_bounds__(TM::kMaxThreads) norm_fwd_kernel(const NormArgs a) {
+  __shared__ Slots<1> slot;
+  clear_slots<TM>(slot);
+  Lane<TM, LY> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);
   DropKey key{};
   if constexpr (DROP) key = drop_key(a.rng);
-  // Teams of one warp share its shuffles, so they take the same number of turns.
-  const long long per = static_cast<long long>(gridDim.x) * TM::kTeams;
-  const int turns = static_cast<int>((a.rows + per - 1) / per);
-  for (int turn = 0; turn < turns; ++turn) {
-    const long long r = turn * per + static_cast<long long>(blockIdx.x) * TM::kTeams + at.team;
-    const bool live = r < a.rows;
+  const Turns tn = turns_of<TM>(a.rows, at.team);
+  const T* const xp = static_cast<const T*>(a.x);
+  const T* const rp = DROP ? static_cast<const T*>(a.residual) : nullptr;
+  Raw8<T> nx[TM::I], nr[TM::I];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < TM::I; ++i) {
+      at.load(xp, a.ldx, row, a.rows, i, n, nx[i]);
+      if (DROP && rp) at.load(rp, a.ldr, row, a.rows, i, n, nr[i]);
+    }
+  };
+  // Aligned parameters are two loads from the first-level cache a row; others stay in registers.
+  float w[TM::I][8], b[TM::I][8];
+  at.set_row(xp + (tn.first < a.rows ? tn.first : 0) * a.ldx);
+  auto params = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM::I; ++i) {
+      at.params(a.w, i, n, w[i]);
+      at.params(a.b, i, n, b[i]);
+    }
+  };
+  if constexpr (LY != kAligned) params();
+  if (tn.first < a.rows) fetch(tn.first);
+  for (int turn = 0; turn < tn.count; ++turn) {
+    const long long row = tn.first + turn * tn.step;
+    const bool live = row < a.rows;
     if (TM::WPR > 0 && !live) return;  // the whole team
-    const long long row = live ? r : a.rows - 1;
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
     float v[TM::I][8];
 #pragma unroll
-    for (int i = 0; i < TM::I; ++i) at.load(x, i, n, 0.f, v[i]);
+    for (int i = 0; i < TM::I; ++i) at.clean(nx[i], i, n, v[i]);
     if constexpr (DROP) {
       float res[TM::I][8];
-      const T* rp = static_cast<const T*>(a.residual);
       if (rp) {
 #pragma unroll
-        for (int i = 0; i < TM::I; ++i) at.load(rp + row * a.ldr, i, n, 0.f, res[i]);
+        for (int i = 0; i < TM::I; ++i) at.clean(nr[i], i, n, res[i]);
       }
+      if (row + tn.step < a.rows) fetch(row + tn.step);
 #pragma unroll
       for (int i = 0; i < TM::I; ++i) {
-        const uint32_t keep = at.keep(key, static_cast<uint32_t>(row), i, a.cut);
+        bool keep[8];
+        at.keep(key, static_cast<uint32_t>(row), i, a.cut, keep);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           // Product and sum rounded apart: the same values as dropout followed by the sum.
-          float d = (keep >> j & 1u) ? __fmul_rn(v[i][j], a.scale) : 0.f;
+          float d = keep[j] ? __fmul_rn(v[i][j], a.scale) : 0.f;
           if (rp) d = __fadd_rn(res[i][j], d);
           // The norm reads the stream as it is stored, so that the backward pass, which reads
           // the stored stream, differentiates what the forward pass computed.
@@ -184,96 +321,124 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormArgs a) {
         }
         if (live) at.store(static_cast<T*>(a.s) + row * a.lds, i, n, v[i]);
       }
-      // Beyond the row's end the generator may have kept nothing but zeros; they stay zero.
+    } else {
+      if (row + tn.step < a.rows) fetch(row + tn.step);
     }
-    float2 sum = make_float2(0.f, 0.f);
+    float sum[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < TM::I; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum.x += v[i][j];
-    const float mean = team_sum<TM>(sum, slot, 0, at.team).x * inv_n;
-    sum = make_float2(0.f, 0.f);
+      for (int j = 0; j < 8; ++j) sum[0] += v[i][j];
+    if constexpr (LY == kAligned) params();
+    team_sum<TM>(sum, slot, 0, at.team);
+    const float mean = sum[0] * inv_n;
+    sum[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < TM::I; ++i)
+    for (int i = 0; i < TM::I; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float c = at.col(i, j) < n ? v[i][j] - mean : 0.f;
-        sum.x = fmaf(c, c, sum.x);
+      for (int j = 0; j < 8; ++j) v[i][j] -= mean;
+      if (at.whole(i, n)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
+      } else if (LY != kAligned) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at.in(i, j, n)) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
       }
-    const float rstd = rsqrtf(team_sum<TM>(sum, slot, 1, at.team).x * inv_n + a.eps);
+    }
+    team_sum<TM>(sum, slot, 1, at.team);
+    const float rstd = rsqrtf(sum[0] * inv_n + a.eps);
     if (!live) continue;
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
-      float w[8], b[8];
-      at.load(a.w, i, n, 0.f, w);
-      at.load(a.b, i, n, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = fmaf((v[i][j] - mean) * rstd, w[j], b[j]);
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, w[i][j], b[i][j]);
       at.store(y, i, n, v[i]);
     }
     if (at.base == 0 && at.lane == 0) a.stats[row] = make_float2(mean, rstd);
   }
 }
 
-template <typename T, typename TM, bool ALIGNED, bool DROP>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a) {
-  __shared__ float2 slot[2][kWarps];
-  __shared__ float part[2][kWarps][256];
+template <typename T, typename TM, Layout LY, bool DROP>
+__global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArgs a) {
+  __shared__ Slots<2> slot;
+  __shared__ float part[TM::kTeams > 1 ? 2 : 1][TM::kTeams > 1 ? kThreads / 32 : 1][256];
+  __shared__ int shifts[TM::kTeams];
   grid_dep_launch_dependents();
-  const Lane<TM, ALIGNED> at;
+  clear_slots<TM>(slot);
+  Lane<TM, LY> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);
   DropKey key{};
   if constexpr (DROP) key = drop_key(a.rng);
-  float dw[TM::I][8], db[TM::I][8];
+  const Turns tn = turns_of<TM>(a.rows, at.team);
+  const T* const xp = static_cast<const T*>(a.x);
+  const T* const gp = static_cast<const T*>(a.dy);
+  const T* const sp = DROP ? static_cast<const T*>(a.ds) : nullptr;
+  Raw8<T> nx[TM::I], ng[TM::I], ns[TM::I];
+  float2 nst = make_float2(0.f, 0.f);
+  auto fetch = [&](long long row) {
 #pragma unroll
-  for (int i = 0; i < TM::I; ++i)
+    for (int i = 0; i < TM::I; ++i) {
+      at.load(xp, a.ldx, row, a.rows, i, n, nx[i]);
+      at.load(gp, a.lddy, row, a.rows, i, n, ng[i]);
+      if (DROP && sp) at.load(sp, a.ldds, row, a.rows, i, n, ns[i]);
+    }
+    nst = a.stats[row];
+  };
+  // As in the forward pass; with dropout, keeping w in registers was the faster (262144 x 256 bf16:
+  // 128 us, and 155 us with w read again).
+  constexpr bool kReload = LY == kAligned && !DROP;
+  float w[TM::I][8], dw[TM::I][8], db[TM::I][8];
+  at.set_row(xp + (tn.first < a.rows ? tn.first : 0) * a.ldx);
+#pragma unroll
+  for (int i = 0; i < TM::I; ++i) {
+    if constexpr (!kReload) at.params(a.w, i, n, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
-  const long long per = static_cast<long long>(gridDim.x) * TM::kTeams;
-  const int turns = static_cast<int>((a.rows + per - 1) / per);
-  for (int turn = 0; turn < turns; ++turn) {
-    const long long r = turn * per + static_cast<long long>(blockIdx.x) * TM::kTeams + at.team;
-    const bool live = r < a.rows;
+  }
+  if (tn.first < a.rows) fetch(tn.first);
+  for (int turn = 0; turn < tn.count; ++turn) {
+    const long long row = tn.first + turn * tn.step;
+    const bool live = row < a.rows;
     if (TM::WPR > 0 && !live) break;  // the whole team
-    const long long row = live ? r : a.rows - 1;
-    const float2 st = a.stats[row];
-    float hat[TM::I][8], g[TM::I][8];
-    float2 sum = make_float2(0.f, 0.f);
+    const float2 st = nst;
+    float hat[TM::I][8], g[TM::I][8], ds[TM::I][8];
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
-      at.load(static_cast<const T*>(a.x) + row * a.ldx, i, n, st.x, hat[i]);
-      at.load(static_cast<const T*>(a.dy) + row * a.lddy, i, n, 0.f, g[i]);
+      if constexpr (kReload) at.params(a.w, i, n, w[i]);
+      at.clean(nx[i], i, n, hat[i]);
+      at.clean(ng[i], i, n, g[i]);
+      if (DROP && sp) at.clean(ns[i], i, n, ds[i]);
     }
+    if (row + tn.step < a.rows) fetch(row + tn.step);
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
-      float w[8];
-      at.load(a.w, i, n, 0.f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        // Outside the row dy is zero, and so is all that it enters.
         const float d = live ? g[i][j] : 0.f;
         hat[i][j] = (hat[i][j] - st.x) * st.y;
         if (live) dw[i][j] = fmaf(d, hat[i][j], dw[i][j]);
         db[i][j] += d;
-        g[i][j] = d * w[j];
-        sum.x += g[i][j];
-        sum.y = fmaf(g[i][j], hat[i][j], sum.y);
+        g[i][j] = d * w[i][j];
+        sum[0] += g[i][j];
+        sum[1] = fmaf(g[i][j], hat[i][j], sum[1]);
       }
     }
-    sum = team_sum<TM>(sum, slot, turn & 1, at.team);
-    const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
+    team_sum<TM>(sum, slot, turn & 1, at.team);
+    const float c1 = sum[0] * inv_n, c2 = sum[1] * inv_n;
     if constexpr (DROP) {
 #pragma unroll
       for (int i = 0; i < TM::I; ++i) {
-        float ds[8];
-        const T* dsp = static_cast<const T*>(a.ds);
-        if (dsp) at.load(dsp + row * a.ldds, i, n, 0.f, ds);
-        const uint32_t keep = at.keep(key, static_cast<uint32_t>(row), i, a.cut);
+        bool keep[8];
+        at.keep(key, static_cast<uint32_t>(row), i, a.cut, keep);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          g[i][j] = st.y * (g[i][j] - c1 - hat[i][j] * c2) + (dsp ? ds[j] : 0.f);
-          hat[i][j] = (keep >> j & 1u) ? g[i][j] * a.scale : 0.f;
+          g[i][j] = st.y * (g[i][j] - c1 - hat[i][j] * c2) + (sp ? ds[i][j] : 0.f);
+          hat[i][j] = keep[j] ? g[i][j] * a.scale : 0.f;
         }
         if (live) {
           if (a.dres) at.store(static_cast<T*>(a.dres) + row * a.lddr, i, n, g[i]);
@@ -297,13 +462,17 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a) {
     for (int i = 0; i < TM::I; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (at.col(i, j) < n) {
+        if (at.in(i, j, n)) {
           pw[at.col(i, j)] = dw[i][j];
           pb[at.col(i, j)] = db[i][j];
         }
   } else {
-    const int w = threadIdx.x / 32;
-    if constexpr (TM::WPR == 0) {
+    // A team's columns lie `shift` further on in its part; teams of one warp are shifted alike
+    // only if they are aligned or scalar, so shifted ones are added one team at a time.
+    const int wp = threadIdx.x / 32;
+    if (at.lane == 0 && at.base == 0) shifts[at.team] = at.shift;
+    constexpr bool kFold = TM::WPR == 0 && LY != kShifted;  // a warp's teams are added first
+    if constexpr (kFold) {
 #pragma unroll
       for (int d = TM::L; d < 32; d <<= 1)
 #pragma unroll
@@ -312,23 +481,32 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a) {
           db[0][j] += __shfl_xor_sync(0xffffffffu, db[0][j], d);
         }
     }
-    constexpr int kSets = TM::WPR > 0 ? TM::kTeams : kWarps;  // warps that hold the same columns
-    constexpr int kPer = TM::WPR > 0 ? TM::WPR : 1;           // warps of one set
+    // Place of a column of this warp's part: within the tile, after the tiles of the warp's
+    // teams before.
+    const int tile = TM::WPR == 0 && !kFold ? (threadIdx.x % 32) / TM::L * (8 * TM::L) : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = at.col(0, j) - at.base;
-      if (TM::WPR > 0 || threadIdx.x % 32 < TM::L) {
-        part[0][w][c] = dw[0][j];
-        part[1][w][c] = db[0][j];
+      const int c = (LY == kScalar ? j * TM::kLanes + at.lane : at.lane * 8 + j) + tile;
+      if (!kFold || threadIdx.x % 32 < TM::L) {
+        part[0][wp][c] = dw[0][j];
+        part[1][wp][c] = db[0][j];
       }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < TM::kCols && c < n; c += kThreads) {
+    constexpr int kPer = TM::WPR > 0 ? TM::WPR : 1;                   // warps of one set
+    constexpr int kSets = kFold ? kThreads / 32 : TM::kTeams;         // sets of the same columns
+    for (int c = threadIdx.x; c < n; c += kThreads) {
       float sw = 0.f, sb = 0.f;
-#pragma unroll
       for (int t = 0; t < kSets; ++t) {
-        sw += part[0][t * kPer + c / 256][c % 256];
-        sb += part[1][t * kPer + c / 256][c % 256];
+        int wt = t * kPer, p = c;
+        if constexpr (LY == kShifted) p += shifts[t];
+        if constexpr (TM::WPR == 0 && !kFold) {
+          constexpr int kIn = 32 / TM::L;  // teams of a warp
+          wt = t / kIn;
+          p += t % kIn * (8 * TM::L);
+        }
+        sw += part[0][wt + (TM::WPR > 0 ? p / 256 : 0)][p % 256];
+        sb += part[1][wt + (TM::WPR > 0 ? p / 256 : 0)][p % 256];
       }
       pw[c] = sw;
       pb[c] = sb;
@@ -340,8 +518,9 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a) {
 // groups of eight columns, one group a thread at a time.
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(kThreads) norm_long_fwd_kernel(const NormArgs a) {
-  using TM = Team<kWarps, 32, 1>;
-  __shared__ float2 slot[2][kWarps];
+  using TM = Team<kWholeCta, 32, 1>;
+  __shared__ Slots<1> slot;
+  clear_slots<TM>(slot);
   const long long row = blockIdx.x;
   const int n = a.n;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -350,10 +529,13 @@ __global__ void __launch_bounds__(kThreads) norm_long_fwd_kernel(const NormArgs 
     const T* rp = static_cast<const T*>(a.residual);
     T* s = static_cast<T*>(a.s) + row * a.lds;
     for (int g = threadIdx.x; g < (n + 7) / 8; g += kThreads) {
-      const uint32_t keep = keep_mask8(key, static_cast<uint32_t>(row), g, a.cut);
-      for (int j = 0; j < 8 && g * 8 + j < n; ++j) {
+      bool keep[8];
+      keep8(key, static_cast<uint32_t>(row), g, a.cut, keep);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
         const int c = g * 8 + j;
-        float d = (keep >> j & 1u) ? __fmul_rn(to_f32(x[c]), a.scale) : 0.f;
+        if (c >= n) break;
+        float d = keep[j] ? __fmul_rn(to_f32(x[c]), a.scale) : 0.f;
         if (rp) d = __fadd_rn(to_f32(rp[row * a.ldr + c]), d);
         s[c] = from_f32<T>(d);
       }
@@ -361,15 +543,17 @@ __global__ void __launch_bounds__(kThreads) norm_long_fwd_kernel(const NormArgs 
     __syncthreads();
     x = s;
   }
-  float2 sum = make_float2(0.f, 0.f);
-  for (int c = threadIdx.x; c < n; c += kThreads) sum.x += to_f32(x[c]);
-  const float mean = team_sum<TM>(sum, slot, 0, 0).x / static_cast<float>(n);
-  sum = make_float2(0.f, 0.f);
+  float sum[1] = {0.f};
+  for (int c = threadIdx.x; c < n; c += kThreads) sum[0] += to_f32(x[c]);
+  team_sum<TM>(sum, slot, 0, 0);
+  const float mean = sum[0] / static_cast<float>(n);
+  sum[0] = 0.f;
   for (int c = threadIdx.x; c < n; c += kThreads) {
     const float d = to_f32(x[c]) - mean;
-    sum.x = fmaf(d, d, sum.x);
+    sum[0] = fmaf(d, d, sum[0]);
   }
-  const float rstd = rsqrtf(team_sum<TM>(sum, slot, 1, 0).x / static_cast<float>(n) + a.eps);
+  team_sum<TM>(sum, slot, 1, 0);
+  const float rstd = rsqrtf(sum[0] / static_cast<float>(n) + a.eps);
   T* y = static_cast<T*>(a.y) + row * a.ldy;
   for (int c = threadIdx.x; c < n; c += kThreads)
     y[c] = from_f32<T>(fmaf((to_f32(x[c]) - mean) * rstd, a.w[c], a.b[c]));
@@ -378,34 +562,37 @@ __global__ void __launch_bounds__(kThreads) norm_long_fwd_kernel(const NormArgs 
 
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(kThreads) norm_long_bwd_kernel(const NormArgs a) {
-  using TM = Team<kWarps, 32, 1>;
-  __shared__ float2 slot[2][kWarps];
+  using TM = Team<kWholeCta, 32, 1>;
+  __shared__ Slots<2> slot;
+  clear_slots<TM>(slot);
   const long long row = blockIdx.x;
   const int n = a.n;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
   const float2 st = a.stats[row];
-  float2 sum = make_float2(0.f, 0.f);
+  float sum[2] = {0.f, 0.f};
   for (int c = threadIdx.x; c < n; c += kThreads) {
     const float g = to_f32(dy[c]) * a.w[c];
-    sum.x += g;
-    sum.y = fmaf(g, (to_f32(x[c]) - st.x) * st.y, sum.y);
+    sum[0] += g;
+    sum[1] = fmaf(g, (to_f32(x[c]) - st.x) * st.y, sum[1]);
   }
-  sum = team_sum<TM>(sum, slot, 0, 0);
-  const float c1 = sum.x / static_cast<float>(n), c2 = sum.y / static_cast<float>(n);
+  team_sum<TM>(sum, slot, 0, 0);
+  const float c1 = sum[0] / static_cast<float>(n), c2 = sum[1] / static_cast<float>(n);
   T* dx = static_cast<T*>(a.dx) + row * a.lddx;
   DropKey key{};
   if constexpr (DROP) key = drop_key(a.rng);
   for (int g = threadIdx.x; g < (n + 7) / 8; g += kThreads) {
-    uint32_t keep = 0xffu;
-    if constexpr (DROP) keep = keep_mask8(key, static_cast<uint32_t>(row), g, a.cut);
-    for (int j = 0; j < 8 && g * 8 + j < n; ++j) {
+    bool keep[8] = {};
+    if constexpr (DROP) keep8(key, static_cast<uint32_t>(row), g, a.cut, keep);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
       const int c = g * 8 + j;
+      if (c >= n) break;
       float d = st.y * (to_f32(dy[c]) * a.w[c] - c1 - (to_f32(x[c]) - st.x) * st.y * c2);
       if constexpr (DROP) {
         if (a.ds) d += to_f32(static_cast<const T*>(a.ds)[row * a.ldds + c]);
         if (a.dres) static_cast<T*>(a.dres)[row * a.lddr + c] = from_f32<T>(d);
-        d = (keep >> j & 1u) ? d * a.scale : 0.f;
+        d = keep[j] ? d * a.scale : 0.f;
       }
       dx[c] = from_f32<T>(d);
     }
@@ -432,28 +619,34 @@ __global__ void __launch_bounds__(kThreads) norm_long_param_kernel(const NormArg
 
 // out = residual + keep * x * scale (a null residual: no sum).  The backward pass is the same
 // kernel on the gradient.
-template <typename T, typename TM, bool ALIGNED>
+template <typename T, typename TM, Layout LY>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const NormArgs a) {
-  const Lane<TM, ALIGNED> at;
+  Lane<TM, LY> at;
   const DropKey key = drop_key(a.rng);
   const int n = a.n;
-  const int pieces = (n + TM::kCols - 1) / TM::kCols;
+  const int pieces = (n + (LY == kShifted ? 7 : 0) + TM::cols() - 1) / TM::cols();
   const long long tiles = static_cast<long long>(a.rows) * pieces;
   const long long per = static_cast<long long>(gridDim.x) * TM::kTeams;
   const long long turns = (tiles + per - 1) / per;
+  const T* const xp = static_cast<const T*>(a.x);
+  const T* const rp = static_cast<const T*>(a.residual);
   for (long long turn = 0; turn < turns; ++turn) {
     const long long t = turn * per + static_cast<long long>(blockIdx.x) * TM::kTeams + at.team;
     const bool live = t < tiles;
     const long long row = live ? t / pieces : a.rows - 1;
     const int piece = live ? static_cast<int>(t % pieces) : 0;
+    at.set_row(xp + row * a.ldx);
+    Raw8<T> rx, rr;
     float v[8], res[8];
-    at.load(static_cast<const T*>(a.x) + row * a.ldx, piece, n, 0.f, v);
-    const T* rp = static_cast<const T*>(a.residual);
-    if (rp) at.load(rp + row * a.ldr, piece, n, 0.f, res);
-    const uint32_t keep = at.keep(key, static_cast<uint32_t>(row), piece, a.cut);
+    at.load(xp, a.ldx, row, a.rows, piece, n, rx);
+    if (rp) at.load(rp, a.ldr, row, a.rows, piece, n, rr);
+    bool keep[8];
+    at.keep(key, static_cast<uint32_t>(row), piece, a.cut, keep);
+    at.clean(rx, piece, n, v);
+    if (rp) at.clean(rr, piece, n, res);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = (keep >> j & 1u) ? __fmul_rn(v[j], a.scale) : 0.f;
+      v[j] = keep[j] ? __fmul_rn(v[j], a.scale) : 0.f;
       if (rp) v[j] = __fadd_rn(res[j], v[j]);
     }
     if (live) at.store(static_cast<T*>(a.s) + row * a.lds, piece, n, v);
@@ -463,86 +656,97 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const NormArgs a) {
 // ---- host side ----
 
 constexpr int kLongCols = 8192;  // widest row that a team holds in registers
-constexpr int kNormCtas = 152 * 4;
 
-bool rows_aligned(const void* p, long long ld, size_t elem) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (8 * elem) == 0 && ld % 8 == 0);
+// How the call's rows are laid out (see Layout); `params`: w and b are read in groups too.
+struct Rows {
+  const void* p;
+  long long ld;
+};
+Layout layout_of(const NormArgs& a, size_t e) {
+  const Rows r[] = {{a.x, a.ldx}, {a.residual, a.ldr}, {a.dy, a.lddy}, {a.ds, a.ldds},
+                    {a.s, a.lds}, {a.y, a.ldy}, {a.dx, a.lddx}, {a.dres, a.lddr}};
+  const uintptr_t start = reinterpret_cast<uintptr_t>(a.x) % (8 * e);
+  const long long ld = a.ldx % 8;
+  for (const Rows& q : r)
+    if (q.p && (reinterpret_cast<uintptr_t>(q.p) % (8 * e) != start || q.ld % 8 != ld)) return kScalar;
+  const bool params = reinterpret_cast<uintptr_t>(a.w) % 32 == 0 && reinterpret_cast<uintptr_t>(a.b) % 32 == 0;
+  return start == 0 && ld == 0 && a.n % 8 == 0 && params ? kAligned : kShifted;
 }
 
-bool norm_aligned(const NormArgs& a, size_t e) {
-  return a.n % 8 == 0 && rows_aligned(a.x, a.ldx, e) && rows_aligned(a.residual, a.ldr, e) &&
-         rows_aligned(a.dy, a.lddy, e) && rows_aligned(a.ds, a.ldds, e) &&
-         rows_aligned(a.s, a.lds, e) && rows_aligned(a.y, a.ldy, e) &&
-         rows_aligned(a.dx, a.lddx, e) && rows_aligned(a.dres, a.lddr, e) &&
-         rows_aligned(a.w, 0, 4) && rows_aligned(a.b, 0, 4);
-}
-
-// Lanes per row of a team (256: one warp tile up to 256 columns, then whole warps).
+// f(team, threads of a CTA) for rows of `n` columns (a shifted row may touch one group more).
 template <typename F>
-cudaError_t by_width(int n, F&& f) {
-  if (n <= 32) return f(Team<0, 4, 1>{});
-  if (n <= 64) return f(Team<0, 8, 1>{});
-  if (n <= 128) return f(Team<0, 16, 1>{});
-  if (n <= 256) return f(Team<1, 32, 1>{});
-  if (n <= 512) return f(Team<2, 32, 1>{});
-  if (n <= 1024) return f(Team<4, 32, 1>{});
-  if (n <= 2048) return f(Team<8, 32, 1>{});
-  if (n <= 4096) return f(Team<8, 32, 2>{});
-  return f(Team<8, 32, 4>{});
+cudaError_t by_width(int n, Layout ly, F&& f) {
+  const int c = ly == kShifted ? n + 7 : n;
+  if (c <= 32) return f(Team<0, 4, 1>{}, kThreads);
+  if (c <= 64) return f(Team<0, 8, 1>{}, kThreads);
+  if (c <= 128) return f(Team<0, 16, 1>{}, kThreads);
+  if (c <= 256) return f(Team<1, 32, 1>{}, kThreads);
+  if (c <= 512) return f(Team<2, 32, 1>{}, kThreads);
+  if (c <= 1024) return f(Team<4, 32, 1>{}, kThreads);
+  return f(Team<kWholeCta, 32, 2>{}, (c + 511) / 512 * 32);
 }
+// Widest row: in two pieces of 16 warps.
+bool long_row(int n, Layout ly) { return n + (ly == kShifted ? 7 : 0) > kLongCols; }
 
-int teams_per_cta(int n) {
-  return n <= 32 ? 64 : n <= 64 ? 32 : n <= 128 ? 16 : n <= 256 ? 8 : n <= 512 ? 4 : n <= 1024 ? 2 : 1;
-}
-
-// CTAs of the backward pass, which is also the number of partial sums: from the sizes alone.
-int bwd_ctas(int rows, int n) {
-  if (n > kLongCols) return rows < 64 ? rows : 64;
-  const int need = (rows + teams_per_cta(n) - 1) / teams_per_cta(n);
-  return need < kNormCtas ? need : kNormCtas;
+// CTAs of the backward pass, which is also the number of partial sums: as many as are resident (two
+// of 256 threads an SM with dropout, else three; 262144 x 256: fp32 125 us with three an SM, 134 and
+// 136 us with two and four; bf16 with dropout 128 us with two, 132 and 155 us with four and three).
+// Multiples of eight, where a team takes several rows.
+constexpr int kLongParts = 64;
+int most_ctas(int n, bool drop) { return 152 * (drop && n <= 256 ? 2 : 3); }
+int ctas_for(int rows, int teams, int most) {
+  const int need = (rows + teams - 1) / teams;
+  return need < most ? need : most;
 }
 
 template <typename T, bool DROP>
 cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
   LaunchCfg c;
-  c.block = dim3(kThreads);
   c.stream = s;
-  if (a.n > kLongCols) {
+  const Layout ly = layout_of(a, sizeof(T));
+  if (long_row(a.n, ly)) {
+    c.block = dim3(kThreads);
     c.grid = dim3(a.rows);
     return launch(c, norm_long_fwd_kernel<T, DROP>, a);
   }
-  const bool al = norm_aligned(a, sizeof(T));
-  return by_width(a.n, [&](auto tm) {
+  return by_width(a.n, ly, [&](auto tm, int threads) {
     using TM = decltype(tm);
-    const int need = (a.rows + TM::kTeams - 1) / TM::kTeams;
-    c.grid = dim3(need < 2 * kNormCtas ? need : 2 * kNormCtas);
-    return al ? launch(c, norm_fwd_kernel<T, TM, true, DROP>, a)
-              : launch(c, norm_fwd_kernel<T, TM, false, DROP>, a);
+    c.block = dim3(threads);
+    c.grid = dim3(ctas_for(a.rows, TM::kTeams, 152 * 8));
+    if (ly == kAligned) return launch(c, norm_fwd_kernel<T, TM, kAligned, DROP>, a);
+    if (ly == kShifted) return launch(c, norm_fwd_kernel<T, TM, kShifted, DROP>, a);
+    return launch(c, norm_fwd_kernel<T, TM, kScalar, DROP>, a);
   });
 }
 
 template <typename T, bool DROP>
 cudaError_t bwd(NormArgs a, float* dw, float* db, float* ws, cudaStream_t s) {
-  const int G = bwd_ctas(a.rows, a.n);
-  // One CTA: its sums are the result.
-  a.pw = G == 1 ? dw : ws;
-  a.pb = G == 1 ? db : ws + static_cast<size_t>(G) * a.n;
   LaunchCfg c;
-  c.block = dim3(kThreads);
   c.stream = s;
+  const Layout ly = layout_of(a, sizeof(T));
+  int G = 1;
+  auto parts = [&](int count) {  // one CTA: its sums are the result
+    G = count;
+    a.pw = G == 1 ? dw : ws;
+    a.pb = G == 1 ? db : ws + static_cast<size_t>(G) * a.n;
+  };
   cudaError_t e;
-  if (a.n > kLongCols) {
+  if (long_row(a.n, ly)) {
+    parts(a.rows < kLongParts ? a.rows : kLongParts);
+    c.block = dim3(kThreads);
     c.grid = dim3((a.n + kThreads - 1) / kThreads, G);
     e = launch(c, norm_long_param_kernel<T>, a);
     c.grid = dim3(a.rows);
     if (e == cudaSuccess) e = launch(c, norm_long_bwd_kernel<T, DROP>, a);
   } else {
-    const bool al = norm_aligned(a, sizeof(T));
-    c.grid = dim3(G);
-    e = by_width(a.n, [&](auto tm) {
+    e = by_width(a.n, ly, [&](auto tm, int threads) {
       using TM = decltype(tm);
-      return al ? launch(c, norm_bwd_kernel<T, TM, true, DROP>, a)
-                : launch(c, norm_bwd_kernel<T, TM, false, DROP>, a);
+      parts(ctas_for(a.rows, TM::kTeams, most_ctas(a.n, DROP)));
+      c.block = dim3(threads);
+      c.grid = dim3(G);
+      if (ly == kAligned) return launch(c, norm_bwd_kernel<T, TM, kAligned, DROP>, a);
+      if (ly == kShifted) return launch(c, norm_bwd_kernel<T, TM, kShifted, DROP>, a);
+      return launch(c, norm_bwd_kernel<T, TM, kScalar, DROP>, a);
     });
   }
   if (e != cudaSuccess || G == 1) return e;
@@ -552,15 +756,24 @@ cudaError_t bwd(NormArgs a, float* dw, float* db, float* ws, cudaStream_t s) {
 template <typename T>
 cudaError_t drop(const NormArgs& a, cudaStream_t s) {
   LaunchCfg c;
-  c.block = dim3(kThreads);
   c.stream = s;
-  const bool al = norm_aligned(a, sizeof(T));
-  return by_width(a.n < 256 ? a.n : 256, [&](auto tm) {
+  const Layout ly = layout_of(a, sizeof(T));
+  const int most = ly == kShifted ? 249 : 256;
+  return by_width(a.n < most ? a.n : most, ly, [&](auto tm, int threads) -> cudaError_t {
     using TM = decltype(tm);
-    const long long tiles = static_cast<long long>(a.rows) * ((a.n + TM::kCols - 1) / TM::kCols);
-    const long long need = (tiles + TM::kTeams - 1) / TM::kTeams;
-    c.grid = dim3(static_cast<unsigned>(need < 2 * kNormCtas ? need : 2 * kNormCtas));
-    return al ? launch(c, dropout_kernel<T, TM, true>, a) : launch(c, dropout_kernel<T, TM, false>, a);
+    if constexpr (TM::WPR > 1) {
+      return cudaErrorInvalidValue;  // not reached: at most one warp a row
+    } else {
+      constexpr int cols = 8 * TM::kLanes;
+      const int shift = ly == kShifted ? 7 : 0;
+      const long long tiles = static_cast<long long>(a.rows) * ((a.n + shift + cols - 1) / cols);
+      const long long need = (tiles + TM::kTeams - 1) / TM::kTeams;
+      c.block = dim3(threads);
+      c.grid = dim3(static_cast<unsigned>(need < 152 * 8 ? need : 152 * 8));
+      if (ly == kAligned) return launch(c, dropout_kernel<T, TM, kAligned>, a);
+      if (ly == kShifted) return launch(c, dropout_kernel<T, TM, kShifted>, a);
+      return launch(c, dropout_kernel<T, TM, kScalar>, a);
+    }
   });
 }
 
@@ -584,9 +797,20 @@ NormArgs to_args(const NormCall& q) {
 
 }  // namespace
 
+// Enough for every layout: shifted rows may take the next wider team, with fewer teams a CTA and
+// so more CTAs.
 size_t norm_ws_floats(int rows, int n) {
-  const int G = bwd_ctas(rows, n);
-  return G == 1 ? 0 : 2 * static_cast<size_t>(G) * n;
+  int most = 1;
+  for (const Layout ly : {kAligned, kShifted}) {
+    int G = rows < kLongParts ? rows : kLongParts;
+    if (!long_row(n, ly))
+      (void)by_width(n, ly, [&](auto tm, int) {
+        G = ctas_for(rows, decltype(tm)::kTeams, most_ctas(n, false));
+        return cudaSuccess;
+      });
+    if (G > most) most = G;
+  }
+  return most == 1 ? 0 : 2 * static_cast<size_t>(most) * n;
 }
 
 cudaError_t norm_fwd_launch(const NormCall& q, cudaStream_t s) {

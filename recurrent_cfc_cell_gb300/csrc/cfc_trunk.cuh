@@ -22,23 +22,49 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// Eight consecutive activations as fp32: 32 bytes of fp32 or 16 bytes of bf16 in one load
-// (p aligned to that size).
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                 "=f"(v[6]), "=f"(v[7])
-               : "l"(p));
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight consecutive activations as they are stored: 32 bytes of fp32 or 16 bytes of bf16, one
+// load each (p aligned to that size), or element by element.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7])
+                 : "l"(p));
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  }
+  __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = v[j];
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+  }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  // Into a cleared place.
+  __device__ __forceinline__ void set(int j, __nv_bfloat16 x) {
+    w[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x)) << (16 * (j % 2));
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo_f32(w[i]);
+      f[2 * i + 1] = bf16_hi_f32(w[i]);
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]),
                "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -115,23 +141,21 @@ __device__ __forceinline__ DropKey drop_key(const unsigned long long* rng) {
           static_cast<uint32_t>(o >> 32)};
 }
 
-// Which of the eight columns 8 * group .. 8 * group + 7 of `row` are kept (bit j: column
-// 8 * group + j): its 16-bit piece of the generator's output, lowest first, is >= cut.
-// Sixteen bits an element hold the drop probability to 2^-17 and cost one generator call for
-// eight elements; the scale uses the held probability, so the expectation is exact.
-__device__ __forceinline__ uint32_t keep_mask8(const DropKey& k, uint32_t row, uint32_t group,
-                                               uint32_t cut) {
-  const uint4 r = philox4x32(make_uint4(group, row, k.o0, k.o1), k.k0, k.k1);
-  uint32_t m = 0;
-  m |= ((r.x & 0xffffu) >= cut) ? 1u : 0u;
-  m |= ((r.x >> 16) >= cut) ? 2u : 0u;
-  m |= ((r.y & 0xffffu) >= cut) ? 4u : 0u;
-  m |= ((r.y >> 16) >= cut) ? 8u : 0u;
-  m |= ((r.z & 0xffffu) >= cut) ? 16u : 0u;
-  m |= ((r.z >> 16) >= cut) ? 32u : 0u;
-  m |= ((r.w & 0xffffu) >= cut) ? 64u : 0u;
-  m |= ((r.w >> 16) >= cut) ? 128u : 0u;
-  return m;
+// Which of the eight columns 8 * group .. 8 * group + 7 of `row` are kept: k[j] where the j-th
+// 16-bit piece of the generator's output, lowest first, is >= cut.  Sixteen bits an element hold
+// the drop probability to 2^-17 and cost one generator call for eight elements; the scale uses
+// the held probability, so the expectation is exact.
+__device__ __forceinline__ void keep8(const DropKey& key, uint32_t row, uint32_t group,
+                                      uint32_t cut, bool (&k)[8]) {
+  const uint4 r = philox4x32(make_uint4(group, row, key.o0, key.o1), key.k0, key.k1);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  const uint32_t high = cut << 16;   // compared against whole words: the low half cannot decide
+  const bool any = cut < 65536u;     // everything is dropped otherwise
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k[2 * i] = any && (w[i] << 16) >= high;
+    k[2 * i + 1] = any && w[i] >= high;
+  }
 }
 
 }  // namespace cfc
