@@ -129,15 +129,51 @@ struct Lane {
           if (!in(piece, j, n)) v[j] = 0.f;
       }
   }
-  // The same of the parameters (in no particular alignment to the rows).
-  __device__ __forceinline__ void params(const float* p, int piece, int n, float (&v)[8]) const {
+  // The same of the parameters (in no particular alignment to the rows).  `buf`: 256 floats of the
+  // warp's own; shifted lanes read their eight columns from there, so that the loads from memory
+  // are consecutive.  Every lane of the warp takes part.
+  __device__ __forceinline__ void params(const float* p, int piece, int n, float* buf,
+                                         float (&v)[8]) const {
     if constexpr (LY == kAligned) {
       Raw8<float> r;
       load(p, 0, 0, 1, piece, n, r);
       r.get(v);
+    } else if constexpr (LY == kShifted && TM::WPR > 0) {
+      const int c = piece * TM::cols() + base - shift;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = c + j * 32 + lane;
+        buf[j * 32 + lane] = static_cast<unsigned>(at) < static_cast<unsigned>(n) ? p[at] : 0.f;
+      }
+      __syncwarp();
+      const float4 lo = *reinterpret_cast<const float4*>(buf + lane * 8);
+      const float4 hi = *reinterpret_cast<const float4*>(buf + lane * 8 + 4);
+      v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+      v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+      __syncwarp();
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = in(piece, j, n) ? p[col(piece, j)] : 0.f;
+    }
+  }
+  // The lane's eight columns into a row of fp32 sums, likewise.
+  __device__ __forceinline__ void put_sums(float* p, int piece, int n, float* buf,
+                                           const float (&v)[8]) const {
+    if constexpr (LY == kShifted && TM::WPR > 0) {
+      *reinterpret_cast<float4*>(buf + lane * 8) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(buf + lane * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      __syncwarp();
+      const int c = piece * TM::cols() + base - shift;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = c + j * 32 + lane;
+        if (static_cast<unsigned>(at) < static_cast<unsigned>(n)) p[at] = buf[j * 32 + lane];
+      }
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in(piece, j, n)) p[col(piece, j)] = v[j];
     }
   }
   template <typename T>
@@ -263,7 +299,9 @@ __device__ __forceinline__ Turns turns_of(int rows, int team) {
 template <typename T, typename TM, Layout LY, bool DROP>
 __global__ void __launch_bounds__(TM::kMaxThreads) norm_fwd_kernel(const NormArgs a) {
   __shared__ Slots<1> slot;
+  __shared__ __align__(16) float bufs[LY == kShifted ? kMaxWarps : 1][256];
   clear_slots<TM>(slot);
+  float* const buf = bufs[LY == kShifted ? threadIdx.x / 32 : 0];
   Lane<TM, LY> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -286,8 +324,8 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_fwd_kernel(const NormArg
   auto params = [&]() {
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
-      at.params(a.w, i, n, w[i]);
-      at.params(a.b, i, n, b[i]);
+      at.params(a.w, i, n, buf, w[i]);
+      at.params(a.b, i, n, buf, b[i]);
     }
   };
   if constexpr (LY != kAligned) params();
@@ -365,8 +403,10 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
   __shared__ Slots<2> slot;
   __shared__ float part[TM::kTeams > 1 ? 2 : 1][TM::kTeams > 1 ? kThreads / 32 : 1][256];
   __shared__ int shifts[TM::kTeams];
+  __shared__ __align__(16) float bufs[LY == kShifted ? kMaxWarps : 1][256];
   grid_dep_launch_dependents();
   clear_slots<TM>(slot);
+  float* const buf = bufs[LY == kShifted ? threadIdx.x / 32 : 0];
   Lane<TM, LY> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -394,7 +434,7 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
   at.set_row(xp + (tn.first < a.rows ? tn.first : 0) * a.ldx);
 #pragma unroll
   for (int i = 0; i < TM::I; ++i) {
-    if constexpr (!kReload) at.params(a.w, i, n, w[i]);
+    if constexpr (!kReload) at.params(a.w, i, n, buf, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
   }
@@ -408,7 +448,7 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
-      if constexpr (kReload) at.params(a.w, i, n, w[i]);
+      if constexpr (kReload) at.params(a.w, i, n, buf, w[i]);
       at.clean(nx[i], i, n, hat[i]);
       at.clean(ng[i], i, n, g[i]);
       if (DROP && sp) at.clean(ns[i], i, n, ds[i]);
@@ -459,13 +499,10 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
   float* pb = a.pb + static_cast<size_t>(blockIdx.x) * n;
   if constexpr (TM::kTeams == 1) {
 #pragma unroll
-    for (int i = 0; i < TM::I; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (at.in(i, j, n)) {
-          pw[at.col(i, j)] = dw[i][j];
-          pb[at.col(i, j)] = db[i][j];
-        }
+    for (int i = 0; i < TM::I; ++i) {
+      at.put_sums(pw, i, n, buf, dw[i]);
+      at.put_sums(pb, i, n, buf, db[i]);
+    }
   } else {
     // A team's columns lie `shift` further on in its part; teams of one warp are shifted alike
     // only if they are aligned or scalar, so shifted ones are added one team at a time.
@@ -712,7 +749,7 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
   return by_width(a.n, ly, [&](auto tm, int threads) {
     using TM = decltype(tm);
     c.block = dim3(threads);
-    c.grid = dim3(ctas_for(a.rows, TM::kTeams, 152 * 8));
+    c.grid = dim3(ctas_for(a.rows, TM::kTeams, ly == kAligned ? 152 * 8 : 152 * 3));
     if (ly == kAligned) return launch(c, norm_fwd_kernel<T, TM, kAligned, DROP>, a);
     if (ly == kShifted) return launch(c, norm_fwd_kernel<T, TM, kShifted, DROP>, a);
     return launch(c, norm_fwd_kernel<T, TM, kScalar, DROP>, a);

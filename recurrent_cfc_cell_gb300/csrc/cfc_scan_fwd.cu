@@ -361,66 +361,73 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
   v[2] = bf16_lo_f32(r.y); v[3] = bf16_hi_f32(r.y);
 }
 
-// VEC: rows of four states are aligned, in the states (16 bytes) and in B and C.
+// VEC: groups of four states are whole and aligned, in the states (16 bytes) and in B and C.  A
+// CTA takes `seqs` sequences, kSeqs at a time; LPC lanes hold all states (4 LPC >= N).
 template <typename T, int LPC, bool VEC>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
+__global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q, const int per_group,
+                                                        const int seqs) {
   constexpr int kOwn = LPC >= kSeqs ? 1 : kSeqs / LPC;  // sequences whose values a lane forms
   const int lane = threadIdx.x % LPC;
   const int d_raw = blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
-  const bool live = d_raw < q.D;
-  const int d = live ? d_raw : q.D - 1;
-  const int group = d / (q.D / q.G);
+  const int d = min(d_raw, q.D - 1);
+  const int group = q.G == 1 ? 0 : d / per_group;
+  const int n = lane * 4;
+  const bool in = n < q.N, live = d_raw < q.D;
   const float bias = q.dt_bias ? q.dt_bias[d] : 0.f, skip = q.skip ? q.skip[d] : 0.f;
-  const int b0 = blockIdx.y * kSeqs;
-  float own_d[kOwn], own_x[kOwn], own_z[kOwn];
+  const size_t row = static_cast<size_t>(q.D) * q.N;  // states of a sequence
+  const size_t ho = static_cast<size_t>(d) * q.N + n, go = static_cast<size_t>(group) * q.N + n;
+  float A2[4];
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int k = lane % kSeqs + i * LPC, b = min(b0 + k, q.B - 1);
-    own_x[i] = to_f32(static_cast<const T*>(q.x)[b * q.x_b + d]);
-    own_z[i] = q.z ? to_f32(static_cast<const T*>(q.z)[b * q.z_b + d]) : 0.f;
-    const float raw = to_f32(static_cast<const T*>(q.dt)[b * q.dt_b + d]) + bias;
-    own_d[i] = q.softplus ? softplus_f(raw) : raw;
-  }
-  float dv[kSeqs], uv[kSeqs], yv[kSeqs] = {};
-#pragma unroll
-  for (int k = 0; k < kSeqs; ++k) {
-    dv[k] = __shfl_sync(0xffffffffu, own_d[k / LPC % kOwn], k % LPC, LPC);
-    uv[k] = dv[k] * __shfl_sync(0xffffffffu, own_x[k / LPC % kOwn], k % LPC, LPC);
-  }
-  for (int n = lane * 4; n < q.N; n += LPC * 4) {
-    float A2[4], h[kSeqs][4], Bv[kSeqs][4], Cv[kSeqs][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      A2[i] = VEC || n + i < q.N ? q.A[static_cast<size_t>(d) * q.N + n + i] * kLog2e : 0.f;
+  for (int i = 0; i < 4; ++i) A2[i] = n + i < q.N ? q.A[ho + i] * kLog2e : 0.f;
+  const int b_end = min(q.B, (static_cast<int>(blockIdx.y) + 1) * seqs);
+  for (int b0 = blockIdx.y * seqs; b0 < b_end; b0 += kSeqs) {
+    // Uniform bases of the sequences (the last one again where there are fewer than kSeqs).
+    const float* hp = q.h0 + b0 * row;
+    const T* Bp = static_cast<const T*>(q.Bm) + b0 * q.Bm_b;
+    const T* Cp = static_cast<const T*>(q.Cm) + b0 * q.Cm_b;
+    const int last = b_end - 1 - b0;
+    float h[kSeqs][4] = {}, Bv[kSeqs][4] = {}, Cv[kSeqs][4] = {};
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
-      const int b = min(b0 + k, q.B - 1);
-      const float* hp = q.h0 + (static_cast<size_t>(b) * q.D + d) * q.N + n;
-      const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N + n;
-      const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N + n;
+      const int kk = min(k, last);
       if constexpr (VEC) {
-        load4(hp, h[k]);
-        load4(Bp, Bv[k]);
-        load4(Cp, Cv[k]);
+        if (in) {
+          load4(hp + kk * row + ho, h[k]);
+          load4(Bp + kk * q.Bm_b + go, Bv[k]);
+          load4(Cp + kk * q.Cm_b + go, Cv[k]);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = n + i < q.N;
-          h[k][i] = in ? hp[i] : 0.f;
-          Bv[k][i] = in ? to_f32(Bp[i]) : 0.f;
-          Cv[k][i] = in ? to_f32(Cp[i]) : 0.f;
-        }
+        for (int i = 0; i < 4; ++i)
+          if (n + i < q.N) {
+            h[k][i] = hp[kk * row + ho + i];
+            Bv[k][i] = to_f32(Bp[kk * q.Bm_b + go + i]);
+            Cv[k][i] = to_f32(Cp[kk * q.Cm_b + go + i]);
+          }
       }
     }
+    float own_d[kOwn], own_x[kOwn], own_z[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int b = b0 + min(lane % kSeqs + i * LPC, last);
+      own_x[i] = to_f32(static_cast<const T*>(q.x)[b * q.x_b + d]);
+      own_z[i] = q.z ? to_f32(static_cast<const T*>(q.z)[b * q.z_b + d]) : 0.f;
+      const float raw = to_f32(static_cast<const T*>(q.dt)[b * q.dt_b + d]) + bias;
+      own_d[i] = q.softplus ? softplus_f(raw) : raw;
+    }
+    float yv[kSeqs];
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
+      const float dv = __shfl_sync(0xffffffffu, own_d[k / LPC % kOwn], k % LPC, LPC);
+      const float uv = dv * __shfl_sync(0xffffffffu, own_x[k / LPC % kOwn], k % LPC, LPC);
+      yv[k] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        h[k][i] = fmaf(exp2_f(dv[k] * A2[i]), h[k][i], uv[k] * Bv[k][i]);
+        h[k][i] = fmaf(exp2_f(dv * A2[i]), h[k][i], uv * Bv[k][i]);
         yv[k] = fmaf(h[k][i], Cv[k][i], yv[k]);
       }
-      if (live && b0 + k < q.B) {
-        float* np = q.h_last + (static_cast<size_t>(b0 + k) * q.D + d) * q.N + n;
+      if (live && in && k <= last) {
+        float* np = q.h_last + (b0 + k) * row + ho;
         if constexpr (VEC) {
           *reinterpret_cast<float4*>(np) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
         } else {
@@ -430,18 +437,18 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q) {
         }
       }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < kSeqs; ++k) {
+    for (int m = LPC / 2; m > 0; m >>= 1)
 #pragma unroll
-    for (int m = LPC / 2; m > 0; m >>= 1) yv[k] += __shfl_xor_sync(0xffffffffu, yv[k], m);
-  }
+      for (int k = 0; k < kSeqs; ++k) yv[k] += __shfl_xor_sync(0xffffffffu, yv[k], m);
 #pragma unroll
-  for (int k = 0; k < kSeqs; ++k) {
-    if (!live || lane != k % LPC || b0 + k >= q.B) continue;
-    float y = fmaf(skip, own_x[k / LPC % kOwn], yv[k]);
-    if (q.z) y *= own_z[k / LPC % kOwn] * sigmoid_f(own_z[k / LPC % kOwn]);
-    static_cast<T*>(q.y)[(b0 + k) * q.y_b + d] = from_f32<T>(y);
+    for (int k = 0; k < kSeqs; ++k) {
+      if (!live || lane != k % LPC || k > last) continue;
+      const float z = own_z[k / LPC % kOwn];
+      float y = fmaf(skip, own_x[k / LPC % kOwn], yv[k]);
+      if (q.z) y *= z * sigmoid_f(z);
+      static_cast<T*>(q.y)[(b0 + k) * q.y_b + d] = from_f32<T>(y);
+    }
   }
 }
 
@@ -545,18 +552,23 @@ cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s) {
                    reinterpret_cast<uintptr_t>(q.Bm) % e == 0 && q.Bm_b % 4 == 0 &&
                    reinterpret_cast<uintptr_t>(q.Cm) % e == 0 && q.Cm_b % 4 == 0;
   int lpc = 1;
-  while (lpc * 4 < q.N && lpc < 32) lpc *= 2;
+  while (lpc * 4 < q.N) lpc *= 2;
   LaunchCfg c;
   c.block = dim3(256);
   c.stream = s;
-  c.grid = dim3((q.D + 256 / lpc - 1) / (256 / lpc), (q.B + kSeqs - 1) / kSeqs);
+  // Sixteen sequences a CTA where that still leaves several CTAs an SM (A and the channel's
+  // parameters are then read once for them), else four.
+  const int tiles = (q.D + 256 / lpc - 1) / (256 / lpc);
+  const int seqs = static_cast<long long>(tiles) * ((q.B + 15) / 16) >= 152 * 8 ? 16 : kSeqs;
+  const int per_group = q.D / q.G;
+  c.grid = dim3(tiles, (q.B + seqs - 1) / seqs);
   auto go = [&](auto L) {
     constexpr int l = decltype(L)::value;
     if (q.bf16)
-      return vec ? launch(c, scan_step_kernel<__nv_bfloat16, l, true>, q)
-                 : launch(c, scan_step_kernel<__nv_bfloat16, l, false>, q);
-    return vec ? launch(c, scan_step_kernel<float, l, true>, q)
-               : launch(c, scan_step_kernel<float, l, false>, q);
+      return vec ? launch(c, scan_step_kernel<__nv_bfloat16, l, true>, q, per_group, seqs)
+                 : launch(c, scan_step_kernel<__nv_bfloat16, l, false>, q, per_group, seqs);
+    return vec ? launch(c, scan_step_kernel<float, l, true>, q, per_group, seqs)
+               : launch(c, scan_step_kernel<float, l, false>, q, per_group, seqs);
   };
   switch (lpc) {
     case 1: return go(std::integral_constant<int, 1>{});
