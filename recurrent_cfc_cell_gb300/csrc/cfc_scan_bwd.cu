@@ -12,14 +12,12 @@
 // that many steps from the last: forwards through the chunk from its kept state (the sums with
 // h_t: y, dC), leaving q_t in shared memory, then backwards (everything with e_t).
 //
-// A lane holds four channels times four states (its arithmetic in packed pairs of channels), and a
-// warp 32 channels times 16 states: the sums over states (y, e B, e A q) then cross four lanes and
-// the sums over channels (dB, dC) eight, each by exchanging halves, so that a step of 512 state
-// updates takes 17 shuffles; with one channel's sixteen states to a lane the sums over channels
-// alone would take 31.  What a step
+// A lane holds a pair of channels (its arithmetic is packed) times four states, and a warp 16
+// channels times 16 states: the sums over states (y, e B, e A q) then cross four lanes and the
+// sums over channels (dB, dC) eight, each by exchanging halves.  What a step
 // needs per channel (d, x, r and the gate's and softplus's derivatives) is formed once per
 // chunk, a thread a value, and read back four channels at a time.  NT warps side by side hold up
-// to 16 NT states, CW warps 32 CW channels.  Sums over warps, channel tiles, sequences and
+// to 16 NT states, CW warps 16 CW channels.  Sums over warps, channel tiles, sequences and
 // splits are added in a fixed order (shared memory, then a merge), without atomics.
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
@@ -31,29 +29,29 @@ namespace {
 constexpr int T8 = kScanPeriod;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+constexpr int kCL = 2;       // channels of a lane, a packed pair
+constexpr int kWC = 8 * kCL;  // channels of a warp
+
 template <int CW, int NT>
 struct Shape {
-  static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = 32 * CW, NP = 16 * NT;
-  // Shared memory, in floats.
-  static constexpr int kPer = T8 * CH;                  // one value per (step, channel)
-  static constexpr int oD = 0, oU = oD + kPer, oR = oU + kPer;  // d, d x, r
-  static constexpr int oX = oR + kPer, oZ = oX + kPer, oS = oZ + kPer;
-  static constexpr int oY = oS + kPer, oV = oY + NT * kPer, oW = oV + NT * kPer;
-  static constexpr int oB = oW + NT * kPer, oC = oB + 2 * T8 * NP;  // every value twice
-  static constexpr int oDB = oC + 2 * T8 * NP, oDC = oDB + CW * T8 * NP;
-  static constexpr int oQ = oDC + CW * T8 * NP;         // [warp][step][4][lane][4]
-  static constexpr int kFloats = oQ + kWarps * T8 * 512;
+  static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = kWC * CW, NP = 16 * NT;
+  static constexpr int kPer = T8 * CH;  // one value per (step, channel)
+  static constexpr int kRows = kThreads / CH;  // threads of a channel in the per-channel phases
+  static constexpr int kHist = T8 * 4 * kCL * 32;  // q_t of a warp
+  // Dynamic shared memory, in floats: q_t as [warp][step][2][lane][4], then what only the
+  // per-channel phases use: x, dy silu'(z), sigmoid(dt + bias), and at NT = 8 the sums W.
+  static constexpr int oQ = 0, oX = kWarps * kHist, oZ = oX + kPer, oS = oZ + kPer;
+  static constexpr int oW = oS + kPer;
+  static constexpr bool kSpill = NT == 8;  // W does not fit the 48 KB of static shared memory
+  static constexpr int kFloats = oW + (kSpill ? NT * kPer : 0);
 };
 
-// Sum of v[0..3] over the four state lanes (lane bits 0, 1): lane nl keeps v[nl].
-__device__ __forceinline__ float sum_states(const float (&v)[4], int lane) {
+// Sum of a pair over the four state lanes (lane bits 0, 1): the lane keeps the first value where
+// bit 1 is clear and the second where it is set.
+__device__ __forceinline__ float sum_states(float2 v, int lane) {
   const bool hi = lane & 2;
-  const float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
-  const float s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
-  const float a = k0 + __shfl_xor_sync(0xffffffffu, s0, 2);
-  const float b = k1 + __shfl_xor_sync(0xffffffffu, s1, 2);
-  const bool lo = lane & 1;
-  return (lo ? b : a) + __shfl_xor_sync(0xffffffffu, lo ? a : b, 1);
+  const float a = (hi ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, hi ? v.x : v.y, 2);
+  return a + __shfl_xor_sync(0xffffffffu, a, 1);
 }
 
 // Sum of v[0..3] over the eight channel lanes (lane bits 2..4): the lane keeps v[lane >> 3].
@@ -78,7 +76,14 @@ struct BwdPlan {
 template <typename T, int CW, int NT>
 __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q, const BwdPlan pl) {
   using Sh = Shape<CW, NT>;
+  // Arrays of their own for what the walks read and what they write, so that a step's loads can
+  // be issued before the last step's stores.
   extern __shared__ __align__(16) float sm[];
+  __shared__ __align__(16) float sD[Sh::kPer], sU[Sh::kPer], sR[Sh::kPer];  // d, d x, r
+  __shared__ __align__(16) float sB[2 * T8 * Sh::NP], sC[2 * T8 * Sh::NP];  // every value twice
+  __shared__ float sY[NT * Sh::kPer], sV[NT * Sh::kPer], sWs[Sh::kSpill ? 1 : NT * Sh::kPer];
+  __shared__ float sDB[CW * T8 * Sh::NP], sDC[CW * T8 * Sh::NP];
+  float* const sW = Sh::kSpill ? sm + Sh::oW : sWs;
   grid_dep_launch_dependents();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int nt = warp % NT, cw = warp / NT;
@@ -90,10 +95,12 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   const int d_base = group * pl.per_group;   // the group's first channel
   const int t_base = tile * Sh::CH;          // the tile's first channel in its group
 
-  // This thread's channel in the per-channel phases, and its steps tf, tf + NT, ...  Addresses
+  // This thread's channel in the per-channel phases, and its steps tf, tf + kRows, ...  Addresses
   // are a uniform base (sequence, tile, step) plus the thread's own offset.
-  const int chf = NT == 1 ? tid : tid % Sh::CH, tf = NT == 1 ? 0 : tid / Sh::CH;
-  const bool livef = t_base + chf < pl.per_group;
+  constexpr int NR = Sh::kRows;
+  const bool busy = NR <= T8 || tid / Sh::CH < T8;  // threads beyond the chunk's steps rest
+  const int chf = tid % Sh::CH, tf = busy ? tid / Sh::CH : 0;
+  const bool livef = busy && t_base + chf < pl.per_group;
   const unsigned own = livef ? chf : 0;
   const int d0 = d_base + t_base;
   const float bias = q.dt_bias ? q.dt_bias[d0 + own] : 0.f, skip = q.skip ? q.skip[d0 + own] : 0.f;
@@ -104,55 +111,50 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   T* dxp = static_cast<T*>(q.dx) + b * q.dx_b + d0;
   T* dtp = static_cast<T*>(q.ddt) + b * q.ddt_b + d0;
   T* dzp = q.dz ? static_cast<T*>(q.dz) + b * q.dz_b + d0 : nullptr;
-  // The thread's element of row `base`, NT rows apart from the thread's first.
-  auto pick = [&](auto* base, long long stride) {
-    if constexpr (NT == 1) return base + own;
-    return base + (own + tf * stride);
-  };
+  // The thread's element of the steps from `base` on.
+  auto pick = [&](auto* base, long long stride) { return base + (own + tf * stride); };
   const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N;
   const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
 
-  // This lane's states: channels c0 .. c0 + 3 of the tile, states n0 .. n0 + 3, in pairs of
-  // channels: v[s][p] holds channels c0 + 2 p and c0 + 2 p + 1 of state n0 + s.
-  const int c0 = cw * 32 + (lane >> 2) * 4, n0 = nt * 16 + (lane & 3) * 4;
-  float2 A2[4][2], e[4][2], dA[4][2], h[4][2];
+  // This lane's states: channels c0 and c0 + 1 of the tile (a pair), states n0 .. n0 + 3.
+  const int c0 = cw * kWC + (lane >> 2) * kCL, n0 = nt * 16 + (lane & 3) * 4;
+  float2 A2[4], e[4], dA[4], h[4];
   auto in_state = [&](int c, int s) { return t_base + c0 + c < pl.per_group && n0 + s < q.N; };
   auto state_at = [&](int c) {  // offset of state n0 of channel c in a [B][D][N] plane
     return (static_cast<size_t>(b) * q.D + d_base + t_base + c0 + c) * q.N + n0;
   };
   // The lane's states of a plane, zero outside.
   const bool quad = q.N % 4 == 0;
-  auto load_states = [&](const float* p, float2 (&v)[4][2]) {
+  const size_t s_at = state_at(0);
+  auto load_states = [&](const float* p, float2 (&v)[4]) {
+    float r[2][4] = {};
+    if (p != nullptr) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float r[4] = {0.f, 0.f, 0.f, 0.f};
-      if (p != nullptr && in_state(c, 0)) {
-        const float* at = p + state_at(c);
+      for (int c = 0; c < 2; ++c) {
+        if (!in_state(c, 0)) continue;
+        const float* at = p + s_at + c * q.N;
         if (quad) {
           const float4 f = *reinterpret_cast<const float4*>(at);
-          r[0] = f.x; r[1] = f.y; r[2] = f.z; r[3] = f.w;
+          r[c][0] = f.x; r[c][1] = f.y; r[c][2] = f.z; r[c][3] = f.w;
         } else {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            if (n0 + s < q.N) r[s] = at[s];
+            if (n0 + s < q.N) r[c][s] = at[s];
         }
       }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) (c & 1 ? v[s][c / 2].y : v[s][c / 2].x) = r[s];
     }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = make_float2(r[0][s], r[1][s]);
   };
   load_states(pl.carry ? pl.carry + split * plane : q.dh_last, e);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const float av = in_state(c, s)
-          ? q.A[static_cast<size_t>(d_base + t_base + c0 + c) * q.N + n0 + s] * kLog2e : 0.f;
-      (c & 1 ? A2[s][c / 2].y : A2[s][c / 2].x) = av;
-      (c & 1 ? dA[s][c / 2].y : dA[s][c / 2].x) = 0.f;
-    }
+  for (int s = 0; s < 4; ++s) {
+    const float* at = q.A + static_cast<size_t>(d_base + t_base + c0) * q.N + n0 + s;
+    A2[s] = make_float2(in_state(0, s) ? at[0] * kLog2e : 0.f, in_state(1, s) ? at[q.N] * kLog2e : 0.f);
+    dA[s] = make_float2(0.f, 0.f);
+  }
   float dskip = 0.f, dbias = 0.f;
-  float* const hist = sm + Sh::oQ + warp * (T8 * 512) + lane * 4;
+  float* const hist = sm + Sh::oQ + warp * Sh::kHist + lane * 4;
 
   // dB / dC of this tile: partial sums, or the outputs themselves.
   auto put_bc = [&](int t, int n, float vb, float vc) {
@@ -169,8 +171,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 
   const int chunks = end > lo ? (end - lo + T8 - 1) / T8 : 0;
   // Steps after the sequence's end: zeros.
-  for (int t = lo + chunks * T8 + tf; t < hi; t += NT) {
-    if (!livef) continue;
+  for (int t = lo + chunks * T8 + tf; livef && t < hi; t += NR < T8 ? NR : T8) {
     dxp[t * q.dx_t + own] = from_f32<T>(0.f);
     dtp[t * q.ddt_t + own] = from_f32<T>(0.f);
     if (dzp) dzp[t * q.dz_t + own] = from_f32<T>(0.f);
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     for (int n = tid; n < q.N; n += Sh::kThreads) put_bc(t, n, 0.f, 0.f);
 
   // The next chunk's inputs, as they are stored.
-  constexpr int kEl = T8 / NT, kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
-  static_assert(T8 % NT == 0, "every thread has the same number of steps");
+  constexpr int kEl = NR < T8 ? T8 / NR : 1, kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
+  static_assert(T8 % NR == 0 || NR % T8 == 0, "every thread has the same number of steps");
   T rx[kEl], rt[kEl], rz[kEl], rg[kEl], rB[kBC], rC[kBC];
   const T none = from_f32<T>(0.f);
   auto fetch_as = [&](int t0, auto all) {
@@ -191,15 +192,15 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     const T* z0 = zp ? zp + t0 * q.z_t : nullptr;
 #pragma unroll
     for (int i = 0; i < kEl; ++i) {
-      const bool in = kAll || t0 + tf + i * NT < end;
-      rx[i] = in ? *pick(x0 + i * NT * q.x_t, q.x_t) : none;
-      rt[i] = in ? *pick(dt0 + i * NT * q.dt_t, q.dt_t) : none;
-      rg[i] = in ? *pick(g0 + i * NT * q.dy_t, q.dy_t) : none;
+      const bool in = kAll || t0 + tf + i * NR < end;
+      rx[i] = in ? *pick(x0 + i * NR * q.x_t, q.x_t) : none;
+      rt[i] = in ? *pick(dt0 + i * NR * q.dt_t, q.dt_t) : none;
+      rg[i] = in ? *pick(g0 + i * NR * q.dy_t, q.dy_t) : none;
     }
     if (zp) {
 #pragma unroll
       for (int i = 0; i < kEl; ++i)
-        rz[i] = kAll || t0 + tf + i * NT < end ? *pick(z0 + i * NT * q.z_t, q.z_t) : none;
+        rz[i] = kAll || t0 + tf + i * NR < end ? *pick(z0 + i * NR * q.z_t, q.z_t) : none;
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       const float2 d2 = q.softplus ? softplus2_f(raw) : raw;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const int i = 2 * j + m, k = tf + i * NT;
-        if (i < kEl) {
+        const int i = 2 * j + m, k = tf + i * NR;
+        if (i < kEl && busy) {
           // Steps past the end and channels past the group's leave the state, its gradient and the
           // sums over channels alone: d = 0, x = 0, r = 0.
           const bool in = livef && t0 + k < end;
@@ -241,9 +242,9 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
             zf = gs * fmaf(z, 1.f - s, 1.f);
           }
           const int at = k * Sh::CH + chf;
-          sm[Sh::oD + at] = dv;
-          sm[Sh::oU + at] = dv * xv;
-          sm[Sh::oR + at] = rv;
+          sD[at] = dv;
+          sU[at] = dv * xv;
+          sR[at] = rv;
           sm[Sh::oX + at] = xv;
           sm[Sh::oZ + at] = zf;
           sm[Sh::oS + at] = !in ? 0.f : q.softplus ? sigmoid_f(m ? raw.y : raw.x) : 1.f;
@@ -255,8 +256,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       const int at = tid + i * Sh::kThreads;
       if (at < T8 * Sh::NP) {
         const float bv = to_f32(rB[i]), cv = to_f32(rC[i]);
-        reinterpret_cast<float2*>(sm + Sh::oB)[at] = make_float2(bv, bv);
-        reinterpret_cast<float2*>(sm + Sh::oC)[at] = make_float2(cv, cv);
+        reinterpret_cast<float2*>(sB)[at] = make_float2(bv, bv);
+        reinterpret_cast<float2*>(sC)[at] = make_float2(cv, cv);
       }
     }
     __syncthreads();
@@ -264,47 +265,44 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 
     // What both directions read of a step: d, d x and r of the lane's four channels in pairs, B
     // and C of its four states, each twice.
-    float2 d2[2], u2[2], r2[2], B2[4], C2[4];
+    float2 d2, u2, r2, B2[4], C2[4];
     auto read = [&](int k) {
-      const float4 dv = *reinterpret_cast<const float4*>(&sm[Sh::oD + k * Sh::CH + c0]);
-      const float4 uv = *reinterpret_cast<const float4*>(&sm[Sh::oU + k * Sh::CH + c0]);
-      const float4 rv = *reinterpret_cast<const float4*>(&sm[Sh::oR + k * Sh::CH + c0]);
-      d2[0] = make_float2(dv.x, dv.y); d2[1] = make_float2(dv.z, dv.w);
-      u2[0] = make_float2(uv.x, uv.y); u2[1] = make_float2(uv.z, uv.w);
-      r2[0] = make_float2(rv.x, rv.y); r2[1] = make_float2(rv.z, rv.w);
+      d2 = *reinterpret_cast<const float2*>(&sD[k * Sh::CH + c0]);
+      u2 = *reinterpret_cast<const float2*>(&sU[k * Sh::CH + c0]);
+      r2 = *reinterpret_cast<const float2*>(&sR[k * Sh::CH + c0]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 bv = *reinterpret_cast<const float4*>(&sm[Sh::oB + 2 * (k * Sh::NP + n0) + 4 * i]);
-        const float4 cv = *reinterpret_cast<const float4*>(&sm[Sh::oC + 2 * (k * Sh::NP + n0) + 4 * i]);
+        const float4 bv = *reinterpret_cast<const float4*>(&sB[2 * (k * Sh::NP + n0) + 4 * i]);
+        const float4 cv = *reinterpret_cast<const float4*>(&sC[2 * (k * Sh::NP + n0) + 4 * i]);
         B2[2 * i] = make_float2(bv.x, bv.y); B2[2 * i + 1] = make_float2(bv.z, bv.w);
         C2[2 * i] = make_float2(cv.x, cv.y); C2[2 * i + 1] = make_float2(cv.z, cv.w);
       }
     };
-    const float2 zero2 = make_float2(0.f, 0.f);
+    const bool even = !(lane & 1);
+    const int y_at = nt * Sh::kPer + cw * kWC + (lane >> 1);  // of a sum over states
 
     // ---- forwards through the chunk
 #pragma unroll 2
     for (int k = 0; k < T8; ++k) {
       read(k);
-      float2 y2[2] = {zero2, zero2}, dc[4], qq[4][2];
+      float2 y2, qq[4];
+      float dc[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float2 m = __fmul2_rn(d2[p], A2[s][p]);
-          qq[s][p] = __fmul2_rn(make_float2(exp2_f(m.x), exp2_f(m.y)), h[s][p]);
-          h[s][p] = fma2(u2[p], B2[s], qq[s][p]);
-          y2[p] = fma2(h[s][p], C2[s], y2[p]);
-        }
-        dc[s] = fma2(r2[1], h[s][1], __fmul2_rn(r2[0], h[s][0]));
-        *reinterpret_cast<float4*>(hist + (k * 4 + s) * 128) =
-            make_float4(qq[s][0].x, qq[s][0].y, qq[s][1].x, qq[s][1].y);
+        const float2 m = __fmul2_rn(d2, A2[s]);
+        qq[s] = __fmul2_rn(make_float2(exp2_f(m.x), exp2_f(m.y)), h[s]);
+        h[s] = fma2(u2, B2[s], qq[s]);
+        y2 = s == 0 ? __fmul2_rn(h[s], C2[s]) : fma2(h[s], C2[s], y2);
+        dc[s] = fmaf(r2.y, h[s].y, r2.x * h[s].x);
       }
-      const float y[4] = {y2[0].x, y2[0].y, y2[1].x, y2[1].y};
-      sm[Sh::oY + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(y, lane);
-      const float dcs[4] = {dc[0].x + dc[0].y, dc[1].x + dc[1].y, dc[2].x + dc[2].y, dc[3].x + dc[3].y};
-      const float sc = sum_channels(dcs, lane);
-      if (!(lane & 4)) sm[Sh::oDC + (cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sc;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float4*>(hist + (k * 2 + i) * 128) =
+            make_float4(qq[2 * i].x, qq[2 * i].y, qq[2 * i + 1].x, qq[2 * i + 1].y);
+      const float y = sum_states(y2, lane);
+      if (even) sY[y_at + k * Sh::CH] = y;
+      const float sc = sum_channels(dc, lane);
+      if (!(lane & 4)) sDC[(cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sc;
     }
     // The next chunk's kept state, on its way during the walk back.
     if (ck > 0) load_states(q.states + (t0 / T8 - 1) * plane, h);
@@ -312,32 +310,33 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 #pragma unroll 2
     for (int k = T8 - 1; k >= 0; --k) {
       read(k);
-      float2 v2[2] = {zero2, zero2}, w2[2] = {zero2, zero2}, db[4];
+      float2 v2, w2;
+      float db[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float4 q4 = *reinterpret_cast<const float4*>(hist + (k * 4 + s) * 128);
-        const float2 qq[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
-        float2 et[2];
+      for (int i = 0; i < 2; ++i) {
+        const float4 q4 = *reinterpret_cast<const float4*>(hist + (k * 2 + i) * 128);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float2 m = __fmul2_rn(d2[p], A2[s][p]);
+        for (int j = 0; j < 2; ++j) {
+          const int s = 2 * i + j;
+          const float2 qq = j ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+          const float2 m = __fmul2_rn(d2, A2[s]);
           const float2 a = make_float2(exp2_f(m.x), exp2_f(m.y));
-          et[p] = fma2(r2[p], C2[s], e[s][p]);
-          const float2 eq = __fmul2_rn(et[p], qq[p]);
-          dA[s][p] = fma2(eq, d2[p], dA[s][p]);
-          w2[p] = fma2(eq, A2[s][p], w2[p]);
-          v2[p] = fma2(et[p], B2[s], v2[p]);
-          e[s][p] = __fmul2_rn(a, et[p]);
+          const float2 et = fma2(r2, C2[s], e[s]);
+          const float2 eq = __fmul2_rn(et, qq);
+          dA[s] = fma2(eq, d2, dA[s]);
+          w2 = s == 0 ? __fmul2_rn(eq, A2[s]) : fma2(eq, A2[s], w2);
+          v2 = s == 0 ? __fmul2_rn(et, B2[s]) : fma2(et, B2[s], v2);
+          db[s] = fmaf(et.y, u2.y, et.x * u2.x);
+          e[s] = __fmul2_rn(a, et);
         }
-        db[s] = fma2(et[1], u2[1], __fmul2_rn(et[0], u2[0]));
       }
-      const float v[4] = {v2[0].x, v2[0].y, v2[1].x, v2[1].y};
-      const float w[4] = {w2[0].x, w2[0].y, w2[1].x, w2[1].y};
-      sm[Sh::oV + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(v, lane);
-      sm[Sh::oW + (nt * T8 + k) * Sh::CH + cw * 32 + lane] = sum_states(w, lane);
-      const float dbs[4] = {db[0].x + db[0].y, db[1].x + db[1].y, db[2].x + db[2].y, db[3].x + db[3].y};
-      const float sb = sum_channels(dbs, lane);
-      if (!(lane & 4)) sm[Sh::oDB + (cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sb;
+      const float v = sum_states(v2, lane), w = sum_states(w2, lane);
+      if (even) {
+        sV[y_at + k * Sh::CH] = v;
+        sW[y_at + k * Sh::CH] = w;
+      }
+      const float sb = sum_channels(db, lane);
+      if (!(lane & 4)) sDB[(cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sb;
     }
     __syncthreads();
 
@@ -348,24 +347,24 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     const bool all = t0 + T8 <= hi;
 #pragma unroll
     for (int i = 0; i < kEl; ++i) {
-      const int k = tf + i * NT;
-      if (!all && t0 + k >= hi) break;
+      const int k = tf + i * NR;
+      if (!busy || (!all && t0 + k >= hi)) break;
       const int at = k * Sh::CH + chf;
-      float y = sm[Sh::oY + at], v = sm[Sh::oV + at], w = sm[Sh::oW + at];
+      float y = sY[at], v = sV[at], w = sW[at];
 #pragma unroll
       for (int m = 1; m < NT; ++m) {
-        y += sm[Sh::oY + m * Sh::kPer + at];
-        v += sm[Sh::oV + m * Sh::kPer + at];
-        w += sm[Sh::oW + m * Sh::kPer + at];
+        y += sY[m * Sh::kPer + at];
+        v += sV[m * Sh::kPer + at];
+        w += sW[m * Sh::kPer + at];
       }
-      const float xv = sm[Sh::oX + at], rv = sm[Sh::oR + at];
+      const float xv = sm[Sh::oX + at], rv = sR[at];
       const float ddt = sm[Sh::oS + at] * fmaf(w, kLn2, xv * v);
       dskip = fmaf(rv, xv, dskip);
       dbias += ddt;
       if (livef) {
-        *pick(dx0 + i * NT * q.dx_t, q.dx_t) = from_f32<T>(fmaf(sm[Sh::oD + at], v, skip * rv));
-        *pick(dt0 + i * NT * q.ddt_t, q.ddt_t) = from_f32<T>(ddt);
-        if (dzp) *pick(dz0 + i * NT * q.dz_t, q.dz_t) = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
+        *pick(dx0 + i * NR * q.dx_t, q.dx_t) = from_f32<T>(fmaf(sD[at], v, skip * rv));
+        *pick(dt0 + i * NR * q.ddt_t, q.ddt_t) = from_f32<T>(ddt);
+        if (dzp) *pick(dz0 + i * NR * q.dz_t, q.dz_t) = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
       }
     }
     for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
@@ -374,8 +373,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       float vb = 0.f, vc = 0.f;
 #pragma unroll
       for (int m = 0; m < CW; ++m) {
-        vb += sm[Sh::oDB + m * T8 * Sh::NP + i];
-        vc += sm[Sh::oDC + m * T8 * Sh::NP + i];
+        vb += sDB[m * T8 * Sh::NP + i];
+        vc += sDC[m * T8 * Sh::NP + i];
       }
       put_bc(t0 + k, n, vb, vc);
     }
@@ -385,26 +384,26 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   // ---- what leaves the split
   float* params = pl.params + (static_cast<size_t>(split) * q.B + b) * q.D * (q.N + 2);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < kCL; ++c) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (!in_state(c, s)) continue;
-      if (split == 0 && q.dh0) q.dh0[state_at(c) + s] = c & 1 ? e[s][c / 2].y : e[s][c / 2].x;
-      params[static_cast<size_t>(d_base + t_base + c0 + c) * (q.N + 2) + n0 + s] =
-          c & 1 ? dA[s][c / 2].y : dA[s][c / 2].x;
+      if (split == 0 && q.dh0) q.dh0[s_at + c * q.N + s] = c ? e[s].y : e[s].x;
+      params[static_cast<size_t>(d_base + t_base + c0 + c) * (q.N + 2) + n0 + s] = c ? dA[s].y : dA[s].x;
     }
   }
-  // The NT threads of a channel, in order (the chunk loop ended with a barrier; the region of
-  // the first per-channel values is free).
-  sm[tid] = dskip;
-  sm[Sh::kThreads + tid] = dbias;
+  // The threads of a channel, in order (the chunk loop ended with a barrier).
+  if (busy) {
+    sD[tid] = dskip;
+    sU[tid] = dbias;
+  }
   __syncthreads();
   if (tid < Sh::CH && livef) {
     float sk = 0.f, bi = 0.f;
 #pragma unroll
-    for (int m = 0; m < NT; ++m) {
-      sk += sm[tid + m * Sh::CH];
-      bi += sm[Sh::kThreads + tid + m * Sh::CH];
+    for (int m = 0; m < (NR < T8 ? NR : T8); ++m) {
+      sk += sD[tid + m * Sh::CH];
+      bi += sU[tid + m * Sh::CH];
     }
     params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N] = sk;
     params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N + 1] = bi;
@@ -465,7 +464,7 @@ BwdLayout bwd_layout(const ScanCall& q) {
 template <typename T, int CW, int NT>
 cudaError_t run_bwd(const ScanCall& q, const BwdLayout& L, cudaStream_t s) {
   using Sh = Shape<CW, NT>;
-  static_assert(2 * Sh::kThreads <= 5 * Sh::kPer, "the last sums fit the per-channel values");
+  static_assert(Sh::kRows <= T8 ? Sh::kThreads <= Sh::kPer : true, "the last sums fit the per-channel values");
   constexpr size_t smem = Sh::kFloats * sizeof(float);
   const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, CW, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
