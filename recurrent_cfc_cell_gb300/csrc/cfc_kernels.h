@@ -297,7 +297,7 @@ cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s);
 struct ScanSplit {
   int splits, steps;               // steps per split, a multiple of 2 kScanPeriod
 };
-ScanSplit scan_split(const ScanCall& q, int warps_wanted);
+ScanSplit scan_split(const ScanCall& q, int warps_wanted, int least_steps);
 size_t scan_carry_floats(const ScanCall& q, const ScanSplit& sp);
 cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool reverse, float* carry,
                               cudaStream_t s);

@@ -8,17 +8,28 @@
 //   ddt_t = dd_t sigmoid(dt_t + dt_bias),  dskip = sum r_t x_t,  ddt_bias = sum ddt_t
 //   dz_t = dy_t (y_t before the gate) silu'(z_t),  dh0 = a_0 e_0
 //
-// The forward pass kept the state before every kScanPeriod-th step, so the pass walks chunks of
-// that many steps from the last: forwards through the chunk from its kept state (the sums with
-// h_t: y, dC), leaving q_t in shared memory, then backwards (everything with e_t).
+// The forward pass kept the state before every kScanPeriod-th (8th) step; the pass walks chunks of
+// that many steps from the last, and a chunk in two halves of four steps, the later one first.  A
+// lane holds one channel's four states (its arithmetic in packed pairs) and goes forwards through
+// the half (the sums with h_t: y, dC), keeping a_t and q_t of its four steps in registers, and then
+// backwards (everything with e_t); the later half's first state is formed again from the chunk's
+// kept one.  Four lanes hold a channel's 16 states and a warp eight channels at a time; it walks
+// over IT such groups for each half, with the half's B and C and the sums dB and dC in registers, so
+// that the sums over channels cross lanes only once per half.  The sums over states (y, e B, e A q)
+// cross four lanes, three shuffles each for four steps of eight channels.  e and dA of a channel
+// wait in shared memory between its halves (so dA is added four steps at a time).
 //
-// A lane holds a pair of channels (its arithmetic is packed) times four states, and a warp 16
-// channels times 16 states: the sums over states (y, e B, e A q) then cross four lanes and the
-// sums over channels (dB, dC) eight, each by exchanging halves.  What a step
-// needs per channel (d, x, r and the gate's and softplus's derivatives) is formed once per
-// chunk, a thread a value, and read back four channels at a time.  NT warps side by side hold up
-// to 16 NT states, CW warps 16 CW channels.  Sums over warps, channel tiles, sequences and
-// splits are added in a fixed order (shared memory, then a merge), without atomics.
+// What a step needs per channel (d, x, r and the gate's and softplus's derivatives) is formed once
+// per chunk, a thread four steps of a channel.  NT warps side by side hold up to 16 NT states, CW
+// warps 8 IT CW channels.  Sums over warps, channel tiles, sequences and splits are added in a
+// fixed order (shared memory, then a merge), without atomics.
+//
+// Bound by instruction issue: a state's step takes 12 multiply-adds and an exponential and a half,
+// beside what is formed per channel.  History: the first form (four channels times four states a
+// lane, q_t of a chunk in shared memory) took 2008 us at 64 x 512 steps x 1024 channels x 16 states,
+// bf16, 920 us with packed arithmetic and loads in flight, and 834 us with half the lane's tile;
+// shared memory's traffic (q_t, and d, x, r, B, C read twice a step) and the sums over channels at
+// every step held it.
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
@@ -29,29 +40,28 @@ namespace {
 constexpr int T8 = kScanPeriod;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-constexpr int kCL = 2;       // channels of a lane, a packed pair
-constexpr int kWC = 8 * kCL;  // channels of a warp
+constexpr int kHalf = T8 / 2;
+constexpr int kStride = 12;  // floats of a channel's eight steps: 16-byte rows without bank conflicts
 
-template <int CW, int NT>
+template <int CW, int NT, int IT>
 struct Shape {
-  static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = kWC * CW, NP = 16 * NT;
-  static constexpr int kPer = T8 * CH;  // one value per (step, channel)
-  static constexpr int kRows = kThreads / CH;  // threads of a channel in the per-channel phases
-  static constexpr int kHist = T8 * 4 * kCL * 32;  // q_t of a warp
-  // Dynamic shared memory, in floats: q_t as [warp][step][2][lane][4], then what only the
-  // per-channel phases use: x, dy silu'(z), sigmoid(dt + bias), and at NT = 8 the sums W.
-  static constexpr int oQ = 0, oX = kWarps * kHist, oZ = oX + kPer, oS = oZ + kPer;
-  static constexpr int oW = oS + kPer;
-  static constexpr bool kSpill = NT == 8;  // W does not fit the 48 KB of static shared memory
-  static constexpr int kFloats = oW + (kSpill ? NT * kPer : 0);
+  static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = 8 * IT * CW, NP = 16 * NT;
+  static constexpr int kSt = NT * CH * 16;       // one value per (channel, state)
+  static constexpr int kRow = CH * kStride;      // one value per (channel, step), padded
+  // Dynamic shared memory, in floats.
+  static constexpr int oE = 0, oDA = oE + kSt, oZ = oDA + kSt, oS = oZ + CH * T8;
+  static constexpr int oY = oS + CH * T8, oV = oY + NT * kRow, oW = oV + NT * kRow;
+  static constexpr int oDB = oW + NT * kRow, oDC = oDB + CW * T8 * NP;
+  static constexpr int kFloats = oDC + CW * T8 * NP;
 };
 
-// Sum of a pair over the four state lanes (lane bits 0, 1): the lane keeps the first value where
-// bit 1 is clear and the second where it is set.
-__device__ __forceinline__ float sum_states(float2 v, int lane) {
+// Sum of v[0..3] over the four state lanes (lane bits 0, 1): lane nl keeps v[nl].
+__device__ __forceinline__ float sum_states(const float (&v)[4], int lane) {
   const bool hi = lane & 2;
-  const float a = (hi ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, hi ? v.x : v.y, 2);
-  return a + __shfl_xor_sync(0xffffffffu, a, 1);
+  const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 2);
+  const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 2);
+  const bool lo = lane & 1;
+  return (lo ? b : a) + __shfl_xor_sync(0xffffffffu, lo ? a : b, 1);
 }
 
 // Sum of v[0..3] over the eight channel lanes (lane bits 2..4): the lane keeps v[lane >> 3].
@@ -73,88 +83,56 @@ struct BwdPlan {
   float *pB, *pC;       // [tiles_per_group][K][B][G][N], or null: straight to dB / dC
 };
 
-template <typename T, int CW, int NT>
+template <typename T, int CW, int NT, int IT>
 __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q, const BwdPlan pl) {
-  using Sh = Shape<CW, NT>;
-  // Arrays of their own for what the walks read and what they write, so that a step's loads can
-  // be issued before the last step's stores.
+  using Sh = Shape<CW, NT, IT>;
   extern __shared__ __align__(16) float sm[];
-  __shared__ __align__(16) float sD[Sh::kPer], sU[Sh::kPer], sR[Sh::kPer];  // d, d x, r
-  __shared__ __align__(16) float sB[2 * T8 * Sh::NP], sC[2 * T8 * Sh::NP];  // every value twice
-  __shared__ float sY[NT * Sh::kPer], sV[NT * Sh::kPer], sWs[Sh::kSpill ? 1 : NT * Sh::kPer];
-  __shared__ float sDB[CW * T8 * Sh::NP], sDC[CW * T8 * Sh::NP];
-  float* const sW = Sh::kSpill ? sm + Sh::oW : sWs;
+  __shared__ __align__(16) float sD[Sh::kRow], sX[Sh::kRow], sR[Sh::kRow];  // [channel][step]
+  __shared__ __align__(16) float sA[Sh::kSt];                               // [nt][channel][16]
+  __shared__ __align__(16) float sB[T8 * Sh::NP], sC[T8 * Sh::NP];
   grid_dep_launch_dependents();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int nt = warp % NT, cw = warp / NT;
+  const int nt = warp % NT, cw = warp / NT, nl = lane & 3, dl = lane >> 2;
   const int group = blockIdx.x / pl.tiles_per_group, tile = blockIdx.x % pl.tiles_per_group;
   const int b = blockIdx.y, split = blockIdx.z;
   const int len = q.lengths ? min(max(q.lengths[b], 0), q.K) : q.K;
   const int lo = split * pl.steps, hi = min(q.K, lo + pl.steps), end = min(hi, len);
   const size_t plane = static_cast<size_t>(q.B) * q.D * q.N;
-  const int d_base = group * pl.per_group;   // the group's first channel
-  const int t_base = tile * Sh::CH;          // the tile's first channel in its group
+  const int d0 = group * pl.per_group + tile * Sh::CH;        // the tile's first channel
+  const int count = min(Sh::CH, pl.per_group - tile * Sh::CH);  // its channels
 
-  // This thread's channel in the per-channel phases, and its steps tf, tf + kRows, ...  Addresses
-  // are a uniform base (sequence, tile, step) plus the thread's own offset.
-  constexpr int NR = Sh::kRows;
-  const bool busy = NR <= T8 || tid / Sh::CH < T8;  // threads beyond the chunk's steps rest
-  const int chf = tid % Sh::CH, tf = busy ? tid / Sh::CH : 0;
-  const bool livef = busy && t_base + chf < pl.per_group;
-  const unsigned own = livef ? chf : 0;
-  const int d0 = d_base + t_base;
-  const float bias = q.dt_bias ? q.dt_bias[d0 + own] : 0.f, skip = q.skip ? q.skip[d0 + own] : 0.f;
-  const T* xp = static_cast<const T*>(q.x) + b * q.x_b + d0;
-  const T* tp = static_cast<const T*>(q.dt) + b * q.dt_b + d0;
-  const T* zp = q.z ? static_cast<const T*>(q.z) + b * q.z_b + d0 : nullptr;
-  const T* gp = static_cast<const T*>(q.dy) + b * q.dy_b + d0;
-  T* dxp = static_cast<T*>(q.dx) + b * q.dx_b + d0;
-  T* dtp = static_cast<T*>(q.ddt) + b * q.ddt_b + d0;
-  T* dzp = q.dz ? static_cast<T*>(q.dz) + b * q.dz_b + d0 : nullptr;
-  // The thread's element of the steps from `base` on.
-  auto pick = [&](auto* base, long long stride) { return base + (own + tf * stride); };
   const T* Bp = static_cast<const T*>(q.Bm) + b * q.Bm_b + static_cast<long long>(group) * q.N;
   const T* Cp = static_cast<const T*>(q.Cm) + b * q.Cm_b + static_cast<long long>(group) * q.N;
+  const size_t tile_at = (static_cast<size_t>(b) * q.D + d0) * q.N;  // of the tile in a plane
 
-  // This lane's states: channels c0 and c0 + 1 of the tile (a pair), states n0 .. n0 + 3.
-  const int c0 = cw * kWC + (lane >> 2) * kCL, n0 = nt * 16 + (lane & 3) * 4;
-  float2 A2[4], e[4], dA[4], h[4];
-  auto in_state = [&](int c, int s) { return t_base + c0 + c < pl.per_group && n0 + s < q.N; };
-  auto state_at = [&](int c) {  // offset of state n0 of channel c in a [B][D][N] plane
-    return (static_cast<size_t>(b) * q.D + d_base + t_base + c0 + c) * q.N + n0;
-  };
-  // The lane's states of a plane, zero outside.
+  // A, e and dA of the tile's channels, zero outside; shared memory [nt][channel][16].
+  const float* c_in = pl.carry ? pl.carry + split * plane : q.dh_last;
+  for (int i = tid; i < Sh::kSt; i += Sh::kThreads) {
+    const int ch = i / 16 % Sh::CH, n = i / (16 * Sh::CH) * 16 + i % 16;
+    const bool in = ch < count && n < q.N;
+    sA[i] = in ? q.A[static_cast<size_t>(d0 + ch) * q.N + n] * kLog2e : 0.f;
+    sm[Sh::oE + i] = in && c_in ? c_in[tile_at + static_cast<size_t>(ch) * q.N + n] : 0.f;
+    sm[Sh::oDA + i] = 0.f;
+  }
+
+  // The lane's four states of channel ch in the kept plane of the chunk, zero outside.
+  const int n0 = nt * 16 + nl * 4;
   const bool quad = q.N % 4 == 0;
-  const size_t s_at = state_at(0);
-  auto load_states = [&](const float* p, float2 (&v)[4]) {
-    float r[2][4] = {};
-    if (p != nullptr) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (!in_state(c, 0)) continue;
-        const float* at = p + s_at + c * q.N;
-        if (quad) {
-          const float4 f = *reinterpret_cast<const float4*>(at);
-          r[c][0] = f.x; r[c][1] = f.y; r[c][2] = f.z; r[c][3] = f.w;
-        } else {
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            if (n0 + s < q.N) r[c][s] = at[s];
-        }
+  auto kept = [&](const float* p, int ch) {
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ch < count && n0 < q.N) {
+      const float* at = p + tile_at + static_cast<size_t>(ch) * q.N + n0;
+      if (quad) {
+        r = *reinterpret_cast<const float4*>(at);
+      } else {
+        r.x = at[0];
+        if (n0 + 1 < q.N) r.y = at[1];
+        if (n0 + 2 < q.N) r.z = at[2];
+        if (n0 + 3 < q.N) r.w = at[3];
       }
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = make_float2(r[0][s], r[1][s]);
+    return r;
   };
-  load_states(pl.carry ? pl.carry + split * plane : q.dh_last, e);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const float* at = q.A + static_cast<size_t>(d_base + t_base + c0) * q.N + n0 + s;
-    A2[s] = make_float2(in_state(0, s) ? at[0] * kLog2e : 0.f, in_state(1, s) ? at[q.N] * kLog2e : 0.f);
-    dA[s] = make_float2(0.f, 0.f);
-  }
-  float dskip = 0.f, dbias = 0.f;
-  float* const hist = sm + Sh::oQ + warp * Sh::kHist + lane * 4;
 
   // dB / dC of this tile: partial sums, or the outputs themselves.
   auto put_bc = [&](int t, int n, float vb, float vc) {
@@ -169,202 +147,320 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     }
   };
 
+  // The per-channel phases: a thread takes PS consecutive steps of one channel, from step k0 of the
+  // chunk on.
+  constexpr int PS = T8 * Sh::CH / Sh::kThreads > 0 ? T8 * Sh::CH / Sh::kThreads : 1;
+  static_assert(T8 % PS == 0 && (T8 / PS) * Sh::CH <= Sh::kThreads, "every piece has a thread");
+  const int ch = Sh::kThreads == Sh::CH ? tid : tid % Sh::CH;
+  const int k0 = Sh::kThreads == Sh::CH ? 0 : tid / Sh::CH * PS;
+  const bool live = ch < count && k0 < T8;
+  const float bias = q.dt_bias && live ? q.dt_bias[d0 + ch] : 0.f;
+  const float skip = q.skip && live ? q.skip[d0 + ch] : 0.f;
+  float dskip = 0.f, dbias = 0.f;
+  const T* xr = static_cast<const T*>(q.x) + b * q.x_b + d0;
+  const T* tr = static_cast<const T*>(q.dt) + b * q.dt_b + d0;
+  const T* zr = q.z ? static_cast<const T*>(q.z) + b * q.z_b + d0 : nullptr;
+  const T* gr = static_cast<const T*>(q.dy) + b * q.dy_b + d0;
+  T* dxr = static_cast<T*>(q.dx) + b * q.dx_b + d0;
+  T* dtr = static_cast<T*>(q.ddt) + b * q.ddt_b + d0;
+  T* dzr = q.dz ? static_cast<T*>(q.dz) + b * q.dz_b + d0 : nullptr;
+
   const int chunks = end > lo ? (end - lo + T8 - 1) / T8 : 0;
   // Steps after the sequence's end: zeros.
-  for (int t = lo + chunks * T8 + tf; livef && t < hi; t += NR < T8 ? NR : T8) {
-    dxp[t * q.dx_t + own] = from_f32<T>(0.f);
-    dtp[t * q.ddt_t + own] = from_f32<T>(0.f);
-    if (dzp) dzp[t * q.dz_t + own] = from_f32<T>(0.f);
-  }
-  for (int t = lo + chunks * T8; t < hi; ++t)
-    for (int n = tid; n < q.N; n += Sh::kThreads) put_bc(t, n, 0.f, 0.f);
-
-  // The next chunk's inputs, as they are stored.
-  constexpr int kEl = NR < T8 ? T8 / NR : 1, kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
-  static_assert(T8 % NR == 0 || NR % T8 == 0, "every thread has the same number of steps");
-  T rx[kEl], rt[kEl], rz[kEl], rg[kEl], rB[kBC], rC[kBC];
-  const T none = from_f32<T>(0.f);
-  auto fetch_as = [&](int t0, auto all) {
-    constexpr bool kAll = decltype(all)::value;  // every step of the chunk counts
-    const T* x0 = xp + t0 * q.x_t;
-    const T* dt0 = tp + t0 * q.dt_t;
-    const T* g0 = gp + t0 * q.dy_t;
-    const T* z0 = zp ? zp + t0 * q.z_t : nullptr;
-#pragma unroll
-    for (int i = 0; i < kEl; ++i) {
-      const bool in = kAll || t0 + tf + i * NR < end;
-      rx[i] = in ? *pick(x0 + i * NR * q.x_t, q.x_t) : none;
-      rt[i] = in ? *pick(dt0 + i * NR * q.dt_t, q.dt_t) : none;
-      rg[i] = in ? *pick(g0 + i * NR * q.dy_t, q.dy_t) : none;
+  for (int t = lo + chunks * T8; t < hi; ++t) {
+    for (int c = tid; c < count; c += Sh::kThreads) {
+      dxr[t * q.dx_t + c] = from_f32<T>(0.f);
+      dtr[t * q.ddt_t + c] = from_f32<T>(0.f);
+      if (dzr) dzr[t * q.dz_t + c] = from_f32<T>(0.f);
     }
-    if (zp) {
+    for (int n = tid; n < q.N; n += Sh::kThreads) put_bc(t, n, 0.f, 0.f);
+  }
+
+  // A chunk's inputs as they are stored: read while the chunk after it (the one before in this
+  // walk) is finished, from the second-level cache, where they were sent for when its sums began.
+  // Addresses are a uniform base (sequence, tile, step) plus the thread's own offset.
+  constexpr int kBC = (T8 * Sh::NP + Sh::kThreads - 1) / Sh::kThreads;
+  const T none = from_f32<T>(0.f);
+  const unsigned own = live ? ch : 0;
+  const int k0s = live ? k0 : 0;
+  auto pick = [&](auto* base, long long stride) {
+    if constexpr (Sh::kThreads == Sh::CH) return base + own;
+    return base + (own + k0s * stride);
+  };
+  T rx[PS], rt[PS], rz[PS], rg[PS], rB[kBC], rC[kBC];
+  auto fetch_as = [&](int t0, auto all) {
+    constexpr bool kAll = decltype(all)::value;  // every step of the chunk and channel counts
+    const T *x0 = xr + t0 * q.x_t, *dt0 = tr + t0 * q.dt_t, *g0 = gr + t0 * q.dy_t;
+    const T* z0 = zr ? zr + t0 * q.z_t : nullptr;
 #pragma unroll
-      for (int i = 0; i < kEl; ++i)
-        rz[i] = kAll || t0 + tf + i * NR < end ? *pick(z0 + i * NR * q.z_t, q.z_t) : none;
+    for (int j = 0; j < PS; ++j) {
+      const bool in = kAll || (live && t0 + k0 + j < end);
+      rx[j] = in ? *pick(x0 + j * q.x_t, q.x_t) : none;
+      rt[j] = in ? *pick(dt0 + j * q.dt_t, q.dt_t) : none;
+      rg[j] = in ? *pick(g0 + j * q.dy_t, q.dy_t) : none;
+    }
+    if (zr) {
+#pragma unroll
+      for (int j = 0; j < PS; ++j)
+        rz[j] = kAll || (live && t0 + k0 + j < end) ? *pick(z0 + j * q.z_t, q.z_t) : none;
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
       const int at = tid + i * Sh::kThreads, k = at / Sh::NP, n = at % Sh::NP;
       const bool in = k < T8 && (kAll || t0 + k < end) && n < q.N;
-      rB[i] = in ? Bp[(t0 + k) * q.Bm_t + n] : none;
-      rC[i] = in ? Cp[(t0 + k) * q.Cm_t + n] : none;
+      rB[i] = in ? (Bp + (t0 + k) * q.Bm_t)[n] : none;
+      rC[i] = in ? (Cp + (t0 + k) * q.Cm_t)[n] : none;
     }
   };
+  constexpr bool kFull = (T8 / PS) * Sh::CH == Sh::kThreads;  // no thread rests
+  auto whole = [&](int t0) { return kFull && count == Sh::CH && t0 + T8 <= end; };
   auto fetch = [&](int t0) {
-    if (t0 + T8 <= end) fetch_as(t0, std::true_type{});
+    if (whole(t0)) fetch_as(t0, std::true_type{});
     else fetch_as(t0, std::false_type{});
   };
-  if (chunks > 0) {
-    fetch(lo + (chunks - 1) * T8);
-    load_states(q.states + ((lo + (chunks - 1) * T8) / T8) * plane, h);
-  }
+  auto send_for = [&](int t0) {
+    constexpr int kLine = 128 / sizeof(T), kLines = (Sh::CH + kLine - 1) / kLine;  // of a row
+    for (int i = tid; i < 4 * T8 * kLines; i += Sh::kThreads) {
+      const int which = i / T8 % 4, at = i / (4 * T8) * kLine;
+      const long long t = t0 + i % T8;
+      const T* row = which == 0 ? xr + t * q.x_t : which == 1 ? tr + t * q.dt_t
+                   : which == 2 ? gr + t * q.dy_t : zr ? zr + t * q.z_t : nullptr;
+      if (row != nullptr && at < count) prefetch_l2(row + at);
+    }
+    const float* p = q.states + (t0 / T8) * plane + tile_at;
+    for (int i = tid * 32; i < count * q.N; i += Sh::kThreads * 32) prefetch_l2(p + i);
+  };
+  auto put = [&](float* p, const float (&f)[PS]) {
+    if constexpr (PS >= 4) {
+#pragma unroll
+      for (int j = 0; j < PS; j += 4)
+        *reinterpret_cast<float4*>(p + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PS; ++j) p[j] = f[j];
+    }
+  };
+  auto get = [&](const float* p, float (&f)[PS]) {
+    if constexpr (PS >= 4) {
+#pragma unroll
+      for (int j = 0; j < PS; j += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(p + j);
+        f[j] = r.x; f[j + 1] = r.y; f[j + 2] = r.z; f[j + 3] = r.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PS; ++j) f[j] = p[j];
+    }
+  };
+  const int at_row = ch * kStride + k0, at_8 = ch * T8 + k0;
+  const bool resting = !kFull && k0 >= T8;
+  if (chunks > 0) fetch(lo + (chunks - 1) * T8);
 
   for (int ck = chunks - 1; ck >= 0; --ck) {
     const int t0 = lo + ck * T8;
-    // ---- per channel and step: d, d x, r, and for the end x, dy silu'(z), sigmoid(dt + bias)
+    const float* const plane_in = q.states + (t0 / T8) * plane;
+    const int c_first = cw * IT * 8 + dl;
+    float4 next = kept(plane_in, c_first);
+    // ---- per channel: d, x, r, and for the end dy silu'(z) and sigmoid(dt + bias)
+    if (!resting) {
+      float dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
 #pragma unroll
-    for (int j = 0; j < (kEl + 1) / 2; ++j) {
-      const int i1 = 2 * j + 1 < kEl ? 2 * j + 1 : 2 * j;
-      const float2 raw = make_float2(to_f32(rt[2 * j]) + bias, to_f32(rt[i1]) + bias);
-      const float2 d2 = q.softplus ? softplus2_f(raw) : raw;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int i = 2 * j + m, k = tf + i * NR;
-        if (i < kEl && busy) {
-          // Steps past the end and channels past the group's leave the state, its gradient and the
-          // sums over channels alone: d = 0, x = 0, r = 0.
-          const bool in = livef && t0 + k < end;
-          const float dv = in ? (m ? d2.y : d2.x) : 0.f, xv = in ? to_f32(rx[i]) : 0.f;
-          float rv = in ? to_f32(rg[i]) : 0.f, zf = 0.f;
-          if (zp) {
-            const float z = in ? to_f32(rz[i]) : 0.f, s = sigmoid_f(z), gs = rv * s;
-            rv = gs * z;
-            zf = gs * fmaf(z, 1.f - s, 1.f);
-          }
-          const int at = k * Sh::CH + chf;
-          sD[at] = dv;
-          sU[at] = dv * xv;
-          sR[at] = rv;
-          sm[Sh::oX + at] = xv;
-          sm[Sh::oZ + at] = zf;
-          sm[Sh::oS + at] = !in ? 0.f : q.softplus ? sigmoid_f(m ? raw.y : raw.x) : 1.f;
+      for (int j = 0; j < PS; j += 2) {
+        const float2 raw = make_float2(to_f32(rt[j]) + bias, to_f32(rt[j + 1 < PS ? j + 1 : j]) + bias);
+        const float2 d2 = q.softplus ? softplus2_f(raw) : raw;
+        dv[j] = d2.x;
+        sg[j] = q.softplus ? sigmoid_f(raw.x) : 1.f;
+        if (j + 1 < PS) {
+          dv[j + 1] = d2.y;
+          sg[j + 1] = q.softplus ? sigmoid_f(raw.y) : 1.f;
         }
       }
+#pragma unroll
+      for (int j = 0; j < PS; ++j) {
+        xv[j] = to_f32(rx[j]);
+        rv[j] = to_f32(rg[j]);
+        zf[j] = 0.f;
+        if (zr) {
+          const float z = to_f32(rz[j]), s = sigmoid_f(z), gs = rv[j] * s;
+          rv[j] = gs * z;
+          zf[j] = gs * fmaf(z, 1.f - s, 1.f);
+        }
+      }
+      if (!whole(t0)) {
+        // Steps past the end and channels past the group's leave the state, its gradient and the
+        // sums alone: d = 0 (x and r were read as 0).
+#pragma unroll
+        for (int j = 0; j < PS; ++j)
+          if (!live || t0 + k0 + j >= end) dv[j] = sg[j] = 0.f;
+      }
+      put(&sD[at_row], dv);
+      put(&sX[at_row], xv);
+      put(&sR[at_row], rv);
+      put(&sm[Sh::oZ + at_8], zf);
+      put(&sm[Sh::oS + at_8], sg);
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
       const int at = tid + i * Sh::kThreads;
       if (at < T8 * Sh::NP) {
-        const float bv = to_f32(rB[i]), cv = to_f32(rC[i]);
-        reinterpret_cast<float2*>(sB)[at] = make_float2(bv, bv);
-        reinterpret_cast<float2*>(sC)[at] = make_float2(cv, cv);
+        sB[at] = to_f32(rB[i]);
+        sC[at] = to_f32(rC[i]);
+      }
+    }
+    if (ck > 0) send_for(t0 - T8);
+    __syncthreads();
+
+    // ---- the two halves
+#pragma unroll
+    for (int half = 1; half >= 0; --half) {
+      float2 Bv[kHalf][2], Cv[kHalf][2], B0[kHalf][2];
+      float2 db[kHalf][2], dc[kHalf][2];
+#pragma unroll
+      for (int j = 0; j < kHalf; ++j) {
+        const int at = (half * kHalf + j) * Sh::NP + n0;
+        const float4 bv = *reinterpret_cast<const float4*>(&sB[at]);
+        const float4 cv = *reinterpret_cast<const float4*>(&sC[at]);
+        Bv[j][0] = make_float2(bv.x, bv.y); Bv[j][1] = make_float2(bv.z, bv.w);
+        Cv[j][0] = make_float2(cv.x, cv.y); Cv[j][1] = make_float2(cv.z, cv.w);
+        if (half) {
+          const float4 b0 = *reinterpret_cast<const float4*>(&sB[j * Sh::NP + n0]);
+          B0[j][0] = make_float2(b0.x, b0.y); B0[j][1] = make_float2(b0.z, b0.w);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) db[j][p] = dc[j][p] = make_float2(0.f, 0.f);
+      }
+#pragma unroll 1
+      for (int it = 0; it < IT; ++it) {
+        const int cl = c_first + it * 8;  // the lane's channel
+        const int row = cl * kStride, st = (nt * Sh::CH + cl) * 16 + nl * 4;
+        float2 h[2] = {make_float2(next.x, next.y), make_float2(next.z, next.w)};
+        // The next group's kept state (after the later half's last, the earlier half's first).
+        if (it + 1 < IT || half) next = kept(plane_in, it + 1 < IT ? cl + 8 : c_first);
+        const float4 a4 = *reinterpret_cast<const float4*>(&sA[st]);
+        const float2 A2[2] = {make_float2(a4.x, a4.y), make_float2(a4.z, a4.w)};
+        if (half) {
+          const float4 d4 = *reinterpret_cast<const float4*>(&sD[row]);
+          const float4 x4 = *reinterpret_cast<const float4*>(&sX[row]);
+          const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) {
+            const float u = dv[j] * xv[j];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const float2 m = __fmul2_rn(make_float2(dv[j], dv[j]), A2[p]);
+              h[p] = fma2(make_float2(exp2_f(m.x), exp2_f(m.y)), h[p],
+                          __fmul2_rn(make_float2(u, u), B0[j][p]));
+            }
+          }
+        }
+        const float4 d4 = *reinterpret_cast<const float4*>(&sD[row + half * kHalf]);
+        const float4 x4 = *reinterpret_cast<const float4*>(&sX[row + half * kHalf]);
+        const float4 r4 = *reinterpret_cast<const float4*>(&sR[row + half * kHalf]);
+        const float4 e4 = *reinterpret_cast<const float4*>(&sm[Sh::oE + st]);
+        const float4 da4 = *reinterpret_cast<const float4*>(&sm[Sh::oDA + st]);
+        const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, rv[4] = {r4.x, r4.y, r4.z, r4.w};
+        const float uv[4] = {d4.x * x4.x, d4.y * x4.y, d4.z * x4.z, d4.w * x4.w};
+        // Forwards.
+        float2 a[kHalf][2], qq[kHalf][2];
+        float y[4], v[4], w[4];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          const float2 d2 = make_float2(dv[j], dv[j]), u2 = make_float2(uv[j], uv[j]);
+          const float2 r2 = make_float2(rv[j], rv[j]);
+          float2 y2;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 m = __fmul2_rn(d2, A2[p]);
+            a[j][p] = make_float2(exp2_f(m.x), exp2_f(m.y));
+            qq[j][p] = __fmul2_rn(a[j][p], h[p]);
+            h[p] = fma2(u2, Bv[j][p], qq[j][p]);
+            y2 = p ? fma2(h[p], Cv[j][p], y2) : __fmul2_rn(h[p], Cv[j][p]);
+            dc[j][p] = fma2(r2, h[p], dc[j][p]);
+          }
+          y[j] = y2.x + y2.y;
+        }
+        // And back.
+        float2 e[2] = {make_float2(e4.x, e4.y), make_float2(e4.z, e4.w)};
+        float2 dA[2];
+#pragma unroll
+        for (int j = kHalf - 1; j >= 0; --j) {
+          const float2 d2 = make_float2(dv[j], dv[j]), u2 = make_float2(uv[j], uv[j]);
+          const float2 r2 = make_float2(rv[j], rv[j]);
+          float2 v2, w2;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 et = fma2(r2, Cv[j][p], e[p]);
+            const float2 eq = __fmul2_rn(et, qq[j][p]);
+            dA[p] = j == kHalf - 1 ? __fmul2_rn(eq, d2) : fma2(eq, d2, dA[p]);
+            w2 = p ? fma2(eq, A2[p], w2) : __fmul2_rn(eq, A2[p]);
+            v2 = p ? fma2(et, Bv[j][p], v2) : __fmul2_rn(et, Bv[j][p]);
+            db[j][p] = fma2(et, u2, db[j][p]);
+            e[p] = __fmul2_rn(a[j][p], et);
+          }
+          v[j] = v2.x + v2.y;
+          w[j] = w2.x + w2.y;
+        }
+        *reinterpret_cast<float4*>(&sm[Sh::oE + st]) = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+        *reinterpret_cast<float4*>(&sm[Sh::oDA + st]) =
+            make_float4(da4.x + dA[0].x, da4.y + dA[0].y, da4.z + dA[1].x, da4.w + dA[1].y);
+        const int out = nt * Sh::kRow + row + half * kHalf + nl;
+        sm[Sh::oY + out] = sum_states(y, lane);
+        sm[Sh::oV + out] = sum_states(v, lane);
+        sm[Sh::oW + out] = sum_states(w, lane);
+      }
+      // The half's dB and dC over the warp's channels.
+#pragma unroll
+      for (int j = 0; j < kHalf; ++j) {
+        const float vb[4] = {db[j][0].x, db[j][0].y, db[j][1].x, db[j][1].y};
+        const float vc[4] = {dc[j][0].x, dc[j][0].y, dc[j][1].x, dc[j][1].y};
+        const float sb = sum_channels(vb, lane), sc = sum_channels(vc, lane);
+        if (!(lane & 4)) {
+          const int at = (cw * T8 + half * kHalf + j) * Sh::NP + n0 + (lane >> 3);
+          sm[Sh::oDB + at] = sb;
+          sm[Sh::oDC + at] = sc;
+        }
       }
     }
     __syncthreads();
     if (ck > 0) fetch(t0 - T8);
 
-    // What both directions read of a step: d, d x and r of the lane's four channels in pairs, B
-    // and C of its four states, each twice.
-    float2 d2, u2, r2, B2[4], C2[4];
-    auto read = [&](int k) {
-      d2 = *reinterpret_cast<const float2*>(&sD[k * Sh::CH + c0]);
-      u2 = *reinterpret_cast<const float2*>(&sU[k * Sh::CH + c0]);
-      r2 = *reinterpret_cast<const float2*>(&sR[k * Sh::CH + c0]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 bv = *reinterpret_cast<const float4*>(&sB[2 * (k * Sh::NP + n0) + 4 * i]);
-        const float4 cv = *reinterpret_cast<const float4*>(&sC[2 * (k * Sh::NP + n0) + 4 * i]);
-        B2[2 * i] = make_float2(bv.x, bv.y); B2[2 * i + 1] = make_float2(bv.z, bv.w);
-        C2[2 * i] = make_float2(cv.x, cv.y); C2[2 * i + 1] = make_float2(cv.z, cv.w);
-      }
-    };
-    const bool even = !(lane & 1);
-    const int y_at = nt * Sh::kPer + cw * kWC + (lane >> 1);  // of a sum over states
-
-    // ---- forwards through the chunk
-#pragma unroll 2
-    for (int k = 0; k < T8; ++k) {
-      read(k);
-      float2 y2, qq[4];
-      float dc[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float2 m = __fmul2_rn(d2, A2[s]);
-        qq[s] = __fmul2_rn(make_float2(exp2_f(m.x), exp2_f(m.y)), h[s]);
-        h[s] = fma2(u2, B2[s], qq[s]);
-        y2 = s == 0 ? __fmul2_rn(h[s], C2[s]) : fma2(h[s], C2[s], y2);
-        dc[s] = fmaf(r2.y, h[s].y, r2.x * h[s].x);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<float4*>(hist + (k * 2 + i) * 128) =
-            make_float4(qq[2 * i].x, qq[2 * i].y, qq[2 * i + 1].x, qq[2 * i + 1].y);
-      const float y = sum_states(y2, lane);
-      if (even) sY[y_at + k * Sh::CH] = y;
-      const float sc = sum_channels(dc, lane);
-      if (!(lane & 4)) sDC[(cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sc;
-    }
-    // The next chunk's kept state, on its way during the walk back.
-    if (ck > 0) load_states(q.states + (t0 / T8 - 1) * plane, h);
-    // ---- and back
-#pragma unroll 2
-    for (int k = T8 - 1; k >= 0; --k) {
-      read(k);
-      float2 v2, w2;
-      float db[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 q4 = *reinterpret_cast<const float4*>(hist + (k * 2 + i) * 128);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int s = 2 * i + j;
-          const float2 qq = j ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
-          const float2 m = __fmul2_rn(d2, A2[s]);
-          const float2 a = make_float2(exp2_f(m.x), exp2_f(m.y));
-          const float2 et = fma2(r2, C2[s], e[s]);
-          const float2 eq = __fmul2_rn(et, qq);
-          dA[s] = fma2(eq, d2, dA[s]);
-          w2 = s == 0 ? __fmul2_rn(eq, A2[s]) : fma2(eq, A2[s], w2);
-          v2 = s == 0 ? __fmul2_rn(et, B2[s]) : fma2(et, B2[s], v2);
-          db[s] = fmaf(et.y, u2.y, et.x * u2.x);
-          e[s] = __fmul2_rn(a, et);
-        }
-      }
-      const float v = sum_states(v2, lane), w = sum_states(w2, lane);
-      if (even) {
-        sV[y_at + k * Sh::CH] = v;
-        sW[y_at + k * Sh::CH] = w;
-      }
-      const float sb = sum_channels(db, lane);
-      if (!(lane & 4)) sDB[(cw * T8 + k) * Sh::NP + n0 + (lane >> 3)] = sb;
-    }
-    __syncthreads();
-
-    // ---- per channel and step: the gradients of the inputs
-    T* const dx0 = dxp + t0 * q.dx_t;
-    T* const dt0 = dtp + t0 * q.ddt_t;
-    T* const dz0 = dzp ? dzp + t0 * q.dz_t : nullptr;
-    const bool all = t0 + T8 <= hi;
-#pragma unroll
-    for (int i = 0; i < kEl; ++i) {
-      const int k = tf + i * NR;
-      if (!busy || (!all && t0 + k >= hi)) break;
-      const int at = k * Sh::CH + chf;
-      float y = sY[at], v = sV[at], w = sW[at];
+    // ---- per channel and step: the gradients of the inputs.  (A thread reads back what it formed
+    // itself, and the sums; the next chunk's values may follow without a barrier.)
+    if (!resting) {
+      float y[PS], v[PS], w[PS], dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
+      get(&sm[Sh::oY + at_row], y);
+      get(&sm[Sh::oV + at_row], v);
+      get(&sm[Sh::oW + at_row], w);
 #pragma unroll
       for (int m = 1; m < NT; ++m) {
-        y += sY[m * Sh::kPer + at];
-        v += sV[m * Sh::kPer + at];
-        w += sW[m * Sh::kPer + at];
+        float o[PS];
+        get(&sm[Sh::oY + m * Sh::kRow + at_row], o);
+#pragma unroll
+        for (int j = 0; j < PS; ++j) y[j] += o[j];
+        get(&sm[Sh::oV + m * Sh::kRow + at_row], o);
+#pragma unroll
+        for (int j = 0; j < PS; ++j) v[j] += o[j];
+        get(&sm[Sh::oW + m * Sh::kRow + at_row], o);
+#pragma unroll
+        for (int j = 0; j < PS; ++j) w[j] += o[j];
       }
-      const float xv = sm[Sh::oX + at], rv = sR[at];
-      const float ddt = sm[Sh::oS + at] * fmaf(w, kLn2, xv * v);
-      dskip = fmaf(rv, xv, dskip);
-      dbias += ddt;
-      if (livef) {
-        *pick(dx0 + i * NR * q.dx_t, q.dx_t) = from_f32<T>(fmaf(sD[at], v, skip * rv));
-        *pick(dt0 + i * NR * q.ddt_t, q.ddt_t) = from_f32<T>(ddt);
-        if (dzp) *pick(dz0 + i * NR * q.dz_t, q.dz_t) = from_f32<T>(sm[Sh::oZ + at] * fmaf(skip, xv, y));
+      get(&sD[at_row], dv);
+      get(&sX[at_row], xv);
+      get(&sR[at_row], rv);
+      get(&sm[Sh::oZ + at_8], zf);
+      get(&sm[Sh::oS + at_8], sg);
+      T *dx0 = dxr + t0 * q.dx_t, *dt0 = dtr + t0 * q.ddt_t, *dz0 = dzr ? dzr + t0 * q.dz_t : nullptr;
+      const bool all = kFull && count == Sh::CH && t0 + T8 <= hi;
+#pragma unroll
+      for (int j = 0; j < PS; ++j) {
+        const float ddt = sg[j] * fmaf(w[j], kLn2, xv[j] * v[j]);
+        dskip = fmaf(rv[j], xv[j], dskip);
+        dbias += ddt;
+        if (all || (live && t0 + k0 + j < hi)) {
+          *pick(dx0 + j * q.dx_t, q.dx_t) = from_f32<T>(fmaf(dv[j], v[j], skip * rv[j]));
+          *pick(dt0 + j * q.ddt_t, q.ddt_t) = from_f32<T>(ddt);
+          if (dzr) *pick(dz0 + j * q.dz_t, q.dz_t) = from_f32<T>(zf[j] * fmaf(skip, xv[j], y[j]));
+        }
       }
     }
     for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
@@ -373,37 +469,34 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       float vb = 0.f, vc = 0.f;
 #pragma unroll
       for (int m = 0; m < CW; ++m) {
-        vb += sDB[m * T8 * Sh::NP + i];
-        vc += sDC[m * T8 * Sh::NP + i];
+        vb += sm[Sh::oDB + m * T8 * Sh::NP + i];
+        vc += sm[Sh::oDC + m * T8 * Sh::NP + i];
       }
       put_bc(t0 + k, n, vb, vc);
     }
-    __syncthreads();
   }
 
   // ---- what leaves the split
   float* params = pl.params + (static_cast<size_t>(split) * q.B + b) * q.D * (q.N + 2);
-#pragma unroll
-  for (int c = 0; c < kCL; ++c) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (!in_state(c, s)) continue;
-      if (split == 0 && q.dh0) q.dh0[s_at + c * q.N + s] = c ? e[s].y : e[s].x;
-      params[static_cast<size_t>(d_base + t_base + c0 + c) * (q.N + 2) + n0 + s] = c ? dA[s].y : dA[s].x;
-    }
+  __syncthreads();
+  for (int i = tid; i < Sh::kSt; i += Sh::kThreads) {
+    const int ch = i / 16 % Sh::CH, n = i / (16 * Sh::CH) * 16 + i % 16;
+    if (ch >= count || n >= q.N) continue;
+    if (split == 0 && q.dh0) q.dh0[tile_at + static_cast<size_t>(ch) * q.N + n] = sm[Sh::oE + i];
+    params[static_cast<size_t>(d0 + ch) * (q.N + 2) + n] = sm[Sh::oDA + i];
   }
-  // The threads of a channel, in order (the chunk loop ended with a barrier).
-  if (busy) {
+  // The pieces of a channel, in order.
+  if (!resting) {
     sD[tid] = dskip;
-    sU[tid] = dbias;
+    sX[tid] = dbias;
   }
   __syncthreads();
-  if (tid < Sh::CH && livef) {
+  if (tid < count) {
     float sk = 0.f, bi = 0.f;
 #pragma unroll
-    for (int m = 0; m < (NR < T8 ? NR : T8); ++m) {
+    for (int m = 0; m < T8 / PS; ++m) {
       sk += sD[tid + m * Sh::CH];
-      bi += sU[tid + m * Sh::CH];
+      bi += sX[tid + m * Sh::CH];
     }
     params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N] = sk;
     params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N + 1] = bi;
@@ -428,14 +521,20 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float* pB, const flo
 
 // ---- host side ----
 
+// f(shape): warps along channels and states, groups of eight channels a warp.  With few channels a
+// warp takes one group, so that there are more warps; with many it takes four, so that the sums over
+// channels, B and C serve more.
 template <typename F>
-cudaError_t by_tiles(int N, F&& f) {
-  using std::integral_constant;
-  if (N <= 16) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  if (N <= 32) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-  if (N <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-  return f(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+cudaError_t by_tiles(const ScanCall& q, F&& f) {
+  const long long groups = static_cast<long long>(q.B) * q.G * ((q.D / q.G + 7) / 8) * ((q.N + 15) / 16);
+  const bool few = groups < 152LL * 12 * 2;
+  if (q.N <= 16) return few ? f(Shape<4, 1, 2>{}) : f(Shape<4, 1, 4>{});
+  if (q.N <= 32) return few ? f(Shape<2, 2, 2>{}) : f(Shape<2, 2, 4>{});
+  if (q.N <= 64) return few ? f(Shape<1, 4, 2>{}) : f(Shape<1, 4, 4>{});
+  return f(Shape<1, 8, 4>{});
 }
+template <int CW, int NT, int IT>
+constexpr int tile_channels(Shape<CW, NT, IT>) { return Shape<CW, NT, IT>::CH; }
 
 struct BwdLayout {
   ScanSplit sp;
@@ -446,11 +545,11 @@ struct BwdLayout {
 BwdLayout bwd_layout(const ScanCall& q) {
   BwdLayout L{};
   int ch = 32;
-  (void)by_tiles(q.N, [&](auto CW, auto NT) {
-    ch = Shape<decltype(CW)::value, decltype(NT)::value>::CH;
+  (void)by_tiles(q, [&](auto sh) {
+    ch = tile_channels(sh);
     return cudaSuccess;
   });
-  L.sp = scan_split(q, 152 * 8);  // eight warps an SM fill it
+  L.sp = scan_split(q, 152 * 12, 64);
   L.tiles = (q.D / q.G + ch - 1) / ch;
   auto up = [](size_t v) { return (v + 3) & ~static_cast<size_t>(3); };
   L.params = 0;
@@ -461,14 +560,17 @@ BwdLayout bwd_layout(const ScanCall& q) {
   return L;
 }
 
-template <typename T, int CW, int NT>
-cudaError_t run_bwd(const ScanCall& q, const BwdLayout& L, cudaStream_t s) {
-  using Sh = Shape<CW, NT>;
-  static_assert(Sh::kRows <= T8 ? Sh::kThreads <= Sh::kPer : true, "the last sums fit the per-channel values");
+template <typename T, int CW, int NT, int IT>
+cudaError_t run_bwd(const ScanCall& q, const BwdLayout& L, Shape<CW, NT, IT>, cudaStream_t s) {
+  using Sh = Shape<CW, NT, IT>;
   constexpr size_t smem = Sh::kFloats * sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, CW, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, CW, NT, IT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(scan_bwd_kernel<T, CW, NT, IT>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   BwdPlan pl{};
   pl.per_group = q.D / q.G;
@@ -486,7 +588,7 @@ cudaError_t run_bwd(const ScanCall& q, const BwdLayout& L, cudaStream_t s) {
   c.block = dim3(Sh::kThreads);
   c.smem = smem;
   c.stream = s;
-  return launch(c, scan_bwd_kernel<T, CW, NT>, q, pl);
+  return launch(c, scan_bwd_kernel<T, CW, NT, IT>, q, pl);
 }
 
 template <typename T>
@@ -495,9 +597,7 @@ cudaError_t bwd_all(const ScanCall& q, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (L.sp.splits > 1) e = scan_carry_launch(q, L.sp, true, q.ws + L.carry, s);
   if (e == cudaSuccess)
-    e = by_tiles(q.N, [&](auto CW, auto NT) {
-      return run_bwd<T, decltype(CW)::value, decltype(NT)::value>(q, L, s);
-    });
+    e = by_tiles(q, [&](auto sh) { return run_bwd<T>(q, L, sh, s); });
   if (e == cudaSuccess && L.tiles > 1) {
     const size_t count = static_cast<size_t>(q.K) * q.B * q.G * q.N;
     const size_t bc = static_cast<size_t>(L.tiles) * count;

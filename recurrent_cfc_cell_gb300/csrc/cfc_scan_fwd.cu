@@ -488,14 +488,14 @@ cudaError_t run_scan(const ScanCall& q, const ScanSplit& sp, float* carry, float
 
 }  // namespace
 
-ScanSplit scan_split(const ScanCall& q, int warps_wanted) {
+ScanSplit scan_split(const ScanCall& q, int warps_wanted, int least_steps) {
   const long long tiles = static_cast<long long>(q.B) * q.G * ((q.D / q.G + 31) / 32);
   const long long warps = tiles * ((q.N + 15) / 16);  // of 32 channels and 16 states
   const int unit = 2 * kScanPeriod;
   ScanSplit sp{1, q.K};
-  if (warps * 2 > warps_wanted || q.K < 16 * unit) return sp;
+  if (warps * 2 > warps_wanted || q.K < 4 * least_steps) return sp;
   long long splits = (warps_wanted + warps - 1) / warps;
-  const long long most = q.K / (4 * unit);
+  const long long most = q.K / least_steps;
   if (splits > most) splits = most;
   sp.steps = static_cast<int>(((q.K + splits - 1) / splits + unit - 1) / unit * unit);
   sp.splits = (q.K + sp.steps - 1) / sp.steps;
@@ -528,7 +528,7 @@ cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool rever
 }
 
 namespace {
-ScanSplit fwd_split(const ScanCall& q) { return scan_split(q, 152 * 12); }
+ScanSplit fwd_split(const ScanCall& q) { return scan_split(q, 152 * 12, 64); }
 }  // namespace
 
 size_t scan_fwd_ws_floats(const ScanCall& q) { return scan_carry_floats(q, fwd_split(q)); }
