@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 
   // The per-channel phases: a thread takes PS consecutive steps of one channel, from step k0 of the
   // chunk on.
-  constexpr int PS = T8 * Sh::CH / Sh::kThreads > 0 ? T8 * Sh::CH / Sh::kThreads : 1;
-  static_assert(T8 % PS == 0 && (T8 / PS) * Sh::CH <= Sh::kThreads, "every piece has a thread");
+  constexpr int PS = T8 * Sh::CH / Sh::kThreads;
+  static_assert(T8 % PS == 0 && T8 / PS * Sh::CH == Sh::kThreads, "a piece a thread");
   const int ch = Sh::kThreads == Sh::CH ? tid : tid % Sh::CH;
   const int k0 = Sh::kThreads == Sh::CH ? 0 : tid / Sh::CH * PS;
-  const bool live = ch < count && k0 < T8;
+  const bool live = ch < count;
   const float bias = q.dt_bias && live ? q.dt_bias[d0 + ch] : 0.f;
   const float skip = q.skip && live ? q.skip[d0 + ch] : 0.f;
   float dskip = 0.f, dbias = 0.f;
@@ -212,8 +212,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       rC[i] = in ? (Cp + (t0 + k) * q.Cm_t)[n] : none;
     }
   };
-  constexpr bool kFull = (T8 / PS) * Sh::CH == Sh::kThreads;  // no thread rests
-  auto whole = [&](int t0) { return kFull && count == Sh::CH && t0 + T8 <= end; };
+  auto whole = [&](int t0) { return count == Sh::CH && t0 + T8 <= end; };
   auto fetch = [&](int t0) {
     if (whole(t0)) fetch_as(t0, std::true_type{});
     else fetch_as(t0, std::false_type{});
@@ -253,7 +252,6 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     }
   };
   const int at_row = ch * kStride + k0, at_8 = ch * T8 + k0;
-  const bool resting = !kFull && k0 >= T8;
   if (chunks > 0) fetch(lo + (chunks - 1) * T8);
 
   for (int ck = chunks - 1; ck >= 0; --ck) {
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     const int c_first = cw * IT * 8 + dl;
     float4 next = kept(plane_in, c_first);
     // ---- per channel: d, x, r, and for the end dy silu'(z) and sigmoid(dt + bias)
-    if (!resting) {
+    {
       float dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
 #pragma unroll
       for (int j = 0; j < PS; j += 2) {
@@ -426,7 +424,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 
     // ---- per channel and step: the gradients of the inputs.  (A thread reads back what it formed
     // itself, and the sums; the next chunk's values may follow without a barrier.)
-    if (!resting) {
+    {
       float y[PS], v[PS], w[PS], dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
       get(&sm[Sh::oY + at_row], y);
       get(&sm[Sh::oV + at_row], v);
@@ -450,7 +448,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       get(&sm[Sh::oZ + at_8], zf);
       get(&sm[Sh::oS + at_8], sg);
       T *dx0 = dxr + t0 * q.dx_t, *dt0 = dtr + t0 * q.ddt_t, *dz0 = dzr ? dzr + t0 * q.dz_t : nullptr;
-      const bool all = kFull && count == Sh::CH && t0 + T8 <= hi;
+      const bool all = count == Sh::CH && t0 + T8 <= hi;
 #pragma unroll
       for (int j = 0; j < PS; ++j) {
         const float ddt = sg[j] * fmaf(w[j], kLn2, xv[j] * v[j]);
@@ -486,10 +484,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     params[static_cast<size_t>(d0 + ch) * (q.N + 2) + n] = sm[Sh::oDA + i];
   }
   // The pieces of a channel, in order.
-  if (!resting) {
-    sD[tid] = dskip;
-    sX[tid] = dbias;
-  }
+  sD[tid] = dskip;
+  sX[tid] = dbias;
   __syncthreads();
   if (tid < count) {
     float sk = 0.f, bi = 0.f;
