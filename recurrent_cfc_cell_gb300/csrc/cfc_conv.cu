@@ -105,10 +105,10 @@ __device__ __forceinline__ void load_x(const ConvCall& q, int t, int b, int c, f
   r.get(v);
 }
 
-constexpr int kU = 8;  // steps whose loads are in flight together
+constexpr int kU = 4;  // steps whose loads are issued together
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kLanes * kRuns, 4) conv_fwd_kernel(const ConvArgs a) {
   const ConvCall& q = a.q;
   const int c = (blockIdx.x * kLanes + threadIdx.x % kLanes) * V;
   if (c >= q.D) return;
@@ -144,13 +144,21 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs
       store_v<T, V>(u + t * q.u_t, o);
       shift(win);
     };
-    Raw<T, V> nx[kU];
-    int t = t0;
-    for (; t + kU <= te; t += kU) {
+    // Whole blocks of kU steps, the next block's loads on their way while one is computed.
+    Raw<T, V> nx[kU], ny[kU];
+    auto block = [&](int tb, Raw<T, V> (&r)[kU]) {
+      const T* xb = x + tb * q.x_t;
 #pragma unroll
-      for (int i = 0; i < kU; ++i) nx[i] = *reinterpret_cast<const Raw<T, V>*>(x + (t + i) * q.x_t);
+      for (int i = 0; i < kU; ++i) r[i] = *reinterpret_cast<const Raw<T, V>*>(xb + i * q.x_t);
+    };
+    int t = t0;
+    if (t + kU <= te) block(t, nx);
+    for (; t + kU <= te; t += kU) {
+      if (t + 2 * kU <= te) block(t + kU, ny);
 #pragma unroll
       for (int i = 0; i < kU; ++i) step(t + i, nx[i]);
+#pragma unroll
+      for (int i = 0; i < kU; ++i) nx[i] = ny[i];
     }
     if (t < te) {
 #pragma unroll
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_fwd_kernel(const ConvArgs
 }
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kLanes * kRuns, 2) conv_bwd_kernel(const ConvArgs a) {
   __shared__ float part[kRuns][(W + 1) * V][kLanes];
   grid_dep_launch_dependents();
   const ConvCall& q = a.q;
@@ -235,18 +243,28 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs
       else if (td < 0 && dx0) store_v<T, V>(dx0 + static_cast<long long>(td + W - 1) * q.D, o);
     };
     const int tl = min(t1 + W - 1, len);  // steps with a gradient that the run needs
-    Raw<T, V> nx[kU / 2], nd[kU / 2];
-    int t = t0;
-    for (; t + kU / 2 <= te; t += kU / 2) {
+    Raw<T, V> nx[kU], nd[kU], px[kU], pd[kU];
+    auto block = [&](int tb, Raw<T, V> (&rx)[kU], Raw<T, V> (&rd)[kU]) {
+      const T *xb = x + tb * q.x_t, *db_ = du + tb * q.du_t;
 #pragma unroll
-      for (int i = 0; i < kU / 2; ++i) {
-        nx[i] = *reinterpret_cast<const Raw<T, V>*>(x + (t + i) * q.x_t);
-        nd[i] = *reinterpret_cast<const Raw<T, V>*>(du + (t + i) * q.du_t);
+      for (int i = 0; i < kU; ++i) {
+        rx[i] = *reinterpret_cast<const Raw<T, V>*>(xb + i * q.x_t);
+        rd[i] = *reinterpret_cast<const Raw<T, V>*>(db_ + i * q.du_t);
       }
+    };
+    int t = t0;
+    if (t + kU <= te) block(t, nx, nd);
+    for (; t + kU <= te; t += kU) {
+      if (t + 2 * kU <= te) block(t + kU, px, pd);
 #pragma unroll
-      for (int i = 0; i < kU / 2; ++i) {
+      for (int i = 0; i < kU; ++i) {
         gradient(nx[i], nd[i], true);
         finish(t + i - (W - 1));
+      }
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        nx[i] = px[i];
+        nd[i] = pd[i];
       }
     }
     for (; t < tl; ++t) {
@@ -254,13 +272,15 @@ __global__ void __launch_bounds__(kLanes * kRuns) conv_bwd_kernel(const ConvArgs
                *reinterpret_cast<const Raw<T, V>*>(du + t * q.du_t), t < te);
       finish(t - (W - 1));
     }
-    // Past the sequence's end the gradients are zero, and so is dx.
-    for (; t < t1 + W - 1; ++t) {
+    // Past the sequence's end the gradients are zero, and W - 1 steps on so is dx.
+    for (; t < min(t1, max(t0, len)) + W - 1; ++t) {
       shift(g);
 #pragma unroll
       for (int v = 0; v < V; ++v) g[W - 1][v] = 0.f;
       finish(t - (W - 1));
     }
+    const float zero[V] = {};
+    for (int td = t - (W - 1); td < t1; ++td) store_v<T, V>(dx + td * q.dx_t, zero);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {

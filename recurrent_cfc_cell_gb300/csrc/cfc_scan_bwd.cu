@@ -262,28 +262,32 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     // ---- per channel: d, x, r, and for the end dy silu'(z) and sigmoid(dt + bias)
     {
       float dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
+      decide(q.softplus, [&](auto sp) {
 #pragma unroll
-      for (int j = 0; j < PS; j += 2) {
-        const float2 raw = make_float2(to_f32(rt[j]) + bias, to_f32(rt[j + 1 < PS ? j + 1 : j]) + bias);
-        const float2 d2 = q.softplus ? softplus2_f(raw) : raw;
-        dv[j] = d2.x;
-        sg[j] = q.softplus ? sigmoid_f(raw.x) : 1.f;
-        if (j + 1 < PS) {
-          dv[j + 1] = d2.y;
-          sg[j + 1] = q.softplus ? sigmoid_f(raw.y) : 1.f;
+        for (int j = 0; j < PS; j += 2) {
+          const int j1 = j + 1 < PS ? j + 1 : j;
+          const float2 raw = make_float2(to_f32(rt[j]) + bias, to_f32(rt[j1]) + bias);
+          float2 d2 = raw;
+          if constexpr (decltype(sp)::value) d2 = softplus2_f(raw);
+          dv[j1] = d2.y;
+          dv[j] = d2.x;
+          sg[j1] = decltype(sp)::value ? sigmoid_f(raw.y) : 1.f;
+          sg[j] = decltype(sp)::value ? sigmoid_f(raw.x) : 1.f;
         }
-      }
+      });
+      decide(zr != nullptr, [&](auto gate) {
 #pragma unroll
-      for (int j = 0; j < PS; ++j) {
-        xv[j] = to_f32(rx[j]);
-        rv[j] = to_f32(rg[j]);
-        zf[j] = 0.f;
-        if (zr) {
-          const float z = to_f32(rz[j]), s = sigmoid_f(z), gs = rv[j] * s;
-          rv[j] = gs * z;
-          zf[j] = gs * fmaf(z, 1.f - s, 1.f);
+        for (int j = 0; j < PS; ++j) {
+          xv[j] = to_f32(rx[j]);
+          rv[j] = to_f32(rg[j]);
+          zf[j] = 0.f;
+          if (decltype(gate)::value) {
+            const float z = to_f32(rz[j]), s = sigmoid_f(z), gs = rv[j] * s;
+            rv[j] = gs * z;
+            zf[j] = gs * fmaf(z, 1.f - s, 1.f);
+          }
         }
-      }
+      });
       if (!whole(t0)) {
         // Steps past the end and channels past the group's leave the state, its gradient and the
         // sums alone: d = 0 (x and r were read as 0).
@@ -448,18 +452,28 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       get(&sm[Sh::oZ + at_8], zf);
       get(&sm[Sh::oS + at_8], sg);
       T *dx0 = dxr + t0 * q.dx_t, *dt0 = dtr + t0 * q.ddt_t, *dz0 = dzr ? dzr + t0 * q.dz_t : nullptr;
-      const bool all = count == Sh::CH && t0 + T8 <= hi;
+      float ddt[PS];
 #pragma unroll
       for (int j = 0; j < PS; ++j) {
-        const float ddt = sg[j] * fmaf(w[j], kLn2, xv[j] * v[j]);
+        ddt[j] = sg[j] * fmaf(w[j], kLn2, xv[j] * v[j]);
         dskip = fmaf(rv[j], xv[j], dskip);
-        dbias += ddt;
-        if (all || (live && t0 + k0 + j < hi)) {
-          *pick(dx0 + j * q.dx_t, q.dx_t) = from_f32<T>(fmaf(dv[j], v[j], skip * rv[j]));
-          *pick(dt0 + j * q.ddt_t, q.ddt_t) = from_f32<T>(ddt);
-          if (dzr) *pick(dz0 + j * q.dz_t, q.dz_t) = from_f32<T>(zf[j] * fmaf(skip, xv[j], y[j]));
-        }
+        dbias += ddt[j];
       }
+      decide(count == Sh::CH && t0 + T8 <= hi, [&](auto all) {
+        auto each = [&](auto&& f) {
+#pragma unroll
+          for (int j = 0; j < PS; ++j)
+            if (decltype(all)::value || (live && t0 + k0 + j < hi)) f(j);
+        };
+        each([&](int j) {
+          *pick(dx0 + j * q.dx_t, q.dx_t) = from_f32<T>(fmaf(dv[j], v[j], skip * rv[j]));
+          *pick(dt0 + j * q.ddt_t, q.ddt_t) = from_f32<T>(ddt[j]);
+        });
+        if (dzr)
+          each([&](int j) {
+            *pick(dz0 + j * q.dz_t, q.dz_t) = from_f32<T>(zf[j] * fmaf(skip, xv[j], y[j]));
+          });
+      });
     }
     for (int i = tid; i < T8 * Sh::NP; i += Sh::kThreads) {
       const int k = i / Sh::NP, n = i % Sh::NP;

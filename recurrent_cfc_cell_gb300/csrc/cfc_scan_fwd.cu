@@ -40,7 +40,7 @@ struct Tile {
 // steps.  MODE 2: the same for the gradient carried backwards, c <- a_t (c + C_t r_t) with r_t the
 // gradient of y_t before the gate (it reads dy in the place of x).
 template <typename T, int S, int CW, int NT, int MODE>
-__global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q, const Tile tl,
+__global__ void __launch_bounds__(32 * CW * NT, CW * NT <= 4 ? 4 : 1) scan_fwd_kernel(const ScanCall q, const Tile tl,
                                                                 const int steps, float* carry,
                                                                 float* dsum) {
   constexpr int kThreads = 32 * CW * NT, CH = 32 * CW, NP = S * NT;
@@ -186,21 +186,24 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
     const bool whole = t0 + kT <= end;
     // ---- per channel and step: d and d x (MODE 2: d and r)
     float x[kEl], z[kEl];
+    decide(gated, [&](auto gate) {
 #pragma unroll
-    for (int i = 0; i < kEl; ++i) {
-      x[i] = to_f32(rx[i]);
-      z[i] = gated ? to_f32(rz[i]) : 0.f;
-    }
+      for (int i = 0; i < kEl; ++i) {
+        x[i] = to_f32(rx[i]);
+        z[i] = decltype(gate)::value ? to_f32(rz[i]) : 0.f;
+      }
+    });
+    decide(q.softplus, [&](auto sp) {
 #pragma unroll
-    for (int j = 0; j < kEl2; ++j) {
-      const int i0 = 2 * j, i1 = 2 * j + 1 < kEl ? 2 * j + 1 : 2 * j;
-      const float2 raw = make_float2(to_f32(rt[i0]) + bias, to_f32(rt[i1]) + bias);
-      const float2 dv = q.softplus ? softplus2_f(raw) : raw;
+      for (int j = 0; j < kEl2; ++j) {
+        const int i0 = 2 * j, i1 = 2 * j + 1 < kEl ? 2 * j + 1 : 2 * j;
+        float2 dv = make_float2(to_f32(rt[i0]) + bias, to_f32(rt[i1]) + bias);
+        if constexpr (decltype(sp)::value) dv = softplus2_f(dv);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int i = 2 * j + m;
-        const int k = tf + i * NT;
-        if (i < kEl) {
+        for (int m = 0; m < 2; ++m) {
+          const int i = 2 * j + m;
+          if (i >= kEl) break;
+          const int k = tf + i * NT;
           // Steps past the end leave the state alone: d = 0, so a = 1 and nothing is added.
           const float dd = whole || t0 + k < end ? (m ? dv.y : dv.x) : 0.f;
           float u = dd * x[i];
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
           if (MODE != 0) total += dd;
         }
       }
-    }
+    });
 #pragma unroll
     for (int i = 0; i < kStepsBC; ++i)
 #pragma unroll
@@ -278,18 +281,28 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_fwd_kernel(const ScanCall q
     // ---- per channel and step: the skip, the gate, the output
     if constexpr (MODE == 0) {
       T* y0 = yp + t0 * q.y_t;
+      decide(gated, [&](auto gate) {
+        float y[kEl];
 #pragma unroll
-      for (int i = 0; i < kEl; ++i) {
-        const int k = tf + i * NT;
-        if (!livef || (!whole && t0 + k >= hi)) continue;
-        float y = sY[0][k][chf];
+        for (int i = 0; i < kEl; ++i) {
+          const int k = tf + i * NT;
+          y[i] = sY[0][k][chf];
 #pragma unroll
-        for (int m = 1; m < NT; ++m) y += sY[m][k][chf];
-        y = fmaf(skip, x[i], y);
-        if (gated) y *= z[i] * sigmoid_f(z[i]);
-        *const_cast<T*>(pick(y0 + i * NT * q.y_t, yo)) =
-            whole || t0 + k < end ? from_f32<T>(y) : none;
-      }
+          for (int m = 1; m < NT; ++m) y[i] += sY[m][k][chf];
+          y[i] = fmaf(skip, x[i], y[i]);
+          if (decltype(gate)::value) y[i] *= z[i] * sigmoid_f(z[i]);
+        }
+        if (!livef) return;
+        decide(whole, [&](auto all) {
+#pragma unroll
+          for (int i = 0; i < kEl; ++i) {
+            const int t = t0 + tf + i * NT;
+            if (decltype(all)::value || t < hi)
+              *const_cast<T*>(pick(y0 + i * NT * q.y_t, yo)) =
+                  decltype(all)::value || t < end ? from_f32<T>(y[i]) : none;
+          }
+        });
+      });
     }
   }
 

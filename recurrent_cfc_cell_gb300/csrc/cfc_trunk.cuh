@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "cfc_ptx.cuh"
 
@@ -156,6 +157,13 @@ __device__ __forceinline__ void keep8(const DropKey& key, uint32_t row, uint32_t
     k[2 * i] = any && (w[i] << 16) >= high;
     k[2 * i + 1] = any && w[i] >= high;
   }
+}
+
+// f(true or false as a constant): a uniform condition decided once for straight-line code.
+template <typename F>
+__device__ __forceinline__ void decide(bool c, F&& f) {
+  if (c) f(std::true_type{});
+  else f(std::false_type{});
 }
 
 }  // namespace cfc
