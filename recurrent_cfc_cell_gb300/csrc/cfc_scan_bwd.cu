@@ -41,16 +41,21 @@ constexpr int T8 = kScanPeriod;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kHalf = T8 / 2;
-constexpr int kStride = 12;  // floats of a channel's eight steps: 16-byte rows without bank conflicts
+
+// Place of a half (four steps) of a channel among [channel][step] values: the halves of every other
+// four channels change places, so that eight channels' sixteen bytes fall in different banks.
+__device__ __forceinline__ int half_at(int ch, int half) {
+  return ch * T8 + ((half ^ (ch >> 2 & 1)) << 2);
+}
 
 template <int CW, int NT, int IT>
 struct Shape {
   static constexpr int kWarps = CW * NT, kThreads = 32 * kWarps, CH = 8 * IT * CW, NP = 16 * NT;
   static constexpr int kSt = NT * CH * 16;       // one value per (channel, state)
-  static constexpr int kRow = CH * kStride;      // one value per (channel, step), padded
+  static constexpr int kRow = CH * T8;           // one value per (channel, step)
   // Dynamic shared memory, in floats.
-  static constexpr int oE = 0, oDA = oE + kSt, oZ = oDA + kSt, oS = oZ + CH * T8;
-  static constexpr int oY = oS + CH * T8, oV = oY + NT * kRow, oW = oV + NT * kRow;
+  static constexpr int oE = 0, oDA = oE + kSt, oZ = oDA + kSt, oS = oZ + kRow;
+  static constexpr int oY = oS + kRow, oV = oY + NT * kRow, oW = oV + NT * kRow;
   static constexpr int oDB = oW + NT * kRow, oDC = oDB + CW * T8 * NP;
   static constexpr int kFloats = oDC + CW * T8 * NP;
 };
@@ -229,29 +234,26 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     const float* p = q.states + (t0 / T8) * plane + tile_at;
     for (int i = tid * 32; i < count * q.N; i += Sh::kThreads * 32) prefetch_l2(p + i);
   };
-  auto put = [&](float* p, const float (&f)[PS]) {
-    if constexpr (PS >= 4) {
-#pragma unroll
-      for (int j = 0; j < PS; j += 4)
-        *reinterpret_cast<float4*>(p + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+  // The thread's steps of its channel in a [channel][step] array, FS (up to four) at a time from
+  // step k of the chunk on.
+  constexpr int FS = PS < kHalf ? PS : kHalf;
+  auto put = [&](float* p, int k, const float (&f)[FS]) {
+    if constexpr (FS == kHalf) {
+      *reinterpret_cast<float4*>(p + half_at(ch, k / kHalf)) = make_float4(f[0], f[1], f[2], f[3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < PS; ++j) p[j] = f[j];
+      for (int j = 0; j < FS; ++j) p[half_at(ch, k / kHalf) + k % kHalf + j] = f[j];
     }
   };
-  auto get = [&](const float* p, float (&f)[PS]) {
-    if constexpr (PS >= 4) {
-#pragma unroll
-      for (int j = 0; j < PS; j += 4) {
-        const float4 r = *reinterpret_cast<const float4*>(p + j);
-        f[j] = r.x; f[j + 1] = r.y; f[j + 2] = r.z; f[j + 3] = r.w;
-      }
+  auto get = [&](const float* p, int k, float (&f)[FS]) {
+    if constexpr (FS == kHalf) {
+      const float4 r = *reinterpret_cast<const float4*>(p + half_at(ch, k / kHalf));
+      f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
     } else {
 #pragma unroll
-      for (int j = 0; j < PS; ++j) f[j] = p[j];
+      for (int j = 0; j < FS; ++j) f[j] = p[half_at(ch, k / kHalf) + k % kHalf + j];
     }
   };
-  const int at_row = ch * kStride + k0, at_8 = ch * T8 + k0;
   if (chunks > 0) fetch(lo + (chunks - 1) * T8);
 
   for (int ck = chunks - 1; ck >= 0; --ck) {
@@ -260,13 +262,14 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     const int c_first = cw * IT * 8 + dl;
     float4 next = kept(plane_in, c_first);
     // ---- per channel: d, x, r, and for the end dy silu'(z) and sigmoid(dt + bias)
-    {
-      float dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
+#pragma unroll
+    for (int f = 0; f < PS; f += FS) {
+      float dv[FS], xv[FS], rv[FS], zf[FS], sg[FS];
       decide(q.softplus, [&](auto sp) {
 #pragma unroll
-        for (int j = 0; j < PS; j += 2) {
-          const int j1 = j + 1 < PS ? j + 1 : j;
-          const float2 raw = make_float2(to_f32(rt[j]) + bias, to_f32(rt[j1]) + bias);
+        for (int j = 0; j < FS; j += 2) {
+          const int j1 = j + 1 < FS ? j + 1 : j;
+          const float2 raw = make_float2(to_f32(rt[f + j]) + bias, to_f32(rt[f + j1]) + bias);
           float2 d2 = raw;
           if constexpr (decltype(sp)::value) d2 = softplus2_f(raw);
           dv[j1] = d2.y;
@@ -277,12 +280,12 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       });
       decide(zr != nullptr, [&](auto gate) {
 #pragma unroll
-        for (int j = 0; j < PS; ++j) {
-          xv[j] = to_f32(rx[j]);
-          rv[j] = to_f32(rg[j]);
+        for (int j = 0; j < FS; ++j) {
+          xv[j] = to_f32(rx[f + j]);
+          rv[j] = to_f32(rg[f + j]);
           zf[j] = 0.f;
           if (decltype(gate)::value) {
-            const float z = to_f32(rz[j]), s = sigmoid_f(z), gs = rv[j] * s;
+            const float z = to_f32(rz[f + j]), s = sigmoid_f(z), gs = rv[j] * s;
             rv[j] = gs * z;
             zf[j] = gs * fmaf(z, 1.f - s, 1.f);
           }
@@ -292,14 +295,14 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
         // Steps past the end and channels past the group's leave the state, its gradient and the
         // sums alone: d = 0 (x and r were read as 0).
 #pragma unroll
-        for (int j = 0; j < PS; ++j)
-          if (!live || t0 + k0 + j >= end) dv[j] = sg[j] = 0.f;
+        for (int j = 0; j < FS; ++j)
+          if (!live || t0 + k0 + f + j >= end) dv[j] = sg[j] = 0.f;
       }
-      put(&sD[at_row], dv);
-      put(&sX[at_row], xv);
-      put(&sR[at_row], rv);
-      put(&sm[Sh::oZ + at_8], zf);
-      put(&sm[Sh::oS + at_8], sg);
+      put(sD, k0 + f, dv);
+      put(sX, k0 + f, xv);
+      put(sR, k0 + f, rv);
+      put(&sm[Sh::oZ], k0 + f, zf);
+      put(&sm[Sh::oS], k0 + f, sg);
     }
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
@@ -315,49 +318,48 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
     // ---- the two halves
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
-      float2 Bv[kHalf][2], Cv[kHalf][2], B0[kHalf][2];
       float2 db[kHalf][2], dc[kHalf][2];
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j) {
-        const int at = (half * kHalf + j) * Sh::NP + n0;
-        const float4 bv = *reinterpret_cast<const float4*>(&sB[at]);
-        const float4 cv = *reinterpret_cast<const float4*>(&sC[at]);
-        Bv[j][0] = make_float2(bv.x, bv.y); Bv[j][1] = make_float2(bv.z, bv.w);
-        Cv[j][0] = make_float2(cv.x, cv.y); Cv[j][1] = make_float2(cv.z, cv.w);
-        if (half) {
-          const float4 b0 = *reinterpret_cast<const float4*>(&sB[j * Sh::NP + n0]);
-          B0[j][0] = make_float2(b0.x, b0.y); B0[j][1] = make_float2(b0.z, b0.w);
-        }
+      for (int j = 0; j < kHalf; ++j)
 #pragma unroll
         for (int p = 0; p < 2; ++p) db[j][p] = dc[j][p] = make_float2(0.f, 0.f);
-      }
+      // B or C of the lane's states at step k of the chunk (a broadcast: one cycle of shared
+      // memory, and registers free for another warp).
+      auto bc = [&](const float* p, int k, float2 (&f)[2]) {
+        const float4 r = *reinterpret_cast<const float4*>(p + k * Sh::NP + n0);
+        f[0] = make_float2(r.x, r.y);
+        f[1] = make_float2(r.z, r.w);
+      };
 #pragma unroll 1
       for (int it = 0; it < IT; ++it) {
         const int cl = c_first + it * 8;  // the lane's channel
-        const int row = cl * kStride, st = (nt * Sh::CH + cl) * 16 + nl * 4;
+        const int st = (nt * Sh::CH + cl) * 16 + nl * 4;
         float2 h[2] = {make_float2(next.x, next.y), make_float2(next.z, next.w)};
         // The next group's kept state (after the later half's last, the earlier half's first).
         if (it + 1 < IT || half) next = kept(plane_in, it + 1 < IT ? cl + 8 : c_first);
         const float4 a4 = *reinterpret_cast<const float4*>(&sA[st]);
         const float2 A2[2] = {make_float2(a4.x, a4.y), make_float2(a4.z, a4.w)};
         if (half) {
-          const float4 d4 = *reinterpret_cast<const float4*>(&sD[row]);
-          const float4 x4 = *reinterpret_cast<const float4*>(&sX[row]);
+          const float4 d4 = *reinterpret_cast<const float4*>(&sD[half_at(cl, 0)]);
+          const float4 x4 = *reinterpret_cast<const float4*>(&sX[half_at(cl, 0)]);
           const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
           for (int j = 0; j < kHalf; ++j) {
             const float u = dv[j] * xv[j];
+            float2 B0[2];
+            bc(sB, j, B0);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const float2 m = __fmul2_rn(make_float2(dv[j], dv[j]), A2[p]);
               h[p] = fma2(make_float2(exp2_f(m.x), exp2_f(m.y)), h[p],
-                          __fmul2_rn(make_float2(u, u), B0[j][p]));
+                          __fmul2_rn(make_float2(u, u), B0[p]));
             }
           }
         }
-        const float4 d4 = *reinterpret_cast<const float4*>(&sD[row + half * kHalf]);
-        const float4 x4 = *reinterpret_cast<const float4*>(&sX[row + half * kHalf]);
-        const float4 r4 = *reinterpret_cast<const float4*>(&sR[row + half * kHalf]);
+        const int at = half_at(cl, half);
+        const float4 d4 = *reinterpret_cast<const float4*>(&sD[at]);
+        const float4 x4 = *reinterpret_cast<const float4*>(&sX[at]);
+        const float4 r4 = *reinterpret_cast<const float4*>(&sR[at]);
         const float4 e4 = *reinterpret_cast<const float4*>(&sm[Sh::oE + st]);
         const float4 da4 = *reinterpret_cast<const float4*>(&sm[Sh::oDA + st]);
         const float dv[4] = {d4.x, d4.y, d4.z, d4.w}, rv[4] = {r4.x, r4.y, r4.z, r4.w};
@@ -369,18 +371,21 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
         for (int j = 0; j < kHalf; ++j) {
           const float2 d2 = make_float2(dv[j], dv[j]), u2 = make_float2(uv[j], uv[j]);
           const float2 r2 = make_float2(rv[j], rv[j]);
-          float2 y2;
+          float2 y2, Bv[2], Cv[2];
+          bc(sB, half * kHalf + j, Bv);
+          bc(sC, half * kHalf + j, Cv);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const float2 m = __fmul2_rn(d2, A2[p]);
             a[j][p] = make_float2(exp2_f(m.x), exp2_f(m.y));
             qq[j][p] = __fmul2_rn(a[j][p], h[p]);
-            h[p] = fma2(u2, Bv[j][p], qq[j][p]);
-            y2 = p ? fma2(h[p], Cv[j][p], y2) : __fmul2_rn(h[p], Cv[j][p]);
+            h[p] = fma2(u2, Bv[p], qq[j][p]);
+            y2 = p ? fma2(h[p], Cv[p], y2) : __fmul2_rn(h[p], Cv[p]);
             dc[j][p] = fma2(r2, h[p], dc[j][p]);
           }
           y[j] = y2.x + y2.y;
         }
+        const float ys = sum_states(y, lane);
         // And back.
         float2 e[2] = {make_float2(e4.x, e4.y), make_float2(e4.z, e4.w)};
         float2 dA[2];
@@ -388,14 +393,16 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
         for (int j = kHalf - 1; j >= 0; --j) {
           const float2 d2 = make_float2(dv[j], dv[j]), u2 = make_float2(uv[j], uv[j]);
           const float2 r2 = make_float2(rv[j], rv[j]);
-          float2 v2, w2;
+          float2 v2, w2, Bv[2], Cv[2];
+          bc(sB, half * kHalf + j, Bv);
+          bc(sC, half * kHalf + j, Cv);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const float2 et = fma2(r2, Cv[j][p], e[p]);
+            const float2 et = fma2(r2, Cv[p], e[p]);
             const float2 eq = __fmul2_rn(et, qq[j][p]);
             dA[p] = j == kHalf - 1 ? __fmul2_rn(eq, d2) : fma2(eq, d2, dA[p]);
             w2 = p ? fma2(eq, A2[p], w2) : __fmul2_rn(eq, A2[p]);
-            v2 = p ? fma2(et, Bv[j][p], v2) : __fmul2_rn(et, Bv[j][p]);
+            v2 = p ? fma2(et, Bv[p], v2) : __fmul2_rn(et, Bv[p]);
             db[j][p] = fma2(et, u2, db[j][p]);
             e[p] = __fmul2_rn(a[j][p], et);
           }
@@ -405,8 +412,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
         *reinterpret_cast<float4*>(&sm[Sh::oE + st]) = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
         *reinterpret_cast<float4*>(&sm[Sh::oDA + st]) =
             make_float4(da4.x + dA[0].x, da4.y + dA[0].y, da4.z + dA[1].x, da4.w + dA[1].y);
-        const int out = nt * Sh::kRow + row + half * kHalf + nl;
-        sm[Sh::oY + out] = sum_states(y, lane);
+        const int out = nt * Sh::kRow + at + nl;
+        sm[Sh::oY + out] = ys;
         sm[Sh::oV + out] = sum_states(v, lane);
         sm[Sh::oW + out] = sum_states(w, lane);
       }
@@ -428,42 +435,46 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
 
     // ---- per channel and step: the gradients of the inputs.  (A thread reads back what it formed
     // itself, and the sums; the next chunk's values may follow without a barrier.)
-    {
-      float y[PS], v[PS], w[PS], dv[PS], xv[PS], rv[PS], zf[PS], sg[PS];
-      get(&sm[Sh::oY + at_row], y);
-      get(&sm[Sh::oV + at_row], v);
-      get(&sm[Sh::oW + at_row], w);
+    const bool all_out = count == Sh::CH && t0 + T8 <= hi;
+#pragma unroll 1
+    for (int f = 0; f < PS; f += FS) {
+      const int k = k0 + f;
+      float y[FS], v[FS], w[FS], dv[FS], xv[FS], rv[FS], zf[FS], sg[FS];
+      get(&sm[Sh::oY], k, y);
+      get(&sm[Sh::oV], k, v);
+      get(&sm[Sh::oW], k, w);
 #pragma unroll
       for (int m = 1; m < NT; ++m) {
-        float o[PS];
-        get(&sm[Sh::oY + m * Sh::kRow + at_row], o);
+        float o[FS];
+        get(&sm[Sh::oY + m * Sh::kRow], k, o);
 #pragma unroll
-        for (int j = 0; j < PS; ++j) y[j] += o[j];
-        get(&sm[Sh::oV + m * Sh::kRow + at_row], o);
+        for (int j = 0; j < FS; ++j) y[j] += o[j];
+        get(&sm[Sh::oV + m * Sh::kRow], k, o);
 #pragma unroll
-        for (int j = 0; j < PS; ++j) v[j] += o[j];
-        get(&sm[Sh::oW + m * Sh::kRow + at_row], o);
+        for (int j = 0; j < FS; ++j) v[j] += o[j];
+        get(&sm[Sh::oW + m * Sh::kRow], k, o);
 #pragma unroll
-        for (int j = 0; j < PS; ++j) w[j] += o[j];
+        for (int j = 0; j < FS; ++j) w[j] += o[j];
       }
-      get(&sD[at_row], dv);
-      get(&sX[at_row], xv);
-      get(&sR[at_row], rv);
-      get(&sm[Sh::oZ + at_8], zf);
-      get(&sm[Sh::oS + at_8], sg);
-      T *dx0 = dxr + t0 * q.dx_t, *dt0 = dtr + t0 * q.ddt_t, *dz0 = dzr ? dzr + t0 * q.dz_t : nullptr;
-      float ddt[PS];
+      get(sD, k, dv);
+      get(sX, k, xv);
+      get(sR, k, rv);
+      get(&sm[Sh::oZ], k, zf);
+      get(&sm[Sh::oS], k, sg);
+      T *dx0 = dxr + (t0 + f) * q.dx_t, *dt0 = dtr + (t0 + f) * q.ddt_t;
+      T* dz0 = dzr ? dzr + (t0 + f) * q.dz_t : nullptr;
+      float ddt[FS];
 #pragma unroll
-      for (int j = 0; j < PS; ++j) {
+      for (int j = 0; j < FS; ++j) {
         ddt[j] = sg[j] * fmaf(w[j], kLn2, xv[j] * v[j]);
         dskip = fmaf(rv[j], xv[j], dskip);
         dbias += ddt[j];
       }
-      decide(count == Sh::CH && t0 + T8 <= hi, [&](auto all) {
-        auto each = [&](auto&& f) {
+      decide(all_out, [&](auto all) {
+        auto each = [&](auto&& f1) {
 #pragma unroll
-          for (int j = 0; j < PS; ++j)
-            if (decltype(all)::value || (live && t0 + k0 + j < hi)) f(j);
+          for (int j = 0; j < FS; ++j)
+            if (decltype(all)::value || (live && t0 + k + j < hi)) f1(j);
         };
         each([&](int j) {
           *pick(dx0 + j * q.dx_t, q.dx_t) = from_f32<T>(fmaf(dv[j], v[j], skip * rv[j]));
