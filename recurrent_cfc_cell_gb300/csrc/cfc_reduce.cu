@@ -22,13 +22,12 @@ constexpr int kRowLanes = 8;
 constexpr int kColLanes = 32;
 
 // Where sum n goes: out[n], or -- for a tail that is rows of `pitch` values (pitch > 0) --
-// columns < ncol of row n / pitch to out[row * ncol + col], column ncol to out2[row], column
-// ncol + 1 to out3[row] (each unless null), and the rest of the row (padding) nowhere.
+// columns < ncol of row n / pitch to out[row * ncol + col], column ncol to out2[row], and the
+// rest of the row (padding) nowhere.
 struct OutMap {
   float* out;
   float* out2;
   int pitch, ncol;
-  float* out3 = nullptr;
 };
 
 __device__ __forceinline__ void put(const OutMap& o, int n, float v) {
@@ -38,8 +37,7 @@ __device__ __forceinline__ void put(const OutMap& o, int n, float v) {
   }
   const int row = n / o.pitch, col = n - row * o.pitch;
   if (col < o.ncol) o.out[static_cast<size_t>(row) * o.ncol + col] = v;
-  else if (col == o.ncol && o.out2) o.out2[row] = v;
-  else if (col == o.ncol + 1 && o.out3) o.out3[row] = v;
+  else if (col == o.ncol) o.out2[row] = v;
 }
 
 // One sum: n_tail columns of n_batch rows, each cluster CTA taking rows_per_cta rows.
@@ -214,8 +212,8 @@ cudaError_t reduce_axis0_launch(const float* in, int n_batch, int n_tail, float*
 
 cudaError_t reduce_axis0_rows_launch(const float* in, int n_batch, int n_tail, int pitch,
                                      int ncol, float* out, float* out2, cudaStream_t s,
-                                     bool pdl, float* out3) {
-  const OutMap o{out, out2, pitch, ncol, out3};
+                                     bool pdl) {
+  const OutMap o{out, out2, pitch, ncol};
   const bool vec = (n_tail % 4 == 0) && (reinterpret_cast<uintptr_t>(in) % 16 == 0);
   return vec ? launch_vec<4>(in, n_batch, n_tail, o, s, pdl)
              : launch_vec<1>(in, n_batch, n_tail, o, s, pdl);

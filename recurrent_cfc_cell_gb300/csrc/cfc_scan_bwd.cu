@@ -20,19 +20,23 @@
 // wait in shared memory between its halves (so dA is added four steps at a time).
 //
 // What a step needs per channel (d, x, r and the gate's and softplus's derivatives) is formed once
-// per chunk, a thread four steps of a channel.  NT warps side by side hold up to 16 NT states, CW
-// warps 8 IT CW channels.  Sums over warps, channel tiles, sequences and splits are added in a
+// per chunk, a thread up to eight steps of a channel.  NT warps side by side hold up to 16 NT states,
+// CW warps 8 IT CW channels.  Sums over warps, channel tiles, sequences and splits are added in a
 // fixed order (shared memory, then a merge), without atomics.
 //
-// Bound by instruction issue: a state's step takes 12 multiply-adds and an exponential and a half,
-// beside what is formed per channel.  History: the first form (four channels times four states a
-// lane, q_t of a chunk in shared memory) took 2008 us at 64 x 512 steps x 1024 channels x 16 states,
-// bf16, 920 us with packed arithmetic and loads in flight, and 834 us with half the lane's tile;
-// shared memory's traffic (q_t, and d, x, r, B, C read twice a step) and the sums over channels at
-// every step held it.
+// Bound by instruction issue: a state's step takes 12 multiply-adds and an exponential and a half, and
+// 512 of them with what their 32 channels need are 399 instructions, issued at 0.55 a clock and
+// scheduler with eight warps an SM (254 registers a thread; 168 or 146 spill, and cost more than the
+// warps they allow bring: 933 and 945 us).  Measured on GB300 at 64 x 512 steps x 1024 channels x 16
+// states, bf16: 766 us (of 425 us per 38 sequences, which fill the SMs evenly; 64 leave a half-empty
+// second wave).  History: 2008 us with four channels times four states a lane and q_t of a chunk in
+// shared memory; 920 us with packed arithmetic and loads in flight; 834 us with half that tile;
+// 823 us in this form, whose sums over channels and shared-memory traffic are a third; 766 us with
+// the uniform choices (gate, softplus, whole chunks) made once per chunk.
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
+#include "cfc_trunk_kernels.h"
 
 namespace cfc {
 namespace {
@@ -84,7 +88,8 @@ __device__ __forceinline__ float sum_channels(const float (&v)[4], int lane) {
 struct BwdPlan {
   int per_group, tiles_per_group, steps;
   const float* carry;   // [splits][B][D][N] or null
-  float* params;        // [splits * B][D][N + 2]
+  float* pA;            // [splits * B][D][N]: dA
+  float* pD;            // [splits * B][D][2]: dskip, ddt_bias
   float *pB, *pC;       // [tiles_per_group][K][B][G][N], or null: straight to dB / dC
 };
 
@@ -500,13 +505,15 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   }
 
   // ---- what leaves the split
-  float* params = pl.params + (static_cast<size_t>(split) * q.B + b) * q.D * (q.N + 2);
+  const size_t part = static_cast<size_t>(split) * q.B + b;
+  float* pA = pl.pA + part * q.D * q.N;
+  float* pD = pl.pD + (part * q.D + d0) * 2;
   __syncthreads();
   for (int i = tid; i < Sh::kSt; i += Sh::kThreads) {
     const int ch = i / 16 % Sh::CH, n = i / (16 * Sh::CH) * 16 + i % 16;
     if (ch >= count || n >= q.N) continue;
     if (split == 0 && q.dh0) q.dh0[tile_at + static_cast<size_t>(ch) * q.N + n] = sm[Sh::oE + i];
-    params[static_cast<size_t>(d0 + ch) * (q.N + 2) + n] = sm[Sh::oDA + i];
+    pA[static_cast<size_t>(d0 + ch) * q.N + n] = sm[Sh::oDA + i];
   }
   // The pieces of a channel, in order.
   sD[tid] = dskip;
@@ -519,8 +526,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
       sk += sD[tid + m * Sh::CH];
       bi += sX[tid + m * Sh::CH];
     }
-    params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N] = sk;
-    params[static_cast<size_t>(d0 + tid) * (q.N + 2) + q.N + 1] = bi;
+    pD[2 * tid] = sk;
+    pD[2 * tid + 1] = bi;
   }
 }
 
@@ -560,7 +567,7 @@ constexpr int tile_channels(Shape<CW, NT, IT>) { return Shape<CW, NT, IT>::CH; }
 struct BwdLayout {
   ScanSplit sp;
   int tiles;          // channel tiles per group
-  size_t params, bc, carry, total;  // offsets in floats
+  size_t pA, pD, spare, bc, carry, total;  // offsets in floats
 };
 
 BwdLayout bwd_layout(const ScanCall& q) {
@@ -573,8 +580,11 @@ BwdLayout bwd_layout(const ScanCall& q) {
   L.sp = scan_split(q, 152 * 12, 64);
   L.tiles = (q.D / q.G + ch - 1) / ch;
   auto up = [](size_t v) { return (v + 3) & ~static_cast<size_t>(3); };
-  L.params = 0;
-  L.bc = up(static_cast<size_t>(L.sp.splits) * q.B * q.D * (q.N + 2));
+  const size_t parts = static_cast<size_t>(L.sp.splits) * q.B;
+  L.pA = 0;
+  L.pD = up(parts * q.D * q.N);
+  L.spare = L.pD + up(parts * q.D * 2);  // for dskip and ddt_bias where they are not wanted
+  L.bc = L.spare + up(static_cast<size_t>(q.D) * 2);
   const size_t bc = static_cast<size_t>(L.tiles) * q.K * q.B * q.G * q.N;
   L.carry = L.bc + (L.tiles > 1 ? 2 * up(bc) : 0);
   L.total = L.carry + scan_carry_floats(q, L.sp);
@@ -598,7 +608,8 @@ cudaError_t run_bwd(const ScanCall& q, const BwdLayout& L, Shape<CW, NT, IT>, cu
   pl.tiles_per_group = L.tiles;
   pl.steps = L.sp.steps;
   pl.carry = L.sp.splits > 1 ? q.ws + L.carry : nullptr;
-  pl.params = q.ws + L.params;
+  pl.pA = q.ws + L.pA;
+  pl.pD = q.ws + L.pD;
   const size_t bc = static_cast<size_t>(L.tiles) * q.K * q.B * q.G * q.N;
   if (L.tiles > 1) {
     pl.pB = q.ws + L.bc;
@@ -634,8 +645,10 @@ cudaError_t bwd_all(const ScanCall& q, cudaStream_t s) {
                static_cast<T*>(q.dC));
   }
   if (e == cudaSuccess)
-    e = reduce_axis0_rows_launch(q.ws + L.params, L.sp.splits * q.B, q.D * (q.N + 2), q.N + 2, q.N,
-                                 q.dA, q.dskip, s, true, q.ddt_bias);
+    e = reduce_axis0_pair_launch(q.ws + L.pD, L.sp.splits * q.B, q.D * 2, 2, 1,
+                                 q.dskip ? q.dskip : q.ws + L.spare,
+                                 q.ddt_bias ? q.ddt_bias : q.ws + L.spare + q.D, q.ws + L.pA,
+                                 L.sp.splits * q.B, q.D * q.N, q.dA, s, true);
   return e;
 }
 

@@ -5,7 +5,7 @@
 #include <cstdint>
 
 #include "cfc.h"
-#include "cfc_kernels.h"
+#include "cfc_trunk_kernels.h"
 
 namespace cfc {
 int device_ready();  // cfc_abi.cu
