@@ -104,17 +104,20 @@ struct Lane {
     return col(piece, 0) >= 0 && col(piece, 7) < n;
   }
   // The lane's eight columns of piece `piece` of row `row` of a tensor of `rows` rows, as they are
-  // stored.  At the row's ends a group reaches into the rows before and after, which is the
-  // tensor's own memory but for its first and last row (and for rows that lie on one another,
-  // ld < n); those ends are read element by element.  clean() drops what is not the row's.
+  // stored.  At the row's ends a group reaches up to seven elements into the rows before and after,
+  // which is the tensor's own memory where it has that many: `near` rows before and after the row
+  // (7 columns' worth).  Groups at the tensor's ends (and those of rows that lie on one another,
+  // ld < n) are read element by element.  clean() drops what is not the row's.
   template <typename T>
   __device__ __forceinline__ void load(const T* p, long long ld, long long row, int rows, int piece,
                                        int n, Raw8<T>& r) const {
     const T* at = p + row * ld;
     bool vec = whole(piece, n);
-    if constexpr (LY == kShifted)
+    if constexpr (LY == kShifted) {
+      const int near = n >= 7 ? 1 : 7;
       vec = vec || (ld >= n && col(piece, 7) >= 0 && col(piece, 0) < n &&
-                    (col(piece, 0) >= 0 || row > 0) && (col(piece, 7) < n || row < rows - 1));
+                    (col(piece, 0) >= 0 || row >= near) && (col(piece, 7) < n || row < rows - near));
+    }
     if (vec) {
       r.load(at + col(piece, 0));
       return;

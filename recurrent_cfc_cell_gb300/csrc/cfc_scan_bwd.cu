@@ -28,7 +28,7 @@
 // 512 of them with what their 32 channels need are 399 instructions, issued at 0.55 a clock and
 // scheduler with eight warps an SM (254 registers a thread; 168 or 146 spill, and cost more than the
 // warps they allow bring: 933 and 945 us).  Measured on GB300 at 64 x 512 steps x 1024 channels x 16
-// states, bf16: 766 us (of 425 us per 38 sequences, which fill the SMs evenly; 64 leave a half-empty
+// states, bf16: 766 us (393 us for 38 sequences, which fill the SMs evenly; 64 leave a half-empty
 // second wave).  History: 2008 us with four channels times four states a lane and q_t of a chunk in
 // shared memory; 920 us with packed arithmetic and loads in flight; 834 us with half that tile;
 // 823 us in this form, whose sums over channels and shared-memory traffic are a third; 766 us with

@@ -114,6 +114,40 @@ def test_layernorm_strided_rows(rows, n, dtype):
         assert (beside == 77.0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n,offset", [(1, 3, 5), (2, 3, 5), (3, 1, 7), (9, 5, 3), (20, 13, 1),
+                                           (5, 255, 6), (3, 2043, 2), (2, 4099, 7)])
+def test_layernorm_packed_rows_from_anywhere(rows, n, offset, dtype):
+    """Rows one after another from any element on, so that a group of eight spans several rows or
+    starts before the first: NaN around the tensor, and the results of the same rows aligned."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import _lib
+
+    i = norm_inputs(rows, n, dtype, offset)
+
+    def packed(v, fill):
+        buf = torch.full((rows * n + 16,), fill, dtype=act(dtype), device="cuda")
+        view = buf[offset:offset + rows * n].view(rows, n)
+        view.copy_(v)
+        return buf, view
+
+    nan = float("nan")
+    (_, x), (_, dy) = packed(cuda(i["x"], dtype), nan), packed(cuda(i["dy"], dtype), nan)
+    (yb, y), (db_, dx) = (packed(torch.zeros(rows, n, device="cuda"), 77.0) for _ in range(2))
+    w, b, stats = cuda(i["w"]), cuda(i["b"]), torch.empty(rows, 2, device="cuda")
+    dw, db = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    ws = torch.empty(max(16, _lib.layernorm_workspace_bytes(rows, n)), dtype=torch.uint8, device="cuda")
+    _lib.cfc_layernorm_forward(x, w, b, y, stats)
+    _lib.cfc_layernorm_backward(dy, x, w, stats, dx, dw, db, ws)
+    check(y, ot.layernorm(i["x"], i["w"], i["b"], 1e-5), EL, "y")
+    for got, want in zip((dx, dw, db), ot.layernorm_backward(i["dy"], i["x"], i["w"], 1e-5)):
+        if n > 1 or want is not None and np.any(want):
+            check(got, want, SUM)
+    for buf in (yb, db_):
+        assert (buf[:offset] == 77.0).all() and (buf[offset + rows * n:] == 77.0).all()
+
+
 def test_layernorm_many_rows_is_reproducible():
     """More rows than the backward's CTAs take in one turn; bitwise the same twice and in a graph."""
     import torch
