@@ -549,15 +549,20 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float* pB, const flo
 
 // ---- host side ----
 
-// f(shape): warps along channels and states, groups of eight channels a warp.  With few channels a
-// warp takes one group, so that there are more warps; with many it takes four, so that the sums over
-// channels, B and C serve more.
+// f(shape): warps along channels and states, groups of eight channels a warp.  With many channels a
+// warp takes four groups, so that the sums over channels, B and C serve more (32 x 128 steps x 1024
+// channels x 16 states: 112 us, 130 us with two); with fewer two, so that there are more warps
+// (16 x 128 x 1024 x 16: 68 us, 83 us with four; 32 x 64 x 256 x 32: 40 and 44 us); and one where
+// even the split steps leave SMs idle, so that a step takes less (4 x 128 x 256 x 16: 22.8 us, 24.9 us
+// with two; 4 x 1024 x 256 x 16: 61.7 and 57.4 us).
 template <typename F>
 cudaError_t by_tiles(const ScanCall& q, F&& f) {
   const long long groups = static_cast<long long>(q.B) * q.G * ((q.D / q.G + 7) / 8) * ((q.N + 15) / 16);
-  const bool few = groups < 152LL * 12 * 2;
-  if (q.N <= 16) return few ? f(Shape<4, 1, 2>{}) : f(Shape<4, 1, 4>{});
-  if (q.N <= 32) return few ? f(Shape<2, 2, 2>{}) : f(Shape<2, 2, 4>{});
+  const bool few = groups < 152LL * 12 * 2, very_few = groups * q.K < 152LL * 256;
+  if (q.N <= 16)
+    return very_few ? f(Shape<4, 1, 1>{}) : few ? f(Shape<4, 1, 2>{}) : f(Shape<4, 1, 4>{});
+  if (q.N <= 32)
+    return very_few ? f(Shape<2, 2, 1>{}) : few ? f(Shape<2, 2, 2>{}) : f(Shape<2, 2, 4>{});
   if (q.N <= 64) return few ? f(Shape<1, 4, 2>{}) : f(Shape<1, 4, 4>{});
   return f(Shape<1, 8, 4>{});
 }
@@ -577,8 +582,10 @@ BwdLayout bwd_layout(const ScanCall& q) {
     ch = tile_channels(sh);
     return cudaSuccess;
   });
-  L.sp = scan_split(q, 152 * 12, 64);
   L.tiles = (q.D / q.G + ch - 1) / ch;
+  // 4 x 128 x 256 x 16: 25 us in eight splits of 16 steps, 50 us unsplit; 15 x 209 x 28 x 4: 26 and
+  // 85 us; 4 x 64 x 908 x 24: 39 and 34 us.
+  L.sp = scan_split(q.K, static_cast<long long>(q.B) * q.G * L.tiles, 152 * 4, 16, 96);
   auto up = [](size_t v) { return (v + 3) & ~static_cast<size_t>(3); };
   const size_t parts = static_cast<size_t>(L.sp.splits) * q.B;
   L.pA = 0;

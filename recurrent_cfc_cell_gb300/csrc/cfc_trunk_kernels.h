@@ -72,13 +72,14 @@ size_t scan_bwd_ws_floats(const ScanCall& q);
 cudaError_t scan_fwd_launch(const ScanCall& q, cudaStream_t s);
 cudaError_t scan_bwd_launch(const ScanCall& q, cudaStream_t s);
 cudaError_t scan_step_launch(const ScanCall& q, cudaStream_t s);
-// Splits of the steps over CTAs (1: none) so that there are about `warps_wanted` warps of 32
-// channels and 16 states, for the forward and the backward recurrence, and the pass that carries the state (or its gradient) over the splits: on return carry
-// [splits][B][D][N] holds what enters each split.
+// Splits of the steps over CTAs (1: none) for a recurrence that takes `ctas` CTAs unsplit, so that
+// about `slots` run: at least `least_steps` steps each, and none with fewer than `least_total` steps
+// or three splits, which would not pay for the pass that carries the state (or its gradient) over
+// the splits.  On return of that pass carry [splits][B][D][N] holds what enters each split.
 struct ScanSplit {
   int splits, steps;               // steps per split, a multiple of 2 kScanPeriod
 };
-ScanSplit scan_split(const ScanCall& q, int warps_wanted, int least_steps);
+ScanSplit scan_split(int K, long long ctas, int slots, int least_steps, int least_total);
 size_t scan_carry_floats(const ScanCall& q, const ScanSplit& sp);
 cudaError_t scan_carry_launch(const ScanCall& q, const ScanSplit& sp, bool reverse, float* carry,
                               cudaStream_t s);
