@@ -14,7 +14,8 @@
 // left, so that a large mean costs no precision), and the next row's loads are on their way
 // meanwhile.  A row belongs to a team of lanes, eight columns to a lane and piece: 4 to 32 lanes
 // of one warp up to 256 columns, 2 or 4 warps up to 1024, a whole CTA of just enough warps up to
-// 8192, two pieces a lane.  Longer rows are read again for each sum (they stay in L2).
+// 8192, two pieces a lane (with the rows on their way in shared memory where they would take too many
+// registers, see Ring).  Longer rows are read again for each sum (they stay in L2).
 //
 // Lanes load and store eight columns at once.  Where rows start anywhere (an odd width), the
 // lanes' groups of eight follow the memory's alignment instead of the row's start, and the row's
@@ -29,12 +30,16 @@
 //
 // Measured on GB300 (copy rate 6.69 TB/s): 262144 x 256 fp32 forward 84 us (6.4 TB/s), backward 125 us
 // (6.4 TB/s); the same rows in bf16 with dropout and residual 99 us (5.4 TB/s; a row's generator calls
-// are a third of its instructions) and 128 us (5.2 TB/s); 6007 x 2501 bf16, rows of every alignment,
-// 21 and 36 us (2.9 and 2.5 TB/s: a CTA's 13 rows are each a barrier or two, and its partial sums 9 MB).
+// are a third of its instructions) and 128 us (5.2 TB/s); 10529 x 3528 fp32 56 and 88 us (5.3 and
+// 5.0 TB/s), bf16 33 and 54 us (4.5 and 4.1 TB/s: a CTA's row is a chain of loads, sums, a barrier
+// and stores, and few rows are in flight on an SM); 6007 x 2501 bf16, rows of every alignment, 21 and
+// 32 us (2.9 and 2.8 TB/s: besides, the rows' ends are taken element by element).
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
 #include "cfc_trunk_kernels.h"
+
+#include <type_traits>
 
 namespace cfc {
 namespace {
@@ -103,30 +108,33 @@ struct Lane {
     if constexpr (LY == kAligned) return col(piece, 0) < n;
     return col(piece, 0) >= 0 && col(piece, 7) < n;
   }
-  // The lane's eight columns of piece `piece` of row `row` of a tensor of `rows` rows, as they are
-  // stored.  At the row's ends a group reaches up to seven elements into the rows before and after,
-  // which is the tensor's own memory where it has that many: `near` rows before and after the row
-  // (7 columns' worth).  Groups at the tensor's ends (and those of rows that lie on one another,
-  // ld < n) are read element by element.  clean() drops what is not the row's.
+  // Whether a lane's eight columns of row `row` of a tensor of `rows` rows are read at once.  At the row's ends a group reaches up to seven elements into the rows before and
+  // after, which is the tensor's own memory where it has that many: `near` rows before and after
+  // the row (7 columns' worth).  Groups at the tensor's ends (and those of rows that lie on one
+  // another, ld < n) are read element by element.
+  // `first`: the group's first column.
+  __device__ __forceinline__ static bool vec(long long ld, long long row, int rows, int first, int n) {
+    if constexpr (LY == kScalar) return false;
+    if constexpr (LY == kAligned) return first < n;
+    const int last = first + 7, near = n >= 7 ? 1 : 7;
+    return (first >= 0 && last < n) || (ld >= n && last >= 0 && first < n &&
+                                        (first >= 0 || row >= near) && (last < n || row < rows - near));
+  }
+  // The lane's eight columns as they are stored; clean() drops what is not the row's.
   template <typename T>
   __device__ __forceinline__ void load(const T* p, long long ld, long long row, int rows, int piece,
                                        int n, Raw8<T>& r) const {
     const T* at = p + row * ld;
-    bool vec = whole(piece, n);
-    if constexpr (LY == kShifted) {
-      const int near = n >= 7 ? 1 : 7;
-      vec = vec || (ld >= n && col(piece, 7) >= 0 && col(piece, 0) < n &&
-                    (col(piece, 0) >= 0 || row >= near) && (col(piece, 7) < n || row < rows - near));
-    }
-    if (vec) {
+    if (vec(ld, row, rows, col(piece, 0), n)) {
       r.load(at + col(piece, 0));
       return;
     }
     r.clear();
-    if constexpr (LY == kAligned) return;
+    if constexpr (LY != kAligned) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (in(piece, j, n)) r.set(j, at[col(piece, j)]);
+      for (int j = 0; j < 8; ++j)
+        if (in(piece, j, n)) r.set(j, at[col(piece, j)]);
+    }
   }
   template <typename T>
   __device__ __forceinline__ void clean(const Raw8<T>& r, int piece, int n, float (&v)[8]) const {
@@ -165,10 +173,10 @@ struct Lane {
       for (int j = 0; j < 8; ++j) v[j] = in(piece, j, n) ? p[col(piece, j)] : 0.f;
     }
   }
-  // The lane's eight columns into a row of fp32 sums, likewise.
+  // The lane's eight columns into a row of fp32 sums (of any alignment), likewise.
   __device__ __forceinline__ void put_sums(float* p, int piece, int n, float* buf,
                                            const float (&v)[8]) const {
-    if constexpr (LY == kShifted && TM::WPR > 0) {
+    if constexpr (LY != kScalar) {
       *reinterpret_cast<float4*>(buf + lane * 8) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4*>(buf + lane * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
       __syncwarp();
@@ -191,10 +199,11 @@ struct Lane {
       store8(row + col(piece, 0), v);
       return;
     }
-    if constexpr (LY == kAligned) return;
+    if constexpr (LY != kAligned) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (in(piece, j, n)) row[col(piece, j)] = from_f32<T>(v[j]);
+      for (int j = 0; j < 8; ++j)
+        if (in(piece, j, n)) row[col(piece, j)] = from_f32<T>(v[j]);
+    }
   }
   // Which of the lane's eight columns are kept.  The generator serves eight consecutive columns
   // from a multiple of eight; where a lane's columns are others, each lane draws for its eight of
@@ -245,8 +254,16 @@ __device__ __forceinline__ void clear_slots(Slots<N>& s) {
     __syncthreads();
   }
 }
-template <typename TM, int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& slot, int turn, int team) {
+__device__ __forceinline__ void half_warp_sum(float& v) {
+#pragma unroll
+  for (int d = kMaxWarps / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+}
+__device__ __forceinline__ void warp_sum(float& v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  half_warp_sum(v);
+}
+template <typename TM, int N, int M>
+__device__ __forceinline__ void team_sum(float (&v)[N], Slots<M>& slot, int turn, int team) {
   constexpr int kSpan = TM::WPR > 0 ? 32 : TM::L;
 #pragma unroll
   for (int d = kSpan / 2; d > 0; d >>= 1)
@@ -263,9 +280,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& slot, int turn
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = slot.v[turn][i][threadIdx.x % kMaxWarps];
 #pragma unroll
-      for (int d = kMaxWarps / 2; d > 0; d >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+      for (int i = 0; i < N; ++i) half_warp_sum(v[i]);
     } else {
       asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TM::WPR * 32) : "memory");
 #pragma unroll
@@ -276,6 +291,122 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& slot, int turn
       }
     }
   }
+}
+
+// The rows on their way: NT tensors, two rows of each in shared memory, for whole-CTA teams whose
+// groups of eight are aligned.  A warp copies its own groups (32 consecutive pieces of 16
+// bytes at a time) and reads them itself, so only its own copies are waited for, and the copies need
+// no registers meanwhile.
+// Shared memory: [row of the ring][tensor][piece][16 bytes of eight columns][thread], then the
+// parameters, likewise.
+template <typename T, typename TM, Layout LY, int NT>
+struct Ring {
+  [[maybe_unused]] static constexpr int kDepth = 2;
+  static constexpr int kQuads = sizeof(T) / 2;  // 16 bytes each, of eight columns
+  static constexpr int kRow = NT * TM::I * kQuads;
+  [[maybe_unused]] static constexpr int kParam = TM::I * 2;      // a parameter's, in fp32
+  uint4* mine;
+  int at = 0;
+  __device__ __forceinline__ explicit Ring(uint4* smem) : mine(smem + threadIdx.x) {}
+  __device__ __forceinline__ uint4* place(int slot, int t, int piece) const {
+    return mine + (slot * kRow + (t * TM::I + piece) * kQuads) * static_cast<int>(blockDim.x);
+  }
+  __device__ __forceinline__ uint4* param(int which, int piece) const {
+    return mine + (kDepth * kRow + which * kParam + piece * 2) * static_cast<int>(blockDim.x);
+  }
+  __device__ __forceinline__ void put_param(int which, int piece, const float (&v)[8]) const {
+    float4* const to = reinterpret_cast<float4*>(param(which, piece));
+    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+    to[blockDim.x] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void get_param(int which, int piece, float (&v)[8]) const {
+    const float4* const from = reinterpret_cast<const float4*>(param(which, piece));
+    const float4 lo = from[0], hi = from[blockDim.x];
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  }
+  // A group with none of the row's columns is never fetched, and stays zero.
+  static __device__ __forceinline__ bool outside(const Lane<TM, LY>& ln, int piece, int n) {
+    return ln.col(piece, 7) < 0 || ln.col(piece, 0) >= n;
+  }
+  __device__ __forceinline__ void clear(const Lane<TM, LY>& ln, int n) const {
+    Raw8<T> zero;
+    zero.clear();
+    for (int slot = 0; slot < kDepth; ++slot)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < TM::I; ++i)
+          if (outside(ln, i, n)) zero.put(place(slot, t, i), static_cast<int>(blockDim.x));
+  }
+  __device__ __forceinline__ void fetch(const Lane<TM, LY>& ln, int slot, int t, const T* p, long long ld,
+                                        long long row, int rows, int n) const {
+    if constexpr (kQuads > 1) __syncwarp();  // all that its lanes have read
+#pragma unroll
+    for (int i = 0; i < TM::I; ++i) {
+      uint4* const to = place(slot, t, i);
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int chunk = q * 32 + ln.lane, of = chunk / kQuads, part = chunk % kQuads;
+        const int first = ln.col(i, 0) + (of - ln.lane) * 8;
+        if (ln.vec(ld, row, rows, first, n))
+          cp_async_16(to + (of - ln.lane) + part * static_cast<int>(blockDim.x),
+                      p + row * ld + first + part * (16 / static_cast<int>(sizeof(T))));
+      }
+      if (LY == kShifted && !outside(ln, i, n) && !ln.vec(ld, row, rows, ln.col(i, 0), n)) {
+        Raw8<T> r;
+        ln.load(p, ld, row, rows, i, n, r);
+        r.put(to, static_cast<int>(blockDim.x));
+      }
+    }
+  }
+  __device__ __forceinline__ void take(int t, int piece, Raw8<T>& r) const {
+    r.pick(place(at, t, piece), static_cast<int>(blockDim.x));
+  }
+  // The oldest row has arrived (this warp's groups of it).
+  __device__ __forceinline__ void wait() const {
+    cp_async_wait<kDepth - 1>();
+    if constexpr (kQuads > 1) __syncwarp();
+  }
+  __device__ __forceinline__ void next() { at ^= 1; }
+};
+
+// Where the rows on their way take too many registers: the ring.  bf16: all but the backward pass of
+// aligned rows without dropout; fp32, whose copies of 16 bytes are twice as many: rows with dropout
+// that are shifted, or above 4096 columns in the backward pass.  Measured (us, with the ring and
+// without):
+//   bf16          10529 x 3528 forward 33, 39; backward 67, 54       3000 x 8185 27 + 45, 29 + 54
+//     dropout     10529 x 3528 66 + 83, 75 + 103                     6007 x 2501 46 + 59, 49 + 79
+//   fp32          10529 x 3528 86 + 108, 56 + 88                     3000 x 8185 57 + 80, 42 + 74
+//     dropout     10529 x 3528 130 + 179, 94 + 147                   6007 x 2501 58 + 83, 79 + 114
+template <typename T, typename TM, Layout LY, bool DROP>
+__host__ __device__ constexpr bool fwd_ring() {
+  return TM::kWhole && LY != kScalar && (sizeof(T) == 2 || (DROP && LY == kShifted));
+}
+template <typename T, typename TM, Layout LY, bool DROP>
+__host__ __device__ constexpr bool bwd_ring() {
+  if (!TM::kWhole || LY == kScalar) return false;
+  if (sizeof(T) == 2) return DROP || LY == kShifted;
+  return DROP && (LY == kShifted || TM::kMaxThreads > kThreads);
+}
+// CTAs of the most threads that an SM's registers must hold (0: as the compiler finds).  Forward,
+// 256 threads: four (64 registers; 262144 x 256 bf16 with dropout 99 us, 105 us with the three that
+// the registers taken freely allow, 125 us with five), but two of shifted rows with dropout, which
+// spill at 64 (28467 x 319 bf16 48 us, 56 us with three); whole CTAs: 128 registers, 64 with a ring
+// that holds the rows without dropout.  Backward: shifted rows three, with dropout two, as the grid
+// has (28467 x 319: bf16 37 us, 50 us freely; fp32 with dropout 73 and 93 us); whole CTAs with shifted
+// rows or a ring 128 registers (6007 x 2501 fp32 49 us, 68 us freely); aligned rows with the loads in
+// registers as the compiler finds (262144 x 256 fp32 125 us; asked for one CTA, it spends the
+// registers on an order of loads that takes 158 us).
+template <typename T, typename TM, Layout LY, bool DROP>
+__host__ __device__ constexpr int fwd_ctas() {
+  if (!TM::kWhole) return LY == kShifted && DROP ? 2 : 4;
+  return (fwd_ring<T, TM, LY, DROP>() && !DROP ? 1024 : 512) / TM::kMaxThreads;
+}
+template <typename T, typename TM, Layout LY, bool DROP>
+__host__ __device__ constexpr int bwd_ctas() {
+  if (!TM::kWhole) return LY != kShifted ? 0 : DROP ? 2 : 3;
+  return LY != kShifted && !bwd_ring<T, TM, LY, DROP>() ? 0 : 512 / TM::kMaxThreads;
 }
 
 struct NormArgs {
@@ -305,14 +436,20 @@ __device__ __forceinline__ Turns turns_of(int rows, int team) {
           static_cast<int>((rows + step - 1) / step)};
 }
 
-// Four CTAs an SM (64 registers a thread) up to 1024 columns: 262144 x 256 bf16 with dropout 99 us,
-// 105 us with the three that the registers taken freely allow, 125 us with five.
 template <typename T, typename TM, Layout LY, bool DROP>
-__global__ void __launch_bounds__(TM::kMaxThreads, TM::kWhole ? 1 : 4) norm_fwd_kernel(const NormArgs a) {
-  __shared__ Slots<1> slot;
-  __shared__ __align__(16) float bufs[LY == kShifted ? kMaxWarps : 1][256];
+__global__ void __launch_bounds__(TM::kMaxThreads, fwd_ctas<T, TM, LY, DROP>())
+    norm_fwd_kernel(const NormArgs a) {
+  __shared__ Slots<2> slot;
+  extern __shared__ uint4 smem[];
+  using Rg = Ring<T, TM, LY, DROP ? 2 : 1>;
+  constexpr bool kRing = fwd_ring<T, TM, LY, DROP>();
+  constexpr int kBufs = !kRing && (LY == kShifted || (TM::kWhole && LY != kScalar)) ? TM::kMaxThreads / 32 : 1;
+  __shared__ __align__(16) float bufs[kBufs][256];
   clear_slots<TM>(slot);
-  float* const buf = bufs[LY == kShifted ? threadIdx.x / 32 : 0];
+  // (A ring's first kilobytes, before and after its use.)
+  float* const buf = kRing ? reinterpret_cast<float*>(smem) + threadIdx.x / 32 * 256
+                           : bufs[kBufs > 1 ? threadIdx.x / 32 : 0];
+  Rg ring(smem);
   Lane<TM, LY> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -329,6 +466,13 @@ __global__ void __launch_bounds__(TM::kMaxThreads, TM::kWhole ? 1 : 4) norm_fwd_
       if (DROP && rp) at.load(rp, a.ldr, row, a.rows, i, n, nr[i]);
     }
   };
+  auto fetch_ring = [&](long long row, int place) {
+    if (row < a.rows) {
+      ring.fetch(at, place, 0, xp, a.ldx, row, a.rows, n);
+      if (DROP && rp) ring.fetch(at, place, DROP ? 1 : 0, rp, a.ldr, row, a.rows, n);
+    }
+    cp_async_commit();
+  };
   // Aligned parameters are two loads from the first-level cache a row; others stay in registers.
   float w[TM::I][8], b[TM::I][8];
   at.set_row(xp + (tn.first < a.rows ? tn.first : 0) * a.ldx);
@@ -339,22 +483,70 @@ __global__ void __launch_bounds__(TM::kMaxThreads, TM::kWhole ? 1 : 4) norm_fwd_
       at.params(a.b, i, n, buf, b[i]);
     }
   };
-  if constexpr (LY != kAligned) params();
-  if (tn.first < a.rows) fetch(tn.first);
+  // Columns of a whole CTA's warp: this one, and (lane % kMaxWarps).
+  auto columns = [&](int warp) {
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < TM::I; ++i) {
+      const int lo = i * TM::cols() + warp * 256 - at.shift;
+      sum += max(0, min(n, lo + 256) - max(0, lo));
+    }
+    return warp < static_cast<int>(blockDim.x) / 32 ? static_cast<float>(sum) : 0.f;
+  };
+  const float own_n = columns(threadIdx.x / 32), other_n = columns(at.lane % kMaxWarps);
+  const float own_inv = own_n > 0.f ? 1.f / own_n : 0.f, other_inv = other_n > 0.f ? 1.f / other_n : 0.f;
+  // v less `from`, and the sum of its squares, of the row's columns alone.
+  auto spread = [&](float (&v)[TM::I][8], float from, float& sq) {
+#pragma unroll
+    for (int i = 0; i < TM::I; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] -= from;
+      if (at.whole(i, n)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sq = fmaf(v[i][j], v[i][j], sq);
+      } else if (LY != kAligned) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at.in(i, j, n)) sq = fmaf(v[i][j], v[i][j], sq);
+      }
+    }
+  };
+  if constexpr (kRing) {
+#pragma unroll
+    for (int i = 0; i < TM::I; ++i) {
+      at.params(a.w, i, n, buf, w[i]);
+      ring.put_param(0, i, w[i]);
+      at.params(a.b, i, n, buf, b[i]);
+      ring.put_param(1, i, b[i]);
+    }
+    __syncthreads();
+    ring.clear(at, n);
+    for (int i = 0; i < Rg::kDepth; ++i) fetch_ring(tn.first + i * tn.step, i);
+  } else {
+    if constexpr (LY != kAligned) params();
+    if (tn.first < a.rows) fetch(tn.first);
+  }
   for (int turn = 0; turn < tn.count; ++turn) {
     const long long row = tn.first + turn * tn.step;
     const bool live = row < a.rows;
     if (TM::WPR > 0 && !live) return;  // the whole team
     float v[TM::I][8];
+    if constexpr (kRing) ring.wait();
 #pragma unroll
-    for (int i = 0; i < TM::I; ++i) at.clean(nx[i], i, n, v[i]);
+    for (int i = 0; i < TM::I; ++i) {
+      if constexpr (kRing) ring.take(0, i, nx[i]);
+      at.clean(nx[i], i, n, v[i]);
+    }
     if constexpr (DROP) {
       float res[TM::I][8];
       if (rp) {
 #pragma unroll
-        for (int i = 0; i < TM::I; ++i) at.clean(nr[i], i, n, res[i]);
+        for (int i = 0; i < TM::I; ++i) {
+          if constexpr (kRing) ring.take(1, i, nr[i]);
+          at.clean(nr[i], i, n, res[i]);
+        }
       }
-      if (row + tn.step < a.rows) fetch(row + tn.step);
+      if (!kRing && row + tn.step < a.rows) fetch(row + tn.step);
 #pragma unroll
       for (int i = 0; i < TM::I; ++i) {
         bool keep[8];
@@ -371,36 +563,63 @@ __global__ void __launch_bounds__(TM::kMaxThreads, TM::kWhole ? 1 : 4) norm_fwd_
         if (live) at.store(static_cast<T*>(a.s) + row * a.lds, i, n, v[i]);
       }
     } else {
-      if (row + tn.step < a.rows) fetch(row + tn.step);
+      if (!kRing && row + tn.step < a.rows) fetch(row + tn.step);
     }
-    float sum[1] = {0.f};
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < TM::I; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[0] += v[i][j];
-    if constexpr (LY == kAligned) params();
-    team_sum<TM>(sum, slot, 0, at.team);
-    const float mean = sum[0] * inv_n;
-    sum[0] = 0.f;
-#pragma unroll
-    for (int i = 0; i < TM::I; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] -= mean;
-      if (at.whole(i, n)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
-      } else if (LY != kAligned) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (at.in(i, j, n)) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
+      for (int j = 0; j < 8; ++j) sum += v[i][j];
+    if constexpr (LY == kAligned && !kRing) params();
+    float mean, var;
+    if constexpr (TM::kWhole) {
+      // Each warp takes its own mean and the squares of what is left; these are put together behind
+      // one barrier: sum of squares = sum over warps of (its own + its columns (its mean - mean)^2).
+      warp_sum(sum);
+      if constexpr (kRing) {  // the warp has read this row
+        fetch_ring(row + Rg::kDepth * tn.step, ring.at);
+        ring.next();
       }
+      const float own = sum * own_inv;
+      float sq = 0.f;
+      spread(v, own, sq);
+      warp_sum(sq);
+      const int w = threadIdx.x / 32, side = turn & 1;
+      if (at.lane == 0) {
+        slot.v[side][0][w] = sum;
+        slot.v[side][1][w] = sq;
+      }
+      __syncthreads();
+      const float their = slot.v[side][0][at.lane % kMaxWarps];
+      mean = their;
+      half_warp_sum(mean);
+      mean *= inv_n;
+      const float off = their * other_inv - mean;
+      var = fmaf(other_n * off, off, slot.v[side][1][at.lane % kMaxWarps]);
+      half_warp_sum(var);
+      var *= inv_n;
+#pragma unroll
+      for (int i = 0; i < TM::I; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += own - mean;
+    } else {
+      float one[1] = {sum};
+      team_sum<TM>(one, slot, 0, at.team);
+      mean = one[0] * inv_n;
+      one[0] = 0.f;
+      spread(v, mean, one[0]);
+      team_sum<TM>(one, slot, 1, at.team);
+      var = one[0] * inv_n;
     }
-    team_sum<TM>(sum, slot, 1, at.team);
-    const float rstd = rsqrtf(sum[0] * inv_n + a.eps);
+    const float rstd = rsqrtf(var + a.eps);
     if (!live) continue;
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
+      if constexpr (kRing) {
+        ring.get_param(0, i, w[i]);
+        ring.get_param(1, i, b[i]);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, w[i][j], b[i][j]);
       at.store(y, i, n, v[i]);
@@ -410,14 +629,21 @@ __global__ void __launch_bounds__(TM::kMaxThreads, TM::kWhole ? 1 : 4) norm_fwd_
 }
 
 template <typename T, typename TM, Layout LY, bool DROP>
-__global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TM::kMaxThreads, bwd_ctas<T, TM, LY, DROP>())
+    norm_bwd_kernel(const NormArgs a) {
   __shared__ Slots<2> slot;
   __shared__ float part[TM::kTeams > 1 ? 2 : 1][TM::kTeams > 1 ? kThreads / 32 : 1][256];
   __shared__ int shifts[TM::kTeams];
-  __shared__ __align__(16) float bufs[LY == kShifted ? kMaxWarps : 1][256];
+  extern __shared__ uint4 smem[];
+  using Rg = Ring<T, TM, LY, DROP ? 3 : 2>;
+  constexpr bool kRing = bwd_ring<T, TM, LY, DROP>();
+  constexpr int kBufs = !kRing && (LY == kShifted || (TM::kWhole && LY != kScalar)) ? TM::kMaxThreads / 32 : 1;
+  __shared__ __align__(16) float bufs[kBufs][256];
   grid_dep_launch_dependents();
   clear_slots<TM>(slot);
-  float* const buf = bufs[LY == kShifted ? threadIdx.x / 32 : 0];
+  float* const buf = kRing ? reinterpret_cast<float*>(smem) + threadIdx.x / 32 * 256
+                           : bufs[kBufs > 1 ? threadIdx.x / 32 : 0];
+  Rg ring(smem);
   Lane<TM, LY> at;
   const int n = a.n;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -438,6 +664,14 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
     }
     nst = a.stats[row];
   };
+  auto fetch_ring = [&](long long row, int place) {
+    if (row < a.rows) {
+      ring.fetch(at, place, 0, xp, a.ldx, row, a.rows, n);
+      ring.fetch(at, place, 1, gp, a.lddy, row, a.rows, n);
+      if (DROP && sp) ring.fetch(at, place, DROP ? 2 : 0, sp, a.ldds, row, a.rows, n);
+    }
+    cp_async_commit();
+  };
   // As in the forward pass; with dropout, keeping w in registers was the faster (262144 x 256 bf16:
   // 128 us, and 155 us with w read again).
   constexpr bool kReload = LY == kAligned && !DROP;
@@ -445,11 +679,19 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
   at.set_row(xp + (tn.first < a.rows ? tn.first : 0) * a.ldx);
 #pragma unroll
   for (int i = 0; i < TM::I; ++i) {
-    if constexpr (!kReload) at.params(a.w, i, n, buf, w[i]);
+    if constexpr (kRing || !kReload) at.params(a.w, i, n, buf, w[i]);
+    if constexpr (kRing) ring.put_param(0, i, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
   }
-  if (tn.first < a.rows) fetch(tn.first);
+  if constexpr (kRing) {
+    __syncthreads();
+    ring.clear(at, n);
+    for (int i = 0; i < Rg::kDepth; ++i) fetch_ring(tn.first + i * tn.step, i);
+    if (tn.first < a.rows) nst = a.stats[tn.first];
+  } else {
+    if (tn.first < a.rows) fetch(tn.first);
+  }
   for (int turn = 0; turn < tn.count; ++turn) {
     const long long row = tn.first + turn * tn.step;
     const bool live = row < a.rows;
@@ -457,14 +699,25 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
     const float2 st = nst;
     float hat[TM::I][8], g[TM::I][8], ds[TM::I][8];
     float sum[2] = {0.f, 0.f};
+    if constexpr (kRing) ring.wait();
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
-      if constexpr (kReload) at.params(a.w, i, n, buf, w[i]);
+      if constexpr (kRing) {
+        ring.get_param(0, i, w[i]);
+        ring.take(0, i, nx[i]);
+        ring.take(1, i, ng[i]);
+      } else if constexpr (kReload) {
+        at.params(a.w, i, n, buf, w[i]);
+      }
       at.clean(nx[i], i, n, hat[i]);
       at.clean(ng[i], i, n, g[i]);
-      if (DROP && sp) at.clean(ns[i], i, n, ds[i]);
+      if (!kRing && DROP && sp) at.clean(ns[i], i, n, ds[i]);
     }
-    if (row + tn.step < a.rows) fetch(row + tn.step);
+    if constexpr (kRing) {
+      if (row + tn.step < a.rows) nst = a.stats[row + tn.step];
+    } else {
+      if (row + tn.step < a.rows) fetch(row + tn.step);
+    }
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
 #pragma unroll
@@ -481,6 +734,15 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
     }
     team_sum<TM>(sum, slot, turn & 1, at.team);
     const float c1 = sum[0] * inv_n, c2 = sum[1] * inv_n;
+    if constexpr (kRing) {  // this row has been read, the stream's gradient apart
+      if (DROP && sp) {
+#pragma unroll
+        for (int i = 0; i < TM::I; ++i) {
+          ring.take(DROP ? 2 : 0, i, ns[i]);
+          at.clean(ns[i], i, n, ds[i]);
+        }
+      }
+    }
     if constexpr (DROP) {
 #pragma unroll
       for (int i = 0; i < TM::I; ++i) {
@@ -504,7 +766,12 @@ __global__ void __launch_bounds__(TM::kMaxThreads) norm_bwd_kernel(const NormArg
         if (live) at.store(static_cast<T*>(a.dx) + row * a.lddx, i, n, g[i]);
       }
     }
+    if constexpr (kRing) {
+      fetch_ring(row + Rg::kDepth * tn.step, ring.at);
+      ring.next();
+    }
   }
+  if constexpr (kRing) __syncthreads();  // before the ring's memory serves the sums
   // The CTA's sums over its teams, in team order.
   float* pw = a.pw + static_cast<size_t>(blockIdx.x) * n;
   float* pb = a.pb + static_cast<size_t>(blockIdx.x) * n;
@@ -737,15 +1004,40 @@ cudaError_t by_width(int n, Layout ly, F&& f) {
 // Widest row: in two pieces of 16 warps.
 bool long_row(int n, Layout ly) { return n + (ly == kShifted ? 7 : 0) > kLongCols; }
 
-// CTAs of the backward pass, which is also the number of partial sums: as many as are resident (two
-// of 256 threads an SM with dropout, else three; 262144 x 256: fp32 125 us with three an SM, 134 and
+// CTAs of the backward pass, which is also the number of partial sums: as many as are resident (whole
+// CTAs 512 threads an SM; of 256 threads two with dropout, else three; 262144 x 256: fp32 125 us with three an SM, 134 and
 // 136 us with two and four; bf16 with dropout 128 us with two, 132 and 155 us with four and three).
 // Multiples of eight, where a team takes several rows.
 constexpr int kLongParts = 64;
-int most_ctas(int n, bool drop) { return 152 * (drop && n <= 256 ? 2 : 3); }
+int most_ctas(int n, int threads, bool drop) {
+  return 152 * (threads != kThreads || n > 1024 ? 512 / threads : drop && n <= 256 ? 2 : 3);
+}
 int ctas_for(int rows, int teams, int most) {
   const int need = (rows + teams - 1) / teams;
   return need < most ? need : most;
+}
+
+template <typename F>
+cudaError_t by_layout(Layout ly, F&& f) {
+  if (ly == kAligned) return f(std::integral_constant<Layout, kAligned>{});
+  if (ly == kShifted) return f(std::integral_constant<Layout, kShifted>{});
+  return f(std::integral_constant<Layout, kScalar>{});
+}
+
+// Shared memory of a ring of NT tensors and `params` parameters (at most 224 KB: 8192 columns, fp32,
+// backward with dropout).
+template <bool RING, typename T, typename TM, Layout LY, int NT>
+cudaError_t launch_rows(void (*kern)(const NormArgs), LaunchCfg c, const NormArgs& a, int params) {
+  if constexpr (RING) {
+    using Rg = Ring<T, TM, LY, NT>;
+    c.smem = 16 * static_cast<size_t>(c.block.x) * (Rg::kDepth * Rg::kRow + params * Rg::kParam);
+    if (c.smem > 40 * 1024) {  // 48 KB, with what the kernel declares, need no leave
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(c.smem));
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch(c, kern, a);
 }
 
 template <typename T, bool DROP>
@@ -761,10 +1053,18 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
   return by_width(a.n, ly, [&](auto tm, int threads) {
     using TM = decltype(tm);
     c.block = dim3(threads);
-    c.grid = dim3(ctas_for(a.rows, TM::kTeams, ly == kAligned ? 152 * 8 : 152 * 3));
-    if (ly == kAligned) return launch(c, norm_fwd_kernel<T, TM, kAligned, DROP>, a);
-    if (ly == kShifted) return launch(c, norm_fwd_kernel<T, TM, kShifted, DROP>, a);
-    return launch(c, norm_fwd_kernel<T, TM, kScalar, DROP>, a);
+    return by_layout(ly, [&](auto layout) {
+      constexpr Layout LY = decltype(layout)::value;
+      constexpr bool ring = fwd_ring<T, TM, LY, DROP>();
+      // As many as are resident where a CTA's first row waits for its parameters (unaligned rows),
+      // or for a ring; aligned rows twice that, so that the last ones are evened out.
+      const int most = ring             ? (DROP ? 512 : 1024) / threads
+                       : LY == kAligned ? 8
+                       : TM::kWhole     ? 3
+                                        : fwd_ctas<T, TM, LY, DROP>();
+      c.grid = dim3(ctas_for(a.rows, TM::kTeams, 152 * most));
+      return launch_rows<ring, T, TM, LY, DROP ? 2 : 1>(norm_fwd_kernel<T, TM, LY, DROP>, c, a, 2);
+    });
   });
 }
 
@@ -790,12 +1090,14 @@ cudaError_t bwd(NormArgs a, float* dw, float* db, float* ws, cudaStream_t s) {
   } else {
     e = by_width(a.n, ly, [&](auto tm, int threads) {
       using TM = decltype(tm);
-      parts(ctas_for(a.rows, TM::kTeams, most_ctas(a.n, DROP)));
+      parts(ctas_for(a.rows, TM::kTeams, most_ctas(a.n, threads, DROP)));
       c.block = dim3(threads);
       c.grid = dim3(G);
-      if (ly == kAligned) return launch(c, norm_bwd_kernel<T, TM, kAligned, DROP>, a);
-      if (ly == kShifted) return launch(c, norm_bwd_kernel<T, TM, kShifted, DROP>, a);
-      return launch(c, norm_bwd_kernel<T, TM, kScalar, DROP>, a);
+      return by_layout(ly, [&](auto layout) {
+        constexpr Layout LY = decltype(layout)::value;
+        return launch_rows<bwd_ring<T, TM, LY, DROP>(), T, TM, LY, DROP ? 3 : 2>(
+            norm_bwd_kernel<T, TM, LY, DROP>, c, a, 1);
+      });
     });
   }
   if (e != cudaSuccess || G == 1) return e;
@@ -819,9 +1121,9 @@ cudaError_t drop(const NormArgs& a, cudaStream_t s) {
       const long long need = (tiles + TM::kTeams - 1) / TM::kTeams;
       c.block = dim3(threads);
       c.grid = dim3(static_cast<unsigned>(need < 152 * 8 ? need : 152 * 8));
-      if (ly == kAligned) return launch(c, dropout_kernel<T, TM, kAligned>, a);
-      if (ly == kShifted) return launch(c, dropout_kernel<T, TM, kShifted>, a);
-      return launch(c, dropout_kernel<T, TM, kScalar>, a);
+      return by_layout(ly, [&](auto layout) {
+        return launch(c, dropout_kernel<T, TM, decltype(layout)::value>, a);
+      });
     }
   });
 }
@@ -853,8 +1155,8 @@ size_t norm_ws_floats(int rows, int n) {
   for (const Layout ly : {kAligned, kShifted}) {
     int G = rows < kLongParts ? rows : kLongParts;
     if (!long_row(n, ly))
-      (void)by_width(n, ly, [&](auto tm, int) {
-        G = ctas_for(rows, decltype(tm)::kTeams, most_ctas(n, false));
+      (void)by_width(n, ly, [&](auto tm, int threads) {
+        G = ctas_for(rows, decltype(tm)::kTeams, most_ctas(n, threads, false));
         return cudaSuccess;
       });
     if (G > most) most = G;

@@ -45,6 +45,18 @@ struct Raw8<float> {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = v[j];
   }
+  // To and from shared memory, in pieces of 16 bytes `stride` of them apart.
+  __device__ __forceinline__ void put(uint4* p, int stride) const {
+    float4* const to = reinterpret_cast<float4*>(p);
+    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+    to[stride] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void pick(const uint4* p, int stride) {
+    const float4* const from = reinterpret_cast<const float4*>(p);
+    const float4 lo = from[0], hi = from[stride];
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  }
 };
 template <>
 struct Raw8<__nv_bfloat16> {
@@ -65,6 +77,11 @@ struct Raw8<__nv_bfloat16> {
       f[2 * i + 1] = bf16_hi_f32(w[i]);
     }
   }
+  __device__ __forceinline__ void put(uint4* p, int) const { *p = make_uint4(w[0], w[1], w[2], w[3]); }
+  __device__ __forceinline__ void pick(const uint4* p, int) {
+    const uint4 r = *p;
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+  }
 };
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]),
@@ -78,6 +95,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   r.z = bf16x2_rn(v[4], v[5]);
   r.w = bf16x2_rn(v[6], v[7]);
   *reinterpret_cast<uint4*>(p) = r;
+}
+
+// Sixteen bytes to shared memory, in the background.
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
 }
 
 // 2^v, a few ulp, 0 for v below the normal range.

@@ -248,6 +248,39 @@ def test_dropout_layernorm(rows, n, with_res, with_ds, dtype):
     check(out["db"], db, SUM, "db")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n", [(6200, 1030), (6200, 1040), (1900, 5001), (1900, 4104)])
+def test_wide_rows_in_many_turns(rows, n, dtype):
+    """Whole-CTA rows, several to a CTA (four and more in every kernel), aligned and not, so that
+    the places where rows wait are used again.  The parameters' sums of N rows: N terms of random
+    sign leave about sqrt(N) 2^-24 sum|t| / max|sum| < 1e-5."""
+    from recurrent_cfc_cell_gb300 import trunk
+
+    p = 0.2
+    i = norm_inputs(rows, n, dtype, rows + n)
+    x, w, b = cuda(i["x"], dtype), cuda(i["w"]), cuda(i["b"])
+    dy = cuda(i["dy"], dtype)
+    st = trunk.LayerNormStep(rows, n, act(dtype)).bind(x, w, b, dy)
+    st.run()
+    out = st.outputs()
+    check(out["y"], ot.layernorm(i["x"], i["w"], i["b"], 1e-5), EL, "y")
+    for name, want in zip(("dx", "dw", "db"), ot.layernorm_backward(i["dy"], i["x"], i["w"], 1e-5)):
+        check(out[name], want, SUM, name)
+    st = trunk.DropoutNormStep(rows, n, p, act(dtype)).bind(
+        x, cuda(i["residual"], dtype), rng_tensor(SEED, OFFSET), w, b, dy, cuda(i["ds"], dtype))
+    st.run()
+    out = st.outputs()
+    keep, scale = ot.dropout_mask(rows, n, p, SEED, OFFSET)
+    check(out["s"], i["residual"] + keep * i["x"] * scale, EL, "s")
+    s = out["s"].double().cpu().numpy()
+    check(out["y"], ot.layernorm(s, i["w"], i["b"], 1e-5), EL, "y")
+    d, dw, db = ot.layernorm_backward(i["dy"], s, i["w"], 1e-5)
+    check(out["dres"], d + i["ds"], SUM, "dres")
+    check(out["dx"], keep * (d + i["ds"]) * scale, SUM, "dx")
+    check(out["dw"], dw, SUM, "dw")
+    check(out["db"], db, SUM, "db")
+
+
 def test_dropout_offset_advances_in_a_graph():
     """The generator's state is read when the kernel runs: a replayed graph draws a new mask once
     the caller has moved the offset."""
