@@ -12,10 +12,11 @@
 //
 // Bound by memory: x is read and u written once (backward: x and du read, dx written), up to
 // W - 1 steps read again where two runs of steps meet.  A thread holds neighbouring channels
-// (8 bytes of them; with 16 the backward pass's windows and sums would not fit in registers) and walks a run of steps with the last W inputs in registers; runs are short where
-// there are few channels and sequences, so that the GPU is full, and long otherwise.  The
-// parameter gradients are summed in registers over the run, over the CTA's eight runs in
-// shared memory and over the CTAs by reduce_axis0.
+// (8 bytes of them; with 16 the backward pass's windows and sums would not fit in registers) and
+// walks a run of steps with the last W inputs in registers; runs are short where there are few
+// channels and sequences, so that the GPU is full, and long otherwise.  The parameter gradients are
+// summed in registers over the run, over the CTA's eight runs in shared memory and over the CTAs by
+// reduce_axis0.
 //
 // Measured on GB300: 64 sequences of up to 1023 steps, 1536 channels, bf16, 4 taps, lengths spread
 // evenly over 0 .. 1023: forward 66 us (4.6 TB/s of what is read and written), backward 121 us

@@ -26,7 +26,7 @@
 // Measured on GB300, 16 states: 64 x 512 steps x 1024 channels, bf16, keeping states, 204 us (2.6e12
 // state steps a second, a quarter of the exponential unit's rate; 130 instructions for 512 of them
 // and what their 32 channels need, issued at 0.6 a clock and scheduler: 13 warps an SM is all there
-// are).  Prompts 2 x 8191 x 1024: 125 us, of which the first pass over the split steps 45.  Tried:
+// are).  Prompts 2 x 8191 x 1024: 135 us, of which the first pass over the split steps 45.  Tried:
 // states spread over more lanes (four each, 279 us), one warp for sixteen states (302 us), chunks of
 // eight steps (242 us), more CTAs an SM at fewer registers (273 us with five).
 #include "cfc_launch.cuh"
@@ -368,7 +368,10 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(const ScanCall q, int sp
 // One token: a lane holds four states of a channel, LPC lanes a channel, for kSeqs sequences, so
 // that A is read once for them.  What a sequence needs per channel (d and d x, later the gate) is
 // formed by one lane of the channel and handed round.  The state may be the new state's own
-// memory: a thread reads what it writes before it writes it.
+// memory: a thread reads what it writes before it writes it.  1024 x 2048 x 64 states 198 us (5.5
+// TB/s).  Tried: the state as what L2 evicts first (203 us among other passes, 81 against 79 us at 16
+// states with the convolution's token, 60 against 63 us at a quarter of the sequences), four CTAs an
+// SM (215 us, spilling).
 constexpr int kSeqs = 4;
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
