@@ -31,9 +31,9 @@
 // Measured on GB300 (copy rate 6.69 TB/s): 262144 x 256 fp32 forward 84 us (6.4 TB/s), backward 125 us
 // (6.4 TB/s); the same rows in bf16 with dropout and residual 99 us (5.4 TB/s; a row's generator calls
 // are a third of its instructions) and 128 us (5.2 TB/s); 10529 x 3528 fp32 56 and 88 us (5.3 and
-// 5.0 TB/s), bf16 33 and 54 us (4.5 and 4.1 TB/s: a CTA's row is a chain of loads, sums, a barrier
-// and stores, and few rows are in flight on an SM); 6007 x 2501 bf16, rows of every alignment, 21 and
-// 32 us (2.9 and 2.8 TB/s: besides, the rows' ends are taken element by element).
+// 5.0 TB/s), bf16 31 and 53 us (4.8 and 4.2 TB/s: a CTA's row is a chain of loads, sums, a barrier
+// and stores, and few rows are in flight on an SM); 6007 x 2501 bf16, rows of every alignment, 20 and
+// 32 us (3.0 and 2.8 TB/s: besides, the rows' ends are taken element by element).
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
@@ -409,6 +409,12 @@ __host__ __device__ constexpr int bwd_ctas() {
   return LY != kShifted && !bwd_ring<T, TM, LY, DROP>() ? 0 : 512 / TM::kMaxThreads;
 }
 
+// Arithmetic goes in pairs of columns, one instruction for two (6007 x 2501 bf16 50.5 us, 51.6 us one
+// by one; 28467 x 319 bf16 58 and 61 us).
+__device__ __forceinline__ float2 pair(const float (&v)[8], int j) { return make_float2(v[2 * j], v[2 * j + 1]); }
+__device__ __forceinline__ void set_pair(float (&v)[8], int j, float2 p) { v[2 * j] = p.x; v[2 * j + 1] = p.y; }
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+
 struct NormArgs {
   const void *x, *residual, *dy, *ds;
   long long ldx, ldr, lddy, ldds;
@@ -500,10 +506,12 @@ __global__ void __launch_bounds__(TM::kMaxThreads, fwd_ctas<T, TM, LY, DROP>())
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] -= from;
+      for (int j = 0; j < 4; ++j) set_pair(v[i], j, __fadd2_rn(pair(v[i], j), twice(-from)));
       if (at.whole(i, n)) {
+        float2 two = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = fmaf(v[i][j], v[i][j], sq);
+        for (int j = 0; j < 4; ++j) two = fma2(pair(v[i], j), pair(v[i], j), two);
+        sq += two.x + two.y;
       } else if (LY != kAligned) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -565,13 +573,14 @@ __global__ void __launch_bounds__(TM::kMaxThreads, fwd_ctas<T, TM, LY, DROP>())
     } else {
       if (!kRing && row + tn.step < a.rows) fetch(row + tn.step);
     }
-    float sum = 0.f;
+    float2 two = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < TM::I; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += v[i][j];
+      for (int j = 0; j < 4; ++j) two = __fadd2_rn(two, pair(v[i], j));
+    float sum = two.x + two.y;
     if constexpr (LY == kAligned && !kRing) params();
-    float mean, var;
+    float mean, var, left = 0.f;  // left: what is still to be added to v
     if constexpr (TM::kWhole) {
       // Each warp takes its own mean and the squares of what is left; these are put together behind
       // one barrier: sum of squares = sum over warps of (its own + its columns (its mean - mean)^2).
@@ -598,10 +607,7 @@ __global__ void __launch_bounds__(TM::kMaxThreads, fwd_ctas<T, TM, LY, DROP>())
       var = fmaf(other_n * off, off, slot.v[side][1][at.lane % kMaxWarps]);
       half_warp_sum(var);
       var *= inv_n;
-#pragma unroll
-      for (int i = 0; i < TM::I; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += own - mean;
+      left = own - mean;
     } else {
       float one[1] = {sum};
       team_sum<TM>(one, slot, 0, at.team);
@@ -621,7 +627,11 @@ __global__ void __launch_bounds__(TM::kMaxThreads, fwd_ctas<T, TM, LY, DROP>())
         ring.get_param(1, i, b[i]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, w[i][j], b[i][j]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 hat = TM::kWhole ? fma2(pair(v[i], j), twice(rstd), twice(left * rstd))
+                                      : __fmul2_rn(pair(v[i], j), twice(rstd));
+        set_pair(v[i], j, fma2(hat, pair(w[i], j), pair(b[i], j)));
+      }
       at.store(y, i, n, v[i]);
     }
     if (at.base == 0 && at.lane == 0) a.stats[row] = make_float2(mean, rstd);
@@ -698,7 +708,8 @@ __global__ void __launch_bounds__(TM::kMaxThreads, bwd_ctas<T, TM, LY, DROP>())
     if (TM::WPR > 0 && !live) break;  // the whole team
     const float2 st = nst;
     float hat[TM::I][8], g[TM::I][8], ds[TM::I][8];
-    float sum[2] = {0.f, 0.f};
+    float sum[2];
+    float2 two[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     if constexpr (kRing) ring.wait();
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
@@ -721,19 +732,28 @@ __global__ void __launch_bounds__(TM::kMaxThreads, bwd_ctas<T, TM, LY, DROP>())
 #pragma unroll
     for (int i = 0; i < TM::I; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         // Outside the row dy is zero, and so is all that it enters.
-        const float d = live ? g[i][j] : 0.f;
-        hat[i][j] = (hat[i][j] - st.x) * st.y;
-        if (live) dw[i][j] = fmaf(d, hat[i][j], dw[i][j]);
-        db[i][j] += d;
-        g[i][j] = d * w[i][j];
-        sum[0] += g[i][j];
-        sum[1] = fmaf(g[i][j], hat[i][j], sum[1]);
+        const float2 d = live ? pair(g[i], j) : make_float2(0.f, 0.f);
+        const float2 ht = __fmul2_rn(__fadd2_rn(pair(hat[i], j), twice(-st.x)), twice(st.y));
+        if (live) set_pair(dw[i], j, fma2(d, ht, pair(dw[i], j)));
+        set_pair(db[i], j, __fadd2_rn(pair(db[i], j), d));
+        const float2 gw = __fmul2_rn(d, pair(w[i], j));
+        set_pair(hat[i], j, ht);
+        set_pair(g[i], j, gw);
+        two[0] = __fadd2_rn(two[0], gw);
+        two[1] = fma2(gw, ht, two[1]);
       }
     }
+    sum[0] = two[0].x + two[0].y;
+    sum[1] = two[1].x + two[1].y;
     team_sum<TM>(sum, slot, turn & 1, at.team);
     const float c1 = sum[0] * inv_n, c2 = sum[1] * inv_n;
+    // st.y (g - c1 - hat c2)
+    auto grad = [&](int i, int j) {
+      const float2 left = fma2(pair(hat[i], j), twice(-c2), __fadd2_rn(pair(g[i], j), twice(-c1)));
+      return __fmul2_rn(left, twice(st.y));
+    };
     if constexpr (kRing) {  // this row has been read, the stream's gradient apart
       if (DROP && sp) {
 #pragma unroll
@@ -749,9 +769,13 @@ __global__ void __launch_bounds__(TM::kMaxThreads, bwd_ctas<T, TM, LY, DROP>())
         bool keep[8];
         at.keep(key, static_cast<uint32_t>(row), i, a.cut, keep);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          g[i][j] = st.y * (g[i][j] - c1 - hat[i][j] * c2) + (sp ? ds[i][j] : 0.f);
-          hat[i][j] = keep[j] ? g[i][j] * a.scale : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          float2 d = grad(i, j);
+          if (sp) d = __fadd2_rn(d, pair(ds[i], j));
+          set_pair(g[i], j, d);
+          d = __fmul2_rn(d, twice(a.scale));
+          hat[i][2 * j] = keep[2 * j] ? d.x : 0.f;
+          hat[i][2 * j + 1] = keep[2 * j + 1] ? d.y : 0.f;
         }
         if (live) {
           if (a.dres) at.store(static_cast<T*>(a.dres) + row * a.lddr, i, n, g[i]);
@@ -762,7 +786,7 @@ __global__ void __launch_bounds__(TM::kMaxThreads, bwd_ctas<T, TM, LY, DROP>())
 #pragma unroll
       for (int i = 0; i < TM::I; ++i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] = st.y * (g[i][j] - c1 - hat[i][j] * c2);
+        for (int j = 0; j < 4; ++j) set_pair(g[i], j, grad(i, j));
         if (live) at.store(static_cast<T*>(a.dx) + row * a.lddx, i, n, g[i]);
       }
     }
