@@ -29,8 +29,8 @@
 // passes draw it again from the counter-based generator, whose counter is the element's place.
 //
 // Measured on GB300 (copy rate 6.69 TB/s): 262144 x 256 fp32 forward 84 us (6.4 TB/s), backward 125 us
-// (6.4 TB/s); the same rows in bf16 with dropout and residual 99 us (5.4 TB/s; a row's generator calls
-// are a third of its instructions) and 128 us (5.2 TB/s); 10529 x 3528 fp32 56 and 88 us (5.3 and
+// (6.4 TB/s); the same rows in bf16 with dropout and residual 98 us (5.5 TB/s; a row's generator calls
+// are a third of its instructions) and 127 us (5.3 TB/s); 10529 x 3528 fp32 56 and 88 us (5.3 and
 // 5.0 TB/s), bf16 31 and 53 us (4.8 and 4.2 TB/s: a CTA's row is a chain of loads, sums, a barrier
 // and stores, and few rows are in flight on an SM); 6007 x 2501 bf16, rows of every alignment, 20 and
 // 32 us (3.0 and 2.8 TB/s: besides, the rows' ends are taken element by element).
