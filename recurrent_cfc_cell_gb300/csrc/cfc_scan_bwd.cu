@@ -354,11 +354,8 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
             float2 B0[2];
             bc(sB, j, B0);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const float2 m = __fmul2_rn(make_float2(dv[j], dv[j]), A2[p]);
-              h[p] = fma2(make_float2(exp2_f(m.x), exp2_f(m.y)), h[p],
-                          __fmul2_rn(make_float2(u, u), B0[p]));
-            }
+            for (int p = 0; p < 2; ++p)
+              h[p] = fma2(decay2_f(dv[j], A2[p]), h[p], __fmul2_rn(make_float2(u, u), B0[p]));
           }
         }
         const int at = half_at(cl, half);
@@ -374,15 +371,14 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
         float y[4], v[4], w[4];
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
-          const float2 d2 = make_float2(dv[j], dv[j]), u2 = make_float2(uv[j], uv[j]);
+          const float2 u2 = make_float2(uv[j], uv[j]);
           const float2 r2 = make_float2(rv[j], rv[j]);
           float2 y2, Bv[2], Cv[2];
           bc(sB, half * kHalf + j, Bv);
           bc(sC, half * kHalf + j, Cv);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const float2 m = __fmul2_rn(d2, A2[p]);
-            a[j][p] = make_float2(exp2_f(m.x), exp2_f(m.y));
+            a[j][p] = decay2_f(dv[j], A2[p]);
             qq[j][p] = __fmul2_rn(a[j][p], h[p]);
             h[p] = fma2(u2, Bv[p], qq[j][p]);
             y2 = p ? fma2(h[p], Cv[p], y2) : __fmul2_rn(h[p], Cv[p]);

@@ -249,10 +249,7 @@ __global__ void __launch_bounds__(32 * CW * NT, CW * NT <= 4 ? 4 : 1) scan_fwd_k
         const float2 du = sDU[MODE == 2 ? kT - 1 - kb - j : kb + j][ch];
         u2[j] = make_float2(du.y, du.y);
 #pragma unroll
-        for (int s = 0; s < S / 2; ++s) {
-          const float2 e = __fmul2_rn(make_float2(du.x, du.x), A2[s]);
-          a[j][s] = make_float2(exp2_f(e.x), exp2_f(e.y));
-        }
+        for (int s = 0; s < S / 2; ++s) a[j][s] = decay2_f(du.x, A2[s]);
       }
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
@@ -360,7 +357,7 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(const ScanCall q, int sp
       const int i = i0 + j, s = reverse ? splits - 1 - i : i;
       if (i >= splits) break;
       carry[s * plane + e] = h;
-      h = fmaf(exp2_f(A2 * a[j]), h, own[j]);
+      h = fmaf(decay_f(a[j], A2), h, own[j]);
     }
   }
 }
@@ -446,7 +443,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q, const 
       yv[k] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        h[k][i] = fmaf(exp2_f(dv * A2[i]), h[k][i], uv * Bv[k][i]);
+        h[k][i] = fmaf(decay_f(dv, A2[i]), h[k][i], uv * Bv[k][i]);
         yv[k] = fmaf(h[k][i], Cv[k][i], yv[k]);
       }
       if (live && in && k <= last) {

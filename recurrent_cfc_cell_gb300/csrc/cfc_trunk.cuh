@@ -111,6 +111,19 @@ __device__ __forceinline__ float exp2_f(float v) {
   return r;
 }
 
+// 2^(d A2), the factor by which a state goes on; 1 where d is 0.  The hardware's 2^v is too small on
+// average, by 2e-8 for v in (-1, -0.003) and 6e-9 nearer to 0, and a recurrence adds that up over all
+// the steps that a state remembers.  What is added to the exponent, in the product's own multiply-add,
+// takes most of that back (1e-8 either way is left, 1.6e-8 at most).  64 x 512 steps x 1024 channels x
+// 16 states, errors against 64 bits (2-norm): dA 1.6e-6 without and 8.2e-7 with it, dh0 1.8e-6 and
+// 9.1e-7, in the same time (step by step with expf they are 8e-7 and 1.4e-6).  2^2e-8 rounds to 1.
+constexpr float kDecayBias = 2e-8f;
+__device__ __forceinline__ float decay_f(float d, float A2) { return exp2_f(fmaf(d, A2, kDecayBias)); }
+__device__ __forceinline__ float2 decay2_f(float d, float2 A2) {
+  const float2 m = fma2(make_float2(d, d), A2, make_float2(kDecayBias, kDecayBias));
+  return make_float2(exp2_f(m.x), exp2_f(m.y));
+}
+
 // 1 / v, one ulp, and the logistic function from it.  The flush-to-zero forms of the hardware's
 // exponential and reciprocal: their subnormal results and arguments (here below 2^-126 of 1)
 // would take three more instructions each.
