@@ -43,7 +43,9 @@ def make_params(D: int, E: int, N: int, C: int, W: int = 4, G: int = 1, seed: in
 
 
 class TrunkBlock:
-    """One training step of the block for K steps of B sequences."""
+    """One training step of the block for K steps of B sequences.  Like the steps it is made of, it
+    owns its results: what forward and backward return is valid until they are called again (clone
+    what has to outlive that, such as gradients that are summed over several steps)."""
 
     def __init__(self, K: int, B: int, params: dict, p_drop: float = 0.1, G: int = 1):
         self.K, self.B, self.G, self.params = K, B, G, params
@@ -150,7 +152,7 @@ class TrunkServe:
         return second.y.view(K, B, D)
 
     def token(self, s) -> torch.Tensor:
-        """n' [B, D] of one token s [B, D] per sequence."""
+        """n' [B, D] of one token s [B, D] per sequence, a tensor of its own as the prompt's is."""
         P, E = self.params, self.E
         self.norms[0].bind(s, P["w1"], P["b1"]).run()
         xz = self.norms[0].y @ P["W_in"].T
@@ -159,5 +161,7 @@ class TrunkServe:
         bc = p[:, E:].unflatten(-1, (2, self.G, self.N))
         y, _ = self.scan.bind(u, p[:, :E], P["A"], bc[:, 0], bc[:, 1], self.state, P["D"],
                               P["dt_bias"], xz[:, E:]).run()
-        self.norms[1].bind(s + y @ P["W_out"].T, P["w2"], P["b2"]).run()
-        return self.norms[1].y
+        last = self.norms[1]
+        last.y = torch.empty_like(last.y)  # not the one that the caller has from the token before
+        last.bind(s + y @ P["W_out"].T, P["w2"], P["b2"]).run()
+        return last.y
