@@ -42,7 +42,7 @@ namespace cfc {
 namespace {
 
 constexpr int T8 = kScanPeriod;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kHalf = T8 / 2;
 
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(32 * CW * NT) scan_bwd_kernel(const ScanCall q
   for (int i = tid; i < Sh::kSt; i += Sh::kThreads) {
     const int ch = i / 16 % Sh::CH, n = i / (16 * Sh::CH) * 16 + i % 16;
     const bool in = ch < count && n < q.N;
-    sA[i] = in ? q.A[static_cast<size_t>(d0 + ch) * q.N + n] * kLog2e : 0.f;
+    sA[i] = in ? rate_f(q.A[static_cast<size_t>(d0 + ch) * q.N + n]) : 0.f;
     sm[Sh::oE + i] = in && c_in ? c_in[tile_at + static_cast<size_t>(ch) * q.N + n] : 0.f;
     sm[Sh::oDA + i] = 0.f;
   }

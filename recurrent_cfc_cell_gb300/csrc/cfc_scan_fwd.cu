@@ -37,7 +37,6 @@ namespace cfc {
 namespace {
 
 constexpr int kT = 2 * kScanPeriod;  // steps of a chunk
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct Tile {
   int tiles_per_group, per_group;  // channel tiles and channels of a group of B / C
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(32 * CW * NT, CW * NT <= 4 ? 4 : 1) scan_fwd_k
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     const bool in = live && n0 + i < q.N;
-    const float av = in ? q.A[static_cast<size_t>(d) * q.N + n0 + i] * kLog2e : 0.f;
+    const float av = in ? rate_f(q.A[static_cast<size_t>(d) * q.N + n0 + i]) : 0.f;
     float hv = 0.f;
     if (MODE == 0 && in) {
       if (carry) hv = carry[split * plane + cn + i];
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(const ScanCall q, int sp
   const size_t e = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (e >= plane) return;
   const size_t bd = e / q.N;
-  const float A2 = q.A[(bd % q.D) * q.N + e % q.N] * kLog2e;
+  const float A2 = rate_f(q.A[(bd % q.D) * q.N + e % q.N]);
   const float* start = reverse ? q.dh_last : q.h0;
   float h = start ? start[e] : 0.f;
   // Eight splits at a time: their loads are in flight together.
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanCall q, const 
   const size_t ho = static_cast<size_t>(d) * q.N + n, go = static_cast<size_t>(group) * q.N + n;
   float A2[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] = n + i < q.N ? q.A[ho + i] * kLog2e : 0.f;
+  for (int i = 0; i < 4; ++i) A2[i] = n + i < q.N ? rate_f(q.A[ho + i]) : 0.f;
   const int b_end = min(q.B, (static_cast<int>(blockIdx.y) + 1) * seqs);
   for (int b0 = blockIdx.y * seqs; b0 < b_end; b0 += kSeqs) {
     // Uniform bases of the sequences (the last one again where there are fewer than kSeqs).

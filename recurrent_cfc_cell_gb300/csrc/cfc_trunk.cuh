@@ -111,6 +111,14 @@ __device__ __forceinline__ float exp2_f(float v) {
   return r;
 }
 
+// A log2 e, finite unless A is not a number: a step that does not count has d = 0, and 0 times an
+// infinity would not be 0.  (Rates from 2.4e38 on decay to 0 in any step that counts all the same.)
+__device__ __forceinline__ float rate_f(float A) {
+  constexpr float kMost = 3.402823466e38f;
+  const float v = A * 1.4426950408889634f;
+  return v < -kMost ? -kMost : v > kMost ? kMost : v;
+}
+
 // 2^(d A2), the factor by which a state goes on; 1 where d is 0.  The hardware's 2^v is too small on
 // average, by 2e-8 for v in (-1, -0.003) and 6e-9 nearer to 0, and a recurrence adds that up over all
 // the steps that a state remembers.  What is added to the exponent, in the product's own multiply-add,

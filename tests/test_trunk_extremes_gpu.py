@@ -1,0 +1,52 @@
+"""Inputs at the edge of what fp32 holds."""
+import pytest
+import torch
+
+import trunk_plain64 as p64
+from test_trunk_gpu import EL, SUM
+from trunk_draws import Draw, check, doubles, scan_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from recurrent_cfc_cell_gb300 import build
+
+    build.build()
+
+
+@pytest.mark.parametrize("K,N", [(20, 16), (300, 16), (9, 5)])
+def test_rates_that_forget_at_once(K, N):
+    """Decay rates so large that A log2 e leaves fp32's range, in sequences that end inside a chunk:
+    such a state is what its last step put in."""
+    from recurrent_cfc_cell_gb300 import trunk
+
+    B, D, G = 4, 40, 1
+    i = scan_inputs(K, B, D, N, G, "f32", K)
+    i["A"][::3, 1] = -3e38
+    i["A"][5] = -2.5e38
+    ends = Draw(1).lengths(B, K, K, 5, 0, K - 1)
+    want = p64.scan(doubles(i), ends.long())
+    assert all(torch.isfinite(v).all() for v in want.values())
+    i["D"] = i.pop("skip")
+    st = trunk.ScanStep(K, B, D, N, G, train=True).bind(**i, lengths=ends)
+    st.run()
+    out = st.outputs()
+    for k, v in want.items():
+        check(out[k], v, EL if k in ("y", "h") else SUM, k)
+    # No state at all is left of before where the rate is infinite.
+    i["A"][5] = float("-inf")
+    st.forward()
+    check(st.h, want["h"], EL, "h")
+    check(st.y, want["y"], EL, "y")
+    # Token by token.
+    tok = trunk.ScanToken(B, D, N, G)
+    state = i["h0"].clone()
+    for t in range(4):
+        tok.bind(*(i[k][t] if k != "A" else i[k] for k in ("x", "dt", "A", "Bm", "Cm")), state,
+                 i["D"], i["dt_bias"], i["z"][t]).run()
+    i["skip"] = i.pop("D")
+    i["A"][5] = -3e38
+    first = {k: v[:4] if k in ("x", "dt", "z", "dy", "Bm", "Cm") else v for k, v in doubles(i).items()}
+    check(state, p64.scan(first, torch.full((B,), 4, device="cuda"), backward=False)["h"], EL, "h")
