@@ -1037,8 +1037,8 @@ int most_ctas(int n, int threads, bool drop) {
   return 152 * (threads != kThreads || n > 1024 ? 512 / threads : drop && n <= 256 ? 2 : 3);
 }
 int ctas_for(int rows, int teams, int most) {
-  const int need = (rows + teams - 1) / teams;
-  return need < most ? need : most;
+  const long long need = (static_cast<long long>(rows) + teams - 1) / teams;
+  return need < most ? static_cast<int>(need) : most;
 }
 
 template <typename F>
