@@ -566,6 +566,13 @@ def _entry(f):
     return call
 
 
+def _dims(*sizes):
+    """The sizes, which the C entry points take as ints (a conversion would keep the low bits)."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes {tuple(sizes)} do not fit the entry points' 32-bit integers")
+    return sizes
+
+
 def _act(t, name: str, shape, dtype=None):
     """(pointer, dtype code) of an activation: fp32 or bf16, the last dimension contiguous."""
     import torch
@@ -643,14 +650,14 @@ def _work(ws):
 def layernorm_workspace_bytes(rows: int, n: int) -> int:
     out = ctypes.c_size_t(0)
     _check("cfc_layernorm_workspace_bytes",
-           load().cfc_layernorm_workspace_bytes(rows, n, ctypes.byref(out)))
+           load().cfc_layernorm_workspace_bytes(*_dims(rows, n), ctypes.byref(out)))
     return out.value
 
 
 @_entry
 def cfc_layernorm_forward(x, w, b, y, stats, eps: float = 1e-5):
     """y [rows, n] and stats [rows, 2] (mean, rstd) <- layer norm of x's rows."""
-    rows, n = x.shape
+    rows, n = _dims(*x.shape)
     return ((_act(x, "x", (rows, n)), _ld(x), _par(w, "w", (n,)), _par(b, "b", (n,)), rows, n, eps,
              _code(x), _act(y, "y", (rows, n), x.dtype), _ld(y), _par(stats, "stats", (rows, 2))),
             (x, w, b, y, stats))
@@ -659,7 +666,7 @@ def cfc_layernorm_forward(x, w, b, y, stats, eps: float = 1e-5):
 @_entry
 def cfc_layernorm_backward(dy, x, w, stats, dx, dw, db, ws=None):
     """dx [rows, n], dw [n], db [n] <- gradient of the layer norm."""
-    rows, n = x.shape
+    rows, n = _dims(*x.shape)
     wp, wn = _work(ws)
     return ((_act(dy, "dy", (rows, n), x.dtype), _ld(dy), _act(x, "x", (rows, n)), _ld(x),
              _par(w, "w", (n,)), _par(stats, "stats", (rows, 2)), rows, n, _code(x),
@@ -670,7 +677,7 @@ def cfc_layernorm_backward(dy, x, w, stats, dx, dw, db, ws=None):
 @_entry
 def cfc_dropout_forward(x, residual, rng, p: float, y):
     """y [rows, n] <- residual (or None) + dropout of x, drawn from rng = {seed, offset}."""
-    rows, n = x.shape
+    rows, n = _dims(*x.shape)
     return ((_act(x, "x", (rows, n)), _ld(x), _act(residual, "residual", (rows, n), x.dtype),
              _ld(residual), _rng(rng), p, rows, n, _code(x), _act(y, "y", (rows, n), x.dtype),
              _ld(y)), (x, residual, rng, y))
@@ -679,7 +686,7 @@ def cfc_dropout_forward(x, residual, rng, p: float, y):
 @_entry
 def cfc_dropout_backward(dy, rng, p: float, dx):
     """dx [rows, n] <- dy through the mask of the forward call with the same rng and p."""
-    rows, n = dy.shape
+    rows, n = _dims(*dy.shape)
     return ((_act(dy, "dy", (rows, n)), _ld(dy), _rng(rng), p, rows, n, _code(dy),
              _act(dx, "dx", (rows, n), dy.dtype), _ld(dx)), (dy, rng, dx))
 
@@ -688,7 +695,7 @@ def cfc_dropout_backward(dy, rng, p: float, dx):
 def cfc_dropout_layernorm_forward(x, residual, rng, p: float, w, b, s, y, stats,
                                   eps: float = 1e-5):
     """s <- residual (or None) + dropout of x; y, stats <- layer norm of s."""
-    rows, n = x.shape
+    rows, n = _dims(*x.shape)
     return ((_act(x, "x", (rows, n)), _ld(x), _act(residual, "residual", (rows, n), x.dtype),
              _ld(residual), _rng(rng), p, _par(w, "w", (n,)), _par(b, "b", (n,)), rows, n, eps,
              _code(x), _act(s, "s", (rows, n), x.dtype), _ld(s),
@@ -699,7 +706,7 @@ def cfc_dropout_layernorm_forward(x, residual, rng, p: float, w, b, s, y, stats,
 @_entry
 def cfc_dropout_layernorm_backward(dy, ds, s, rng, p: float, w, stats, dx, dres, dw, db, ws=None):
     """dres (or None) <- ds (or None) + the norm's gradient; dx <- dres through the mask; dw, db."""
-    rows, n = s.shape
+    rows, n = _dims(*s.shape)
     wp, wn = _work(ws)
     return ((_act(dy, "dy", (rows, n), s.dtype), _ld(dy), _act(ds, "ds", (rows, n), s.dtype),
              _ld(ds), _act(s, "s", (rows, n)), _ld(s), _rng(rng), p, _par(w, "w", (n,)),
@@ -712,13 +719,13 @@ def cfc_dropout_layernorm_backward(dy, ds, s, rng, p: float, w, stats, dx, dres,
 def conv_workspace_bytes(B: int, K: int, D: int, W: int, dtype: int) -> int:
     out = ctypes.c_size_t(0)
     _check("cfc_conv_workspace_bytes",
-           load().cfc_conv_workspace_bytes(B, K, D, W, dtype, ctypes.byref(out)))
+           load().cfc_conv_workspace_bytes(*_dims(B, K, D, W), dtype, ctypes.byref(out)))
     return out.value
 
 
 def _conv_args(x, w, bias, x0, lengths, silu):
-    K, B, D = x.shape
-    W = w.shape[1]
+    K, B, D = _dims(*x.shape)
+    W = _dims(w.shape[1])[0]
     return ConvArgs(B, K, D, W, _code(x), int(silu), _lengths(lengths, B), _act(x, "x", (K, B, D)),
                     *_tb(x), _par(w, "w", (D, W)), _par(bias, "bias", (D,)),
                     _con(x0, "x0", (B, W - 1, D), x.dtype))
@@ -751,8 +758,8 @@ def cfc_conv_backward(du, x, w, dx, dw, dbias, bias=None, x0=None, lengths=None,
 @_entry
 def cfc_conv_step(x, w, state, new_state, u, bias=None, silu: bool = True):
     """u [B, D], new_state [B, W-1, D] (may be state) <- one token of the causal convolution."""
-    B, D = x.shape
-    W = w.shape[1]
+    B, D = _dims(*x.shape)
+    W = _dims(w.shape[1])[0]
     return ((_act(x, "x", (B, D)), _ld(x), _par(w, "w", (D, W)), _par(bias, "bias", (D,)),
              _con(state, "state", (B, W - 1, D), x.dtype), B, D, W, _code(x), int(silu),
              _act(u, "u", (B, D), x.dtype), _ld(u),
@@ -761,6 +768,7 @@ def cfc_conv_step(x, w, state, new_state, u, bias=None, silu: bool = True):
 
 
 def _scan_sizes(K, B, D, N, G, dtype):
+    _dims(B, K, D, N, G)
     return ScanArgs(B=B, K=K, D=D, N=N, G=G, dtype=dtype)
 
 
@@ -786,8 +794,8 @@ def _groups(t, name, shape, dtype):
 
 
 def _scan_args(x, dt, A, Bm, Cm, D, dt_bias, z, h0, lengths, softplus):
-    K, B, Dn = x.shape
-    G, N = Bm.shape[-2:]
+    K, B, Dn = _dims(*x.shape)
+    G, N = _dims(*Bm.shape[-2:])
     rows, bc = (K, B, Dn), (K, B, G, N)
     return ScanArgs(B, K, Dn, N, G, _code(x), int(softplus), _lengths(lengths, B),
                     _act(x, "x", rows), _act(dt, "dt", rows, x.dtype), _act(z, "z", rows, x.dtype),
