@@ -613,7 +613,8 @@ def _con(t, name: str, shape, dtype):
 
 
 def _ld(t) -> int:
-    return 0 if t is None else t.stride(0)
+    """Elements from a row to the next (of a single row, whose stride may be anything, its length)."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _tb(t) -> tuple[int, int]:

@@ -50,3 +50,33 @@ def test_rates_that_forget_at_once(K, N):
     i["A"][5] = -3e38
     first = {k: v[:4] if k in ("x", "dt", "z", "dy", "Bm", "Cm") else v for k, v in doubles(i).items()}
     check(state, p64.scan(first, torch.full((B,), 4, device="cuda"), backward=False)["h"], EL, "h")
+
+
+@pytest.mark.parametrize("n", [1, 8, 37, 256])
+def test_one_row_of_any_stride(n):
+    """A single row's stride means nothing, whatever torch says it is: a column turned on its side
+    is contiguous, and as good an output as any."""
+    from recurrent_cfc_cell_gb300 import _lib
+    from test_trunk_gpu import rng_tensor
+
+    d = Draw(n)
+    x, w, b = d.normal(1, n), d.f32(n), d.f32(n)
+    rng, stats = rng_tensor(1, 2), torch.empty(1, 2, device="cuda")
+
+    def row():
+        t = torch.full((n, 1), float("nan"), device="cuda").T
+        assert t.shape == (1, n) and t.is_contiguous()
+        return t
+
+    y, want, g, dx = row(), torch.empty_like(x), row(), row()
+    _lib.cfc_layernorm_forward(x, w, b, want, stats)
+    _lib.cfc_layernorm_forward(x, w, b, y, stats)
+    assert torch.equal(y, want)
+    _lib.cfc_dropout_forward(x, None, rng, 0.5, want)
+    _lib.cfc_dropout_forward(x, None, rng, 0.5, y)
+    assert torch.equal(y, want)
+    g.copy_(x)
+    dw, db = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    _lib.cfc_layernorm_backward(g, x, w, stats, dx, dw, db)
+    _lib.cfc_layernorm_backward(x, x, w, stats, want, dw, db)
+    assert torch.equal(dx, want) and torch.equal(db, x[0])
