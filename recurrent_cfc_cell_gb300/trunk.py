@@ -28,9 +28,7 @@ class _Step:
 
     def __init__(self, device):
         self.device = _device(device)
-        self.inputs = None
-        self.graph = None
-        self._forward, self._backward = (), ()
+        self._unbind()
 
     def _act(self, *shape):
         return torch.empty(shape, dtype=self.dtype, device=self.device)
@@ -38,7 +36,14 @@ class _Step:
     def _f32(self, *shape):
         return torch.empty(shape, dtype=torch.float32, device=self.device)
 
+    def _unbind(self):
+        """What every bind begins with, so that one that is refused leaves nothing bound."""
+        self.inputs, self.graph = None, None
+        self._forward, self._backward = (), ()
+
     def forward(self, stream=None) -> None:
+        if not self._forward:
+            raise ValueError("no inputs are bound")
         for call in self._forward:
             call(stream)
 
@@ -51,8 +56,7 @@ class _Step:
     def run(self, stream=None) -> None:
         """The forward pass and, where a gradient is bound, the backward pass, enqueued on
         ``stream`` (default: the current stream)."""
-        for call in self._forward:
-            call(stream)
+        self.forward(stream)
         for call in self._backward:
             call(stream)
 
@@ -88,14 +92,15 @@ class LayerNormStep(_Step):
             self.ws = _workspace(_lib.layernorm_workspace_bytes(self.rows, self.n), self.device)
 
     def bind(self, x, w, b, dy=None) -> "LayerNormStep":
-        self.inputs = dict(x=x, w=w, b=b, dy=dy)
-        self.graph = None
-        self._forward = (_lib.cfc_layernorm_forward.prepare(x, w, b, self.y, self.stats, self.eps),)
-        self._backward = ()
+        self._unbind()
+        forward = (_lib.cfc_layernorm_forward.prepare(x, w, b, self.y, self.stats, self.eps),)
+        backward = ()
         if dy is not None:
             self._alloc_grads()
-            self._backward = (_lib.cfc_layernorm_backward.prepare(
+            backward = (_lib.cfc_layernorm_backward.prepare(
                 dy, x, w, self.stats, self.dx, self.dw, self.db, self.ws),)
+        self.inputs = dict(x=x, w=w, b=b, dy=dy)
+        self._forward, self._backward = forward, backward
         return self
 
     def outputs(self) -> dict:
@@ -118,20 +123,21 @@ class DropoutNormStep(_Step):
         self.dx = self.dres = self.dw = self.db = self.ws = None
 
     def bind(self, x, residual, rng, w, b, dy=None, ds=None) -> "DropoutNormStep":
-        self.inputs = dict(x=x, residual=residual, rng=rng, w=w, b=b, dy=dy, ds=ds)
-        self.graph = None
-        self._forward = (_lib.cfc_dropout_layernorm_forward.prepare(
+        self._unbind()
+        forward = (_lib.cfc_dropout_layernorm_forward.prepare(
             x, residual, rng, self.p, w, b, self.s, self.y, self.stats, self.eps),)
-        self._backward = ()
+        backward = ()
         if dy is not None:
             if self.dx is None:
                 self.dx, self.dres = self._act(self.rows, self.n), self._act(self.rows, self.n)
                 self.dw, self.db = self._f32(self.n), self._f32(self.n)
                 self.ws = _workspace(_lib.layernorm_workspace_bytes(self.rows, self.n),
                                      self.device)
-            self._backward = (_lib.cfc_dropout_layernorm_backward.prepare(
+            backward = (_lib.cfc_dropout_layernorm_backward.prepare(
                 dy, ds, self.s, rng, self.p, w, self.stats, self.dx, self.dres, self.dw, self.db,
                 self.ws),)
+        self.inputs = dict(x=x, residual=residual, rng=rng, w=w, b=b, dy=dy, ds=ds)
+        self._forward, self._backward = forward, backward
         return self
 
     def outputs(self) -> dict:
@@ -153,11 +159,10 @@ class ConvStep(_Step):
         self.dx = self.dx0 = self.dw = self.dbias = self.ws = None
 
     def bind(self, x, w, bias=None, x0=None, lengths=None, dy=None) -> "ConvStep":
-        self.inputs = dict(x=x, w=w, bias=bias, x0=x0, lengths=lengths, dy=dy)
-        self.graph = None
-        self._forward = (_lib.cfc_conv_forward.prepare(x, w, self.u, bias, x0, lengths, self.last,
-                                                       self.silu),)
-        self._backward = ()
+        self._unbind()
+        forward = (_lib.cfc_conv_forward.prepare(x, w, self.u, bias, x0, lengths, self.last,
+                                                 self.silu),)
+        backward = ()
         if dy is not None:
             if self.dx is None:
                 self.dx, self.dx0 = self._act(self.K, self.B, self.D), torch.empty_like(self.last)
@@ -165,9 +170,11 @@ class ConvStep(_Step):
                 code = _lib.CFC_BF16 if self.dtype == torch.bfloat16 else _lib.CFC_F32
                 self.ws = _workspace(_lib.conv_workspace_bytes(self.B, self.K, self.D, self.W,
                                                                code), self.device)
-            self._backward = (_lib.cfc_conv_backward.prepare(
+            backward = (_lib.cfc_conv_backward.prepare(
                 dy, x, w, self.dx, self.dw, self.dbias, bias, x0, lengths, self.dx0, self.ws,
                 self.silu),)
+        self.inputs = dict(x=x, w=w, bias=bias, x0=x0, lengths=lengths, dy=dy)
+        self._forward, self._backward = forward, backward
         return self
 
     def outputs(self) -> dict:
@@ -201,21 +208,22 @@ class ScanStep(_Step):
 
     def bind(self, x, dt, A, Bm, Cm, D=None, dt_bias=None, z=None, h0=None, lengths=None, dy=None,
              dh_last=None) -> "ScanStep":
-        self.inputs = dict(x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D=D, dt_bias=dt_bias, z=z, h0=h0,
-                           lengths=lengths, dy=dy, dh_last=dh_last)
-        self.graph = None
+        self._unbind()
         opt = dict(D=D, dt_bias=dt_bias, z=z, h0=h0, lengths=lengths, softplus=self.softplus)
-        self._forward = (_lib.cfc_scan_forward.prepare(x, dt, A, Bm, Cm, self.y, h_last=self.h,
-                                                       states=self.states, ws=self.ws, **opt),)
-        self._backward = ()
+        forward = (_lib.cfc_scan_forward.prepare(x, dt, A, Bm, Cm, self.y, h_last=self.h,
+                                                 states=self.states, ws=self.ws, **opt),)
+        backward = ()
         if dy is not None:
             if not self.train:
                 raise ValueError("a ScanStep made without train keeps no states to go back through")
-            self._backward = (_lib.cfc_scan_backward.prepare(
+            backward = (_lib.cfc_scan_backward.prepare(
                 dy, x, dt, A, Bm, Cm, self.states, self.dx, self.ddt, self.dA, self.dB, self.dC,
                 dh_last=dh_last, dD=self.dD if D is not None else None,
                 ddt_bias=self.ddt_bias if dt_bias is not None else None,
                 dz=self.dz if z is not None else None, dh0=self.dh0, ws=self.bws, **opt),)
+        self.inputs = dict(x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D=D, dt_bias=dt_bias, z=z, h0=h0,
+                           lengths=lengths, dy=dy, dh_last=dh_last)
+        self._forward, self._backward = forward, backward
         return self
 
     def outputs(self) -> dict:
@@ -242,8 +250,9 @@ class ConvToken:
 
     def bind(self, x, w, state, bias=None, new_state=None) -> "ConvToken":
         """new_state None: the state moves on in place."""
-        self.state = state if new_state is None else new_state
-        self._call = _lib.cfc_conv_step.prepare(x, w, state, self.state, self.u, bias, self.silu)
+        new_state = state if new_state is None else new_state
+        self._call = _lib.cfc_conv_step.prepare(x, w, state, new_state, self.u, bias, self.silu)
+        self.state = new_state
         return self
 
     def run(self, stream=None):
@@ -262,9 +271,10 @@ class ScanToken:
     def bind(self, x, dt, A, Bm, Cm, state, D=None, dt_bias=None, z=None,
              new_state=None) -> "ScanToken":
         """new_state None: the state is updated in place."""
-        self.state = state if new_state is None else new_state
-        self._call = _lib.cfc_scan_step.prepare(x, dt, A, Bm, Cm, state, self.state, self.y, D,
+        new_state = state if new_state is None else new_state
+        self._call = _lib.cfc_scan_step.prepare(x, dt, A, Bm, Cm, state, new_state, self.y, D,
                                                 dt_bias, z, self.softplus)
+        self.state = new_state
         return self
 
     def run(self, stream=None):

@@ -80,3 +80,23 @@ def test_one_row_of_any_stride(n):
     _lib.cfc_layernorm_backward(g, x, w, stats, dx, dw, db)
     _lib.cfc_layernorm_backward(x, x, w, stats, want, dw, db)
     assert torch.equal(dx, want) and torch.equal(db, x[0])
+
+
+def test_a_refused_gradient_leaves_nothing_bound():
+    """Not the forward pass alone, with the gradients of a step before."""
+    from recurrent_cfc_cell_gb300 import trunk
+
+    d = Draw(1)
+    x, w, dy = d.normal(4, 8), d.f32(8), d.normal(4, 7)
+    st = trunk.LayerNormStep(4, 8).bind(x, w, w, x)
+    with pytest.raises(ValueError):
+        st.bind(x, w, w, dy)
+    with pytest.raises(ValueError, match="bound"):
+        st.run()
+    x, dt = d.normal(4, 2, 8), d.normal(4, 2, 8)
+    bc, A = d.normal(4, 2, 1, 4), -torch.ones(8, 4, device="cuda")
+    st = trunk.ScanStep(4, 2, 8, 4)
+    with pytest.raises(ValueError):
+        st.bind(x, dt, A, bc, bc, dy=x)  # made without train
+    with pytest.raises(ValueError, match="bound"):
+        st.run()
