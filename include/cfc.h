@@ -420,14 +420,17 @@ int cfc_copy(const void* src, void* dst, size_t bytes, cfc_stream_t stream);
  *   - Activations may be strided views whose innermost dimension is contiguous: rows of a matrix
  *     are `ld` elements apart, steps and sequences of a time-major [K][B][D] tensor are `_t` and
  *     `_b` elements apart (slices of a packed projection, or batch-first memory, are used in
- *     place; what is read may have stride 0, what is written has ld >= n, or _t and _b >= 1).  They need their element's alignment only: aligned ones (16
- *     bytes for bf16, 32 for fp32, strides in multiples of 8) take vector loads.  Other tensors
- *     are contiguous; fp32 ones need 4-byte, workspaces and scan states 16-byte alignment.
+ *     place; what is read may have stride 0, what is written has ld >= n, or _t and _b >= 1).
+ *     They need their element's alignment only: aligned ones (16 bytes for bf16, 32 for fp32,
+ *     strides in multiples of 8) take vector loads.  Other tensors are contiguous; fp32 ones
+ *     need 4-byte, workspaces and scan states 16-byte alignment.
  *   - Outputs are overwritten and do not overlap inputs, but where a call says otherwise.
  *   - `lengths` (or NULL: all sequences have K steps) holds B ints on the device, one length per
  *     sequence; they are used clamped to 0 .. K.  Steps at or beyond a sequence's length are not
  *     read; outputs and gradients there are 0, and a carried state is the one at the length.
- *   - Results are bitwise reproducible: orders of summation depend on sizes alone.
+ *   - Results are bitwise reproducible.  Orders of summation depend on sizes alone, in the layer
+ *     norm (also behind dropout) on the alignment of its rows, their strides and w and b as well:
+ *     the same values aligned otherwise may round otherwise.
  */
 #define CFC_F32 0
 #define CFC_BF16 1

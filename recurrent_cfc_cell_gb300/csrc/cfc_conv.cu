@@ -19,10 +19,13 @@
 // reduce_axis0.
 //
 // Measured on GB300: 64 sequences of up to 1023 steps, 1536 channels, bf16, 4 taps, lengths spread
-// evenly over 0 .. 1023: forward 66 us (4.6 TB/s of what is read and written), backward 121 us
-// (3.5 TB/s); both wait for memory at 16 to 32 warps an SM.  Four steps' loads go out while the four
-// before them are computed (backward 123 us; without, 144 us).  One token of 1024 sequences of 2048
-// channels 10.4 us, of which the taps, read once for four sequences, had been most (36 us).
+// evenly over 0 .. 1023, so that half the steps are read and all are written: forward 66 us (4.6 TB/s),
+// which waits for memory, backward 121 us (3.3 TB/s), whose first stall is the barrier before its sums
+// (2.0 of 7 cycles an instruction; memory 1.1, DRAM 38% busy): a CTA's runs are eight in a row of one
+// sequence, and those past its end hold their registers until the longest is done.  Four steps' loads
+// go out while the four before them are computed (backward 123 us; without, 144 us).  One token of
+// 1024 sequences of 2048 channels 10.4 us for 33.5 MB (5 us): each lane reads its taps, once for four
+// sequences, one by one (36 us with a read for every sequence).
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"

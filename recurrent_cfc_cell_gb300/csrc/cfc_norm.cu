@@ -31,9 +31,14 @@
 // Measured on GB300 (copy rate 6.69 TB/s): 262144 x 256 fp32 forward 84 us (6.4 TB/s), backward 125 us
 // (6.4 TB/s); the same rows in bf16 with dropout and residual 98 us (5.5 TB/s; a row's generator calls
 // are a third of its instructions) and 127 us (5.3 TB/s); 10529 x 3528 fp32 56 and 88 us (5.3 and
-// 5.0 TB/s), bf16 31 and 53 us (4.8 and 4.2 TB/s: a CTA's row is a chain of loads, sums, a barrier
-// and stores, and few rows are in flight on an SM); 6007 x 2501 bf16, rows of every alignment, 20 and
-// 32 us (3.0 and 2.8 TB/s: besides, the rows' ends are taken element by element).
+// 5.0 TB/s), bf16 31 and 53 us (4.8 and 4.2 TB/s); 6007 x 2501 bf16, rows of every alignment, 20 and
+// 32 us (3.0 and 2.8 TB/s).  What bounds wide bf16 rows are instructions and shared memory: 21.5 and
+// 29.4 instructions an element at 2501 columns (an aligned fp32 row of 256 takes 15), issued at 2.6 and
+// 2.4 a clock of 4, the shared-memory pipe busy to 68% and 44%: w and b are read from it again, in
+// fp32, for every row.  The rows' ends, element by element, and a barrier a row come on top.
+// Dropout alone with the residual, 262144 x 256: fp32 127 us (6.3 TB/s), bf16 68 us (5.9 TB/s); its
+// backward pass 90 us (6.0 TB/s) and 60 us (4.5 TB/s); 24028 x 2501 bf16 121 and 111 us (3.0 and
+// 2.2 TB/s).
 #include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
@@ -397,7 +402,9 @@ __host__ __device__ constexpr bool bwd_ring() {
 // has (28467 x 319: bf16 37 us, 50 us freely; fp32 with dropout 73 and 93 us); whole CTAs with shifted
 // rows or a ring 128 registers (6007 x 2501 fp32 49 us, 68 us freely); aligned rows with the loads in
 // registers as the compiler finds (262144 x 256 fp32 125 us; asked for one CTA, it spends the
-// registers on an order of loads that takes 158 us).
+// registers on an order of loads that takes 158 us).  Where a figure is bf16's alone, fp32 has not
+// been timed apart; it spills there: 36 to 48 bytes a thread forwards (aligned rows with dropout), 40
+// to 104 backwards (shifted rows without).
 template <typename T, typename TM, Layout LY, bool DROP>
 __host__ __device__ constexpr int fwd_ctas() {
   if (!TM::kWhole) return LY == kShifted && DROP ? 2 : 4;
