@@ -367,7 +367,7 @@ def _exact_held8(v):
     for c in range(0, v.shape[-1], BLOCK):
         part = v[..., c:c + BLOCK]
         top = part.abs().max(-1, keepdim=True).values.clamp(min=2.0 ** -200)
-        k = _magnitude(top) - 9  # top < 512 * 2^k
+        k = _magnitude(top) - 8  # top < 512 * 2^k
         k = torch.where(448.0 * _power(k) < top, k + 1, k)
         k = torch.where(448.0 * _power(k - 1) >= top, k - 1, k).clamp(min=-126)
         u = part * _power(-k)
