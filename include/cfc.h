@@ -607,6 +607,158 @@ int cfc_scan_backward(const cfc_scan_args* a, const float* states, const void* d
 int cfc_scan_step(const cfc_scan_args* a, void* y, long long y_b, float* new_state,
                   cfc_stream_t stream);
 
+/*
+ * ---- The gated block's operators ----
+ *
+ * A second trunk beside the selective scan's: root-mean-square norm with the residual's addition, a
+ * gated linear recurrence, what a training step keeps for its backward pass in 8 bits, and products
+ * with 4-bit weights for single tokens.  The conventions of the trunk operators hold.
+ *
+ * Values in 8 bits.  A row of n columns is held as n codes (one byte each, e4m3) and
+ * ceil(n / CFC_HELD8_BLOCK) scales (one byte each, e8m0: 2^(byte - 127), 255 is NaN), one for
+ * CFC_HELD8_BLOCK columns (the last block may be shorter); codes [rows][n] and scales
+ * [rows][ceil(n / CFC_HELD8_BLOCK)] are contiguous, the layout of the OCP microscaling formats.  A
+ * block's scale is the smallest power of two, 2^-126 at least, for which the largest magnitude is at
+ * most 448 times it; a value is v / scale rounded to e4m3, to nearest even: off by at most 2^-4 of it,
+ * or by 2^-10 of the scale.  A block with an infinity or a NaN is held as NaN throughout.  Codes that
+ * are 8-byte aligned, with n a multiple of 8, take vector accesses.
+ */
+#define CFC_HELD8_BLOCK 32
+typedef struct cfc_held8 {
+  void* codes;             /* [rows][n] bytes                                                    */
+  void* scales;            /* [rows][ceil(n / CFC_HELD8_BLOCK)] bytes                            */
+} cfc_held8;
+
+/* cfc_pack8 -- held <- x [rows][n] in 8 bits.  cfc_unpack8 -- y [rows][n] <- what held stands for
+ * (in fp32 and bf16 exact, but for magnitudes below bf16's smallest normal number, in bf16). */
+int cfc_pack8(const void* x, long long ldx, int rows, int n, int dtype, const cfc_held8* held,
+              cfc_stream_t stream);
+int cfc_unpack8(const cfc_held8* held, int rows, int n, int dtype, void* y, long long ldy,
+                cfc_stream_t stream);
+
+/*
+ * Root-mean-square norm: s = x + residual, rounded to dtype (residual NULL: s = x);
+ * rstd = (sum s^2 / n + eps)^-1/2;  y = s rstd w.  The norm reads s as rounded.
+ */
+typedef struct cfc_rmsnorm_args {
+  int rows, n;             /* n <= 2^24                                                          */
+  int dtype;
+  float eps;               /* >= 0; the backward pass does not use it                            */
+  const void* x;           /* [rows][n] (ldx)                                                    */
+  const void* residual;    /* [rows][n] (ldr) or NULL                                            */
+  long long ldx, ldr;
+  const float* w;          /* [n]                                                                */
+} cfc_rmsnorm_args;
+
+/*
+ * cfc_rmsnorm_forward -- each output is written where its pointer is not NULL:
+ *   s [rows][n] (lds; may be x's or residual's own memory), y [rows][n] (ldy),
+ *   s8, y8: s and y in 8 bits (y8 from y before it is rounded to dtype),
+ *   rstd [rows], which the backward pass reads.
+ */
+int cfc_rmsnorm_forward(const cfc_rmsnorm_args* a, void* s, long long lds, void* y, long long ldy,
+                        const cfc_held8* s8, const cfc_held8* y8, float* rstd,
+                        cfc_stream_t stream);
+
+/* cfc_rmsnorm_workspace_bytes -- workspace of cfc_rmsnorm_backward.  Writes *bytes (0: none). */
+int cfc_rmsnorm_workspace_bytes(int rows, int n, size_t* bytes);
+
+/*
+ * cfc_rmsnorm_backward -- from dy (of y), ds (of s as it goes on, NULL: none), the stream and rstd:
+ * dx = rstd (dy w - hat sum(dy w hat) / n) + ds with hat = s rstd, the gradient of x and of the
+ * residual alike, dw = sum_rows dy hat, and y formed again (NULL: not wanted), for a product's weight
+ * gradient.  The stream is a->x (rows ldx; a->residual is not used), or s8 where that is not NULL (a->x
+ * is not read then): what it holds takes the place of s, with the rstd of the forward pass.
+ * dx may be dy's, ds's or a->x's own memory.
+ */
+int cfc_rmsnorm_backward(const cfc_rmsnorm_args* a, const cfc_held8* s8, const float* rstd,
+                         const void* dy, long long lddy, const void* ds, long long ldds, void* dx,
+                         long long lddx, void* y, long long ldy, float* dw, void* ws,
+                         size_t ws_bytes, cfc_stream_t stream);
+
+/*
+ * Gated linear recurrence: per sequence and channel
+ *   g_t = 1 / (1 + exp(-(f_t + bias)))                      (bias NULL: 0)
+ *   h_t = g_t h_{t-1} + (1 - g_t) x_t,                      h_{-1} = h0 (NULL: zeros)
+ *   y_t = h_t (z ? z_t / (1 + exp(-z_t)) : 1)
+ * Strides of the step's form (cfc_gated_step) are the `_b` ones; K and lengths are not used there.
+ */
+typedef struct cfc_gated_args {
+  int B, K, D;             /* sequences (<= 65535), steps (<= 2^24), channels (<= 2^24)          */
+  int dtype;
+  const int* lengths;      /* [B] or NULL                                                        */
+  const void *x, *f, *z;   /* [K][B][D]; z may be NULL                                           */
+  long long x_t, x_b, f_t, f_b, z_t, z_b;
+  const float* bias;       /* [D] or NULL                                                        */
+  const float* h0;         /* [B][D] or NULL                                                     */
+} cfc_gated_args;
+
+/* x, f and z (where there is one) in 8 bits, as rows t B + b of D columns.  Rows at or beyond a
+ * sequence's length are not written, and not read. */
+typedef struct cfc_gated_kept {
+  cfc_held8 x, f, z;
+} cfc_gated_kept;
+
+/* Steps between the states that a training forward keeps: [ceil(K / CFC_GATED_PERIOD)][B][D] fp32,
+ * the state before every CFC_GATED_PERIOD-th step (beyond a sequence's length: not read). */
+#define CFC_GATED_PERIOD 8
+
+/*
+ * cfc_gated_forward -- y [K][B][D] (strides y_t, y_b), h_last [B][D] (or NULL; may be h0's own
+ * memory), and for training states (NULL: none kept) and kept (NULL: nothing is kept in 8 bits).
+ */
+int cfc_gated_forward(const cfc_gated_args* a, void* y, long long y_t, long long y_b,
+                      float* h_last, float* states, const cfc_gated_kept* kept,
+                      cfc_stream_t stream);
+
+/* cfc_gated_workspace_bytes -- workspace of cfc_gated_backward.  Writes *bytes (0: none). */
+int cfc_gated_workspace_bytes(int B, int K, int D, int dtype, size_t* bytes);
+
+/*
+ * cfc_gated_backward -- from dy (of y), dh_last (of h_last, NULL: none) and the forward pass's
+ * states: the gradients in g (NULL is allowed for dz where there is no z, dbias and dh0), and y formed
+ * again (NULL: not wanted).  Within a period h is formed again from the state before it.  With
+ * kept, x, f and z are what it holds (a->x, a->f, a->z and their strides are not used; there is a z
+ * where kept->z.codes is not NULL), and the gradients are those of the periods on these values.
+ */
+typedef struct cfc_gated_grads {
+  void *dx, *df, *dz, *y;
+  long long dx_t, dx_b, df_t, df_b, dz_t, dz_b, y_t, y_b;
+  float *dbias, *dh0;      /* [D], [B][D]                                                        */
+} cfc_gated_grads;
+int cfc_gated_backward(const cfc_gated_args* a, const cfc_gated_kept* kept, const float* states,
+                       const void* dy, long long dy_t, long long dy_b, const float* dh_last,
+                       const cfc_gated_grads* g, void* ws, size_t ws_bytes, cfc_stream_t stream);
+
+/*
+ * cfc_gated_step -- one token per sequence: x, f, z [B][D] (strides _b), the state a->h0 [B][D]
+ * (required); y [B][D] (y_b) and new_state (which may be h0's own memory).
+ */
+int cfc_gated_step(const cfc_gated_args* a, void* y, long long y_b, float* new_state,
+                   cfc_stream_t stream);
+
+/*
+ * Products with 4-bit weights: W[n][k] = (code - 8) scale with codes 0 .. 15, two to a byte (column
+ * 2 i in the low half of byte i of a row, rows of ceil(K / 2) bytes), and a bf16 scale for each
+ * `group` columns of a row (32, 64 or 128; scales [N][ceil(K / group)], the last group may be
+ * shorter).  1 <= N, K <= 2^24, N K <= 2^36, M <= 2^19.
+ *
+ * cfc_weights4_quantize -- codes, scales <- W [N][K] (rows ldw; fp32 or bf16): a group's scale is its
+ * largest magnitude / 7, rounded to bf16, and its codes the nearest ones.
+ * cfc_weights4_bytes -- size of the laid-out weights.
+ * cfc_weights4_lay_out -- weights (16-byte aligned) <- codes and scales in the order in which
+ * cfc_matvec4 reads them; done once for a matrix.
+ * cfc_matvec4 -- y [M][N] (ldy) <- x [M][K] (ldx) W^T, with fp32 sums of exact products.  The
+ * weights are read once for every eight rows of x.
+ */
+int cfc_weights4_quantize(const void* W, long long ldw, int N, int K, int group, int dtype,
+                          void* codes, void* scales, cfc_stream_t stream);
+int cfc_weights4_bytes(int N, int K, int group, size_t* bytes);
+int cfc_weights4_lay_out(const void* codes, const void* scales, int N, int K, int group,
+                         void* weights, size_t weights_bytes, cfc_stream_t stream);
+int cfc_matvec4(const void* x, long long ldx, const void* weights, int M, int N, int K, int group,
+                int dtype, void* y, long long ldy, cfc_stream_t stream);
+
 /* cfc_error_string -- static English text for a status code (never NULL). */
 const char* cfc_error_string(int code);
 

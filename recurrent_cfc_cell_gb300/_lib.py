@@ -40,9 +40,15 @@ EXPORTED = ("cfc_workspace_bytes", "cfc_forward", "cfc_backward", "cfc_backward_
             "cfc_dropout_forward", "cfc_dropout_backward", "cfc_dropout_layernorm_forward",
             "cfc_dropout_layernorm_backward", "cfc_conv_forward", "cfc_conv_workspace_bytes",
             "cfc_conv_backward", "cfc_conv_step", "cfc_scan_workspace_bytes",
-            "cfc_scan_states_bytes", "cfc_scan_forward", "cfc_scan_backward", "cfc_scan_step")
+            "cfc_scan_states_bytes", "cfc_scan_forward", "cfc_scan_backward", "cfc_scan_step",
+            "cfc_pack8", "cfc_unpack8", "cfc_rmsnorm_forward", "cfc_rmsnorm_workspace_bytes",
+            "cfc_rmsnorm_backward", "cfc_gated_forward", "cfc_gated_workspace_bytes",
+            "cfc_gated_backward", "cfc_gated_step", "cfc_weights4_quantize", "cfc_weights4_bytes",
+            "cfc_weights4_lay_out", "cfc_matvec4")
 CFC_F32, CFC_BF16 = 0, 1          # activation types of the trunk operators
 SCAN_PERIOD = 8                   # steps between the states a training scan keeps
+GATED_PERIOD = 8                  # and a training gated recurrence
+HELD8_BLOCK = 32                  # columns that share a scale in 8 bits
 CFC_ERR_SCRATCH_LIMIT = -10
 NOALLOC_SCRATCH_BYTES = 32 << 20  # size of cfc_backward_noalloc's built-in device scratch
 
@@ -70,6 +76,39 @@ class ScanGrads(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "ddt", "dz")] + [
         (k, ctypes.c_longlong) for k in ("dx_t", "dx_b", "ddt_t", "ddt_b", "dz_t", "dz_b")] + [
         (k, ctypes.c_void_p) for k in ("dB", "dC", "dA", "dskip", "ddt_bias", "dh0")]
+
+
+class Held8Ptrs(ctypes.Structure):
+    """cfc_held8 of include/cfc.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class RmsnormArgs(ctypes.Structure):
+    """cfc_rmsnorm_args of include/cfc.h."""
+    _fields_ = [(k, ctypes.c_int) for k in ("rows", "n", "dtype")] + [
+        ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+        ("ldx", ctypes.c_longlong), ("ldr", ctypes.c_longlong), ("w", ctypes.c_void_p)]
+
+
+class GatedArgs(ctypes.Structure):
+    """cfc_gated_args of include/cfc.h."""
+    _fields_ = [(k, ctypes.c_int) for k in ("B", "K", "D", "dtype")] + [
+        (k, ctypes.c_void_p) for k in ("lengths", "x", "f", "z")] + [
+        (k, ctypes.c_longlong) for k in ("x_t", "x_b", "f_t", "f_b", "z_t", "z_b")] + [
+        (k, ctypes.c_void_p) for k in ("bias", "h0")]
+
+
+class GatedKept(ctypes.Structure):
+    """cfc_gated_kept of include/cfc.h."""
+    _fields_ = [(k, Held8Ptrs) for k in ("x", "f", "z")]
+
+
+class GatedGrads(ctypes.Structure):
+    """cfc_gated_grads of include/cfc.h."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "df", "dz", "y")] + [
+        (k, ctypes.c_longlong) for k in ("dx_t", "dx_b", "df_t", "df_b", "dz_t", "dz_b", "y_t",
+                                         "y_b")] + [
+        (k, ctypes.c_void_p) for k in ("dbias", "dh0")]
 
 
 class CfcError(RuntimeError):
@@ -146,6 +185,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.cfc_copy.restype = i
     ll, fl, szp = ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(sz)
     conv, scan, grads = (ctypes.POINTER(c) for c in (ConvArgs, ScanArgs, ScanGrads))
+    held, rms, gated, kept, ggrads = (ctypes.POINTER(c) for c in (
+        Held8Ptrs, RmsnormArgs, GatedArgs, GatedKept, GatedGrads))
     for name, args in {
         "cfc_layernorm_forward": [vp, ll, vp, vp, i, i, fl, i, vp, ll, vp, vp],
         "cfc_layernorm_workspace_bytes": [i, i, szp],
@@ -165,6 +206,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "cfc_scan_forward": [scan, vp, ll, ll, vp, vp, vp, sz, vp],
         "cfc_scan_backward": [scan, vp, vp, ll, ll, vp, grads, vp, sz, vp],
         "cfc_scan_step": [scan, vp, ll, vp, vp],
+        "cfc_pack8": [vp, ll, i, i, i, held, vp],
+        "cfc_unpack8": [held, i, i, i, vp, ll, vp],
+        "cfc_rmsnorm_forward": [rms, vp, ll, vp, ll, held, held, vp, vp],
+        "cfc_rmsnorm_workspace_bytes": [i, i, szp],
+        "cfc_rmsnorm_backward": [rms, held, vp, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, sz, vp],
+        "cfc_gated_forward": [gated, vp, ll, ll, vp, vp, kept, vp],
+        "cfc_gated_workspace_bytes": [i] * 4 + [szp],
+        "cfc_gated_backward": [gated, kept, vp, vp, ll, ll, vp, ggrads, vp, sz, vp],
+        "cfc_gated_step": [gated, vp, ll, vp, vp],
+        "cfc_weights4_quantize": [vp, ll, i, i, i, i, vp, vp, vp],
+        "cfc_weights4_bytes": [i, i, i, szp],
+        "cfc_weights4_lay_out": [vp, vp, i, i, i, vp, sz, vp],
+        "cfc_matvec4": [vp, ll, vp, i, i, i, i, i, vp, ll, vp],
     }.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
@@ -857,3 +911,245 @@ def cfc_scan_step(x, dt, A, Bm, Cm, state, new_state, y, D=None, dt_bias=None, z
     return ((ctypes.byref(a), _act(y, "y", (B, Dn), x.dtype), _ld(y),
              _par(new_state, "new_state", (B, Dn, A.shape[1]))),
             (x, dt, A, Bm, Cm, state, new_state, y, D, dt_bias, z, a))
+
+
+# ---- the gated block's operators: values in 8 bits, root-mean-square norm, gated linear
+# recurrence, products with 4-bit weights ----
+
+class Held8:
+    """Rows held in 8 bits: `codes` [.., n] (e4m3) and `scales` [.., ceil(n / HELD8_BLOCK)] (e8m0),
+    contiguous uint8 CUDA tensors of their own unless they are given."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, shape, device=None, codes=None, scales=None):
+        import torch
+
+        blocks = (*shape[:-1], -(-shape[-1] // HELD8_BLOCK))
+        new = dict(dtype=torch.uint8, device=device or "cuda")
+        self.codes = torch.empty(shape, **new) if codes is None else codes
+        self.scales = torch.empty(blocks, **new) if scales is None else scales
+
+
+def _bytes8(t, name: str, shape):
+    """Address of a contiguous uint8 tensor."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _held8(h, name: str, shape):
+    """The pointers of rows in 8 bits (None stays None)."""
+    if h is None:
+        return None
+    if not isinstance(h, Held8):
+        raise TypeError(f"{name} must be a Held8")
+    return Held8Ptrs(_bytes8(h.codes, name + ".codes", shape),
+                     _bytes8(h.scales, name + ".scales",
+                             (*shape[:-1], -(-shape[-1] // HELD8_BLOCK))))
+
+
+def _by(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _parts8(*held):
+    """The tensors of the rows in 8 bits that there are."""
+    return tuple(t for h in held if h is not None for t in (h.codes, h.scales))
+
+
+@_entry
+def cfc_pack8(x, held):
+    """held (Held8) <- the rows of x [rows, n] in 8 bits."""
+    rows, n = _dims(*x.shape)
+    h = _held8(held, "held", (rows, n))
+    if h is None:
+        raise TypeError("held must be a Held8")
+    return ((_act(x, "x", (rows, n)), _ld(x), rows, n, _code(x), ctypes.byref(h)),
+            (x, *_parts8(held), h))
+
+
+@_entry
+def cfc_unpack8(held, y):
+    """y [rows, n] <- what the rows in 8 bits stand for."""
+    rows, n = _dims(*y.shape)
+    h = _held8(held, "held", (rows, n))
+    if h is None:
+        raise TypeError("held must be a Held8")
+    return ((ctypes.byref(h), rows, n, _code(y), _act(y, "y", (rows, n)), _ld(y)),
+            (y, *_parts8(held), h))
+
+
+def rmsnorm_workspace_bytes(rows: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("cfc_rmsnorm_workspace_bytes",
+           load().cfc_rmsnorm_workspace_bytes(*_dims(rows, n), ctypes.byref(out)))
+    return out.value
+
+
+@_entry
+def cfc_rmsnorm_forward(x, w, residual=None, s=None, y=None, s8=None, y8=None, rstd=None,
+                        eps: float = 1e-5):
+    """s <- x + residual (or None); y <- its root-mean-square norm; s8, y8 <- both in 8 bits; rstd
+    [rows].  Each output may be None; s may be x or residual."""
+    rows, n = _dims(*x.shape)
+    a = RmsnormArgs(rows, n, _code(x), eps, _act(x, "x", (rows, n)),
+                    _act(residual, "residual", (rows, n), x.dtype), _ld(x), _ld(residual),
+                    _par(w, "w", (n,)))
+    h, k = _held8(s8, "s8", (rows, n)), _held8(y8, "y8", (rows, n))
+    return ((ctypes.byref(a), _act(s, "s", (rows, n), x.dtype), _ld(s),
+             _act(y, "y", (rows, n), x.dtype), _ld(y), _by(h), _by(k),
+             _par(rstd, "rstd", (rows,))),
+            (x, w, residual, s, y, rstd, *_parts8(s8, y8), a, h, k))
+
+
+@_entry
+def cfc_rmsnorm_backward(dy, s, w, rstd, dx, dw, ds=None, y=None, ws=None):
+    """dx [rows, n] (plus ds, or None), dw [n] and y formed again (or None) from the stream s, a
+    tensor or a Held8."""
+    rows, n = _dims(*dy.shape)
+    held = isinstance(s, Held8)
+    h = _held8(s, "s", (rows, n)) if held else None
+    a = RmsnormArgs(rows, n, _code(dy), 0.0, None if held else _act(s, "s", (rows, n), dy.dtype),
+                    None, 0 if held else _ld(s), 0, _par(w, "w", (n,)))
+    wp, wn = _work(ws)
+    return ((ctypes.byref(a), _by(h), _par(rstd, "rstd", (rows,)), _act(dy, "dy", (rows, n)),
+             _ld(dy), _act(ds, "ds", (rows, n), dy.dtype), _ld(ds),
+             _act(dx, "dx", (rows, n), dy.dtype), _ld(dx), _act(y, "y", (rows, n), dy.dtype),
+             _ld(y), _par(dw, "dw", (n,)), wp, wn),
+            (dy, w, rstd, dx, dw, ds, y, ws, *(_parts8(s) if held else (s,)), a, h))
+
+
+def gated_workspace_bytes(K: int, B: int, D: int, dtype: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("cfc_gated_workspace_bytes",
+           load().cfc_gated_workspace_bytes(*_dims(B, K, D), dtype, ctypes.byref(out)))
+    return out.value
+
+
+def _gated_args(shape, dtype, x, f, bias, z, h0, lengths):
+    K, B, D = _dims(*shape)
+    code = CFC_BF16 if "bfloat16" in str(dtype) else CFC_F32
+    return GatedArgs(B, K, D, code, _lengths(lengths, B), _act(x, "x", shape, dtype),
+                     _act(f, "f", shape, dtype), _act(z, "z", shape, dtype), *_tb(x), *_tb(f),
+                     *_tb(z), _par(bias, "bias", (D,)), _par(h0, "h0", (B, D)))
+
+
+def _gated_kept(kept, shape):
+    """cfc_gated_kept of a tuple (x, f, z) of Held8, z None where there is none; None stays None."""
+    if kept is None:
+        return None
+    if len(kept) != 3 or kept[0] is None or kept[1] is None:
+        raise ValueError("kept must be (x, f, z) as Held8, z None where the recurrence has none")
+    return GatedKept(*(_held8(h, "kept", shape) or Held8Ptrs() for h in kept))
+
+
+@_entry
+def cfc_gated_forward(x, f, y, bias=None, z=None, h0=None, lengths=None, h_last=None, states=None,
+                      kept=None):
+    """y [K, B, D], h_last [B, D] (or None; may be h0) and, for training, states
+    [ceil(K / GATED_PERIOD), B, D] and kept, a tuple (x, f, z) of Held8 (or None) <- gated linear
+    recurrence."""
+    K, B, D = x.shape
+    a = _gated_args((K, B, D), x.dtype, x, f, bias, z, h0, lengths)
+    k = _gated_kept(kept, (K, B, D))
+    if kept is not None and (kept[2] is None) != (z is None):
+        raise ValueError("kept holds a z where the recurrence has one")
+    return ((ctypes.byref(a), _act(y, "y", (K, B, D), x.dtype), *_tb(y),
+             _par(h_last, "h_last", (B, D)),
+             _par(states, "states", (-(-K // GATED_PERIOD), B, D)), _by(k)),
+            (x, f, y, bias, z, h0, lengths, h_last, states, *_parts8(*(kept or ())), a, k))
+
+
+@_entry
+def cfc_gated_backward(dy, x, f, states, dx, df, bias=None, z=None, lengths=None, dh_last=None,
+                       dz=None, dbias=None, dh0=None, y=None, kept=None, ws=None):
+    """The gated linear recurrence's gradients from dy and dh_last (or None), and y formed again (or
+    None).  With kept, what it holds takes the place of x, f and z, which are None then."""
+    K, B, D = dy.shape
+    rows, act = (K, B, D), dy.dtype
+    if (kept is None) == (x is None) or (kept is None) == (f is None):
+        raise ValueError("the backward pass reads either x and f or what was kept of them")
+    if kept is not None and z is not None:
+        raise ValueError("z is read from what was kept")
+    a = _gated_args(rows, act, x, f, bias, z, None, lengths)
+    k = _gated_kept(kept, rows)
+    g = GatedGrads(_act(dx, "dx", rows, act), _act(df, "df", rows, act),
+                   _act(dz, "dz", rows, act), _act(y, "y", rows, act), *_tb(dx), *_tb(df),
+                   *_tb(dz), *_tb(y), _par(dbias, "dbias", (D,)), _par(dh0, "dh0", (B, D)))
+    wp, wn = _work(ws)
+    return ((ctypes.byref(a), _by(k), _par(states, "states", (-(-K // GATED_PERIOD), B, D)),
+             _act(dy, "dy", rows), *_tb(dy), _par(dh_last, "dh_last", (B, D)),
+             ctypes.byref(g), wp, wn),
+            (dy, x, f, states, dx, df, bias, z, lengths, dh_last, dz, dbias, dh0, y, ws,
+             *_parts8(*(kept or ())), a, k, g))
+
+
+@_entry
+def cfc_gated_step(x, f, state, new_state, y, bias=None, z=None):
+    """y [B, D], new_state [B, D] (may be state) <- one token of the gated linear recurrence."""
+    def steps(t):
+        return None if t is None else t[None]
+
+    B, D = x.shape
+    a = _gated_args((1, B, D), x.dtype, x[None], steps(f), bias, steps(z), state, None)
+    return ((ctypes.byref(a), _act(y, "y", (B, D), x.dtype), _ld(y),
+             _par(new_state, "new_state", (B, D))),
+            (x, f, state, new_state, y, bias, z, a))
+
+
+def _scales4(t, shape):
+    """Address of the bf16 scales of 4-bit weights."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("scales must be a torch.Tensor")
+    if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("scales must be a contiguous bfloat16 CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"scales has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def weights4_bytes(N: int, K: int, group: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("cfc_weights4_bytes",
+           load().cfc_weights4_bytes(*_dims(N, K), group, ctypes.byref(out)))
+    return out.value
+
+
+@_entry
+def cfc_weights4_quantize(W, codes, scales, group: int):
+    """codes [N, ceil(K / 2)], scales [N, ceil(K / group)] (bf16) <- the nearest 4-bit weights."""
+    N, K = _dims(*W.shape)
+    group = max(int(group), 1)
+    return ((_act(W, "W", (N, K)), _ld(W), N, K, group, _code(W),
+             _bytes8(codes, "codes", (N, (K + 1) // 2)), _scales4(scales, (N, -(-K // group)))),
+            (W, codes, scales))
+
+
+@_entry
+def cfc_weights4_lay_out(codes, scales, K: int, group: int, weights):
+    """weights (uint8, weights4_bytes() of them) <- codes and scales in the order of cfc_matvec4."""
+    N = _dims(codes.shape[0], K)[0]
+    group = max(int(group), 1)
+    wp, wn = _work(weights)
+    return ((_bytes8(codes, "codes", (N, (K + 1) // 2)), _scales4(scales, (N, -(-K // group))), N,
+             K, group, wp, wn), (codes, scales, weights))
+
+
+@_entry
+def cfc_matvec4(x, weights, N: int, group: int, y):
+    """y [M, N] <- x [M, K] times the transposed 4-bit weights of cfc_weights4_lay_out."""
+    M, K = _dims(*x.shape)
+    wp, wn = _work(weights)
+    if wn < weights4_bytes(N, K, group):
+        raise ValueError("weights are shorter than weights4_bytes() of these sizes")
+    return ((_act(x, "x", (M, K)), _ld(x), wp, M, N, K, group, _code(x),
+             _act(y, "y", (M, N), x.dtype), _ld(y)), (x, weights, y))

@@ -5,43 +5,14 @@
 #include <cstdint>
 
 #include "cfc.h"
+#include "cfc_trunk_checks.h"
 #include "cfc_trunk_kernels.h"
 
-namespace cfc {
-int device_ready();  // cfc_abi.cu
-}
+using namespace cfc::checks;
 
 namespace {
 
-int launched(cudaError_t e) {
-  if (e == cudaSuccess) return CFC_OK;
-  (void)cudaGetLastError();
-  return CFC_ERR_LAUNCH_FAILED;
-}
-
-bool valid_dtype(int t) { return t == CFC_F32 || t == CFC_BF16; }
-bool off(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0; }
-// An activation of this type is misaligned for its element.
-bool off_act(const void* p, int dtype) { return off(p, dtype == CFC_BF16 ? 2 : 4); }
-
-constexpr int kMaxSequences = 65535;   // a grid dimension
-constexpr int kMaxSteps = 1 << 24;
-constexpr int kMaxWidth = 1 << 24;     // columns of a row, channels
-
-int ws_check(const void* ws, size_t have, size_t need) {
-  if (need == 0) return CFC_OK;
-  if (!ws) return CFC_ERR_NULL_PTR;
-  if (off(ws, 16)) return CFC_ERR_MISALIGNED;
-  return have < need ? CFC_ERR_WS_TOO_SMALL : CFC_OK;
-}
-
 // ---- layer norm and dropout ----
-
-int rows_check(int rows, int n, int dtype) {
-  if (rows <= 0 || n <= 0 || n > kMaxWidth) return CFC_ERR_INVALID_DIM;
-  return valid_dtype(dtype) ? CFC_OK : CFC_ERR_INVALID_ARG;
-}
-bool bad_eps(float eps) { return !(eps >= 0.f) || std::isinf(eps); }
 
 // The held drop probability and its scale.
 bool set_drop(float p, const void* rng, cfc::NormCall* q) {
@@ -50,27 +21,6 @@ bool set_drop(float p, const void* rng, cfc::NormCall* q) {
   q->scale = q->cut < 65536u ? static_cast<float>(65536.0 / (65536.0 - q->cut)) : 0.f;
   q->rng = static_cast<const unsigned long long*>(rng);
   return true;
-}
-
-// A tensor that a call reads or writes, or may do without.  What is read may repeat in memory
-// (stride 0); what is written may not.
-enum Use { kIn, kInOpt, kOut, kOutOpt };
-bool required(Use u) { return u == kIn || u == kOut; }
-bool written(Use u) { return u == kOut || u == kOutOpt; }
-
-struct Rows {
-  const void* p;
-  long long ld;
-  Use use;
-};
-int rows_ok(const Rows* r, int count, int n, int dtype) {
-  for (int i = 0; i < count; ++i)
-    if (!r[i].p && required(r[i].use)) return CFC_ERR_NULL_PTR;
-  for (int i = 0; i < count; ++i)
-    if (r[i].p && r[i].ld < (written(r[i].use) ? n : 0)) return CFC_ERR_INVALID_DIM;
-  for (int i = 0; i < count; ++i)
-    if (off_act(r[i].p, dtype)) return CFC_ERR_MISALIGNED;
-  return CFC_OK;
 }
 
 int norm_forward(cfc::NormCall q, int dtype, cfc_stream_t stream) {
@@ -103,23 +53,6 @@ int conv_check(int B, int K, int D, int W, int dtype) {
       W > 4)
     return CFC_ERR_INVALID_DIM;
   return valid_dtype(dtype) ? CFC_OK : CFC_ERR_INVALID_ARG;
-}
-
-struct Seq {  // a [K][B][..] activation and its strides
-  const void* p;
-  long long t, b;
-  Use use;
-};
-int seqs_ok(const Seq* r, int count, int dtype, bool steps = true) {
-  for (int i = 0; i < count; ++i)
-    if (!r[i].p && required(r[i].use)) return CFC_ERR_NULL_PTR;
-  for (int i = 0; i < count; ++i) {
-    const long long least = written(r[i].use) ? 1 : 0;
-    if (r[i].p && ((steps && r[i].t < least) || r[i].b < least)) return CFC_ERR_INVALID_DIM;
-  }
-  for (int i = 0; i < count; ++i)
-    if (off_act(r[i].p, dtype)) return CFC_ERR_MISALIGNED;
-  return CFC_OK;
 }
 
 // Fills the common part of a call; the argument errors of the struct itself.

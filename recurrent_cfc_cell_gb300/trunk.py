@@ -23,6 +23,13 @@ def _workspace(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
+def _expect(t, name: str, shape, dtype):
+    """The sizes and the type that a step was made for (the binding checks the rest against them)."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} is {tuple(t.shape)} of {t.dtype}, but the step was made for "
+                         f"{tuple(shape)} of {dtype}")
+
+
 class _Step:
     """Prepared calls, run in order."""
 
@@ -280,3 +287,220 @@ class ScanToken:
     def run(self, stream=None):
         self._call(stream)
         return self.y, self.state
+
+
+class Pack8Step:
+    """The rows of x [rows, n] in 8 bits: `held`, a Held8."""
+
+    def __init__(self, rows: int, n: int, dtype=torch.float32, device=None):
+        self.rows, self.n, self.dtype = rows, n, dtype
+        self.held = _lib.Held8((rows, n), _device(device))
+
+    def bind(self, x) -> "Pack8Step":
+        _expect(x, "x", (self.rows, self.n), self.dtype)
+        self._call = _lib.cfc_pack8.prepare(x, self.held)
+        return self
+
+    def run(self, stream=None):
+        self._call(stream)
+        return self.held
+
+
+class Unpack8Step:
+    """What rows in 8 bits stand for: y [rows, n]."""
+
+    def __init__(self, rows: int, n: int, dtype=torch.float32, device=None):
+        self.y = torch.empty((rows, n), dtype=dtype, device=_device(device))
+
+    def bind(self, held) -> "Unpack8Step":
+        self._call = _lib.cfc_unpack8.prepare(held, self.y)
+        return self
+
+    def run(self, stream=None):
+        self._call(stream)
+        return self.y
+
+
+class RMSNormStep(_Step):
+    """s = x + residual (without one s is x) and its root-mean-square norm y over `rows` rows of n
+    columns; with dy (and the stream's gradient ds) bound also dx (of x and of the residual) and dw.
+    With ``out8`` y is held in 8 bits (``y8``, a Held8).  With ``keep8`` the stream is kept in 8 bits
+    (``s8``) and the backward pass reads that in its place and forms y again (``y_again``)."""
+
+    def __init__(self, rows: int, n: int, dtype=torch.float32, eps: float = 1e-5,
+                 out8: bool = False, keep8: bool = False, device=None):
+        super().__init__(device)
+        self.rows, self.n, self.dtype, self.eps = rows, n, dtype, eps
+        self.out8, self.keep8 = out8, keep8
+        self.y = None if out8 else self._act(rows, n)
+        self.y8 = _lib.Held8((rows, n), self.device) if out8 else None
+        self.s8 = _lib.Held8((rows, n), self.device) if keep8 else None
+        self.rstd = self._f32(rows)
+        self.s = self.dx = self.dw = self.y_again = self.ws = None
+
+    def bind(self, x, w, residual=None, dy=None, ds=None) -> "RMSNormStep":
+        self._unbind()
+        _expect(x, "x", (self.rows, self.n), self.dtype)
+        if residual is not None and self.s is None:
+            self.s = self._act(self.rows, self.n)
+        s = None if residual is None else self.s
+        forward = (_lib.cfc_rmsnorm_forward.prepare(
+            x, w, residual, s, self.y, self.s8, self.y8, self.rstd, self.eps),)
+        backward = ()
+        if dy is not None:
+            if self.dx is None:
+                self.dx, self.dw = self._act(self.rows, self.n), self._f32(self.n)
+                self.y_again = self._act(self.rows, self.n) if self.keep8 else None
+                self.ws = _workspace(_lib.rmsnorm_workspace_bytes(self.rows, self.n), self.device)
+            stream = self.s8 if self.keep8 else x if residual is None else self.s
+            backward = (_lib.cfc_rmsnorm_backward.prepare(
+                dy, stream, w, self.rstd, self.dx, self.dw, ds, self.y_again, self.ws),)
+        self.inputs = dict(x=x, w=w, residual=residual, dy=dy, ds=ds)
+        self._forward, self._backward = forward, backward
+        return self
+
+    def outputs(self) -> dict:
+        out = {"y8": self.y8} if self.out8 else {"y": self.y}
+        if self.inputs is not None and self.inputs["residual"] is not None:
+            out["s"] = self.s
+        if self._backward:
+            out.update(dx=self.dx, dw=self.dw)
+            if self.keep8:
+                out["y_again"] = self.y_again
+        return out
+
+
+class GatedStep(_Step):
+    """Gated linear recurrence over [K, B, D]: y and the last state h.  With ``train`` it keeps the
+    states that the backward pass starts from, and a bound dy (and dh_last) gives every gradient.
+    With ``keep8`` it keeps x, f and z in 8 bits (``kept``), and the backward pass reads those in
+    their place, so that the inputs may be gone by then, and forms y again (``y_again``)."""
+
+    def __init__(self, K: int, B: int, D: int, dtype=torch.float32, train: bool = False,
+                 keep8: bool = False, device=None):
+        super().__init__(device)
+        if keep8 and not train:
+            raise ValueError("a GatedStep made without train keeps nothing")
+        self.K, self.B, self.D, self.dtype = K, B, D, dtype
+        self.train, self.keep8 = train, keep8
+        self.y, self.h = self._act(K, B, D), self._f32(B, D)
+        self.states = self.kept = self.y_again = self.ws = None
+        if train:
+            self.states = self._f32(-(-K // _lib.GATED_PERIOD), B, D)
+            code = _lib.CFC_BF16 if dtype == torch.bfloat16 else _lib.CFC_F32
+            self.ws = _workspace(_lib.gated_workspace_bytes(K, B, D, code), self.device)
+            self.dx, self.df = self._act(K, B, D), self._act(K, B, D)
+            self.dz = None
+            self.dbias, self.dh0 = self._f32(D), self._f32(B, D)
+
+    def _keep(self, z):
+        if not self.keep8:
+            return None
+        shape = (self.K, self.B, self.D)
+        if self.kept is None:
+            self.kept = (_lib.Held8(shape, self.device), _lib.Held8(shape, self.device), None)
+        if z is not None and self.kept[2] is None:
+            self.kept = (*self.kept[:2], _lib.Held8(shape, self.device))
+        return self.kept if z is not None else (*self.kept[:2], None)
+
+    def bind(self, x, f, bias=None, z=None, h0=None, lengths=None, dy=None,
+             dh_last=None) -> "GatedStep":
+        self._unbind()
+        _expect(x, "x", (self.K, self.B, self.D), self.dtype)
+        kept = self._keep(z)
+        forward = (_lib.cfc_gated_forward.prepare(x, f, self.y, bias, z, h0, lengths, self.h,
+                                                  self.states, kept),)
+        backward = ()
+        if dy is not None:
+            if not self.train:
+                raise ValueError("a GatedStep made without train keeps no states to go back from")
+            if z is not None and self.dz is None:
+                self.dz = self._act(self.K, self.B, self.D)
+            if self.keep8 and self.y_again is None:
+                self.y_again = self._act(self.K, self.B, self.D)
+            read = (None, None) if kept else (x, f)
+            backward = (_lib.cfc_gated_backward.prepare(
+                dy, *read, self.states, self.dx, self.df, bias, None if kept else z, lengths, dh_last,
+                None if z is None else self.dz, None if bias is None else self.dbias, self.dh0,
+                self.y_again, kept, self.ws),)
+        self.inputs = dict(x=x, f=f, bias=bias, z=z, h0=h0, lengths=lengths, dy=dy,
+                           dh_last=dh_last)
+        self._forward, self._backward = forward, backward
+        return self
+
+    def outputs(self) -> dict:
+        out = {"y": self.y, "h": self.h}
+        if self._backward:
+            out.update(dx=self.dx, df=self.df)
+            if self.inputs["z"] is not None:
+                out["dz"] = self.dz
+            if self.inputs["bias"] is not None:
+                out["dbias"] = self.dbias
+            out["dh0"] = self.dh0
+            if self.keep8:
+                out["y_again"] = self.y_again
+        return out
+
+
+class GatedToken:
+    """One token per sequence of the gated linear recurrence: y [B, D] and the new state [B, D]."""
+
+    def __init__(self, B: int, D: int, dtype=torch.float32, device=None):
+        self.y = torch.empty((B, D), dtype=dtype, device=_device(device))
+
+    def bind(self, x, f, state, bias=None, z=None, new_state=None) -> "GatedToken":
+        """new_state None: the state is updated in place."""
+        new_state = state if new_state is None else new_state
+        self._call = _lib.cfc_gated_step.prepare(x, f, state, new_state, self.y, bias, z)
+        self.state = new_state
+        return self
+
+    def run(self, stream=None):
+        self._call(stream)
+        return self.y, self.state
+
+
+class Weights4:
+    """A matrix [N, K] of 4-bit weights in the order in which the products read them, laid out once
+    (on the current stream) from codes [N, ceil(K / 2)] (uint8, two to a byte, the even column in
+    the low half) and scales [N, ceil(K / group)] (bfloat16)."""
+
+    def __init__(self, codes, scales, K: int, group: int):
+        self.N, self.K, self.group = codes.shape[0], K, group
+        self.data = torch.empty(_lib.weights4_bytes(self.N, K, group), dtype=torch.uint8,
+                                device=codes.device)
+        _lib.cfc_weights4_lay_out(codes, scales, K, group, self.data)
+
+    @staticmethod
+    def quantized(W, group: int):
+        """(codes, scales) of the 4-bit weights nearest to W [N, K]."""
+        N, K = W.shape
+        codes = torch.empty((N, (K + 1) // 2), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((N, -(-K // max(group, 1))), dtype=torch.bfloat16, device=W.device)
+        _lib.cfc_weights4_quantize(W, codes, scales, group)
+        return codes, scales
+
+    @classmethod
+    def of(cls, W, group: int = 128) -> "Weights4":
+        """The 4-bit weights nearest to W [N, K] (float32 or bfloat16), laid out."""
+        return cls(*cls.quantized(W, group), W.shape[1], group)
+
+
+class MatvecStep(_Step):
+    """y [M, N] = x W^T for M rows and a matrix of 4-bit weights."""
+
+    def __init__(self, M: int, weights: Weights4, dtype=torch.float32, device=None):
+        super().__init__(device)
+        self.M, self.weights, self.dtype = M, weights, dtype
+        self.y = self._act(M, weights.N)
+
+    def bind(self, x) -> "MatvecStep":
+        self._unbind()
+        w = self.weights
+        _expect(x, "x", (self.M, w.K), self.dtype)
+        self._forward = (_lib.cfc_matvec4.prepare(x, w.data, w.N, w.group, self.y),)
+        self.inputs = dict(x=x)
+        return self
+
+    def outputs(self) -> dict:
+        return {"y": self.y}
