@@ -180,7 +180,7 @@ int cfc_gated_forward(const cfc_gated_args* a, void* y, long long y_t, long long
   if (rc == CFC_OK) rc = kept_call(kept, false, &q);
   if (rc != CFC_OK) return rc;
   if (off(h_last, 4) || off(states, 4)) return CFC_ERR_MISALIGNED;
-  rc = cfc::device_ready();
+  rc = cfc::device_ready(&q.status);
   if (rc != CFC_OK) return rc;
   q.y = y; q.y_t = y_t; q.y_b = y_b; q.h_last = h_last; q.states = states;
   return launched(cfc::gated_fwd_launch(q, on(stream)));
@@ -212,7 +212,7 @@ int cfc_gated_backward(const cfc_gated_args* a, const cfc_gated_kept* kept, cons
   if (off(states, 4) || off(dh_last, 4) || off(g->dbias, 4) || off(g->dh0, 4))
     return CFC_ERR_MISALIGNED;
   rc = ws_check(ws, ws_bytes, cfc::gated_ws_floats(q.B, q.K, q.D, q.bf16) * sizeof(float));
-  if (rc == CFC_OK) rc = cfc::device_ready();
+  if (rc == CFC_OK) rc = cfc::device_ready(&q.status);
   if (rc != CFC_OK) return rc;
   q.states = const_cast<float*>(states);
   q.dy = dy; q.dy_t = dy_t; q.dy_b = dy_b; q.dh_last = dh_last;

@@ -17,6 +17,9 @@ struct Held8 {
   uint8_t *codes, *scales;
 };
 
+// out[n] <- the sum of `rows` rows of n partial sums (cfc_merge.cu); `pdl`: as a dependent launch.
+cudaError_t merge_launch(const float* in, int rows, int n, float* out, cudaStream_t s, bool pdl);
+
 struct RmsCall {
   const void *x, *residual, *dy, *ds;  // backward: x is the stream s (null: s8 is read)
   long long ldx, ldr, lddy, ldds;
@@ -61,6 +64,7 @@ struct GatedCall {
   void *dx, *df, *dz;
   long long dx_t, dx_b, df_t, df_b, dz_t, dz_b;
   float *dbias, *dh0, *ws;
+  int* status;                         // device word for waits that ran out
 };
 size_t gated_ws_floats(int B, int K, int D, bool bf16);
 cudaError_t gated_fwd_launch(const GatedCall& q, cudaStream_t s);

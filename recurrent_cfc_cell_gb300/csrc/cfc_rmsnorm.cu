@@ -7,20 +7,22 @@
 //             dx = rstd (g - hat sum(g hat) / n) + ds,  dw = sum_rows dy hat
 //
 // Every pass is bound by memory: a row stays in registers between its sum and its results.  A row
-// belongs to a team: 4 to 32 lanes of a warp up to 1024 columns, a CTA of 128 to 512 threads up to
-// 8192.  Longer rows are read twice (the second time from L2).  Where all tensors are aligned and n
-// is a multiple of 8, a lane loads and stores eight columns at once, and four neighbouring lanes
-// hold a block of the 8-bit form; otherwise neighbouring lanes have neighbouring columns, a warp's
-// loads are consecutive whatever the rows' alignment, and a warp holds a block.
+// belongs to a team: 4 to 32 lanes of a warp up to 256 columns, a CTA of up to 1024 threads up to 8192.
+// Longer rows are read twice (the second time from L2).  Lanes load and store eight columns at once;
+// where rows start anywhere (an odd width) their groups of eight follow the memory's alignment, and
+// the row's two ends are stored element by element.  Tensors that are aligned differently from one
+// another, and odd widths in 8 bits, whose blocks begin with the row, are done element by element:
+// neighbouring lanes have neighbouring columns, and a warp holds a block.
 //
 // dw is summed in each lane's registers over the rows of its team, over the CTA's teams in shared
-// memory, and over the CTAs by reduce_axis0: no atomics, an order that depends on the sizes and on
-// which of the two layouts runs.
+// memory, and over the CTAs by a second launch: no atomics, an order that depends on the sizes and on
+// the rows' alignment.
 #include "cfc_gated_kernels.h"
 #include "cfc_held8.cuh"
-#include "cfc_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
+
+#include <type_traits>
 
 namespace cfc {
 namespace {
@@ -28,98 +30,183 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kLongRow = 8192;   // columns from which rows are read twice
 
-// A team of TPR threads a row, SLOTS pieces a thread; a piece is eight columns (VEC) or one.
-template <int TPR_, int SLOTS_, bool VEC_>
+// How rows lie.  kScalar: anyhow; a thread's columns are a team apart, so that a warp's accesses are
+// consecutive.  kAligned: every row of every tensor starts on a group of eight columns.  kShifted:
+// row r of every tensor starts at the same place within a group of eight (an odd width, say): a
+// thread's groups follow the memory's alignment, and what of a group lies in the rows before and
+// after is left out.
+enum Layout { kScalar, kAligned, kShifted };
+
+// A team of up to TPR threads a row, SLOTS pieces a thread; a piece is eight columns, or one
+// (kScalar).  Teams of a warp's lanes have TPR of them; the others are a whole CTA, of as many warps
+// as the row needs.
+template <int TPR_, int SLOTS_, Layout LY_>
 struct Team {
   static constexpr int TPR = TPR_, SLOTS = SLOTS_;
-  static constexpr bool VEC = VEC_, kWarp = TPR <= 32;
+  static constexpr Layout LY = LY_;
+  static constexpr bool VEC = LY != kScalar, kWarp = TPR <= 32;
   static constexpr int W = VEC ? 8 : 1;            // columns of a piece
   static constexpr int E = SLOTS * W;              // columns of a thread
   static constexpr int kThreads = kWarp ? 256 : TPR;
   static constexpr int kTeams = kThreads / TPR;
   static constexpr int kCols = TPR * E;
-  static __device__ __forceinline__ int team() { return threadIdx.x / TPR; }
-  static __device__ __forceinline__ int col(int slot) {
-    return (slot * TPR + static_cast<int>(threadIdx.x) % TPR) * W;
+  static __device__ __forceinline__ int team() { return kWarp ? threadIdx.x / TPR : 0; }
+};
+
+// A thread's columns.
+template <typename TM>
+struct At {
+  int n, rows, first, step;  // first: its first column, step: from a piece's to the next one's
+  // `row0`: the team's first row of a tensor (kShifted: all its rows start at the same place).
+  template <typename T>
+  __device__ __forceinline__ At(int n_, int rows_, const T* row0) : n(n_), rows(rows_) {
+    const int lane = TM::kWarp ? threadIdx.x % TM::TPR : threadIdx.x;
+    first = lane * TM::W;
+    step = (TM::kWarp ? TM::TPR : static_cast<int>(blockDim.x)) * TM::W;
+    if constexpr (TM::LY == kShifted)
+      first -= static_cast<int>(reinterpret_cast<uintptr_t>(row0) / sizeof(T) % 8);
+  }
+  __device__ __forceinline__ int col(int slot) const { return first + slot * step; }
+  // Column i of a piece is in the row.
+  __device__ __forceinline__ bool in(int slot, int i) const {
+    return static_cast<unsigned>(col(slot) + i) < static_cast<unsigned>(n);
+  }
+  // Some of the piece is in the row; all of it is.
+  __device__ __forceinline__ bool some(int slot) const {
+    return col(slot) < n && (TM::LY != kShifted || col(slot) > -8);
+  }
+  __device__ __forceinline__ bool whole(int slot) const {
+    return TM::LY != kShifted || (col(slot) >= 0 && col(slot) + 8 <= n);
   }
 };
 
-// A thread's columns of a row as they are stored; columns that do not exist are 0.
+__device__ __forceinline__ void add8(Raw8<float>& a, const Raw8<float>& b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a.v[j] += b.v[j];
+}
+__device__ __forceinline__ void add8(Raw8<__nv_bfloat16>& a, const Raw8<__nv_bfloat16>& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    a.w[j] = bf16x2_rn(bf16_lo_f32(a.w[j]) + bf16_lo_f32(b.w[j]),
+                       bf16_hi_f32(a.w[j]) + bf16_hi_f32(b.w[j]));
+}
+__device__ __forceinline__ void store_raw(float* p, const Raw8<float>& r) { store8(p, r.v); }
+__device__ __forceinline__ void store_raw(__nv_bfloat16* p, const Raw8<__nv_bfloat16>& r) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+}
+
+// A thread's columns of row `row` as they are stored; columns that are not in the row come out as 0.
 template <typename T, typename TM>
-struct Piece;
-template <typename T, int TPR, int SLOTS>
-struct Piece<T, Team<TPR, SLOTS, true>> {
-  using TM = Team<TPR, SLOTS, true>;
-  Raw8<T> raw[SLOTS];
-  __device__ __forceinline__ void load(const T* row, int n, bool ok) {
+struct Piece {
+  std::conditional_t<TM::VEC, Raw8<T>, T> raw[TM::SLOTS];
+  __device__ __forceinline__ void load(const At<TM>& at, const T* p, long long row, bool ok) {
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j) {
-      if (ok && TM::col(j) < n) raw[j].load(row + TM::col(j));
-      else raw[j].clear();
+    for (int j = 0; j < TM::SLOTS; ++j) {
+      const int c = at.col(j);
+      if constexpr (!TM::VEC) {
+        raw[j] = ok && c < at.n ? p[c] : from_f32<T>(0.f);
+      } else if (!(ok && at.some(j))) {
+        raw[j].clear();
+      } else if (TM::LY == kAligned || ((c >= 0 || row > 0) && (c + 8 <= at.n || row + 1 < at.rows))) {
+        // At its row's ends a group reaches into the rows before and after, but for the tensor's
+        // first and last one.
+        raw[j].load(p + c);
+      } else {
+        raw[j].clear();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at.in(j, i)) raw[j].set(i, p[c + i]);
+      }
     }
   }
-  __device__ __forceinline__ void get(float (&v)[TM::E]) const {
+  __device__ __forceinline__ void get(const At<TM>& at, float (&v)[TM::E]) const {
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j) {
-      float p[8];
-      raw[j].get(p);
+    for (int j = 0; j < TM::SLOTS; ++j) {
+      if constexpr (!TM::VEC) {
+        v[j] = to_f32(raw[j]);
+      } else {
+        float p[8];
+        raw[j].get(p);
+        if (!at.whole(j)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * j + i] = p[i];
+          for (int i = 0; i < 8; ++i) p[i] = at.in(j, i) ? p[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * j + i] = p[i];
+      }
     }
   }
-};
-template <typename T, int TPR, int SLOTS>
-struct Piece<T, Team<TPR, SLOTS, false>> {
-  using TM = Team<TPR, SLOTS, false>;
-  T raw[SLOTS];
-  __device__ __forceinline__ void load(const T* row, int n, bool ok) {
+  // The sum with another row's, rounded to T.
+  __device__ __forceinline__ void add(const Piece& r) {
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j)
-      raw[j] = ok && TM::col(j) < n ? row[TM::col(j)] : from_f32<T>(0.f);
-  }
-  __device__ __forceinline__ void get(float (&v)[TM::E]) const {
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) v[j] = to_f32(raw[j]);
+    for (int j = 0; j < TM::SLOTS; ++j) {
+      if constexpr (TM::VEC) add8(raw[j], r.raw[j]);
+      else raw[j] = from_f32<T>(to_f32(raw[j]) + to_f32(r.raw[j]));
+    }
   }
 };
 
 template <typename TM, typename T>
-__device__ __forceinline__ void store_row(T* row, const float (&v)[TM::E], int n, bool ok) {
+__device__ __forceinline__ void store_row(const At<TM>& at, T* row, const float (&v)[TM::E], bool ok) {
 #pragma unroll
   for (int j = 0; j < TM::SLOTS; ++j) {
-    if (!(ok && TM::col(j) < n)) continue;
+    if (!(ok && at.some(j))) continue;
     if constexpr (TM::VEC) {
-      float p[8];
+      if (at.whole(j)) {
+        float p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = v[8 * j + i];
-      store8(row + TM::col(j), p);
+        for (int i = 0; i < 8; ++i) p[i] = v[8 * j + i];
+        store8(row + at.col(j), p);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at.in(j, i)) row[at.col(j) + i] = from_f32<T>(v[8 * j + i]);
+      }
     } else {
-      row[TM::col(j)] = from_f32<T>(v[j]);
+      row[at.col(j)] = from_f32<T>(v[j]);
+    }
+  }
+}
+// The same of values that are held as T already.
+template <typename TM, typename T>
+__device__ __forceinline__ void store_row(const At<TM>& at, T* row, const Piece<T, TM>& x,
+                                          const float (&v)[TM::E], bool ok) {
+#pragma unroll
+  for (int j = 0; j < TM::SLOTS; ++j) {
+    if (!(ok && at.some(j))) continue;
+    if constexpr (TM::VEC) {
+      if (at.whole(j)) {
+        store_raw(row + at.col(j), x.raw[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at.in(j, i)) row[at.col(j) + i] = from_f32<T>(v[8 * j + i]);
+      }
+    } else {
+      row[at.col(j)] = x.raw[j];
     }
   }
 }
 
 template <typename TM>
-__device__ __forceinline__ void load_par(const float* p, float (&v)[TM::E], int n) {
+__device__ __forceinline__ void load_par(const At<TM>& at, const float* p, float (&v)[TM::E]) {
 #pragma unroll
   for (int j = 0; j < TM::SLOTS; ++j)
 #pragma unroll
-    for (int i = 0; i < TM::W; ++i) {
-      const int c = TM::col(j) + i;
-      v[j * TM::W + i] = c < n ? __ldg(p + c) : 0.f;
-    }
+    for (int i = 0; i < TM::W; ++i)
+      v[j * TM::W + i] = at.in(j, i) ? __ldg(p + at.col(j) + i) : 0.f;
 }
 
 // A row to 8 bits (all lanes of every warp call; columns that do not exist hold 0).
 template <typename TM>
-__device__ __forceinline__ void store_held(const Held8& h, long long row, const float (&v)[TM::E],
-                                           int n, bool ok) {
-  uint8_t* const codes = h.codes + row * n;
-  uint8_t* const scales = h.scales + row * held_blocks(n);
+__device__ __forceinline__ void store_held(const At<TM>& at, const Held8& h, long long row,
+                                           const float (&v)[TM::E], bool ok) {
+  uint8_t* const codes = h.codes + row * at.n;
+  uint8_t* const scales = h.scales + row * held_blocks(at.n);
 #pragma unroll
   for (int j = 0; j < TM::SLOTS; ++j) {
-    const int c = TM::col(j);
-    const bool in = ok && c < n;
+    const int c = at.col(j);
+    const bool in = ok && c < at.n;
     uint32_t byte;
     if constexpr (TM::VEC) {
       float p[8];
@@ -134,57 +221,53 @@ __device__ __forceinline__ void store_held(const Held8& h, long long row, const 
     if (in && c % kHeldBlock == 0) scales[c / kHeldBlock] = static_cast<uint8_t>(byte);
   }
 }
+// A thread's columns of a row in 8 bits, as they are held.
 template <typename TM>
-__device__ __forceinline__ void load_held(const Held8& h, long long row, float (&v)[TM::E], int n,
-                                          bool ok) {
-  const uint8_t* const codes = h.codes + row * n;
-  const uint8_t* const scales = h.scales + row * held_blocks(n);
-  if constexpr (TM::VEC) {
-    uint2 r[TM::SLOTS];
-    uint32_t byte[TM::SLOTS];
+struct HeldPiece {
+  using C = std::conditional_t<TM::VEC, uint2, uint8_t>;
+  C codes[TM::SLOTS];
+  uint8_t byte[TM::SLOTS];
+  __device__ __forceinline__ void load(const At<TM>& at, const Held8& h, long long row, bool ok) {
 #pragma unroll
     for (int j = 0; j < TM::SLOTS; ++j) {
-      const int c = TM::col(j);
-      const bool in = ok && c < n;
-      r[j] = in ? *reinterpret_cast<const uint2*>(codes + c) : make_uint2(0u, 0u);
-      byte[j] = in ? scales[c / kHeldBlock] : 1u;
+      const int c = at.col(j);
+      const bool in = ok && c < at.n;
+      codes[j] = in ? *reinterpret_cast<const C*>(h.codes + row * at.n + c) : C{};
+      byte[j] = in ? h.scales[row * held_blocks(at.n) + c / kHeldBlock] : uint8_t(1);
     }
-#pragma unroll
-    for (int j = 0; j < TM::SLOTS; ++j) {
-      float p[8];
-      held_unpack8(r[j], byte[j], p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * j + i] = p[i];
-    }
-  } else {
-    uint32_t r[TM::SLOTS], byte[TM::SLOTS];
-#pragma unroll
-    for (int j = 0; j < TM::SLOTS; ++j) {
-      const int c = TM::col(j);
-      const bool in = ok && c < n;
-      r[j] = in ? codes[c] : 0u;
-      byte[j] = in ? scales[c / kHeldBlock] : 1u;
-    }
-#pragma unroll
-    for (int j = 0; j < TM::SLOTS; ++j) v[j] = held_values2(r[j]).x * held_up(byte[j]);
   }
-}
+  __device__ __forceinline__ void get(float (&v)[TM::E]) const {
+#pragma unroll
+    for (int j = 0; j < TM::SLOTS; ++j) {
+      if constexpr (TM::VEC) {
+        float p[8];
+        held_unpack8(codes[j], byte[j], p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * j + i] = p[i];
+      } else {
+        v[j] = held_values2(codes[j]).x * held_up(byte[j]);
+      }
+    }
+  }
+};
 
 // The sum over a row's team, in every thread.  `part` holds two rows' partial sums in turn, so that
 // one barrier a row is enough.
 template <typename TM>
-__device__ __forceinline__ float team_sum(float v, float (*part)[16], int turn) {
+__device__ __forceinline__ float team_sum(float v, float (*part)[32], int turn) {
   constexpr int kLanes = TM::kWarp ? TM::TPR : 32;
 #pragma unroll
   for (int d = kLanes / 2; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
   if constexpr (!TM::kWarp) {
-    constexpr int kWarps = TM::TPR / 32;
     float* const p = part[turn & 1];
-    if (threadIdx.x % 32 == 0) p[threadIdx.x / 32] = v;
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) p[threadIdx.x / 32] = v;
     __syncthreads();
-    v = 0.f;
+    v = lane < static_cast<int>(blockDim.x) / 32 ? p[lane] : 0.f;
+    constexpr int kMost = TM::TPR / 32;  // a power of two
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += p[i];
+    for (int d = kMost / 2; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    v = __shfl_sync(0xffffffffu, v, 0);
   }
   return v;
 }
@@ -205,74 +288,102 @@ __device__ __forceinline__ float normed(float s, float w, float rstd) {
   return fmaf(p, rstd, low * rstd);
 }
 
+// The next row's loads are on their way while a row is worked on.  Teams' rows are a multiple of
+// eight apart, so that a team's rows start at the same place within a group of eight.
 template <typename T, typename TM>
 __global__ void __launch_bounds__(TM::kThreads) rms_fwd_kernel(const RmsCall q) {
-  __shared__ float part[2][16];
-  const int n = q.n;
+  __shared__ float part[2][32];
+  const long long step = static_cast<long long>(gridDim.x) * TM::kTeams;
+  long long row = static_cast<long long>(blockIdx.x) * TM::kTeams + TM::team();
+  const At<TM> at(q.n, q.rows, static_cast<const T*>(q.x) + row * q.ldx);
   float w[TM::E];
-  load_par<TM>(q.w, w, n);
-  int turn = 0;
-  for (long long base = static_cast<long long>(blockIdx.x) * TM::kTeams; base < q.rows;
-       base += static_cast<long long>(gridDim.x) * TM::kTeams, ++turn) {
-    const long long row = base + TM::team();
+  load_par<TM>(at, q.w, w);
+  Piece<T, TM> x_next, res_next;
+  auto fetch = [&](long long row) {
     const bool ok = row < q.rows;
-    Piece<T, TM> x, res;
-    x.load(static_cast<const T*>(q.x) + row * q.ldx, n, ok);
-    if (q.residual) res.load(static_cast<const T*>(q.residual) + row * q.ldr, n, ok);
+    x_next.load(at, static_cast<const T*>(q.x) + row * q.ldx, row, ok);
+    if (q.residual)
+      res_next.load(at, static_cast<const T*>(q.residual) + row * q.ldr, row, ok);
+  };
+  fetch(row);
+  int turn = 0;
+  // Warps stay together: `row` is the first of its CTA's teams' where the loop ends.
+  for (; row - TM::team() < q.rows; row += step, ++turn) {
+    const bool ok = row < q.rows;
+    Piece<T, TM> x = x_next;
+    if (q.residual) x.add(res_next);
+    if (row - TM::team() + step < q.rows) fetch(row + step);
     float s[TM::E];
-    x.get(s);
-    if (q.residual) {
-      float r[TM::E];
-      res.get(r);
-#pragma unroll
-      for (int i = 0; i < TM::E; ++i) s[i] = to_f32(from_f32<T>(s[i] + r[i]));
-    }
-    if (q.s) store_row<TM>(static_cast<T*>(q.s) + row * q.lds, s, n, ok);
+    x.get(at, s);
+    if (q.s) store_row<TM>(at, static_cast<T*>(q.s) + row * q.lds, x, s, ok);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < TM::E; ++i) sum = fmaf(s[i], s[i], sum);
-    const float rstd = rstd_of(team_sum<TM>(sum, part, turn), n, q.eps);
+    const float rstd = rstd_of(team_sum<TM>(sum, part, turn), q.n, q.eps);
     if (ok && q.rstd && threadIdx.x % TM::TPR == 0) q.rstd[row] = rstd;
-    if (q.s8.codes) store_held<TM>(q.s8, row, s, n, ok);
+    if constexpr (TM::LY != kShifted) {
+      if (q.s8.codes) store_held<TM>(at, q.s8, row, s, ok);
+    }
     if (!q.y && !q.y8.codes) continue;
 #pragma unroll
     for (int i = 0; i < TM::E; ++i) s[i] = normed(s[i], w[i], rstd);
-    if (q.y) store_row<TM>(static_cast<T*>(q.y) + row * q.ldy, s, n, ok);
-    if (q.y8.codes) store_held<TM>(q.y8, row, s, n, ok);
+    if (q.y) store_row<TM>(at, static_cast<T*>(q.y) + row * q.ldy, s, ok);
+    if constexpr (TM::LY != kShifted) {
+      if (q.y8.codes) store_held<TM>(at, q.y8, row, s, ok);
+    }
   }
 }
 
+// CTAs of the backward pass that an SM holds, which sets their registers and the number of partial
+// sums of dw: 1024 threads of an SM in bf16 (16384 x 2048 54 us; 768 threads 59 us; 131072 x 512 94 and
+// 102 us), 768 where a warp has a row or rows are shifted (262144 x 256 95 us; 1024 threads 105 us;
+// 9001 x 1537 33 and 35 us), 512 in fp32, whose rows take twice the registers.
+template <typename T, typename TM>
+constexpr int bwd_per_sm() {
+  const int threads = sizeof(T) == 4 || !TM::VEC ? 512 : TM::TPR == 32 || TM::LY == kShifted ? 768 : 1024;
+  return threads > TM::kThreads ? threads / TM::kThreads : 1;
+}
+
 template <typename T, typename TM, bool KEPT>
-__global__ void __launch_bounds__(TM::kThreads) rms_bwd_kernel(const RmsCall q, float* dw) {
-  __shared__ float part[2][16];
-  extern __shared__ float sums[];  // [warps][kCols], teams of a warp only
+__global__ void __launch_bounds__(TM::kThreads, bwd_per_sm<T, TM>()) rms_bwd_kernel(const RmsCall q, float* dw) {
+  __shared__ float part[2][32];
+  extern __shared__ float sums[];  // [teams][kCols], teams of a warp only
+  grid_dep_launch_dependents();
   const int n = q.n;
+  const long long step = static_cast<long long>(gridDim.x) * TM::kTeams;
+  long long row = static_cast<long long>(blockIdx.x) * TM::kTeams + TM::team();
+  const At<TM> at(n, q.rows, static_cast<const T*>(q.dy) + row * q.lddy);
   float w[TM::E], acc[TM::E];
-  load_par<TM>(q.w, w, n);
+  load_par<TM>(at, q.w, w);
 #pragma unroll
   for (int i = 0; i < TM::E; ++i) acc[i] = 0.f;
-  int turn = 0;
-  for (long long base = static_cast<long long>(blockIdx.x) * TM::kTeams; base < q.rows;
-       base += static_cast<long long>(gridDim.x) * TM::kTeams, ++turn) {
-    const long long row = base + TM::team();
+  Piece<T, TM> dy_next, s_next;
+  HeldPiece<TM> held_next;
+  float rstd_next = 0.f;
+  auto fetch = [&](long long row) {
     const bool ok = row < q.rows;
-    Piece<T, TM> pdy, ps, pds;
+    dy_next.load(at, static_cast<const T*>(q.dy) + row * q.lddy, row, ok);
+    if constexpr (KEPT) held_next.load(at, q.s8, row, ok);
+    else s_next.load(at, static_cast<const T*>(q.x) + row * q.ldx, row, ok);
+    rstd_next = ok ? q.rstd[row] : 0.f;
+  };
+  fetch(row);
+  int turn = 0;
+  for (; row - TM::team() < q.rows; row += step, ++turn) {
+    const bool ok = row < q.rows;
+    const float rstd = rstd_next;
     float s[TM::E], dy[TM::E];
-    pdy.load(static_cast<const T*>(q.dy) + row * q.lddy, n, ok);
-    if (q.ds) pds.load(static_cast<const T*>(q.ds) + row * q.ldds, n, ok);
-    if constexpr (KEPT) {
-      load_held<TM>(q.s8, row, s, n, ok);
-    } else {
-      ps.load(static_cast<const T*>(q.x) + row * q.ldx, n, ok);
-      ps.get(s);
-    }
-    pdy.get(dy);
-    const float rstd = ok ? q.rstd[row] : 0.f;
+    if constexpr (KEPT) held_next.get(s);
+    else s_next.get(at, s);
+    dy_next.get(at, dy);
+    Piece<T, TM> ds;  // wanted last
+    if (q.ds) ds.load(at, static_cast<const T*>(q.ds) + row * q.ldds, row, ok);
+    if (row - TM::team() + step < q.rows) fetch(row + step);
     if (q.y) {
       float y[TM::E];
 #pragma unroll
       for (int i = 0; i < TM::E; ++i) y[i] = normed(s[i], w[i], rstd);
-      store_row<TM>(static_cast<T*>(q.y) + row * q.ldy, y, n, ok);
+      store_row<TM>(at, static_cast<T*>(q.y) + row * q.ldy, y, ok);
     }
     float dot = 0.f;
 #pragma unroll
@@ -286,30 +397,25 @@ __global__ void __launch_bounds__(TM::kThreads) rms_bwd_kernel(const RmsCall q, 
 #pragma unroll
     for (int i = 0; i < TM::E; ++i) s[i] = rstd * fmaf(-mean, s[i], dy[i]);
     if (q.ds) {
-      pds.get(dy);
+      ds.get(at, dy);
 #pragma unroll
       for (int i = 0; i < TM::E; ++i) s[i] += dy[i];
     }
-    store_row<TM>(static_cast<T*>(q.dx) + row * q.lddx, s, n, ok);
+    store_row<TM>(at, static_cast<T*>(q.dx) + row * q.lddx, s, ok);
   }
   float* const out = dw + static_cast<size_t>(blockIdx.x) * n;
   if constexpr (TM::kWarp) {
+    float* const mine = sums + TM::team() * TM::kCols;
 #pragma unroll
-    for (int i = 0; i < TM::E; ++i)
+    for (int j = 0; j < TM::SLOTS; ++j)
 #pragma unroll
-      for (int d = TM::TPR; d < 32; d *= 2) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
-    float* const mine = sums + threadIdx.x / 32 * TM::kCols;
-    if (threadIdx.x % 32 < TM::TPR) {
-#pragma unroll
-      for (int j = 0; j < TM::SLOTS; ++j)
-#pragma unroll
-        for (int i = 0; i < TM::W; ++i) mine[TM::col(j) + i] = acc[j * TM::W + i];
-    }
+      for (int i = 0; i < TM::W; ++i)
+        if (at.in(j, i)) mine[at.col(j) + i] = acc[j * TM::W + i];
     __syncthreads();
     for (int c = threadIdx.x; c < n; c += TM::kThreads) {
       float v = sums[c];
-#pragma unroll
-      for (int i = 1; i < TM::kThreads / 32; ++i) v += sums[i * TM::kCols + c];
+#pragma unroll 8
+      for (int i = 1; i < TM::kTeams; ++i) v += sums[i * TM::kCols + c];
       out[c] = v;
     }
   } else {
@@ -317,7 +423,7 @@ __global__ void __launch_bounds__(TM::kThreads) rms_bwd_kernel(const RmsCall q, 
     for (int j = 0; j < TM::SLOTS; ++j)
 #pragma unroll
       for (int i = 0; i < TM::W; ++i)
-        if (TM::col(j) + i < n) out[TM::col(j) + i] = acc[j * TM::W + i];
+        if (at.in(j, i)) out[at.col(j) + i] = acc[j * TM::W + i];
   }
 }
 
@@ -325,11 +431,11 @@ __global__ void __launch_bounds__(TM::kThreads) rms_bwd_kernel(const RmsCall q, 
 // passes ----
 
 constexpr int kLongThreads = 512;
-using LongTeam = Team<kLongThreads, 1, false>;
+using LongTeam = Team<kLongThreads, 1, kScalar>;
 
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) rms_long_fwd_kernel(const RmsCall q) {
-  __shared__ float part[2][16];
+  __shared__ float part[2][32];
   const int n = q.n, whole = held_blocks(n) * kHeldBlock;
   int turn = 0;
   for (long long row = blockIdx.x; row < q.rows; row += gridDim.x, ++turn) {
@@ -403,7 +509,7 @@ __global__ void __launch_bounds__(256) rms_long_dw_kernel(const RmsCall q, int p
 
 template <typename T, bool KEPT>
 __global__ void __launch_bounds__(kLongThreads) rms_long_bwd_kernel(const RmsCall q) {
-  __shared__ float part[2][16];
+  __shared__ float part[2][32];
   const int n = q.n;
   int turn = 0;
   for (long long row = blockIdx.x; row < q.rows; row += gridDim.x, ++turn) {
@@ -425,60 +531,85 @@ __global__ void __launch_bounds__(kLongThreads) rms_long_bwd_kernel(const RmsCal
 
 // ---- launches ----
 
-bool aligned(const void* p, long long ld, bool bf16) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % (bf16 ? 16 : 32) == 0 && ld % 8 == 0);
-}
-bool held_aligned(const Held8& h) { return reinterpret_cast<uintptr_t>(h.codes) % 8 == 0; }
-bool vectors(const RmsCall& q) {
-  return q.n % 8 == 0 && aligned(q.x, q.ldx, q.bf16) && aligned(q.residual, q.ldr, q.bf16) &&
-         aligned(q.dy, q.lddy, q.bf16) && aligned(q.ds, q.ldds, q.bf16) &&
-         aligned(q.s, q.lds, q.bf16) && aligned(q.y, q.ldy, q.bf16) &&
-         aligned(q.dx, q.lddx, q.bf16) && held_aligned(q.y8) && held_aligned(q.s8);
-}
-
-// f of the smallest team that covers n columns.
-template <typename F>
-cudaError_t with_team(int n, bool vec, F&& f) {
-  if (vec) {
-    if (n <= 32) return f(Team<4, 1, true>{});
-    if (n <= 64) return f(Team<8, 1, true>{});
-    if (n <= 128) return f(Team<16, 1, true>{});
-    if (n <= 256) return f(Team<32, 1, true>{});
-    if (n <= 512) return f(Team<32, 2, true>{});
-    if (n <= 1024) return f(Team<128, 1, true>{});
-    if (n <= 2048) return f(Team<256, 1, true>{});
-    if (n <= 4096) return f(Team<512, 1, true>{});
-    return f(Team<512, 2, true>{});
+struct Rows {
+  const void* p;
+  long long ld;
+};
+// The layout that all rows there are allow; what is held in 8 bits has blocks that begin with the row.
+Layout layout(const RmsCall& q) {
+  const Rows r[] = {{q.x, q.ldx}, {q.residual, q.ldr}, {q.dy, q.lddy}, {q.ds, q.ldds},
+                    {q.s, q.lds}, {q.y, q.ldy}, {q.dx, q.lddx}};
+  const bool held = q.s8.codes || q.y8.codes;
+  const uintptr_t e = q.bf16 ? 2 : 4;
+  bool aligned = q.n % 8 == 0 && reinterpret_cast<uintptr_t>(q.s8.codes) % 8 == 0 &&
+                 reinterpret_cast<uintptr_t>(q.y8.codes) % 8 == 0;
+  bool alike = !held && q.n >= 8 && q.n <= kLongRow - 7;
+  const Rows* first = nullptr;
+  for (const Rows& a : r) {
+    if (!a.p) continue;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.p);
+    aligned = aligned && at % (8 * e) == 0 && a.ld % 8 == 0;
+    alike = alike && a.ld >= q.n;
+    if (first)
+      alike = alike && (at - reinterpret_cast<uintptr_t>(first->p)) % (8 * e) == 0 &&
+              (a.ld - first->ld) % 8 == 0;
+    else
+      first = &a;
   }
-  if (n <= 32) return f(Team<32, 1, false>{});
-  if (n <= 64) return f(Team<32, 2, false>{});
-  if (n <= 128) return f(Team<32, 4, false>{});
-  if (n <= 256) return f(Team<32, 8, false>{});
-  if (n <= 512) return f(Team<128, 4, false>{});
-  if (n <= 1024) return f(Team<128, 8, false>{});
-  if (n <= 2048) return f(Team<256, 8, false>{});
-  if (n <= 4096) return f(Team<512, 8, false>{});
-  return f(Team<512, 16, false>{});
+  return aligned ? kAligned : alike ? kShifted : kScalar;
 }
 
-int most_ctas(int threads) { return kSms * (2048 / threads); }
-int ctas_of(int rows, int teams, int threads) {
-  const int need = (rows - 1) / teams + 1, most = most_ctas(threads);
+// f of the smallest team that covers n columns and of the threads of its CTA.
+template <Layout LY, typename F>
+cudaError_t with_vec_team(int n, F&& f) {
+  const int span = LY == kShifted ? n + 7 : n, cta = (span + 255) / 256 * 32;
+  if (span <= 32) return f(Team<4, 1, LY>{}, 256);
+  if (span <= 64) return f(Team<8, 1, LY>{}, 256);
+  if (span <= 128) return f(Team<16, 1, LY>{}, 256);
+  if (span <= 256) return f(Team<32, 1, LY>{}, 256);
+  if (span <= 512) return f(Team<64, 1, LY>{}, cta);
+  if (span <= 1024) return f(Team<128, 1, LY>{}, cta);
+  if (span <= 2048) return f(Team<256, 1, LY>{}, cta);
+  if (span <= 4096) return f(Team<512, 1, LY>{}, cta);
+  return f(Team<1024, 1, LY>{}, cta);
+}
+template <typename F>
+cudaError_t with_team(int n, Layout ly, F&& f) {
+  if (ly == kAligned) return with_vec_team<kAligned>(n, f);
+  if (ly == kShifted) return with_vec_team<kShifted>(n, f);
+  const int cta = (n + 255) / 256 * 32;
+  if (n <= 32) return f(Team<32, 1, kScalar>{}, 256);
+  if (n <= 64) return f(Team<32, 2, kScalar>{}, 256);
+  if (n <= 128) return f(Team<32, 4, kScalar>{}, 256);
+  if (n <= 256) return f(Team<32, 8, kScalar>{}, 256);
+  if (n <= 512) return f(Team<64, 8, kScalar>{}, cta);
+  if (n <= 1024) return f(Team<128, 8, kScalar>{}, cta);
+  if (n <= 2048) return f(Team<256, 8, kScalar>{}, cta);
+  if (n <= 4096) return f(Team<512, 8, kScalar>{}, cta);
+  return f(Team<1024, 8, kScalar>{}, cta);
+}
+
+// CTAs for `rows`: a multiple of eight (152 is one) where a CTA has one team.
+int in_eights(int ctas, int teams) { return teams % 8 == 0 ? ctas : (ctas - 1) / 8 * 8 + 8; }
+int fwd_ctas(int rows, int teams, int threads) {
+  const int need = in_eights((rows - 1) / teams + 1, teams), most = kSms * (2048 / threads);
   return need < most ? need : most;
 }
 // CTAs of the backward pass, and so rows of the partial sums of dw: a row of them costs 8 bytes a
 // column to write and read, so a CTA takes four rows of a team at least once all SMs have one.
-int bwd_ctas(int rows, int teams, int threads) {
-  const int most = kSms * (1024 / threads), need = (rows - 1) / teams + 1;
-  const int want = need / 4 > kSms ? need / 4 : kSms;
+template <typename T, typename TM>
+int bwd_ctas(int rows) {
+  const int most = kSms * bwd_per_sm<T, TM>(), need = in_eights((rows - 1) / TM::kTeams + 1, TM::kTeams);
+  const int want = need / 4 > kSms ? in_eights(need / 4, TM::kTeams) : kSms;
   return need < want ? need : want < most ? want : most;
 }
 int long_splits(int rows) { return rows < 64 ? 1 : rows / 64 < 64 ? rows / 64 : 64; }
-int partials(int rows, int n, bool vec) {
+template <typename T>
+int partials(int rows, int n, Layout ly) {
   if (n > kLongRow) return long_splits(rows);
   int p = 1;
-  (void)with_team(n, vec, [&](auto tm) {
-    p = bwd_ctas(rows, decltype(tm)::kTeams, decltype(tm)::kThreads);
+  (void)with_team(n, ly, [&](auto tm, int) {
+    p = rows == 1 ? 1 : bwd_ctas<T, decltype(tm)>(rows);
     return cudaSuccess;
   });
   return p;
@@ -489,14 +620,14 @@ cudaError_t fwd(const RmsCall& q, cudaStream_t s) {
   LaunchCfg c;
   c.stream = s;
   if (q.n > kLongRow) {
-    c.grid = dim3(ctas_of(q.rows, 1, kLongThreads));
+    c.grid = dim3(fwd_ctas(q.rows, 8, kLongThreads));
     c.block = dim3(kLongThreads);
     return launch(c, rms_long_fwd_kernel<T>, q);
   }
-  return with_team(q.n, vectors(q), [&](auto tm) {
+  return with_team(q.n, layout(q), [&](auto tm, int threads) {
     using TM = decltype(tm);
-    c.grid = dim3(ctas_of(q.rows, TM::kTeams, TM::kThreads));
-    c.block = dim3(TM::kThreads);
+    c.grid = dim3(fwd_ctas(q.rows, TM::kTeams, threads));
+    c.block = dim3(threads);
     return launch(c, rms_fwd_kernel<T, TM>, q);
   });
 }
@@ -505,8 +636,8 @@ template <typename T, bool KEPT>
 cudaError_t bwd(const RmsCall& q, float* dw, float* ws, cudaStream_t s) {
   LaunchCfg c;
   c.stream = s;
-  const bool vec = vectors(q);
-  const int P = partials(q.rows, q.n, vec);
+  const Layout ly = layout(q);
+  const int P = partials<T>(q.rows, q.n, ly);
   float* const first = P == 1 ? dw : ws;
   cudaError_t e;
   if (q.n > kLongRow) {
@@ -514,27 +645,36 @@ cudaError_t bwd(const RmsCall& q, float* dw, float* ws, cudaStream_t s) {
     c.block = dim3(256);
     e = launch(c, rms_long_dw_kernel<T, KEPT>, q, (q.rows - 1) / P + 1, first);
     if (e != cudaSuccess) return e;
-    c.grid = dim3(ctas_of(q.rows, 1, kLongThreads));
+    c.grid = dim3(fwd_ctas(q.rows, 8, kLongThreads));
     c.block = dim3(kLongThreads);
     e = launch(c, rms_long_bwd_kernel<T, KEPT>, q);
   } else {
-    e = with_team(q.n, vec, [&](auto tm) {
+    e = with_team(q.n, ly, [&](auto tm, int threads) {
       using TM = decltype(tm);
-      c.grid = dim3(P);
-      c.block = dim3(TM::kThreads);
-      c.smem = TM::kWarp ? sizeof(float) * TM::kThreads / 32 * TM::kCols : 0;
-      return launch(c, rms_bwd_kernel<T, TM, KEPT>, q, first);
+      if constexpr (KEPT && TM::LY == kShifted) return cudaErrorInvalidValue;  // never chosen
+      else {
+        c.grid = dim3(P);
+        c.block = dim3(threads);
+        c.smem = TM::kWarp ? sizeof(float) * TM::kTeams * TM::kCols : 0;
+        return launch(c, rms_bwd_kernel<T, TM, KEPT>, q, first);
+      }
     });
   }
   if (e != cudaSuccess || P == 1) return e;
-  return reduce_axis0_launch(ws, P, q.n, dw, s, false);
+  return merge_launch(ws, P, q.n, dw, s, q.n <= kLongRow);
 }
 
 }  // namespace
 
 size_t rms_ws_floats(int rows, int n) {
-  // Which layout runs depends on the tensors, which the sizing call does not have.
-  const int a = partials(rows, n, true), b = partials(rows, n, false), p = a > b ? a : b;
+  // Which layout and type runs depends on the tensors, which the sizing call does not have.
+  int p = 1;
+  for (const Layout ly : {kScalar, kAligned, kShifted}) {
+    if (ly == kShifted && n > kLongRow - 7) continue;
+    const int a = partials<float>(rows, n, ly), b = partials<__nv_bfloat16>(rows, n, ly);
+    p = a > p ? a : p;
+    p = b > p ? b : p;
+  }
   return p == 1 ? 0 : static_cast<size_t>(p) * n;
 }
 cudaError_t rms_fwd_launch(const RmsCall& q, cudaStream_t s) {

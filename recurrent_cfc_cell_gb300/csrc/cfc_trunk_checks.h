@@ -10,7 +10,9 @@
 #include "cfc.h"
 
 namespace cfc {
-int device_ready();  // cfc_abi.cu
+// cfc_abi.cu; the second one also gives the address of the device status word.
+int device_ready();
+int device_ready(int** status);
 
 namespace checks {
 
