@@ -12,7 +12,8 @@
 // tiles.  In a tile lane 4 g + t of a warp owns rows g and g + 8 (one 16-byte load each) and of
 // every 32 columns the eight from 8 t on, in one 32-bit word: columns j and j + 4 of the eight are
 // 16 bits apart, a pair as the tensor cores take it, and the order of columns within a product is
-// free as long as x follows it.  Scales follow the codes, 16 rows of a group together.
+// free as long as x follows it.  Scales follow the codes, 16 rows of a group together, rows g and g + 8
+// side by side.
 #include "cfc_gated_kernels.h"
 #include "cfc_launch.cuh"
 #include "cfc_trunk.cuh"
@@ -21,7 +22,9 @@ namespace cfc {
 namespace {
 
 constexpr int kTileN = 16, kTileK = 128, kTileBytes = kTileN * kTileK / 2;
-constexpr int kWarps = 8;
+// Tiles whose weights a warp has on their way together: two, so that four CTAs fit an SM (16384 x 4096,
+// one row of bf16: 12.5 us; four tiles and three CTAs 13.9, four and four 15.5, which spills).
+constexpr int kAhead = 2;
 
 struct Shape4 {
   int tn, tk, groups;   // tiles along N and K, groups of a row (padded to whole tiles)
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(256) lay_out4_kernel(const Weights4Call q) {
     const int in = static_cast<int>(i % kTileN);
     const long long rest = i / kTileN;
     const int g = static_cast<int>(rest % s.groups);
-    const int n = static_cast<int>(rest / s.groups) * kTileN + in;
+    const int n = static_cast<int>(rest / s.groups) * kTileN + in / 2 + in % 2 * 8;
     to[i] = n < q.N && g < have ? q.scales[static_cast<size_t>(n) * have + g] : uint16_t(0);
   }
 }
@@ -120,147 +123,268 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same onto sums of 0.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(at));
+  return r;
+}
+
+// Weights are read once: they do not stay in L1, where x is.
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // Codes j and j + 4 of a word, minus 8, as a pair of bf16: 0x4300 is 128, whose last place is 1.
 template <int J>
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t word) {
-  const uint32_t v = ((word >> (4 * J)) & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
+  uint32_t v;  // (word >> 4 J & 0x000f000f) | 0x43004300, in one instruction behind the shift
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * J)), "r"(0x000f000fu), "r"(0x43004300u));
+  uint32_t r;  // v * 1 - 136
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3f803f80u), "r"(0xc308c308u));
+  return r;
 }
 
 // Eight neighbouring values of a row of x in the order of the codes' pairs (0 4, 1 5, 2 6, 3 7), in
-// as many bf16 terms as their type needs.  Columns from K on are not read.
+// as many bf16 terms as their type needs.
 template <typename T>
 struct XPiece;
 template <>
 struct XPiece<__nv_bfloat16> {
   static constexpr int kTerms = 1;
-  uint32_t term[1][4];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int left, bool vec, bool in) {
-    Raw8<__nv_bfloat16> raw;
-    raw.clear();
-    if (in && left > 0) {
-      if (vec && left >= 8) {
-        raw.load(p);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) raw.set(j, p[j]);
-      }
-    }
-    term[0][0] = __byte_perm(raw.w[0], raw.w[2], 0x5410);
-    term[0][1] = __byte_perm(raw.w[0], raw.w[2], 0x7632);
-    term[0][2] = __byte_perm(raw.w[1], raw.w[3], 0x5410);
-    term[0][3] = __byte_perm(raw.w[1], raw.w[3], 0x7632);
+  static __device__ __forceinline__ void split(const Raw8<__nv_bfloat16>& r, uint4 (&term)[1]) {
+    term[0] = make_uint4(__byte_perm(r.w[0], r.w[2], 0x5410), __byte_perm(r.w[0], r.w[2], 0x7632),
+                         __byte_perm(r.w[1], r.w[3], 0x5410), __byte_perm(r.w[1], r.w[3], 0x7632));
   }
 };
 template <>
 struct XPiece<float> {
   static constexpr int kTerms = 3;
-  uint32_t term[3][4];
+  // A term is the upper half of what is left, eight bits of it, so that three of them are all 24 and
+  // every difference is exact (of an infinity it is not a number: nothing is left).
   static __device__ __forceinline__ float rest(float a) {
     const float r = a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
     return r == r ? r : 0.f;
   }
-  __device__ __forceinline__ void load(const float* p, int left, bool vec, bool in) {
-    Raw8<float> raw;
-    raw.clear();
-    if (in && left > 0) {
-      if (vec && left >= 8) {
-        raw.load(p);
-      } else {
+  static __device__ __forceinline__ void split(const Raw8<float>& r, uint4 (&term)[3]) {
+    float v[8];
+    r.get(v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) raw.set(j, p[j]);
+    for (int i = 0; i < 3; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = __byte_perm(__float_as_uint(v[j]), __float_as_uint(v[j + 4]), 0x7632);
+        v[j] = rest(v[j]);
+        v[j + 4] = rest(v[j + 4]);
       }
-    }
-    // A term is the upper half of what is left, eight bits of it, so that three of them are all 24
-    // and every difference is exact (of an infinity it is not a number: nothing is left).
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a = raw.v[j], b = raw.v[j + 4];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        term[i][j] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-        a = rest(a);
-        b = rest(b);
-      }
+      term[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 };
 
-// A CTA: 16 rows of W against 8 rows of x; its warps take the tiles along K in turn.
-template <typename T, int GROUP>
-__global__ void __launch_bounds__(32 * kWarps) matvec4_kernel(const Weights4Call q, bool vec) {
-  __shared__ float sums[kWarps][32][4];
-  const Shape4 sh = shape4(q.N, q.K, GROUP);
+// How a CTA's warps are spread: over 1 << `rows` tiles of 16 rows of W, and `deep` of them over K.
+struct Spread {
+  int rows, deep;
+  int m;            // rows of x of a CTA, at most
+  int chunk;        // tiles along K whose part of x is in shared memory at a time
+  bool vec;         // x is read 8 values at a time
+};
+
+// A CTA: its tiles of W against up to 8 NT columns of x, a column being a term of a row of x, so that
+// two rows of fp32 and eight of bf16 cost the same.  x waits in shared memory, split and in the order
+// in which lanes take it (16 bytes for a lane's part of a product), so that the loop over the weights is
+// little but turning codes into numbers; what a code becomes serves all columns.  Columns that there are
+// not are computed from the last one and dropped.  A warp has kAhead tiles of weights on their way
+// together, the first of them while x is brought in.
+template <typename T, int GROUP, int NT>
+__global__ void __launch_bounds__(256, NT == 1 ? 4 : 2)
+    matvec4_kernel(const Weights4Call q, const Spread sp) {
+  extern __shared__ uint4 xs[];  // [tiles of a chunk][4][columns][4]; later the warps' sums
+  using X = XPiece<T>;
+  constexpr int kTerms = X::kTerms, kPer = kTileK / GROUP;  // groups of a tile
+  const int tk = (q.K - 1) / kTileK + 1, tn = (q.N - 1) / kTileN + 1;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32, g = lane / 4, t = lane % 4;
-  const int m = blockIdx.y * 8 + g;
-  const T* const x = static_cast<const T*>(q.x) + static_cast<long long>(m) * q.ldx;
-  const size_t tile0 = static_cast<size_t>(blockIdx.x) * sh.tk;
-  const uint4* const codes = reinterpret_cast<const uint4*>(q.weights) + tile0 * 64 + lane;
-  constexpr int kPer = kTileK / GROUP;  // groups of a tile
-  const uint16_t* const scales = reinterpret_cast<const uint16_t*>(q.weights + sh.codes_bytes) +
-                                 tile0 * (kPer * kTileN) + g;
-  float acc[4] = {};
-  for (int kb = w; kb < sh.tk; kb += kWarps) {
-    const uint4 lo = __ldg(codes + static_cast<size_t>(kb) * 64);
-    const uint4 hi = __ldg(codes + static_cast<size_t>(kb) * 64 + 32);
-    const uint32_t wa[4] = {lo.x, lo.y, lo.z, lo.w}, wb[4] = {hi.x, hi.y, hi.z, hi.w};
-    float part[4] = {};
+  const int m0 = blockIdx.y * sp.m, mm = min(q.M - m0, sp.m), cols = mm * kTerms;
+  const int deep = w >> sp.rows;
+  // Beyond the last tile of rows the last one is computed again, and dropped.
+  const int row_tile = min((static_cast<int>(blockIdx.x) << sp.rows) + (w & ((1 << sp.rows) - 1)), tn - 1);
+  const size_t tile0 = static_cast<size_t>(row_tile) * tk + deep;
+  const uint4* codes = reinterpret_cast<const uint4*>(q.weights) + tile0 * 64 + lane;
+  const uint32_t* scales = reinterpret_cast<const uint32_t*>(
+                               q.weights + static_cast<size_t>(tn) * tk * kTileBytes) +
+                           tile0 * (kPer * kTileN / 2) + g;
+  const int code_step = sp.deep * 64, scale_step = sp.deep * (kPer * kTileN / 2);
+  const uint32_t step = 64 * cols;  // bytes of 32 values of K in xs
+  uint32_t from[NT];                // this lane's column
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      XPiece<T> xp;
-      const int k = kb * kTileK + 32 * s + 8 * t;
-      xp.load(x + k, q.K - k, vec, m < q.M);
-      const uint32_t a0[4] = {codes_bf16<0>(wa[s]), codes_bf16<0>(wb[s]), codes_bf16<1>(wa[s]),
-                              codes_bf16<1>(wb[s])};
-      const uint32_t a1[4] = {codes_bf16<2>(wa[s]), codes_bf16<2>(wb[s]), codes_bf16<3>(wa[s]),
-                              codes_bf16<3>(wb[s])};
+  for (int nt = 0; nt < NT; ++nt)
+    from[nt] = smem_addr(xs) + (min(8 * nt + g, cols - 1) * 4 + t) * 16 + deep * 4 * step;
+  float acc[NT][4] = {};
+  uint4 lo[kAhead], hi[kAhead];
+  uint32_t sc[kAhead][kPer];
+  auto fetch = [&](int left) {  // the next kAhead tiles of the warp, of which `left` are there
 #pragma unroll
-      for (int i = 0; i < XPiece<T>::kTerms; ++i) {
-        mma_bf16(part, a0, xp.term[i][0], xp.term[i][1]);
-        mma_bf16(part, a1, xp.term[i][2], xp.term[i][3]);
+    for (int a = 0; a < kAhead; ++a) {
+      if (a >= left) break;
+      lo[a] = ld_once(codes);
+      hi[a] = ld_once(codes + 32);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sc[a][i] = __ldg(scales + i * (kTileN / 2));
+      codes += code_step;
+      scales += scale_step;
+    }
+  };
+  // Tiles of this warp in a chunk that begins at c0 (a multiple of `deep`, as chunks are).
+  auto tiles = [&](int c0) {
+    return (min(sp.chunk, tk - c0) - deep + sp.deep - 1) / sp.deep;
+  };
+  for (int c0 = 0; c0 < tk; c0 += sp.chunk) {
+    int left = tiles(c0);
+    fetch(left);
+    if (c0 > 0) __syncthreads();
+    // x of the chunk, in pieces of 8 values: 16 threads a row's part of a tile.
+    const unsigned count = min(sp.chunk, tk - c0) * mm;
+    for (unsigned i = threadIdx.x / 16; i < count; i += blockDim.x / 16) {
+      const unsigned kb = mm == 1 ? i : i / mm, m = i - kb * mm, p = threadIdx.x % 16;
+      const int k = (c0 + kb) * kTileK + 8 * p;
+      const T* const x = static_cast<const T*>(q.x) + static_cast<long long>(m0 + m) * q.ldx + k;
+      Raw8<T> raw;
+      raw.clear();
+      if (sp.vec && k + 8 <= q.K) {
+        raw.load(x);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (k + j < q.K) raw.set(j, x[j]);
       }
-      if ((s + 1) * 32 % GROUP == 0) {
-        const uint16_t* const sc = scales + (static_cast<size_t>(kb) * kPer + s * 32 / GROUP) * kTileN;
-        const float s0 = __uint_as_float(static_cast<uint32_t>(__ldg(sc)) << 16);
-        const float s1 = __uint_as_float(static_cast<uint32_t>(__ldg(sc + 8)) << 16);
-        acc[0] = fmaf(part[0], s0, acc[0]);
-        acc[1] = fmaf(part[1], s0, acc[1]);
-        acc[2] = fmaf(part[2], s1, acc[2]);
-        acc[3] = fmaf(part[3], s1, acc[3]);
-        part[0] = part[1] = part[2] = part[3] = 0.f;
+      uint4 term[kTerms];
+      X::split(raw, term);
+#pragma unroll
+      for (int j = 0; j < kTerms; ++j)
+        xs[((4 * kb + p / 4) * cols + m * kTerms + j) * 4 + p % 4] = term[j];
+    }
+    __syncthreads();
+    uint32_t at = 0;
+    while (left > 0) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a, at += 4 * sp.deep * step) {
+        if (a >= left) break;
+        const uint32_t wa[4] = {lo[a].x, lo[a].y, lo[a].z, lo[a].w};
+        const uint32_t wb[4] = {hi[a].x, hi[a].y, hi[a].z, hi[a].w};
+        float part[NT][4];
+        uint32_t xk = at;
+#pragma unroll
+        for (int s = 0; s < 4; ++s, xk += step) {
+          const uint32_t a0[4] = {codes_bf16<0>(wa[s]), codes_bf16<0>(wb[s]), codes_bf16<1>(wa[s]),
+                                  codes_bf16<1>(wb[s])};
+          const uint32_t a1[4] = {codes_bf16<2>(wa[s]), codes_bf16<2>(wb[s]), codes_bf16<3>(wa[s]),
+                                  codes_bf16<3>(wb[s])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint4 b = ld_shared(from[nt] + xk);
+            if (s * 32 % GROUP == 0) mma_first(part[nt], a0, b.x, b.y);
+            else mma_bf16(part[nt], a0, b.x, b.y);
+            mma_bf16(part[nt], a1, b.z, b.w);
+          }
+          if ((s + 1) * 32 % GROUP == 0) {
+            const uint32_t two = sc[a][s * 32 / GROUP];
+            const float s0 = bf16_lo_f32(two), s1 = bf16_hi_f32(two);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              acc[nt][0] = fmaf(part[nt][0], s0, acc[nt][0]);
+              acc[nt][1] = fmaf(part[nt][1], s0, acc[nt][1]);
+              acc[nt][2] = fmaf(part[nt][2], s1, acc[nt][2]);
+              acc[nt][3] = fmaf(part[nt][3], s1, acc[nt][3]);
+            }
+          }
+        }
       }
+      left -= kAhead;
+      fetch(left);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sums[w][lane][i] = acc[i];
   __syncthreads();
-  // Sum i of lane 4 g + t is row g + 8 (i / 2) of the tile and row 2 t + i % 2 of x.
-  if (threadIdx.x >= 128) return;
-  const int row = threadIdx.x % 16, col = threadIdx.x / 16;
-  const int from = 4 * (row % 8) + col / 2, i = 2 * (row / 8) + col % 2;
-  float v = 0.f;
+  float4* const sums = reinterpret_cast<float4*>(xs);
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) v += sums[k][from][i];
-  const int n = blockIdx.x * kTileN + row, mm = blockIdx.y * 8 + col;
-  if (n < q.N && mm < q.M)
-    static_cast<T*>(q.y)[static_cast<long long>(mm) * q.ldy + n] = from_f32<T>(v);
+  for (int nt = 0; nt < NT; ++nt)
+    sums[(w * NT + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+  __syncthreads();
+  // Sum i of lane 4 g + t is row g + 8 (i / 2) of the tile and column 2 t + i % 2.
+  const float* const all = reinterpret_cast<const float*>(sums);
+  for (int at = threadIdx.x; at < mm << (4 + sp.rows); at += blockDim.x) {
+    const int row = at % 16, m = at >> (4 + sp.rows), r = (at >> 4) - (m << sp.rows);
+    const int n = ((static_cast<int>(blockIdx.x) << sp.rows) + r) * kTileN + row;
+    if (n >= q.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i) {
+      const int col = m * kTerms + i, of = 4 * (row % 8) + col % 8 / 2, j = 2 * (row / 8) + col % 2;
+      const float* p = all + ((r * NT + col / 8) * 32 + of) * 4 + j;
+#pragma unroll 4
+      for (int k = 0; k < sp.deep; ++k, p += (NT * 128) << sp.rows) v += *p;
+    }
+    static_cast<T*>(q.y)[static_cast<long long>(m0 + m) * q.ldy + n] = from_f32<T>(v);
+  }
 }
 
-template <typename T>
+template <typename T, int GROUP>
 cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
-  const Shape4 sh = shape4(q.N, q.K, q.group);
-  const bool vec = reinterpret_cast<uintptr_t>(q.x) % (q.bf16 ? 16 : 32) == 0 && q.ldx % 8 == 0;
+  constexpr int kTerms = XPiece<T>::kTerms;
+  const Shape4 sh = shape4(q.N, q.K, GROUP);
+  const int nt = q.M * kTerms <= 8 ? 1 : q.M * kTerms <= 16 ? 2 : 4;
+  Spread sp;
+  sp.vec = reinterpret_cast<uintptr_t>(q.x) % (q.bf16 ? 16 : 32) == 0 && q.ldx % 8 == 0;
+  sp.m = 8 * nt / kTerms;
+  if (q.M < sp.m) sp.m = q.M;
+  // More tiles of rows at a time share what a CTA reads of x, where there are enough of them to give
+  // most SMs a CTA: 32 x 16384 x 4096 39 us (one tile 98 us), 16 x 8192 x 8192 34 us with two (one
+  // 51 us, four 39 us); one row of x has little to share (1 x 4096 x 16384 14.5 us, with two 20 us).
+  sp.rows = sp.m * kTerms <= 2 ? 0 : 2;
+  while (sp.rows > 0 && sh.tn >> sp.rows < 152 * 5 / 4) --sp.rows;
+  sp.deep = 8 >> sp.rows;
+  if (sh.tk < sp.deep) sp.deep = sh.tk;
+  const int bytes = 256 * sp.m * kTerms;  // of x for a tile along K; at most 8 KB
+  sp.chunk = 64 * 1024 / bytes / sp.deep * sp.deep;
+  if (sp.chunk > sh.tk) sp.chunk = sh.tk;
   LaunchCfg c;
-  c.grid = dim3(sh.tn, (q.M - 1) / 8 + 1);
-  c.block = dim3(32 * kWarps);
+  c.grid = dim3((sh.tn - 1 >> sp.rows) + 1, (q.M - 1) / sp.m + 1);
+  c.block = dim3(32 * (sp.deep << sp.rows));
+  const size_t sums = sizeof(float4) * c.block.x * nt, xs = static_cast<size_t>(sp.chunk) * bytes;
+  c.smem = sums > xs ? sums : xs;
   c.stream = s;
-  if (q.group == 32) return launch(c, matvec4_kernel<T, 32>, q, vec);
-  if (q.group == 64) return launch(c, matvec4_kernel<T, 64>, q, vec);
-  return launch(c, matvec4_kernel<T, 128>, q, vec);
+  auto run = [&](auto* kern) {
+    if (c.smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(c.smem));
+      if (e != cudaSuccess) return e;
+    }
+    return launch(c, kern, q, sp);
+  };
+  if (nt == 1) return run(matvec4_kernel<T, GROUP, 1>);
+  if (nt == 2) return run(matvec4_kernel<T, GROUP, 2>);
+  return run(matvec4_kernel<T, GROUP, 4>);
+}
+template <typename T>
+cudaError_t by_group(const Weights4Call& q, cudaStream_t s) {
+  if (q.group == 32) return matvec<T, 32>(q, s);
+  if (q.group == 64) return matvec<T, 64>(q, s);
+  return matvec<T, 128>(q, s);
 }
 
 }  // namespace
@@ -287,7 +411,7 @@ cudaError_t weights4_lay_out_launch(const Weights4Call& q, cudaStream_t s) {
   return launch(c, lay_out4_kernel, q);
 }
 cudaError_t weights4_matvec_launch(const Weights4Call& q, cudaStream_t s) {
-  return q.bf16 ? matvec<__nv_bfloat16>(q, s) : matvec<float>(q, s);
+  return q.bf16 ? by_group<__nv_bfloat16>(q, s) : by_group<float>(q, s);
 }
 
 }  // namespace cfc
