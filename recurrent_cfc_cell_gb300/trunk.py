@@ -338,6 +338,12 @@ class RMSNormStep(_Step):
         self.rstd = self._f32(rows)
         self.s = self.dx = self.dw = self.y_again = self.ws = None
 
+    def _alloc_grads(self):
+        if self.dx is None:
+            self.dx, self.dw = self._act(self.rows, self.n), self._f32(self.n)
+            self.y_again = self._act(self.rows, self.n) if self.keep8 else None
+            self.ws = _workspace(_lib.rmsnorm_workspace_bytes(self.rows, self.n), self.device)
+
     def bind(self, x, w, residual=None, dy=None, ds=None) -> "RMSNormStep":
         self._unbind()
         _expect(x, "x", (self.rows, self.n), self.dtype)
@@ -348,10 +354,7 @@ class RMSNormStep(_Step):
             x, w, residual, s, self.y, self.s8, self.y8, self.rstd, self.eps),)
         backward = ()
         if dy is not None:
-            if self.dx is None:
-                self.dx, self.dw = self._act(self.rows, self.n), self._f32(self.n)
-                self.y_again = self._act(self.rows, self.n) if self.keep8 else None
-                self.ws = _workspace(_lib.rmsnorm_workspace_bytes(self.rows, self.n), self.device)
+            self._alloc_grads()
             stream = self.s8 if self.keep8 else x if residual is None else self.s
             backward = (_lib.cfc_rmsnorm_backward.prepare(
                 dy, stream, w, self.rstd, self.dx, self.dw, ds, self.y_again, self.ws),)
