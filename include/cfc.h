@@ -703,16 +703,17 @@ typedef struct cfc_gated_kept {
  * the state before every CFC_GATED_PERIOD-th step (beyond a sequence's length: not read). */
 #define CFC_GATED_PERIOD 8
 
+/* cfc_gated_workspace_bytes -- workspace of cfc_gated_forward (backward = 0) or cfc_gated_backward
+ * (backward = 1).  Writes *bytes (0: none). */
+int cfc_gated_workspace_bytes(int B, int K, int D, int backward, size_t* bytes);
+
 /*
  * cfc_gated_forward -- y [K][B][D] (strides y_t, y_b), h_last [B][D] (or NULL; may be h0's own
  * memory), and for training states (NULL: none kept) and kept (NULL: nothing is kept in 8 bits).
  */
 int cfc_gated_forward(const cfc_gated_args* a, void* y, long long y_t, long long y_b,
-                      float* h_last, float* states, const cfc_gated_kept* kept,
-                      cfc_stream_t stream);
-
-/* cfc_gated_workspace_bytes -- workspace of cfc_gated_backward.  Writes *bytes (0: none). */
-int cfc_gated_workspace_bytes(int B, int K, int D, int dtype, size_t* bytes);
+                      float* h_last, float* states, const cfc_gated_kept* kept, void* ws,
+                      size_t ws_bytes, cfc_stream_t stream);
 
 /*
  * cfc_gated_backward -- from dy (of y), dh_last (of h_last, NULL: none) and the forward pass's

@@ -211,7 +211,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "cfc_rmsnorm_forward": [rms, vp, ll, vp, ll, held, held, vp, vp],
         "cfc_rmsnorm_workspace_bytes": [i, i, szp],
         "cfc_rmsnorm_backward": [rms, held, vp, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, sz, vp],
-        "cfc_gated_forward": [gated, vp, ll, ll, vp, vp, kept, vp],
+        "cfc_gated_forward": [gated, vp, ll, ll, vp, vp, kept, vp, sz, vp],
         "cfc_gated_workspace_bytes": [i] * 4 + [szp],
         "cfc_gated_backward": [gated, kept, vp, vp, ll, ll, vp, ggrads, vp, sz, vp],
         "cfc_gated_step": [gated, vp, ll, vp, vp],
@@ -1026,10 +1026,10 @@ def cfc_rmsnorm_backward(dy, s, w, rstd, dx, dw, ds=None, y=None, ws=None):
             (dy, w, rstd, dx, dw, ds, y, ws, *(_parts8(s) if held else (s,)), a, h))
 
 
-def gated_workspace_bytes(K: int, B: int, D: int, dtype: int) -> int:
+def gated_workspace_bytes(K: int, B: int, D: int, backward: bool) -> int:
     out = ctypes.c_size_t(0)
     _check("cfc_gated_workspace_bytes",
-           load().cfc_gated_workspace_bytes(*_dims(B, K, D), dtype, ctypes.byref(out)))
+           load().cfc_gated_workspace_bytes(*_dims(B, K, D), int(backward), ctypes.byref(out)))
     return out.value
 
 
@@ -1052,7 +1052,7 @@ def _gated_kept(kept, shape):
 
 @_entry
 def cfc_gated_forward(x, f, y, bias=None, z=None, h0=None, lengths=None, h_last=None, states=None,
-                      kept=None):
+                      kept=None, ws=None):
     """y [K, B, D], h_last [B, D] (or None; may be h0) and, for training, states
     [ceil(K / GATED_PERIOD), B, D] and kept, a tuple (x, f, z) of Held8 (or None) <- gated linear
     recurrence."""
@@ -1063,8 +1063,8 @@ def cfc_gated_forward(x, f, y, bias=None, z=None, h0=None, lengths=None, h_last=
         raise ValueError("kept holds a z where the recurrence has one")
     return ((ctypes.byref(a), _act(y, "y", (K, B, D), x.dtype), *_tb(y),
              _par(h_last, "h_last", (B, D)),
-             _par(states, "states", (-(-K // GATED_PERIOD), B, D)), _by(k)),
-            (x, f, y, bias, z, h0, lengths, h_last, states, *_parts8(*(kept or ())), a, k))
+             _par(states, "states", (-(-K // GATED_PERIOD), B, D)), _by(k), *_work(ws)),
+            (x, f, y, bias, z, h0, lengths, h_last, states, ws, *_parts8(*(kept or ())), a, k))
 
 
 @_entry

@@ -279,13 +279,6 @@ int device_ready() {
   DeviceState* st = nullptr;
   return device_state(&st);
 }
-int device_ready(int** status) {
-  std::lock_guard<std::mutex> lock(g_mu);
-  DeviceState* st = nullptr;
-  const int rc = device_state(&st);
-  if (rc == CFC_OK) *status = st->status;
-  return rc;
-}
 }  // namespace cfc
 
 extern "C" {

@@ -2,12 +2,18 @@
 //
 //   f_t = sigmoid(f_t + bias),   h_t = f_t h_{t-1} + (1 - f_t) x_t,   y_t = h_t silu(z_t)
 //
-// A warp takes kGatedPeriod steps of 32 V neighbouring channels (V = 2, or 1 where channels are not
-// aligned in pairs) of one sequence.  A composition of steps is again one: over a run of them
-// h_out = A h_in + H with A = prod f and H the state that the run reaches from 0.  So the warps of
-// a cluster take runs one after another in time, each forms its A and H at once, and what enters a
-// run is folded from those of the runs before it: K / (steps of a cluster) rounds with an exchange
-// each take the place of K steps one after another, and every input is read once.
+// A warp takes kGatedPeriod steps, a run, of 32 V neighbouring channels (V = 2, or 1 where channels are
+// not aligned in pairs) of one sequence at a time.  A composition of steps is again one: over any number
+// of them h_out = A h_in + H with A = prod f and H the state that they reach from 0.  Two ways to go
+// along the steps from that:
+//
+//   rounds    the warps of a CTA take runs one after another in time, each forms its A and H at once, and
+//             what enters a run is folded from those of the runs before it: a barrier for every 32 or 64
+//             steps, and every input is read once.  For as many sequences and channels as fill the GPU.
+//   segments  every warp has a stretch of the steps of its own.  A first launch (the summary) forms A and
+//             H of each, the second one folds what enters a stretch from those before it and goes through
+//             it without a barrier.  For few sequences and channels and many steps: x and f are read
+//             twice, but any number of warps takes part.
 #pragma once
 #include "cfc_gated_kernels.h"
 #include "cfc_held8.cuh"
@@ -18,7 +24,12 @@ namespace cfc {
 
 constexpr int kGS = kGatedPeriod;      // steps of a run
 constexpr int kGatedWarps = 8;         // most runs of a CTA
-constexpr int kGatedCluster = 16;      // most CTAs of a cluster
+constexpr int kMostSplits = 32;        // most CTAs of segments along a sequence
+enum GatedMode { kRounds, kSummary, kSegments };
+// How a warp reads its runs, by how the tensors are aligned: in pieces of 16 bytes or in pairs of
+// channels, both on their way through shared memory (V = 2), or channel by channel into registers.
+enum GatedPath { kSixteens, kPairs, kSingles };
+__host__ __device__ constexpr int path_v(GatedPath p) { return p == kSingles ? 1 : 2; }
 
 // V channels in a lane's registers: a float, or a pair that the packed fp32 instructions take.
 template <int V>
@@ -206,37 +217,19 @@ struct RawHeldV {
 
 // ---- what enters a run ----
 
-// A and H of every run of a round and, in a cluster, of every CTA's runs together; two rounds in
-// turn, so that one barrier a round is enough: a round's values are written over two rounds later,
-// behind a barrier that every reader has passed in between (of other CTAs' values: behind this CTA's
-// own values of the round in between, which the others wait for).  In dynamic shared memory.
+__host__ __device__ constexpr int ah_bytes(int V) { return 32 * V * 2 * static_cast<int>(sizeof(float)); }
+
+// A and H of every run of a round; two rounds in turn, so that one barrier a round is enough: a round's
+// values are written over two rounds later, behind a barrier that every reader has passed in between.
+// In dynamic shared memory.
 template <int V>
 struct Exchange {
-  static constexpr int kBytes = 32 * V * 2 * sizeof(float);  // a run's values
+  static constexpr int kBytes = ah_bytes(V);
   char* base;
-  int warps, ctas;
-  uint32_t bars;   // two barriers: the values of all CTAs have arrived
-  int* status;     // where a wait that ran out is reported
-  static size_t bytes(int warps, int ctas) {
-    return static_cast<size_t>(2 * kBytes) * (warps + (ctas > 1 ? ctas : 0));
-  }
+  int warps;
+  static size_t bytes(int warps) { return static_cast<size_t>(2 * kBytes) * warps; }
   __device__ __forceinline__ char* run(int turn, int i) const {
     return base + (turn * warps + i) * kBytes + threadIdx.x % 32 * (V * 8);
-  }
-  __device__ __forceinline__ char* cta(int turn, int i) const {
-    return base + (2 * warps + turn * ctas + i) * kBytes + threadIdx.x % 32 * (V * 8);
-  }
-  // All threads call, before the first round.  Behind it other CTAs may write to this one.
-  __device__ __forceinline__ void start() const {
-    if (ctas == 1) return;
-    if (threadIdx.x == 0) {
-      mbar_init(bars, 1);
-      mbar_init(bars + 8, 1);
-      fence_mbar_init_cluster();
-      mbar_arrive_expect_tx(bars, ctas * kBytes);
-      mbar_arrive_expect_tx(bars + 8, ctas * kBytes);
-    }
-    cluster_sync_all();
   }
 };
 
@@ -256,16 +249,6 @@ __device__ __forceinline__ void get_ah(const char* p, Fv<2>& a, Fv<2>& h) {
   a.v = make_float2(r.x, r.y);
   h.v = make_float2(r.z, r.w);
 }
-__device__ __forceinline__ void send_ah(uint32_t at, Fv<1> a, Fv<1> h, uint32_t bar) {
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(at),
-      "r"(__float_as_uint(a.v)), "r"(__float_as_uint(h.v)), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void send_ah(uint32_t at, Fv<2> a, Fv<2> h, uint32_t bar) {
-  st_async_v4(at, a.v.x, a.v.y, h.v.x, h.v.y, bar);
-}
-
 // v through the compositions at p, p + step, ...; most of the time there are N of them.
 template <int V, int N>
 __device__ __forceinline__ Fv<V> through(Fv<V> v, const char* p, int step, int count) {
@@ -287,52 +270,87 @@ __device__ __forceinline__ Fv<V> through(Fv<V> v, const char* p, int step, int c
   return v;
 }
 
-// From what entered the round (`carry`) to what enters run w of CTA `rank` (the result), and on to
-// what leaves the round (`carry`), folded in the order of the runs; `REV`: from the last to the
-// first.  `n` counts the rounds.  All threads of the cluster call.
+// From what entered the round (`carry`) to what enters run w (the result), and on to what leaves the
+// round (`carry`), folded in the order of the runs; `REV`: from the last to the first.  `n` counts the
+// rounds.  All threads of the CTA call.
 template <int V, bool REV>
-__device__ __forceinline__ Fv<V> enter(const Exchange<V>& ex, int n, int w, int rank, Fv<V> A,
-                                       Fv<V> H, Fv<V>& carry) {
-  const int warps = ex.warps, ctas = ex.ctas, turn = n & 1;
+__device__ __forceinline__ Fv<V> enter(const Exchange<V>& ex, int n, int w, Fv<V> A, Fv<V> H,
+                                       Fv<V>& carry) {
+  const int warps = ex.warps, turn = n & 1;
   constexpr int kStep = REV ? -Exchange<V>::kBytes : Exchange<V>::kBytes;
   put_ah(ex.run(turn, w), A, H);
   __syncthreads();
   const char* const runs = ex.run(turn, REV ? warps - 1 : 0);
-  const int before = REV ? warps - 1 - w : w;
-  if (ctas == 1) {
-    const Fv<V> in = through<V, 0>(carry, runs, kStep, before);
-    carry = through<V, 4>(carry, runs, kStep, warps);
-    return in;
+  const Fv<V> in = through<V, 0>(carry, runs, kStep, REV ? warps - 1 - w : w);
+  carry = through<V, 4>(carry, runs, kStep, warps);
+  return in;
+}
+
+// What the two launches over segments share, for one sequence and tile of channels: A and H of every
+// warp's segment, of every CTA's segments together, and the state before the first step.
+template <int V>
+struct Segments {
+  static constexpr int kBytes = ah_bytes(V);
+  char* base;
+  int ctas;
+  // Floats of one sequence and tile.
+  static size_t floats(int ctas) {
+    return static_cast<size_t>(kBytes / sizeof(float)) * (ctas * (kGatedWarps + 1) + 1);
   }
-  const uint32_t bar = ex.bars + 8 * turn;
-  // Each warp sends the CTA's A and H to the CTAs w, w + warps, ...
-  if (w < ctas) {
+  __device__ __forceinline__ Segments(float* ws, int tiles, int tile, int b, int ctas_)
+      : base(reinterpret_cast<char*>(ws + (static_cast<size_t>(b) * tiles + tile) * (kBytes / sizeof(float)) *
+                                              (ctas_ * (kGatedWarps + 1) + 1)) +
+             threadIdx.x % 32 * (V * 8)),
+        ctas(ctas_) {}
+  __device__ __forceinline__ char* warp(int c, int w) const {
+    return base + (c * kGatedWarps + w) * kBytes;
+  }
+  __device__ __forceinline__ char* cta(int c) const { return base + (ctas * kGatedWarps + c) * kBytes; }
+  __device__ __forceinline__ char* start() const { return base + ctas * (kGatedWarps + 1) * kBytes; }
+
+  // A warp's A and H, and its CTA's.  All threads of the CTA call; `ex` lies in shared memory.
+  template <bool REV>
+  __device__ __forceinline__ void put(const Exchange<V>& ex, int c, int w, Fv<V> A, Fv<V> H) const {
+    put_ah(ex.run(0, w), A, H);
+    put_ah(warp(c, w), A, H);
+    __syncthreads();
+    if (w > 0) return;
     Fv<V> a(1.f), h(0.f);
 #pragma unroll
     for (int i = 0; i < kGatedWarps; ++i) {
-      if (i >= warps) break;
       Fv<V> ra, rh;
-      get_ah(runs + i * kStep, ra, rh);
+      get_ah(ex.run(0, REV ? kGatedWarps - 1 - i : i), ra, rh);
       h = fma(ra, h, rh);
       a = a * ra;
     }
-    const uint32_t mine = smem_addr(ex.cta(turn, rank));
-    for (int to = w; to < ctas; to += warps)
-      send_ah(map_to_rank(mine, to), a, h, map_to_rank(bar, to));
+    put_ah(cta(c), a, h);
   }
-  __syncwarp();
-  (void)mbar_wait_bounded_cluster(bar, (n >> 1) & 1, ex.status);
-  if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, ctas * Exchange<V>::kBytes);  // for n + 2
-  const char* const all = ex.cta(turn, REV ? ctas - 1 : 0);
-  const Fv<V> in = through<V, 0>(carry, all, kStep, REV ? ctas - 1 - rank : rank);
-  carry = through<V, kGatedCluster>(carry, all, kStep, ctas);
-  return through<V, 0>(in, runs, kStep, before);
-}
+  // What enters warp w's segment of CTA c: v through those before it, `REV`: behind it.
+  template <bool REV>
+  __device__ __forceinline__ Fv<V> enter(Fv<V> v, int c, int w) const {
+    constexpr int kStep = REV ? -kBytes : kBytes;
+    v = batches(v, cta(REV ? ctas - 1 : 0), kStep, REV ? ctas - 1 - c : c);
+    return batches(v, warp(c, REV ? kGatedWarps - 1 : 0), kStep, REV ? kGatedWarps - 1 - w : w);
+  }
+  // Eight values on their way from L2 at a time.
+  static __device__ __forceinline__ Fv<V> batches(Fv<V> v, const char* p, int step, int count) {
+    for (int i = 0; i < count; i += 8) {
+      Fv<V> a[8], h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < count) get_ah(p + (i + j) * step, a[j], h[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < count) v = fma(a[j], v, h[j]);
+    }
+    return v;
+  }
+};
 
 // ---- runs on their way ----
 
 // One tensor's runs of kGS steps x 64 channels on their way to shared memory, copied in the background
-// 8 or 16 bytes (CB) a lane.  A warp copies and reads its own runs only, so no barrier is needed but
+// 4, 8 or 16 bytes (CB) a lane.  A warp copies and reads its own runs only, so no barrier is needed but
 // the warp's.
 template <int ES, int CB>  // bytes of an element, of a copy
 struct RingRun {
@@ -344,8 +362,11 @@ struct RingRun {
     if constexpr (CB == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(bytes)
                    : "memory");
-    else
+    else if constexpr (CB == 8)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(bytes)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p), "r"(bytes)
                    : "memory");
   }
   // `base`: the tensor at step 0 and the tile's first channel, `stride` elements a step; t0: the
@@ -355,8 +376,8 @@ struct RingRun {
     from = static_cast<const char*>(base) + (c < left * ES ? c : 0) +
            (t0 + lane / kLanes) * stride * ES;
   }
-  // The run `ahead` bytes further to `dst`: zeros for its steps from `on` on and for channels that do not exist, neither of
-  // which is read.
+  // The run `ahead` bytes further to `dst`: zeros for its steps from `on` on and for channels that do
+  // not exist, neither of which is read.
   __device__ __forceinline__ void copy(uint32_t dst, long long ahead, long long stride, int on,
                                        int left) const {
     const int lane = threadIdx.x % 32;
@@ -388,30 +409,42 @@ inline bool group_aligned(const void* p, long long t, long long b, int bytes, in
   return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && t % per == 0 && b % per == 0);
 }
 
-// How the runs of a sequence are spread: warps of a CTA, CTAs of a cluster.
+// How the steps of a sequence are gone along: by CTAs of `warps` warps in rounds (ctas = 0), or by `ctas`
+// CTAs of kGatedWarps segments of `steps` steps.
 struct GatedShape {
-  int warps, ctas;
+  int warps, ctas, steps;
 };
-// A CTA of four warps where there are columns enough for two CTAs an SM: its barrier waits least
-// (64 x 1024 steps x 1536 channels, bf16: forward 148 us, backward 247; eight warps 163 and 259, two
-// 167 and 305).  Fewer columns take longer rounds, and at last clusters.
-inline GatedShape gated_shape(const GatedCall& q, int tiles) {
-  const int runs = (q.K - 1) / kGS + 1;
-  const long long columns = static_cast<long long>(tiles) * q.B;
-  GatedShape s{columns >= 2 * 152 ? 4 : kGatedWarps, 1};
+// `slots`: CTAs of segments that the GPU holds.
+inline GatedShape gated_shape(int B, int K, int tiles, int slots) {
+  const int runs = (K - 1) / kGS + 1;
+  const long long columns = static_cast<long long>(tiles) * B;
+  // Rounds of four warps where there are columns enough for two CTAs an SM: their barrier waits least
+  // (64 x 1024 steps x 1536 channels, bf16: forward 133 us, backward 249; eight warps 143 and 312, two
+  // 167 and 305).
+  GatedShape s{columns >= 2 * 152 ? 4 : kGatedWarps, 0, 0};
   if (runs < s.warps) s.warps = runs;
-  while (s.ctas < kGatedCluster && columns * s.ctas < 152 && runs > s.warps * s.ctas) s.ctas *= 2;
+  // Segments from 448 steps and below 100 columns: with 64 columns of 4096 steps they take 41 us forward
+  // and 74 backward (rounds 82 and 109), with 128 of 2048 steps 41 and 73 (43 and 60), with 64 of 512
+  // steps 10 and 16 (13 and 19), with 128 of 256 steps 10 and 16 (8 and 12).
+  if (columns >= 100 || K < 448) return s;
+  // Full waves of them, two or one.
+  long long ctas = 2 * slots / columns;
+  if (ctas > kMostSplits) ctas = slots / columns;
+  if (ctas > kMostSplits) ctas = kMostSplits;
+  if (ctas > runs / (2 * kGatedWarps)) ctas = runs / (2 * kGatedWarps);
+  if (ctas < 1) return s;
+  const int segments = static_cast<int>(ctas) * kGatedWarps;
+  s.steps = ((runs - 1) / segments + 1) * kGS;
+  s.ctas = (K - 1) / (s.steps * kGatedWarps) + 1;
+  s.warps = kGatedWarps;
   return s;
 }
+constexpr int kFwdSlots = 3 * 152, kBwdSlots = 2 * 152;
 template <typename F>
-cudaError_t gated_attributes(F* kern, size_t smem, int ctas) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 16 * 1024)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
-  if (e == cudaSuccess && ctas > 8)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e;
+cudaError_t gated_smem(F* kern, size_t smem) {
+  return smem > 16 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem))
+                          : cudaSuccess;
 }
 
 }  // namespace cfc

@@ -80,6 +80,11 @@ int kept_call(const cfc_gated_kept* kept, bool read, cfc::GatedCall* q) {
   return CFC_OK;
 }
 
+size_t gated_bytes(int B, int K, int D, bool backward) {
+  return sizeof(float) * (cfc::gated_segments_floats(B, K, D, backward) +
+                          (backward ? cfc::gated_partials_floats(B, K, D) : 0));
+}
+
 int weights4_check(int N, int K, int group) {
   if (N <= 0 || K <= 0 || N > kMaxWidth || K > kMaxWidth ||
       static_cast<long long>(N) * K > 1ll << 36)
@@ -170,8 +175,8 @@ int cfc_rmsnorm_backward(const cfc_rmsnorm_args* a, const cfc_held8* s8, const f
 }
 
 int cfc_gated_forward(const cfc_gated_args* a, void* y, long long y_t, long long y_b,
-                      float* h_last, float* states, const cfc_gated_kept* kept,
-                      cfc_stream_t stream) {
+                      float* h_last, float* states, const cfc_gated_kept* kept, void* ws,
+                      size_t ws_bytes, cfc_stream_t stream) {
   cfc::GatedCall q{};
   int rc = gated_call(a, true, true, &q);
   if (rc != CFC_OK) return rc;
@@ -180,17 +185,19 @@ int cfc_gated_forward(const cfc_gated_args* a, void* y, long long y_t, long long
   if (rc == CFC_OK) rc = kept_call(kept, false, &q);
   if (rc != CFC_OK) return rc;
   if (off(h_last, 4) || off(states, 4)) return CFC_ERR_MISALIGNED;
-  rc = cfc::device_ready(&q.status);
+  rc = ws_check(ws, ws_bytes, gated_bytes(q.B, q.K, q.D, false));
+  if (rc == CFC_OK) rc = cfc::device_ready();
   if (rc != CFC_OK) return rc;
   q.y = y; q.y_t = y_t; q.y_b = y_b; q.h_last = h_last; q.states = states;
+  q.ws = static_cast<float*>(ws);
   return launched(cfc::gated_fwd_launch(q, on(stream)));
 }
 
-int cfc_gated_workspace_bytes(int B, int K, int D, int dtype, size_t* bytes) {
-  const int rc = gated_check(B, K, D, dtype, true);
+int cfc_gated_workspace_bytes(int B, int K, int D, int backward, size_t* bytes) {
+  const int rc = gated_check(B, K, D, CFC_F32, true);
   if (rc != CFC_OK) return rc;
   if (!bytes) return CFC_ERR_NULL_PTR;
-  *bytes = cfc::gated_ws_floats(B, K, D, dtype == CFC_BF16) * sizeof(float);
+  *bytes = gated_bytes(B, K, D, backward != 0);
   return CFC_OK;
 }
 
@@ -211,8 +218,8 @@ int cfc_gated_backward(const cfc_gated_args* a, const cfc_gated_kept* kept, cons
   if (rc != CFC_OK) return rc;
   if (off(states, 4) || off(dh_last, 4) || off(g->dbias, 4) || off(g->dh0, 4))
     return CFC_ERR_MISALIGNED;
-  rc = ws_check(ws, ws_bytes, cfc::gated_ws_floats(q.B, q.K, q.D, q.bf16) * sizeof(float));
-  if (rc == CFC_OK) rc = cfc::device_ready(&q.status);
+  rc = ws_check(ws, ws_bytes, gated_bytes(q.B, q.K, q.D, true));
+  if (rc == CFC_OK) rc = cfc::device_ready();
   if (rc != CFC_OK) return rc;
   q.states = const_cast<float*>(states);
   q.dy = dy; q.dy_t = dy_t; q.dy_b = dy_b; q.dh_last = dh_last;

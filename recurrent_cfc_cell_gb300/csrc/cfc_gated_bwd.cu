@@ -12,7 +12,7 @@ namespace cfc {
 namespace {
 
 template <typename T, int V, bool KEEP>
-struct Input {  // an activation that the backward pass reads as it is, or in 8 bits
+struct Input {  // a run of an activation that the backward pass reads as it is, or in 8 bits
   RawV<T, V> raw[kGS];
   __device__ __forceinline__ void load(int k, const T* p, const Held8&, const HeldAt&) {
     raw[k].load(p);
@@ -26,16 +26,16 @@ struct Input<T, V, true> {
   }
 };
 
-// Rounds on their way to shared memory, and the one being worked on, of a warp: x, f and dy, and z,
-// the first ones as kept where they are.
-template <typename T, bool Z, bool KEEP>
+// Rounds on their way to shared memory, and the one being worked on, of a warp: dy, and x, f and z where
+// IN, the first ones as kept where they are.
+template <typename T, bool Z, bool KEEP, GatedPath PATH>
 struct Ring {
-  using Run = RingRun<sizeof(T), 16>;
-  using Codes = RingRun<1, 8>;
+  static constexpr bool IN = !KEEP || PATH == kSixteens;
+  using Run = RingRun<sizeof(T), PATH == kSixteens ? 16 : 2 * sizeof(T)>;
+  using In = std::conditional_t<KEEP, RingRun<1, 8>, Run>;
   static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
-  using In = std::conditional_t<KEEP, Codes, Run>;
-  static constexpr int kInput = KEEP ? Codes::kBytes : Run::kBytes;
-  static constexpr int kStage = Run::kBytes + (Z ? 3 : 2) * kInput, kWarp = kStages * kStage;
+  static constexpr int kInput = In::kBytes;
+  static constexpr int kStage = Run::kBytes + (IN ? (Z ? 3 : 2) * kInput : 0), kWarp = kStages * kStage;
 };
 
 // The scales of a run of 64 channels in 8 bits: lane 2 k + i holds the one of step k's block i.
@@ -52,18 +52,22 @@ __device__ __forceinline__ Fv<2> ring_get_held(const char* run, int k, float up)
   return v * Fv<2>(__shfl_sync(0xffffffffu, up, 2 * k + lane / 16));
 }
 
-template <typename T, int V, bool Z, bool KEEP, bool RING>
+// kRounds: grid (tiles, B), CTAs of any number of warps.  kSummary and kSegments: grid (tiles x CTAs of
+// segments, B), kGatedWarps warps.
+template <typename T, bool Z, bool KEEP, GatedPath PATH, GatedMode MODE>
 __global__ void __launch_bounds__(32 * kGatedWarps, 2)
-    gated_bwd_kernel(const GatedCall q, int ctas, float* dbias, int* status) {
-  grid_dep_launch_dependents();
+    gated_bwd_kernel(const GatedCall q, const GatedShape sh, float* dbias) {
   extern __shared__ __align__(128) char shared[];  // the rounds on their way, the exchange
-  __shared__ uint64_t bars[2];
-  using Rg = Ring<T, Z, KEEP>;
-  const int warps = blockDim.x / 32;
-  const Exchange<V> ex{shared + (RING ? warps * Rg::kWarp : 0), warps, ctas, smem_addr(bars),
-                       status};
-  const int w = threadIdx.x / 32;
-  const int b = blockIdx.y, K = q.K, tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  constexpr bool RING = PATH != kSingles;
+  constexpr int V = path_v(PATH);
+  using Rg = Ring<T, Z, KEEP, PATH>;
+  constexpr bool IN = RING && Rg::IN;        // x, f and z come through the ring
+  constexpr bool AHEAD = !RING && !KEEP;     // everything comes to registers, a run ahead
+  grid_dep_launch_dependents();
+  const int warps = blockDim.x / 32, w = threadIdx.x / 32;
+  const Exchange<V> ex{shared + (RING ? warps * Rg::kWarp : 0), warps};
+  const int ctas = MODE == kRounds ? 1 : sh.ctas;
+  const int b = blockIdx.y, K = q.K, tile = blockIdx.x / ctas, cta = blockIdx.x % ctas;
   const Channels<V> ch(tile, q.D);
   const int len = q.lengths ? min(max(q.lengths[b], 0), K) : K;
   const int from = RING ? tile * 64 : ch.d;
@@ -77,9 +81,14 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
   T* const yp = q.y ? static_cast<T*>(q.y) + b * q.y_b + ch.d : nullptr;
   const Fv<V> bias2 = load_par_v<V>(q.bias, ch) * Fv<V>(kLog2e);
   Fv<V> dsum(0.f);
-  Fv<V> carry = load_par_v<V>(q.dh_last ? q.dh_last + static_cast<size_t>(b) * q.D : nullptr, ch);
-  const int round = ctas * warps * kGS, first = (rank * warps + w) * kGS;
-  const int last = (K - 1) / round;  // rounds are taken from the last to the first
+  // The warp's steps, `round` of them from a run to its next one; where its first one begins, and the
+  // run that it takes first, the last one.
+  const int round = MODE == kRounds ? warps * kGS : kGS;
+  const int first = MODE == kRounds ? w * kGS : (cta * kGatedWarps + w) * sh.steps;
+  const int end = MODE == kRounds ? K : min(first + sh.steps, K);
+  // Rounds are taken from the last to the first; a segment that there is not has none.
+  const int last = MODE == kRounds ? (K - 1) / round : first < end ? (end - first - 1) / round : -1;
+  const Segments<V> seg(q.ws, MODE == kRounds ? 0 : gridDim.x / ctas, tile, b, ctas);
 
   char* const mine = shared + w * Rg::kWarp;
   RawV<float, V> start_next;
@@ -91,23 +100,27 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
   const long long kept_t = static_cast<long long>(q.B) * q.D;
   const long long xs = KEEP ? kept_t : q.x_t, fs = KEEP ? kept_t : q.f_t, zs = KEEP ? kept_t : q.z_t;
   if constexpr (RING) {
-    const size_t at = static_cast<size_t>(b) * q.D + tile * 64;
     rdy.start(dyp, q.dy_t, first, left);
+  }
+  if constexpr (IN) {
+    const size_t at = static_cast<size_t>(b) * q.D + tile * 64;
     rx.start(KEEP ? static_cast<const void*>(q.x8.codes + at) : xp, xs, first, left);
     rf.start(KEEP ? static_cast<const void*>(q.f8.codes + at) : fp, fs, first, left);
     if constexpr (Z) rz.start(KEEP ? static_cast<const void*>(q.z8.codes + at) : zp, zs, first, left);
   }
   uint32_t filled = 0;  // the stage that is filled next
   auto fetch = [&]() {
-    const int on = fetched >= 0 ? len - fetched : 0;
+    const int on = fetched >= first ? len - fetched : 0;
     if (on > 0) {
       const uint32_t to = smem_addr(mine) + filled, in = to + Rg::Run::kBytes;
       const long long ahead = fetched - first;
       const long long inputs = ahead * (KEEP ? 1 : static_cast<int>(sizeof(T)));
       rdy.copy(to, ahead * static_cast<int>(sizeof(T)) * q.dy_t, q.dy_t, on, left);
-      rx.copy(in, inputs * xs, xs, on, left);
-      rf.copy(in + Rg::kInput, inputs * fs, fs, on, left);
-      if constexpr (Z) rz.copy(in + 2 * Rg::kInput, inputs * zs, zs, on, left);
+      if constexpr (IN) {
+        if constexpr (MODE != kSummary) rx.copy(in, inputs * xs, xs, on, left);
+        rf.copy(in + Rg::kInput, inputs * fs, fs, on, left);
+        if constexpr (Z) rz.copy(in + 2 * Rg::kInput, inputs * zs, zs, on, left);
+      }
     }
     fetched -= round;
     filled = filled == (Rg::kStages - 1) * Rg::kStage ? 0 : filled + Rg::kStage;
@@ -117,15 +130,40 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
   auto fetch_next = [&](int n) {
     const int t0 = (last - n) * round + first;
     const bool on = n <= last && t0 < len;
-    if (on && ch.in)
+    if (MODE != kSummary && on && ch.in)
       start_next.load(q.states + (static_cast<size_t>(t0 / kGS) * q.B + b) * q.D + ch.d);
     else
       start_next.clear();
-    if constexpr (KEEP && RING) {
+    if constexpr (KEEP && IN) {
       if (on) {
-        sx_next = run_scales(q.x8, q, b, tile, t0, len);
+        if constexpr (MODE != kSummary) sx_next = run_scales(q.x8, q, b, tile, t0, len);
         sf_next = run_scales(q.f8, q, b, tile, t0, len);
         if constexpr (Z) sz_next = run_scales(q.z8, q, b, tile, t0, len);
+      }
+    }
+  };
+  // What does not come through the ring: without one the next run's loads are on their way to
+  // registers; what is kept and not aligned for a ring is loaded for the run at hand.
+  struct Inputs {
+    Input<T, V, KEEP> x, f, z;
+    RawV<T, V> dy[kGS];
+  };
+  Inputs in_next;
+  auto load = [&](Inputs& to, int t0) {
+#pragma unroll
+    for (int k = 0; k < kGS; ++k) {
+      const long long t = t0 + k;
+      if (t0 >= first && t < len && ch.in) {
+        const HeldAt at = held_at<V>(q, t0 + k, b, ch.d);
+        if constexpr (MODE != kSummary) to.x.load(k, xp + t * q.x_t, q.x8, at);
+        to.f.load(k, fp + t * q.f_t, q.f8, at);
+        if (Z) to.z.load(k, zp + t * q.z_t, q.z8, at);
+        if constexpr (!RING) to.dy[k].load(dyp + t * q.dy_t);
+      } else {
+        if constexpr (MODE != kSummary) to.x.raw[k].clear();
+        to.f.raw[k].clear();
+        if (Z) to.z.raw[k].clear();
+        if constexpr (!RING) to.dy[k].clear();
       }
     }
   };
@@ -133,8 +171,16 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
 #pragma unroll
     for (int n = 0; n < Rg::kStages - 1; ++n) fetch();
   }
+  if constexpr (AHEAD) load(in_next, last * round + first);
   fetch_next(0);
-  ex.start();
+  // What comes back into the warp's last run; kSummary: 0, and A of the runs so far.
+  Fv<V> carry(0.f), through_all(1.f);
+  if constexpr (MODE != kSummary)
+    carry = load_par_v<V>(q.dh_last ? q.dh_last + static_cast<size_t>(b) * q.D : nullptr, ch);
+  if constexpr (MODE == kSegments) {
+    grid_dep_wait();
+    carry = seg.template enter<true>(carry, cta, w);
+  }
 
   int done = 0;  // rounds that had steps
   for (int n = 0; n <= last; ++n) {
@@ -143,9 +189,11 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     T* const dfr = dfp + t0 * q.df_t;
     T* const dzr = Z ? dzp + t0 * q.dz_t : nullptr;
     T* const yr = yp ? yp + t0 * q.y_t : nullptr;
-    if (base >= len) {
+    if ((MODE == kRounds ? base : t0) >= len) {
       if constexpr (RING) fetch();
+      if constexpr (AHEAD) load(in_next, t0 - round);
       fetch_next(n + 1);
+      if constexpr (MODE == kSummary) continue;
 #pragma unroll
       for (int k = 0; k < kGS; ++k) {
         if (t0 + k >= K || !ch.in) continue;
@@ -156,60 +204,47 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
       }
       continue;
     }
-    Input<T, V, KEEP> x, f, z;
-    RawV<T, V> dy[kGS];
+    Inputs in;
     const char* const stage = mine + n % Rg::kStages * Rg::kStage;
     Fv<V> h = start_next.get();
     float ux = 0.f, uf = 0.f, uz = 0.f;  // the scales' values
+    if constexpr (KEEP && IN) ux = held_up(sx_next), uf = held_up(sf_next), uz = held_up(sz_next);
+    if constexpr (AHEAD) {
+      in = in_next;
+      load(in_next, t0 - round);
+    } else if constexpr (!IN) {
+      load(in, t0);
+    }
     if constexpr (RING) {
-      if constexpr (KEEP) ux = held_up(sx_next), uf = held_up(sf_next), uz = held_up(sz_next);
       __syncwarp();  // the stage that is filled next has been read by all lanes
       fetch();
-      fetch_next(n + 1);
+    }
+    fetch_next(n + 1);
+    if constexpr (RING) {
       cp_async_wait<Rg::kStages - 1>();
       __syncwarp();
-    } else {
-#pragma unroll
-      for (int k = 0; k < kGS; ++k) {
-        const long long t = t0 + k;
-        if (t < len && ch.in) {
-          const HeldAt at = held_at<V>(q, t0 + k, b, ch.d);
-          x.load(k, xp + t * q.x_t, q.x8, at);
-          f.load(k, fp + t * q.f_t, q.f8, at);
-          if (Z) z.load(k, zp + t * q.z_t, q.z8, at);
-          dy[k].load(dyp + t * q.dy_t);
-        } else {
-          x.raw[k].clear();
-          f.raw[k].clear();
-          if (Z) z.raw[k].clear();
-          dy[k].clear();
-        }
-      }
-      fetch_next(n + 1);
     }
     Fv<V> a[kGS], i[kGS], u[kGS], dh[kGS];
     auto gather = [&](auto whole) {
       T *to_z = dzr, *to_y = yr;
 #pragma unroll
       for (int k = 0; k < kGS; ++k) {
-        Fv<V> xv, fv, zv, dyv, dz(0.f), y;
-        if constexpr (RING) {
-          const char* const in = stage + Rg::Run::kBytes;
-          dyv = ring_get<T>(stage, k);
-          if constexpr (KEEP) {
-            xv = ring_get_held(in, k, ux);
-            fv = ring_get_held(in + Rg::kInput, k, uf);
-            if constexpr (Z) zv = ring_get_held(in + 2 * Rg::kInput, k, uz);
-          } else {
-            xv = ring_get<T>(in, k);
-            fv = ring_get<T>(in + Rg::kInput, k);
-            if constexpr (Z) zv = ring_get<T>(in + 2 * Rg::kInput, k);
-          }
+        Fv<V> xv(0.f), fv, zv, dyv, dz(0.f), y;
+        if constexpr (RING) dyv = ring_get<T>(stage, k);
+        else dyv = in.dy[k].get();
+        [[maybe_unused]] const char* const runs = stage + Rg::Run::kBytes;
+        if constexpr (IN && KEEP) {
+          if constexpr (MODE != kSummary) xv = ring_get_held(runs, k, ux);
+          fv = ring_get_held(runs + Rg::kInput, k, uf);
+          if constexpr (Z) zv = ring_get_held(runs + 2 * Rg::kInput, k, uz);
+        } else if constexpr (IN) {
+          if constexpr (MODE != kSummary) xv = ring_get<T>(runs, k);
+          fv = ring_get<T>(runs + Rg::kInput, k);
+          if constexpr (Z) zv = ring_get<T>(runs + 2 * Rg::kInput, k);
         } else {
-          xv = x.raw[k].get();
-          fv = f.raw[k].get();
-          if constexpr (Z) zv = z.raw[k].get();
-          dyv = dy[k].get();
+          if constexpr (MODE != kSummary) xv = in.x.raw[k].get();
+          fv = in.f.raw[k].get();
+          if constexpr (Z) zv = in.z.raw[k].get();
         }
         gates<V>(fv, bias2, a[k], i[k]);
         u[k] = fma(xv, Fv<V>(-1.f), h) * (a[k] * i[k]);
@@ -228,7 +263,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
           a[k] = Fv<V>(1.f);
           i[k] = u[k] = dh[k] = dz = y = Fv<V>(0.f);
         }
-        if ((decltype(whole)::value || t0 + k < K) && ch.in) {
+        if (MODE != kSummary && (decltype(whole)::value || t0 + k < K) && ch.in) {
           if (Z) store_v(to_z, dz);
           if (yr) store_v(to_y, y);
         }
@@ -245,7 +280,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
       H = a[k] * (dh[k] + H);
       A = A * a[k];
     }
-    Fv<V> g = enter<V, true>(ex, done++, w, rank, A, H, carry);
+    if constexpr (MODE == kSummary) {
+      carry = fma(A, carry, H);
+      through_all = through_all * A;
+      continue;
+    }
+    Fv<V> g = carry;
+    if constexpr (MODE == kRounds) g = enter<V, true>(ex, done++, w, A, H, carry);
     auto finish = [&](auto whole) {
       T *to_x = dxr + (kGS - 1) * q.dx_t, *to_f = dfr + (kGS - 1) * q.df_t;
 #pragma unroll
@@ -261,9 +302,15 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
       }
     };
     decide(whole, finish);
+    if (MODE == kSegments) carry = g;
   }
   if constexpr (RING) cp_async_wait<0>();
-  if (q.dh0 && rank == 0 && w == 0 && ch.in)
+  if constexpr (MODE == kSummary) {
+    seg.template put<true>(ex, cta, w, through_all, carry);
+    return;
+  }
+  // In rounds every warp ends with it.
+  if (q.dh0 && cta == 0 && w == 0 && ch.in)
     store_v(q.dh0 + static_cast<size_t>(b) * q.D + ch.d, carry);
   if (!dbias) return;
   __syncthreads();
@@ -276,7 +323,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
       get_ah(ex.run(0, n), part, same);
       v = v + part;
     }
-    store_v(dbias + (static_cast<size_t>(b) * ctas + rank) * q.D + ch.d, v);
+    store_v(dbias + (static_cast<size_t>(b) * ctas + cta) * q.D + ch.d, v);
   }
 }
 
@@ -302,41 +349,58 @@ bool sixteens(const GatedCall& q) {
          group_aligned(q.z, q.z_t, q.z_b, 16, per);
 }
 
-template <typename T, int V, bool Z, bool KEEP, bool RING>
-cudaError_t bwd(const GatedCall& q, cudaStream_t s) {
-  auto* const kern = gated_bwd_kernel<T, V, Z, KEEP, RING>;
-  const int tiles = (q.D - 1) / (32 * V) + 1;
-  const GatedShape sh = gated_shape(q, tiles);
+template <typename T, bool Z, bool KEEP, GatedPath PATH, GatedMode MODE>
+cudaError_t bwd_mode(const GatedCall& q, const GatedShape& sh, int tiles, float* dbias,
+                     cudaStream_t s) {
+  auto* const kern = gated_bwd_kernel<T, Z, KEEP, PATH, MODE>;
   LaunchCfg c;
-  c.grid = dim3(tiles * sh.ctas, q.B);
+  c.grid = dim3(MODE == kRounds ? tiles : tiles * sh.ctas, q.B);
   c.block = dim3(32 * sh.warps);
   c.stream = s;
-  if (sh.ctas > 1) c.cluster = dim3(sh.ctas, 1, 1);
-  c.smem = Exchange<V>::bytes(sh.warps, sh.ctas);
-  if (RING) c.smem += static_cast<size_t>(sh.warps) * Ring<T, Z, KEEP>::kWarp;
-  cudaError_t e = gated_attributes(kern, c.smem, sh.ctas);
-  const int P = q.B * sh.ctas;
-  float* const first = q.dbias && P > 1 ? q.ws : q.dbias;
-  if (e == cudaSuccess) e = launch(c, kern, q, sh.ctas, first, q.status);
-  if (e != cudaSuccess || first == q.dbias) return e;
-  return merge_launch(q.ws, P, q.D, q.dbias, s, true);
+  c.pdl = MODE == kSegments;
+  c.smem = Exchange<path_v(PATH)>::bytes(sh.warps);
+  if (PATH != kSingles) c.smem += static_cast<size_t>(sh.warps) * Ring<T, Z, KEEP, PATH>::kWarp;
+  const cudaError_t e = gated_smem(kern, c.smem);
+  return e == cudaSuccess ? launch(c, kern, q, sh, dbias) : e;
 }
-template <typename T, int V, bool RING>
-cudaError_t bwd_v(const GatedCall& q, cudaStream_t s) {
-  if (q.keep)
-    return q.has_z ? bwd<T, V, true, true, RING>(q, s) : bwd<T, V, false, true, RING>(q, s);
-  return q.has_z ? bwd<T, V, true, false, RING>(q, s) : bwd<T, V, false, false, RING>(q, s);
+template <typename T, bool Z, bool KEEP, GatedPath PATH>
+cudaError_t bwd(const GatedCall& q, cudaStream_t s) {
+  const int tiles = (q.D - 1) / (32 * path_v(PATH)) + 1;
+  const GatedShape sh = gated_shape(q.B, q.K, tiles, kBwdSlots);
+  const int P = q.B * (sh.ctas ? sh.ctas : 1);
+  // Partial sums of dbias behind what the launches over segments share.
+  float* const parts = q.ws + gated_segments_floats(q.B, q.K, q.D, true);
+  float* const first = q.dbias && P > 1 ? parts : q.dbias;
+  cudaError_t e;
+  if (sh.ctas == 0) {
+    e = bwd_mode<T, Z, KEEP, PATH, kRounds>(q, sh, tiles, first, s);
+  } else {
+    e = bwd_mode<T, Z, KEEP, PATH, kSummary>(q, sh, tiles, nullptr, s);
+    if (e == cudaSuccess) e = bwd_mode<T, Z, KEEP, PATH, kSegments>(q, sh, tiles, first, s);
+  }
+  if (e != cudaSuccess || first == q.dbias) return e;
+  return merge_launch(parts, P, q.D, q.dbias, s, true);
+}
+template <typename T, GatedPath PATH>
+cudaError_t bwd_path(const GatedCall& q, cudaStream_t s) {
+  if (q.keep) return q.has_z ? bwd<T, true, true, PATH>(q, s) : bwd<T, false, true, PATH>(q, s);
+  return q.has_z ? bwd<T, true, false, PATH>(q, s) : bwd<T, false, false, PATH>(q, s);
 }
 template <typename T>
 cudaError_t bwd_t(const GatedCall& q, cudaStream_t s) {
-  if (!pairs(q)) return bwd_v<T, 1, false>(q, s);
-  return sixteens(q) ? bwd_v<T, 2, true>(q, s) : bwd_v<T, 2, false>(q, s);
+  if (!pairs(q)) return bwd_path<T, kSingles>(q, s);
+  return sixteens(q) ? bwd_path<T, kSixteens>(q, s) : bwd_path<T, kPairs>(q, s);
 }
 
 }  // namespace
 
-size_t gated_ws_floats(int B, int, int D, bool) {
-  return static_cast<size_t>(B) * kGatedCluster * D;
+size_t gated_partials_floats(int B, int K, int D) {
+  int most = 1;
+  for (int V = 1; V <= 2; ++V) {
+    const int ctas = gated_shape(B, K, (D - 1) / (32 * V) + 1, kBwdSlots).ctas;
+    most = ctas > most ? ctas : most;
+  }
+  return static_cast<size_t>(B) * most * D;
 }
 cudaError_t gated_bwd_launch(const GatedCall& q, cudaStream_t s) {
   return q.bf16 ? bwd_t<__nv_bfloat16>(q, s) : bwd_t<float>(q, s);

@@ -64,9 +64,11 @@ struct GatedCall {
   void *dx, *df, *dz;
   long long dx_t, dx_b, df_t, df_b, dz_t, dz_b;
   float *dbias, *dh0, *ws;
-  int* status;                         // device word for waits that ran out
 };
-size_t gated_ws_floats(int B, int K, int D, bool bf16);
+// Workspace: what the launches over segments share (forward and backward), and behind it the partial
+// sums of dbias (backward).
+size_t gated_segments_floats(int B, int K, int D, bool backward);
+size_t gated_partials_floats(int B, int K, int D);
 cudaError_t gated_fwd_launch(const GatedCall& q, cudaStream_t s);
 cudaError_t gated_bwd_launch(const GatedCall& q, cudaStream_t s);
 cudaError_t gated_step_launch(const GatedCall& q, cudaStream_t s);

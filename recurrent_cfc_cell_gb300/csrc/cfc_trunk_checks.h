@@ -10,9 +10,7 @@
 #include "cfc.h"
 
 namespace cfc {
-// cfc_abi.cu; the second one also gives the address of the device status word.
-int device_ready();
-int device_ready(int** status);
+int device_ready();  // cfc_abi.cu
 
 namespace checks {
 

@@ -387,11 +387,12 @@ class GatedStep(_Step):
         self.K, self.B, self.D, self.dtype = K, B, D, dtype
         self.train, self.keep8 = train, keep8
         self.y, self.h = self._act(K, B, D), self._f32(B, D)
-        self.states = self.kept = self.y_again = self.ws = None
+        self.states = self.kept = self.y_again = None
+        # One workspace for both passes, which follow one another.
+        self.ws = _workspace(max(_lib.gated_workspace_bytes(K, B, D, back)
+                                for back in (False, train)), self.device)
         if train:
             self.states = self._f32(-(-K // _lib.GATED_PERIOD), B, D)
-            code = _lib.CFC_BF16 if dtype == torch.bfloat16 else _lib.CFC_F32
-            self.ws = _workspace(_lib.gated_workspace_bytes(K, B, D, code), self.device)
             self.dx, self.df = self._act(K, B, D), self._act(K, B, D)
             self.dz = None
             self.dbias, self.dh0 = self._f32(D), self._f32(B, D)
@@ -412,7 +413,7 @@ class GatedStep(_Step):
         _expect(x, "x", (self.K, self.B, self.D), self.dtype)
         kept = self._keep(z)
         forward = (_lib.cfc_gated_forward.prepare(x, f, self.y, bias, z, h0, lengths, self.h,
-                                                  self.states, kept),)
+                                                  self.states, kept, self.ws),)
         backward = ()
         if dy is not None:
             if not self.train:

@@ -108,7 +108,7 @@ def grads(**over):
     (dict(f=None), NULL_PTR), (dict(x=ODD), MISALIGNED), (dict(z=ODD), MISALIGNED),
     (dict(bias=ODD), MISALIGNED), (dict(h0=ODD), MISALIGNED), (dict(lengths=F + 2), MISALIGNED)])
 def test_gated_refusals(lib, over, code):
-    assert lib.cfc_gated_forward(gated(**over), F, 16, 8, None, None, None, None) == code
+    assert lib.cfc_gated_forward(gated(**over), F, 16, 8, None, None, None, F, 1 << 30, None) == code
     assert lib.cfc_gated_backward(gated(**over), None, F, F, 16, 8, None, grads(dz=F), F, 1 << 30,
                                   None) == code
     if "K" not in over and "x_t" not in over:
@@ -116,7 +116,7 @@ def test_gated_refusals(lib, over, code):
 
 
 def test_gated_output_refusals(lib):
-    fwd = [gated(), F, 16, 8, None, None, None, None]
+    fwd = [gated(), F, 16, 8, None, None, None, None, 0, None]
     assert lib.cfc_gated_forward(*change(fwd, a0=None)) == NULL_PTR
     assert lib.cfc_gated_forward(*change(fwd, a1=None)) == NULL_PTR
     assert lib.cfc_gated_forward(*change(fwd, a2=0)) == INVALID_DIM
@@ -125,7 +125,12 @@ def test_gated_output_refusals(lib):
     assert lib.cfc_gated_forward(*change(fwd, a6=kept(x=(None, F)))) == NULL_PTR
     assert lib.cfc_gated_forward(*change(fwd, a6=kept(f=(F, None)))) == NULL_PTR
     assert lib.cfc_gated_forward(*change(fwd, a0=gated(z=F), a6=kept())) == NULL_PTR
-    need = _lib.gated_workspace_bytes(4, 2, 8, 0)
+    need = _lib.gated_workspace_bytes(4096, 2, 8, False)  # few channels, many steps: segments
+    long = [gated(K=4096), F, 16, 8, None, None, None, F, need - 1, None]
+    assert lib.cfc_gated_forward(*long) == WS_TOO_SMALL
+    assert lib.cfc_gated_forward(*change(long, a7=None)) == NULL_PTR
+    assert lib.cfc_gated_forward(*change(long, a7=F + 8)) == MISALIGNED
+    need = _lib.gated_workspace_bytes(4, 2, 8, True)
     bwd = [gated(), None, F, F, 16, 8, None, grads(), F, need, None]
     for k in (2, 3, 7):
         assert lib.cfc_gated_backward(*change(bwd, **{f"a{k}": None})) == NULL_PTR
@@ -142,7 +147,7 @@ def test_gated_output_refusals(lib):
     assert lib.cfc_gated_step(*change(step, a1=None)) == NULL_PTR
     assert lib.cfc_gated_step(*change(step, a3=None)) == NULL_PTR
     assert lib.cfc_gated_step(*change(step, a3=ODD)) == MISALIGNED
-    assert lib.cfc_gated_workspace_bytes(0, 4, 8, 0, ctypes.byref(ctypes.c_size_t())) == INVALID_DIM
+    assert lib.cfc_gated_workspace_bytes(0, 4, 8, 1, ctypes.byref(ctypes.c_size_t())) == INVALID_DIM
     assert lib.cfc_gated_workspace_bytes(2, 4, 8, 0, None) == NULL_PTR
 
 

@@ -360,6 +360,46 @@ def test_gated_ragged_strided(D, pad, dtype):
     gated_check(st, i, dh_last=True)
 
 
+# Few channels and many steps, which go in segments of the steps: channels in sixteens of bytes, in
+# pairs and singly, segments that end inside a run's 8 steps and ones that there are not.
+SEGMENTS = [(448, 1, 64), (1500, 2, 72), (1001, 3, 50), (2047, 1, 33), (5000, 1, 8), (777, 2, 130)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("K,B,D", SEGMENTS)
+def test_gated_segments(K, B, D, keep8, dtype):
+    ends = [K, K // 3, 0][:B]
+    i = gated_inputs(K, B, D, dtype, K + D, ends)
+    st = gated_step(i, K, B, D, dtype, keep8=keep8, dh_last=True, gate=D != 50)
+    gated_check(st, i, kept=keep8, dh_last=True, gate=D != 50)
+    first = {k: v.clone() for k, v in st.outputs().items()}
+    g = st.capture()
+    for v in st.outputs().values():
+        v.fill_(float("nan"))
+    g.replay()
+    assert all((first[k] == v).all() for k, v in st.outputs().items())
+
+
+@pytest.mark.parametrize("K", [40, 900])
+def test_gated_state_in_its_own_place(K):
+    """The last state over the initial one, in rounds and in segments."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import _lib
+
+    B, D = 2, 96
+    i = gated_inputs(K, B, D, "f32", K, [K, 17])
+    x, f, h = cuda(i["x"]), cuda(i["f"]), cuda(i["h0"])
+    y, le = torch.empty_like(x), torch.tensor(i["ends"], dtype=torch.int32).cuda()
+    ws = torch.empty(max(_lib.gated_workspace_bytes(K, B, D, False), 16), dtype=torch.uint8,
+                     device="cuda")
+    _lib.cfc_gated_forward(x, f, y, cuda(i["bias"]), h0=h, lengths=le, h_last=h, ws=ws)
+    want, last, _ = og.gated(i["x"], i["f"], i["bias"], None, i["h0"], i["ends"])
+    check(y, want, EL, "y")
+    check(h, last, EL, "h")
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_gated_batch_first_memory(dtype):
     """Sequences stored one after another, the outputs written the same way."""
