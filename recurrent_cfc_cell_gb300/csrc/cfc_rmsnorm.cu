@@ -288,16 +288,110 @@ __device__ __forceinline__ float normed(float s, float w, float rstd) {
   return fmaf(p, rstd, low * rstd);
 }
 
+// ---- y to 8 bits ----
+//
+// Next to a border between two codes an error in the last place of y decides which one it becomes, and
+// a code is 2^-3 of the value.  So y is formed in two fp32 parts, from a sum of squares in two parts
+// (relative error below 1e-12), and rounded to fp32 to odd: where something is left behind the last
+// place, that place is set, so that a value beside a border stays on its side of it in the rounding to
+// three bits that follows.
+
+struct Two {  // hi + lo, |lo| at most half a place of hi
+  float hi, lo;
+};
+// a + b where |a| >= |b| or a is 0; Dekker's sum.
+__device__ __forceinline__ Two fast_two(float a, float b) {
+  const float s = a + b;
+  return {s, b - (s - a)};
+}
+// a + b of two sums; Knuth's sum of the high parts, whose rest joins the low ones, which nothing but
+// sums of theirs follows: they are put right at the end.
+__device__ __forceinline__ Two plus(Two a, Two b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float rest = (a.hi - (s - t)) + (b.hi - t);
+  return {s, a.lo + b.lo + rest};
+}
+
+// The same for the two columns of a pair, in packed arithmetic.
+struct Pair {
+  float2 hi, lo;
+};
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+// v + a^2.  `EXACT`: the squares of bf16 values are exact in fp32.
+template <bool EXACT>
+__device__ __forceinline__ Pair plus_square(Pair v, float2 a) {
+  const float2 p = __fmul2_rn(a, a);
+  const float2 s = __fadd2_rn(v.hi, p), t = __fadd2_rn(s, neg2(v.hi));
+  float2 rest = __fadd2_rn(__fadd2_rn(v.hi, neg2(__fadd2_rn(s, neg2(t)))), __fadd2_rn(p, neg2(t)));
+  if (!EXACT) rest = __fadd2_rn(rest, fma2(a, a, neg2(p)));
+  return {s, __fadd2_rn(v.lo, rest)};
+}
+__device__ __forceinline__ Two both(Pair v) {
+  return plus(Two{v.hi.x, v.lo.x}, Two{v.hi.y, v.lo.y});
+}
+// (sum / n + eps)^-1/2 in two parts.  r = m^-1/2 (1 - e / 2 + ...) with e = m r^2 - 1.
+__device__ __forceinline__ Two rstd_two(Two sum, float nf, float over_n, float eps) {
+  const float q = sum.hi * over_n;  // within a place of the quotient, so that its rest is exact
+  const Two m = plus(Two{q, (fmaf(-q, nf, sum.hi) + sum.lo) * over_n}, Two{eps, 0.f});
+  const float r = rsqrtf(m.hi);
+  const float rr = r * r, rr_low = fmaf(r, r, -rr);
+  const float p = m.hi * rr;  // near 1
+  const float e = (p - 1.f) + (fmaf(m.hi, rr, -p) + (m.hi * rr_low + m.lo * rr));
+  const float low = r * e * fmaf(0.375f, e, -0.5f);
+  return r > 0.f && r < 1e18f && m.hi < 1e38f ? fast_two(r, low) : Two{r, 0.f};
+}
+// s w rstd in two parts.
+__device__ __forceinline__ Pair normed_two(float2 s, float2 w, Two rstd) {
+  const float2 hi = make_float2(rstd.hi, rstd.hi), lo = make_float2(rstd.lo, rstd.lo);
+  const float2 p = __fmul2_rn(s, w), p_low = fma2(s, w, neg2(p));
+  const float2 y = __fmul2_rn(p, hi);
+  const float2 low = __fadd2_rn(fma2(p, hi, neg2(y)), fma2(p, lo, __fmul2_rn(p_low, hi)));
+  const float2 sum = __fadd2_rn(y, low);
+  return {sum, __fadd2_rn(low, neg2(__fadd2_rn(sum, neg2(y))))};
+}
+// To odd: a last place of 0 becomes 1, upwards or downwards to where the rest lies.
+__device__ __forceinline__ float to_odd(float hi, float lo) {
+  const uint32_t bits = __float_as_uint(hi), some = fabsf(lo) > 0.f ? 1u : 0u;
+  const uint32_t less = ((bits ^ __float_as_uint(lo)) >> 31) & some;  // the rest points to 0
+  return __uint_as_float((bits - less) | some);
+}
+
+// The sum over a row's team in two parts, in the order of team_sum.
+template <typename TM>
+__device__ __forceinline__ Two team_sum_two(Two v, Two (*part)[32], int turn) {
+  constexpr int kLanes = TM::kWarp ? TM::TPR : 32;
+  auto add = [&](int d) {
+    const Two o{__shfl_xor_sync(0xffffffffu, v.hi, d), __shfl_xor_sync(0xffffffffu, v.lo, d)};
+    v = plus(v, o);
+  };
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d /= 2) add(d);
+  if constexpr (!TM::kWarp) {
+    Two* const p = part[turn & 1];
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) p[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = lane < static_cast<int>(blockDim.x) / 32 ? p[lane] : Two{0.f, 0.f};
+#pragma unroll
+    for (int d = TM::TPR / 64; d > 0; d /= 2) add(d);
+    v.hi = __shfl_sync(0xffffffffu, v.hi, 0);
+    v.lo = __shfl_sync(0xffffffffu, v.lo, 0);
+  }
+  return v;
+}
+
 // The next row's loads are on their way while a row is worked on.  Teams' rows are a multiple of
 // eight apart, so that a team's rows start at the same place within a group of eight.
-template <typename T, typename TM>
+// OUT8: y is held in 8 bits.
+template <typename T, typename TM, bool OUT8>
 __global__ void __launch_bounds__(TM::kThreads) rms_fwd_kernel(const RmsCall q) {
-  __shared__ float part[2][32];
+  __shared__ std::conditional_t<OUT8, Two, float> part[2][32];
   const long long step = static_cast<long long>(gridDim.x) * TM::kTeams;
   long long row = static_cast<long long>(blockIdx.x) * TM::kTeams + TM::team();
   const At<TM> at(q.n, q.rows, static_cast<const T*>(q.x) + row * q.ldx);
   float w[TM::E];
   load_par<TM>(at, q.w, w);
+  const float nf = static_cast<float>(q.n), over_n = 1.f / nf;  // n, at most 2^24, is exact
   Piece<T, TM> x_next, res_next;
   auto fetch = [&](long long row) {
     const bool ok = row < q.rows;
@@ -316,20 +410,43 @@ __global__ void __launch_bounds__(TM::kThreads) rms_fwd_kernel(const RmsCall q) 
     float s[TM::E];
     x.get(at, s);
     if (q.s) store_row<TM>(at, static_cast<T*>(q.s) + row * q.lds, x, s, ok);
-    float sum = 0.f;
+    if constexpr (OUT8) {
+      constexpr bool EXACT = sizeof(T) == 2;
+      Pair sum{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < TM::E; ++i) sum = fmaf(s[i], s[i], sum);
-    const float rstd = rstd_of(team_sum<TM>(sum, part, turn), q.n, q.eps);
-    if (ok && q.rstd && threadIdx.x % TM::TPR == 0) q.rstd[row] = rstd;
-    if constexpr (TM::LY != kShifted) {
+      for (int i = 0; i < TM::E; i += 2)
+        sum = plus_square<EXACT>(sum, make_float2(s[i], i + 1 < TM::E ? s[i + 1] : 0.f));
+      const Two rstd = rstd_two(team_sum_two<TM>(both(sum), part, turn), nf, over_n, q.eps);
+      if (ok && q.rstd && threadIdx.x % TM::TPR == 0) q.rstd[row] = rstd.hi;
       if (q.s8.codes) store_held<TM>(at, q.s8, row, s, ok);
-    }
-    if (!q.y && !q.y8.codes) continue;
+      float y[TM::E];
 #pragma unroll
-    for (int i = 0; i < TM::E; ++i) s[i] = normed(s[i], w[i], rstd);
-    if (q.y) store_row<TM>(at, static_cast<T*>(q.y) + row * q.ldy, s, ok);
-    if constexpr (TM::LY != kShifted) {
-      if (q.y8.codes) store_held<TM>(at, q.y8, row, s, ok);
+      for (int i = 0; i < TM::E; i += 2) {
+        const bool two = i + 1 < TM::E;
+        const Pair v = normed_two(make_float2(s[i], two ? s[i + 1] : 0.f),
+                                  make_float2(w[i], two ? w[i + 1] : 0.f), rstd);
+        y[i] = v.hi.x;
+        s[i] = to_odd(v.hi.x, v.lo.x);
+        if (two) {
+          y[i + 1] = v.hi.y;
+          s[i + 1] = to_odd(v.hi.y, v.lo.y);
+        }
+      }
+      if (q.y) store_row<TM>(at, static_cast<T*>(q.y) + row * q.ldy, y, ok);
+      store_held<TM>(at, q.y8, row, s, ok);
+    } else {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < TM::E; ++i) sum = fmaf(s[i], s[i], sum);
+      const float rstd = rstd_of(team_sum<TM>(sum, part, turn), q.n, q.eps);
+      if (ok && q.rstd && threadIdx.x % TM::TPR == 0) q.rstd[row] = rstd;
+      if constexpr (TM::LY != kShifted) {
+        if (q.s8.codes) store_held<TM>(at, q.s8, row, s, ok);
+      }
+      if (!q.y) continue;
+#pragma unroll
+      for (int i = 0; i < TM::E; ++i) s[i] = normed(s[i], w[i], rstd);
+      store_row<TM>(at, static_cast<T*>(q.y) + row * q.ldy, s, ok);
     }
   }
 }
@@ -433,17 +550,25 @@ __global__ void __launch_bounds__(TM::kThreads, bwd_per_sm<T, TM>()) rms_bwd_ker
 constexpr int kLongThreads = 512;
 using LongTeam = Team<kLongThreads, 1, kScalar>;
 
-template <typename T>
+template <typename T, bool OUT8>
 __global__ void __launch_bounds__(kLongThreads) rms_long_fwd_kernel(const RmsCall q) {
-  __shared__ float part[2][32];
+  __shared__ std::conditional_t<OUT8, Two, float> part[2][32];
   const int n = q.n, whole = held_blocks(n) * kHeldBlock;
   int turn = 0;
+  // Columns past n (to a whole block) hold 0, so that whole warps pack.
+  auto hold = [&](const Held8& h, long long row, int c, float v) {
+    uint32_t byte;
+    const uint32_t r = held_pack1(v, byte);
+    if (c < n) h.codes[row * n + c] = static_cast<uint8_t>(r);
+    if (c % kHeldBlock == 0)
+      h.scales[row * held_blocks(n) + c / kHeldBlock] = static_cast<uint8_t>(byte);
+  };
   for (long long row = blockIdx.x; row < q.rows; row += gridDim.x, ++turn) {
     const T* const x = static_cast<const T*>(q.x) + row * q.ldx;
     const T* const res = q.residual ? static_cast<const T*>(q.residual) + row * q.ldr : nullptr;
     T* const so = q.s ? static_cast<T*>(q.s) + row * q.lds : nullptr;
-    // Columns past n (to a whole block) hold 0, so that whole warps pack.
-    float sum = 0.f;
+    Two sum{0.f, 0.f};
+    [[maybe_unused]] Pair squares{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     for (int c = threadIdx.x; c < whole; c += kLongThreads) {
       float v = 0.f;
       if (c < n) {
@@ -451,34 +576,31 @@ __global__ void __launch_bounds__(kLongThreads) rms_long_fwd_kernel(const RmsCal
         if (res) v = to_f32(from_f32<T>(v + to_f32(res[c])));
         if (so) so[c] = from_f32<T>(v);
       }
-      sum = fmaf(v, v, sum);
-      if (q.s8.codes) {
-        uint32_t byte;
-        const uint32_t r = held_pack1(v, byte);
-        if (c < n) q.s8.codes[row * n + c] = static_cast<uint8_t>(r);
-        if (c % kHeldBlock == 0)
-          q.s8.scales[row * held_blocks(n) + c / kHeldBlock] = static_cast<uint8_t>(byte);
-      }
+      if constexpr (OUT8) squares = plus_square<false>(squares, make_float2(v, 0.f));
+      else sum.hi = fmaf(v, v, sum.hi);
+      if (q.s8.codes) hold(q.s8, row, c, v);
     }
-    const float rstd = rstd_of(team_sum<LongTeam>(sum, part, turn), n, q.eps);
-    if (q.rstd && threadIdx.x == 0) q.rstd[row] = rstd;
-    if (!q.y && !q.y8.codes) continue;
+    Two rstd{0.f, 0.f};
+    if constexpr (OUT8)
+      rstd = rstd_two(team_sum_two<LongTeam>(both(squares), part, turn), static_cast<float>(n),
+                      1.f / static_cast<float>(n), q.eps);
+    else
+      rstd.hi = rstd_of(team_sum<LongTeam>(sum.hi, part, turn), n, q.eps);
+    if (q.rstd && threadIdx.x == 0) q.rstd[row] = rstd.hi;
+    if (!q.y && !OUT8) continue;
     for (int c = threadIdx.x; c < whole; c += kLongThreads) {
-      float v = 0.f;
+      Two y{0.f, 0.f};
       if (c < n) {
         // s where it was written: x and the residual may have been in its place.
-        v = to_f32(so ? so[c] : x[c]);
+        float v = to_f32(so ? so[c] : x[c]);
         if (res && !so) v = to_f32(from_f32<T>(v + to_f32(res[c])));
-        v = normed(v, __ldg(q.w + c), rstd);
-        if (q.y) static_cast<T*>(q.y)[row * q.ldy + c] = from_f32<T>(v);
+        if constexpr (OUT8) {
+          const Pair p = normed_two(make_float2(v, 0.f), make_float2(__ldg(q.w + c), 0.f), rstd);
+          y = {p.hi.x, p.lo.x};
+        } else y.hi = normed(v, __ldg(q.w + c), rstd.hi);
+        if (q.y) static_cast<T*>(q.y)[row * q.ldy + c] = from_f32<T>(y.hi);
       }
-      if (q.y8.codes) {
-        uint32_t byte;
-        const uint32_t r = held_pack1(v, byte);
-        if (c < n) q.y8.codes[row * n + c] = static_cast<uint8_t>(r);
-        if (c % kHeldBlock == 0)
-          q.y8.scales[row * held_blocks(n) + c / kHeldBlock] = static_cast<uint8_t>(byte);
-      }
+      if constexpr (OUT8) hold(q.y8, row, c, to_odd(y.hi, y.lo));
     }
   }
 }
@@ -615,20 +737,23 @@ int partials(int rows, int n, Layout ly) {
   return p;
 }
 
-template <typename T>
+template <typename T, bool OUT8>
 cudaError_t fwd(const RmsCall& q, cudaStream_t s) {
   LaunchCfg c;
   c.stream = s;
   if (q.n > kLongRow) {
     c.grid = dim3(fwd_ctas(q.rows, 8, kLongThreads));
     c.block = dim3(kLongThreads);
-    return launch(c, rms_long_fwd_kernel<T>, q);
+    return launch(c, rms_long_fwd_kernel<T, OUT8>, q);
   }
   return with_team(q.n, layout(q), [&](auto tm, int threads) {
     using TM = decltype(tm);
-    c.grid = dim3(fwd_ctas(q.rows, TM::kTeams, threads));
-    c.block = dim3(threads);
-    return launch(c, rms_fwd_kernel<T, TM>, q);
+    if constexpr (OUT8 && TM::LY == kShifted) return cudaErrorInvalidValue;  // never chosen
+    else {
+      c.grid = dim3(fwd_ctas(q.rows, TM::kTeams, threads));
+      c.block = dim3(threads);
+      return launch(c, rms_fwd_kernel<T, TM, OUT8>, q);
+    }
   });
 }
 
@@ -678,7 +803,8 @@ size_t rms_ws_floats(int rows, int n) {
   return p == 1 ? 0 : static_cast<size_t>(p) * n;
 }
 cudaError_t rms_fwd_launch(const RmsCall& q, cudaStream_t s) {
-  return q.bf16 ? fwd<__nv_bfloat16>(q, s) : fwd<float>(q, s);
+  if (q.y8.codes) return q.bf16 ? fwd<__nv_bfloat16, true>(q, s) : fwd<float, true>(q, s);
+  return q.bf16 ? fwd<__nv_bfloat16, false>(q, s) : fwd<float, false>(q, s);
 }
 cudaError_t rms_bwd_launch(const RmsCall& q, float* dw, float* ws, cudaStream_t s) {
   if (q.x)

@@ -198,6 +198,34 @@ def test_rmsnorm_in_8_bits(rows, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n", [(20000, 96), (6000, 1024), (3000, 777), (700, 5000), (300, 9000)])
+def test_rmsnorm_8_bits_beside_borders(rows, n, dtype):
+    """Codes are the ones of the exact y, also beside the borders between two codes: fp32 alone would
+    take the other one about once in a million values, and these are several million."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import trunk
+
+    g = torch.Generator(device="cuda").manual_seed(n)
+    r = lambda *a: torch.randn(*a, generator=g, device="cuda")  # noqa: E731
+    x, res, w = r(rows, n).to(act(dtype)), r(rows, n).to(act(dtype)), r(n) * 0.2 + 1.0
+    st = trunk.RMSNormStep(rows, n, act(dtype), out8=True).bind(x, w, res)
+    st.run()
+    s = st.s.double()
+    eps = float(np.float32(1e-5))
+    y = s * w.double() / torch.sqrt((s * s).mean(1, keepdim=True) + eps)
+    got = trunk.Unpack8Step(rows, n).bind(st.y8).run().double()
+    for c in range(0, n, 32):
+        v = y[:, c:c + 32]
+        top = v.abs().amax(1, keepdim=True)
+        m, e = torch.frexp(top)  # 448 = 0.875 * 2^9
+        k = torch.where(m > 0.875, e - 8, e - 9).double()
+        u = v * torch.exp2(-k)
+        step = torch.exp2(torch.clamp(torch.floor(torch.log2(u.abs().clamp(min=1e-30))), min=-6.0) - 3.0)
+        assert torch.equal(got[:, c:c + 32], torch.round(u / step) * step * torch.exp2(k)), c
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", [64, 300, 8200])
 def test_rmsnorm_alone_strided_in_place(n, dtype):
     """No residual and no stream gradient, rows further apart than they are long, the results in
