@@ -638,7 +638,8 @@ int cfc_unpack8(const cfc_held8* held, int rows, int n, int dtype, void* y, long
 
 /*
  * Root-mean-square norm: s = x + residual, rounded to dtype (residual NULL: s = x);
- * rstd = (sum s^2 / n + eps)^-1/2;  y = s rstd w.  The norm reads s as rounded.
+ * rstd = (sum s^2 / n + eps)^-1/2;  y = s rstd w.  The norm reads s as rounded.  (A row of zeros with
+ * eps = 0 gives NaN; squares beyond fp32, from magnitudes of 1.8e19, make rstd 0.)
  */
 typedef struct cfc_rmsnorm_args {
   int rows, n;             /* n <= 2^24                                                          */
@@ -653,7 +654,8 @@ typedef struct cfc_rmsnorm_args {
 /*
  * cfc_rmsnorm_forward -- each output is written where its pointer is not NULL:
  *   s [rows][n] (lds; may be x's or residual's own memory), y [rows][n] (ldy),
- *   s8, y8: s and y in 8 bits (y8 from y before it is rounded to dtype),
+ *   s8, y8: s and y in 8 bits (y8 from the exact y: its codes are the nearest ones also beside the
+ *   border between two),
  *   rstd [rows], which the backward pass reads.
  */
 int cfc_rmsnorm_forward(const cfc_rmsnorm_args* a, void* s, long long lds, void* y, long long ldy,

@@ -712,18 +712,21 @@ cudaError_t with_team(int n, Layout ly, F&& f) {
 }
 
 // CTAs for `rows`: a multiple of eight (152 is one) where a CTA has one team.
-int in_eights(int ctas, int teams) { return teams % 8 == 0 ? ctas : (ctas - 1) / 8 * 8 + 8; }
+long long in_eights(long long ctas, int teams) {
+  return teams % 8 == 0 ? ctas : (ctas - 1) / 8 * 8 + 8;
+}
 int fwd_ctas(int rows, int teams, int threads) {
-  const int need = in_eights((rows - 1) / teams + 1, teams), most = kSms * (2048 / threads);
-  return need < most ? need : most;
+  const long long need = in_eights((rows - 1) / teams + 1, teams), most = kSms * (2048 / threads);
+  return static_cast<int>(need < most ? need : most);
 }
 // CTAs of the backward pass, and so rows of the partial sums of dw: a row of them costs 8 bytes a
 // column to write and read, so a CTA takes four rows of a team at least once all SMs have one.
 template <typename T, typename TM>
 int bwd_ctas(int rows) {
-  const int most = kSms * bwd_per_sm<T, TM>(), need = in_eights((rows - 1) / TM::kTeams + 1, TM::kTeams);
-  const int want = need / 4 > kSms ? in_eights(need / 4, TM::kTeams) : kSms;
-  return need < want ? need : want < most ? want : most;
+  const long long most = kSms * bwd_per_sm<T, TM>();
+  const long long need = in_eights((rows - 1) / TM::kTeams + 1, TM::kTeams);
+  const long long want = need / 4 > kSms ? in_eights(need / 4, TM::kTeams) : kSms;
+  return static_cast<int>(need < want ? need : want < most ? want : most);
 }
 int long_splits(int rows) { return rows < 64 ? 1 : rows / 64 < 64 ? rows / 64 : 64; }
 template <typename T>

@@ -446,6 +446,33 @@ def test_gated_batch_first_memory(dtype):
     check(h, last, EL, "h")  # in its initial state's place
 
 
+@pytest.mark.parametrize("K,D", [(20, 64), (700, 50)])
+def test_gated_backward_forms_y_again(K, D):
+    """y formed again from inputs that are kept as they are, without the gradients that are not
+    wanted; z's gate strided apart from the others."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import _lib
+
+    B = 2
+    i = gated_inputs(K, B, D, "f32", D)
+    t = {k: cuda(i[k]) for k in ("x", "f", "dy", "bias", "h0")}
+    z = wide(cuda(i["z"]), 5)
+    y, again, states = torch.empty_like(t["x"]), torch.empty_like(t["x"]), torch.empty(
+        -(-K // _lib.GATED_PERIOD), B, D, device="cuda")
+    ws = torch.empty(max(_lib.gated_workspace_bytes(K, B, D, b) for b in (False, True)) + 16,
+                     dtype=torch.uint8, device="cuda")
+    _lib.cfc_gated_forward(t["x"], t["f"], y, t["bias"], z, t["h0"], states=states, ws=ws)
+    dx, df, dz = (torch.empty_like(y) for _ in range(3))
+    _lib.cfc_gated_backward(t["dy"], t["x"], t["f"], states, dx, df, t["bias"], z, dz=dz, y=again,
+                            ws=ws)
+    want, y64 = og.gated_backward(i["dy"], i["x"], i["f"], i["bias"], i["z"], i["h0"], i["ends"])
+    check(again, y64, EL, "y")
+    check(y, y64, EL, "y")
+    for name, got in (("dx", dx), ("df", df), ("dz", dz)):
+        check(got, want[name], SUM, name)
+
+
 def test_gated_continues():
     """A sequence in three calls, and tokens that go on from there."""
     import torch
