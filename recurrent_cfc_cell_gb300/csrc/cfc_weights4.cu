@@ -176,10 +176,11 @@ template <>
 struct XPiece<float> {
   static constexpr int kTerms = 3;
   // A term is the upper half of what is left, eight bits of it, so that three of them are all 24 and
-  // every difference is exact (of an infinity it is not a number: nothing is left).
+  // every difference is exact.  Of an infinity nothing is left; of a NaN whose upper half alone would be
+  // an infinity the difference is one in every half.
   static __device__ __forceinline__ float rest(float a) {
     const float r = a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-    return r == r ? r : 0.f;
+    return (__float_as_uint(a) & 0x7fffffffu) == 0x7f800000u ? 0.f : r;
   }
   static __device__ __forceinline__ void split(const Raw8<float>& r, uint4 (&term)[3]) {
     float v[8];

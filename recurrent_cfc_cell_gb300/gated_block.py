@@ -20,7 +20,7 @@ import torch
 
 from . import _lib
 from .step import KLoopStep
-from .trunk import GatedStep, GatedToken, MatvecStep, RMSNormStep, Weights4
+from .trunk import GatedStep, GatedToken, MatvecStep, RMSNormStep, Weights4, _expect
 
 
 def make_gated_params(layers: int, D: int, E: int, C: int, seed: int = 0, device=None) -> dict:
@@ -174,6 +174,7 @@ class GatedServe:
 
     def token(self, s) -> torch.Tensor:
         """The last norm's output [B, D] of one token s [B, D] per sequence, a tensor of its own."""
+        _expect(s, "s", (self.B, self.D), torch.float32)  # a copy would repeat one row for all
         if self._token is None:
             B, E = self.B, self.E
             self.s = torch.empty(B, self.D, device=s.device)
