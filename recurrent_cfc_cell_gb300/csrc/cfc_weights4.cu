@@ -8,6 +8,12 @@
 // which hold all of its 24 bits, and the scale multiplies each group's sum in fp32.  Nothing is
 // rounded before the sums.
 //
+// Measured, groups of 128: 1 x 16384 x 4096 bf16 12.3 us and fp32 14 us (35 MB of weights, 5.2 us at
+// the rate of a copy), 8 rows 18 us, 32 rows (groups of 64) 39 us, 1 x 4096 x 16384 14 us,
+// 16 x 8192 x 8192 34 us, 1 x 4096 x 4096 6.2 us.  One row is bound by instructions and latency: 1.4
+// instructions for a code, 5 us of issue, before a launch and the first weights' way, which a warp's four
+// to eight tiles do not hide; the tensor cores are busy for 1.8 us of it.
+//
 // Laid-out weights: tiles of 16 rows x 128 columns of 1024 bytes, one after another along a row of
 // tiles.  In a tile lane 4 g + t of a warp owns rows g and g + 8 (one 16-byte load each) and of
 // every 32 columns the eight from 8 t on, in one 32-bit word: columns j and j + 4 of the eight are
@@ -239,17 +245,13 @@ __global__ void __launch_bounds__(256, NT == 1 ? 4 : 2)
   float acc[NT][4] = {};
   uint4 lo[kAhead], hi[kAhead];
   uint32_t sc[kAhead][kPer];
-  auto fetch = [&](int left) {  // the next kAhead tiles of the warp, of which `left` are there
+  auto fetch = [&](int a) {  // the warp's next tile
+    lo[a] = ld_once(codes);
+    hi[a] = ld_once(codes + 32);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (a >= left) break;
-      lo[a] = ld_once(codes);
-      hi[a] = ld_once(codes + 32);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sc[a][i] = __ldg(scales + i * (kTileN / 2));
-      codes += code_step;
-      scales += scale_step;
-    }
+    for (int i = 0; i < kPer; ++i) sc[a][i] = __ldg(scales + i * (kTileN / 2));
+    codes += code_step;
+    scales += scale_step;
   };
   // Tiles of this warp in a chunk that begins at c0 (a multiple of `deep`, as chunks are).
   auto tiles = [&](int c0) {
@@ -257,7 +259,9 @@ __global__ void __launch_bounds__(256, NT == 1 ? 4 : 2)
   };
   for (int c0 = 0; c0 < tk; c0 += sp.chunk) {
     int left = tiles(c0);
-    fetch(left);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (a < left) fetch(a);
     if (c0 > 0) __syncthreads();
     // x of the chunk, in pieces of 8 values: 16 threads a row's part of a tile.
     const unsigned count = min(sp.chunk, tk - c0) * mm;
@@ -315,9 +319,9 @@ __global__ void __launch_bounds__(256, NT == 1 ? 4 : 2)
             }
           }
         }
+        if (a + kAhead < left) fetch(a);
       }
       left -= kAhead;
-      fetch(left);
     }
   }
   __syncthreads();
@@ -359,6 +363,10 @@ cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
   sp.rows = sp.m * kTerms <= 2 ? 0 : 2;
   while (sp.rows > 0 && sh.tn >> sp.rows < 152 * 5 / 4) --sp.rows;
   sp.deep = 8 >> sp.rows;
+  // Shorter columns of warps where the CTAs are more than the GPU holds at a time, so that a warp has
+  // more tiles for what it does once (1 x 12288 x 4096 10.3 us, always eight 11.6 us; 65536 x 1024 12.4
+  // and 18.2 us); where they are not, all eight (1 x 8192 x 4096 8.6 us, four 10.2 us).
+  while (sp.rows == 0 && sp.deep > 2 && sh.tn > 152 * 32 / sp.deep) sp.deep /= 2;
   if (sh.tk < sp.deep) sp.deep = sh.tk;
   const int bytes = 256 * sp.m * kTerms;  // of x for a tile along K; at most 8 KB
   sp.chunk = 64 * 1024 / bytes / sp.deep * sp.deep;
