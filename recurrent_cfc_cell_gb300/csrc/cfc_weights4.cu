@@ -8,11 +8,12 @@
 // which hold all of its 24 bits, and the scale multiplies each group's sum in fp32.  Nothing is
 // rounded before the sums.
 //
-// Measured, groups of 128: 1 x 16384 x 4096 bf16 12.3 us and fp32 14 us (35 MB of weights, 5.2 us at
-// the rate of a copy), 8 rows 18 us, 32 rows (groups of 64) 39 us, 1 x 4096 x 16384 14 us,
-// 16 x 8192 x 8192 34 us, 1 x 4096 x 4096 6.2 us.  One row is bound by instructions and latency: 1.4
-// instructions for a code, 5 us of issue, before a launch and the first weights' way, which a warp's four
-// to eight tiles do not hide; the tensor cores are busy for 1.8 us of it.
+// Measured, groups of 128: 1 x 16384 x 4096 12.3 us, bf16 and fp32 (35 MB of weights, 5.2 us at the rate
+// of a copy), 8 rows 14 us, 16 rows 24 us, 32 rows 39 us, 1 x 4096 x 16384 14 us, 16 x 8192 x 8192
+// 25 us, 1 x 4096 x 4096 6.2 us.  One row is bound by instructions and latency: 1.4 instructions for a
+// code, 5 us of issue, before a launch and the first weights' way, which a warp's four to eight tiles
+// do not hide; the tensor cores are busy for 1.8 us of it.  32 rows wait for weights, of which 16 warps
+// an SM (their sums take 128 registers) have too few on their way.
 //
 // Laid-out weights: tiles of 16 rows x 128 columns of 1024 bytes, one after another along a row of
 // tiles.  In a tile lane 4 g + t of a warp owns rows g and g + 8 (one 16-byte load each) and of
@@ -220,7 +221,7 @@ struct Spread {
 // not are computed from the last one and dropped.  A warp has kAhead tiles of weights on their way
 // together, the first of them while x is brought in.
 template <typename T, int GROUP, int NT>
-__global__ void __launch_bounds__(256, NT == 1 ? 4 : 2)
+__global__ void __launch_bounds__(512, NT == 1 ? 2 : 1)
     matvec4_kernel(const Weights4Call q, const Spread sp) {
   extern __shared__ uint4 xs[];  // [tiles of a chunk][4][columns][4]; later the warps' sums
   using X = XPiece<T>;
@@ -357,12 +358,17 @@ cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
   sp.vec = reinterpret_cast<uintptr_t>(q.x) % (q.bf16 ? 16 : 32) == 0 && q.ldx % 8 == 0;
   sp.m = 8 * nt / kTerms;
   if (q.M < sp.m) sp.m = q.M;
-  // More tiles of rows at a time share what a CTA reads of x, where there are enough of them to give
-  // most SMs a CTA: 32 x 16384 x 4096 39 us (one tile 98 us), 16 x 8192 x 8192 34 us with two (one
-  // 51 us, four 39 us); one row of x has little to share (1 x 4096 x 16384 14.5 us, with two 20 us).
+  // More tiles of rows at a time share what a CTA reads of x, as long as half of the SMs have a CTA:
+  // with four tiles 16 x 8192 x 8192 takes 25 us (two 37 us, one 53 us) and 8 x 16384 x 4096 14 us (18 and
+  // 27 us), with two 8 x 4096 x 4096 8.8 us (four 10.3 us).  One row of x has little to share (1 x 4096
+  // x 16384 14.5 us, with two 20 us).
   sp.rows = sp.m * kTerms <= 2 ? 0 : 2;
-  while (sp.rows > 0 && sh.tn >> sp.rows < 152 * 5 / 4) --sp.rows;
-  sp.deep = 8 >> sp.rows;
+  while (sp.rows > 0 && sh.tn >> sp.rows < 152 / 2) --sp.rows;
+  // Sixteen warps where the GPU holds all CTAs at a time (8 x 16384 x 4096 14 us, eight 17 us), else eight
+  // (32 x 16384 x 4096 39 us, sixteen 42.5 us).  In one column of tiles eight, whose parts of x fit shared
+  // memory for any number of rows.
+  const long long ctas = ((sh.tn - 1ll >> sp.rows) + 1) * ((q.M - 1) / sp.m + 1);
+  sp.deep = sp.rows > 0 && ctas <= (nt == 1 ? 304 : 152) ? 16 >> sp.rows : 8 >> sp.rows;
   // Shorter columns of warps where the CTAs are more than the GPU holds at a time, so that a warp has
   // more tiles for what it does once (1 x 12288 x 4096 10.3 us, always eight 11.6 us; 65536 x 1024 12.4
   // and 18.2 us); where they are not, all eight (1 x 8192 x 4096 8.6 us, four 10.2 us).

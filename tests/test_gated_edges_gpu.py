@@ -184,6 +184,24 @@ def test_another_stream():
         assert all(torch.equal(a, b) for a, b in zip(st.outputs().values(), want.outputs().values()))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", [(1, 19500, 300, 128), (1, 40000, 130, 32), (3, 2450, 1100, 64),
+                                         (8, 5000, 2050, 128), (12, 9000, 1000, 64),
+                                         (30, 2500, 2100, 128), (33, 5000, 700, 32), (70, 20, 260, 64)])
+def test_matvec4_spreads(M, N, K, group, dtype):
+    """Every way in which a product's warps are spread over rows and columns of W, with odd ends."""
+    from recurrent_cfc_cell_gb300 import trunk
+    from gated_cases import weights4_inputs
+    from test_gated_gpu import act
+    import torch
+
+    i = weights4_inputs(M, N, K, group, dtype, N + K)
+    weights = trunk.Weights4(torch.from_numpy(i["codes"]).cuda(), cuda(i["scales"], "bf16"), K, group)
+    st = trunk.MatvecStep(M, weights, dtype=act(dtype)).bind(cuda(i["x"], dtype))
+    st.run()
+    check(st.y, i["x"] @ og.weights4(i["codes"], i["scales"], K, group).T, EL, "y")
+
+
 def test_matvec4_of_every_nan():
     """A NaN whose upper 16 bits are an infinity's."""
     import torch
