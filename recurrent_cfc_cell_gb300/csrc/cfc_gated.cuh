@@ -177,41 +177,19 @@ __device__ __forceinline__ HeldAt held_at(const GatedCall& q, int t, int b, int 
   const size_t row = static_cast<size_t>(t) * q.B + b;
   return {row * q.D + d, row * held_blocks(q.D) + d / kHeldBlock};
 }
-// V channels a lane to 8 bits: a block is 32 / V lanes.
-template <int V>
-__device__ __forceinline__ void store_held_v(const Held8& h, const HeldAt& at, Fv<V> v, bool in) {
-  uint32_t byte, codes;
-  if constexpr (V == 1) {
-    codes = held_pack1(v[0], byte);
-    if (in) h.codes[at.code] = static_cast<uint8_t>(codes);
-  } else {
-    uint32_t most = max(magnitude_bits(v[0]), magnitude_bits(v[1]));
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-    byte = held_scale_byte(most);
-    const float down = held_down(byte);
-    codes = held_codes2(v[0] * down, v[1] * down);
-    if (in) *reinterpret_cast<uint16_t*>(h.codes + at.code) = static_cast<uint16_t>(codes);
-  }
-  if (in && threadIdx.x % (32 / V) == 0) h.scales[at.scale] = static_cast<uint8_t>(byte);
-}
-
-// V channels of one step in 8 bits, as they are stored.
-template <int V>
-struct RawHeldV {
+// Two channels of one step in 8 bits, as they are stored.
+struct RawHeld2 {
   uint16_t codes;
   uint8_t byte;
   __device__ __forceinline__ void load(const Held8& h, const HeldAt& at) {
-    codes = V == 1 ? h.codes[at.code] : *reinterpret_cast<const uint16_t*>(h.codes + at.code);
+    codes = *reinterpret_cast<const uint16_t*>(h.codes + at.code);
     byte = h.scales[at.scale];
   }
   __device__ __forceinline__ void clear() { codes = 0; byte = 1; }
-  __device__ __forceinline__ Fv<V> get() const {
-    const float2 p = held_values2(codes);
-    Fv<V> o;
-    o[0] = p.x;
-    if constexpr (V == 2) o[1] = p.y;
-    return o * Fv<V>(held_up(byte));
+  __device__ __forceinline__ Fv<2> get() const {
+    Fv<2> o;
+    o.v = held_values2(codes);
+    return o * Fv<2>(held_up(byte));
   }
 };
 

@@ -25,9 +25,23 @@ struct Input {  // a run of an activation that the backward pass reads as it is,
 };
 template <typename T, int V>
 struct Input<T, V, true> {
-  RawHeldV<V> raw[kGS];
+  RawHeld2 raw[kGS];
   __device__ __forceinline__ void load(int k, const T*, const Held8& h, const HeldAt& at) {
     raw[k].load(h, at);
+  }
+};
+// One channel a lane: a warp's channels are one block, whose scales lanes hold for each other.
+template <typename T>
+struct Input<T, 1, true> {
+  struct Code {
+    uint8_t v;
+    __device__ __forceinline__ void clear() { v = 0; }
+  } raw[kGS];
+  __device__ __forceinline__ void load(int k, const T*, const Held8& h, const HeldAt& at) {
+    raw[k].v = h.codes[at.code];
+  }
+  __device__ __forceinline__ Fv<1> get(int k, float up) const {
+    return Fv<1>(held_values2(raw[k].v).x * __shfl_sync(0xffffffffu, up, k));
   }
 };
 
@@ -43,11 +57,12 @@ struct Ring {
   static constexpr int kStage = Run::kBytes + (IN ? (Z ? 3 : 2) * kInput : 0), kWarp = kStages * kStage;
 };
 
-// The scales of a run of 64 channels in 8 bits: lane 2 k + i holds the one of step k's block i.
+// The scales of a run of 32 V channels in 8 bits: lane V k + i holds the one of step k's block i.
+template <int V>
 __device__ __forceinline__ uint32_t run_scales(const Held8& h, const GatedCall& q, int b, int tile,
                                                int t0, int len) {
-  const int lane = threadIdx.x % 32, t = t0 + lane / 2, block = 2 * tile + lane % 2;
-  const bool in = lane < 2 * kGS && t < len && block < held_blocks(q.D);
+  const int lane = threadIdx.x % 32, t = t0 + lane / V, block = V * tile + lane % V;
+  const bool in = lane < V * kGS && t < len && block < held_blocks(q.D);
   return in ? h.scales[(static_cast<size_t>(t) * q.B + b) * held_blocks(q.D) + block] : 1u;
 }
 __device__ __forceinline__ Fv<2> ring_get_held(const char* run, int k, float up) {
@@ -67,7 +82,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
   constexpr int V = path_v(PATH);
   using Rg = Ring<T, Z, KEEP, PATH>;
   constexpr bool IN = RING && Rg::IN;        // x, f and z come through the ring
-  constexpr bool AHEAD = !RING && !KEEP;     // everything comes to registers, a run ahead
+  constexpr bool AHEAD = !RING;              // everything comes to registers, a run ahead
+  constexpr bool SCALES = KEEP && (IN || !RING);  // scales come a run ahead, a lane one of them
   grid_dep_launch_dependents();
   const int warps = blockDim.x / 32, w = threadIdx.x / 32;
   const Exchange<V> ex{shared + (RING ? warps * Rg::kWarp : 0), warps};
@@ -139,16 +155,16 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
       start_next.load(q.states + (static_cast<size_t>(t0 / kGS) * q.B + b) * q.D + ch.d);
     else
       start_next.clear();
-    if constexpr (KEEP && IN) {
+    if constexpr (SCALES) {
       if (on) {
-        if constexpr (MODE != kSummary) sx_next = run_scales(q.x8, q, b, tile, t0, len);
-        sf_next = run_scales(q.f8, q, b, tile, t0, len);
-        if constexpr (Z) sz_next = run_scales(q.z8, q, b, tile, t0, len);
+        if constexpr (MODE != kSummary) sx_next = run_scales<V>(q.x8, q, b, tile, t0, len);
+        sf_next = run_scales<V>(q.f8, q, b, tile, t0, len);
+        if constexpr (Z) sz_next = run_scales<V>(q.z8, q, b, tile, t0, len);
       }
     }
   };
   // What does not come through the ring: without one the next run's loads are on their way to
-  // registers; what is kept and not aligned for a ring is loaded for the run at hand.
+  // registers; what is kept and aligned in pairs only is loaded for the run at hand.
   struct Inputs {
     Input<T, V, KEEP> x, f, z;
     RawV<T, V> dy[kGS];
@@ -213,7 +229,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     const char* const stage = mine + n % Rg::kStages * Rg::kStage;
     Fv<V> h = start_next.get();
     float ux = 0.f, uf = 0.f, uz = 0.f;  // the scales' values
-    if constexpr (KEEP && IN) ux = held_up(sx_next), uf = held_up(sf_next), uz = held_up(sz_next);
+    if constexpr (SCALES) ux = held_up(sx_next), uf = held_up(sf_next), uz = held_up(sz_next);
     if constexpr (AHEAD) {
       in = in_next;
       load(in_next, t0 - round);
@@ -246,6 +262,10 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
           if constexpr (MODE != kSummary) xv = ring_get<T>(runs, k);
           fv = ring_get<T>(runs + Rg::kInput, k);
           if constexpr (Z) zv = ring_get<T>(runs + 2 * Rg::kInput, k);
+        } else if constexpr (KEEP && !RING) {
+          if constexpr (MODE != kSummary) xv = in.x.get(k, ux);
+          fv = in.f.get(k, uf);
+          if constexpr (Z) zv = in.z.get(k, uz);
         } else {
           if constexpr (MODE != kSummary) xv = in.x.raw[k].get();
           fv = in.f.raw[k].get();

@@ -84,6 +84,29 @@ __device__ __forceinline__ void keep_run(const char* run, const Held8& h, size_t
   }
 }
 
+// A run of one channel a lane, kGS steps x the 32 of a block, to 8 bits: lane k finds the scale of step k.
+// `code`, `scale`: where the first step's go.
+template <typename T>
+__device__ __forceinline__ void keep_singles(const RawV<T, 1> (&v)[kGS], const Held8& h, size_t code,
+                                             size_t scale, size_t code_t, size_t scale_t, int on, bool in) {
+  const int lane = threadIdx.x % 32;
+  uint32_t most = 0u;
+#pragma unroll
+  for (int k = 0; k < kGS; ++k) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, magnitude_bits(v[k].get()[0]));
+    if (lane == k) most = m;
+  }
+  const uint32_t byte = held_scale_byte(most);
+  if (lane < kGS && lane < on) h.scales[scale + lane * scale_t] = static_cast<uint8_t>(byte);
+  const float down = held_down(byte);
+  uint8_t* to = h.codes + code;
+#pragma unroll
+  for (int k = 0; k < kGS; ++k, to += code_t) {
+    const float s = __shfl_sync(0xffffffffu, down, k);
+    if (in && k < on) *to = static_cast<uint8_t>(held_codes2(v[k].get()[0] * s, 0.f));
+  }
+}
+
 // kRounds: grid (tiles, B), CTAs of any number of warps.  kSummary and kSegments: grid (tiles x CTAs of
 // segments, B), kGatedWarps warps.
 template <typename T, bool Z, bool KEEP, GatedPath PATH, GatedMode MODE>
@@ -218,6 +241,15 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
       x = x_next, f = f_next;
       if (Z) z = z_next;
       load(t0 + round);
+      if constexpr (KEEP) {
+        const int on = stop - t0;
+        if (on > 0) {
+          const HeldAt at = held_at<V>(q, t0, b, ch.d);
+          keep_singles<T>(x.v, q.x8, at.code, at.scale, code_t, scale_t, on, ch.in);
+          keep_singles<T>(f.v, q.f8, at.code, at.scale, code_t, scale_t, on, ch.in);
+          if constexpr (Z) keep_singles<T>(z.v, q.z8, at.code, at.scale, code_t, scale_t, on, ch.in);
+        }
+      }
     }
     auto gate = [&](int k) {
       if constexpr (RING) return ring_get<T>(stage + 2 * Rg::Run::kBytes, k);
@@ -236,14 +268,6 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
           if constexpr (RING) return ring_get<T>(stage + Rg::Run::kBytes, k);
           else return f.v[k].get();
         }();
-        if constexpr (KEEP && !RING) {
-          if (t0 + k < len) {
-            const HeldAt at = held_at<V>(q, t0 + k, b, ch.d);
-            store_held_v<V>(q.x8, at, xv, ch.in);
-            store_held_v<V>(q.f8, at, fv, ch.in);
-            if constexpr (Z) store_held_v<V>(q.z8, at, gate(k), ch.in);
-          }
-        }
         Fv<V> i;
         gates<V>(fv, bias2, a[k], i);
         c[k] = i * xv;
