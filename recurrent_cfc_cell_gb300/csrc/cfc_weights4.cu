@@ -374,7 +374,8 @@ cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
   // and 18.2 us); where they are not, all eight (1 x 8192 x 4096 8.6 us, four 10.2 us).
   while (sp.rows == 0 && sp.deep > 2 && sh.tn > 152 * 32 / sp.deep) sp.deep /= 2;
   if (sh.tk < sp.deep) sp.deep = sh.tk;
-  const int bytes = 256 * sp.m * kTerms;  // of x for a tile along K; at most 8 KB
+  const int bytes = 256 * sp.m * kTerms;  // of x for a tile along K; at most 8 KB,
+                                              // so a chunk has eight tiles, and deep is at most 8
   sp.chunk = 64 * 1024 / bytes / sp.deep * sp.deep;
   if (sp.chunk > sh.tk) sp.chunk = sh.tk;
   LaunchCfg c;
