@@ -8,11 +8,12 @@ linear recurrence, and the product back into the stream; then the last norm and 
     H = cell(norm(s' + o'))                       [K, B, C]   behind the last layer
 
 ``GatedTrunk`` trains it.  With ``keep8`` a layer keeps the stream and x, f and z in 8 bits for its
-backward pass, 3 E + D bytes a step and sequence beside the recurrence's states, and what the
-products' weight gradients need (n and the recurrence's y) is formed again by the backward passes,
-so that those buffers are the same ones for all layers.  ``GatedServe`` runs prompts and then single
-tokens with carried states on 4-bit weights, a token as one CUDA graph, up to the last norm.  The
-training products are torch's; everything else is this library's kernels.  All float32, as the cell.
+backward pass, 3 E + D bytes a step and sequence (and a scale's byte for every 32) beside the
+recurrence's states, and what the products' weight gradients need (n and the recurrence's y) is
+formed again by the backward passes, so that those buffers are the same ones for all layers.
+``GatedServe`` runs prompts and then single tokens with carried states on 4-bit weights, a token as
+one CUDA graph, up to the last norm.  The training products are torch's; everything else is this
+library's kernels.  All float32, as the cell.
 """
 from __future__ import annotations
 
@@ -49,37 +50,31 @@ class GatedTrunk:
         self.D, self.E = params["layers"][0]["W_out"].shape
         rows, D, E = K * B, self.D, self.E
         layers = len(params["layers"])
-        self.norms = [RMSNormStep(rows, D, keep8=keep8) for _ in range(layers)]
-        self.mixers = [GatedStep(K, B, E, train=True, keep8=keep8) for _ in range(layers)]
         self.last = RMSNormStep(rows, D)
         self.cell = KLoopStep(B, K, params["cell_b"].shape[1], D)
-        dev = self.last.device
-        self.xfz = [torch.empty(K, B, 3 * E, device=dev) for _ in range(1 if keep8 else layers)]
-        self.o = torch.empty(rows, D, device=dev)
-        # Gradients on their way back, the same buffers for all layers.
-        self.dy = torch.empty(K, B, E, device=dev)
-        self.dn = torch.empty(rows, D, device=dev)
-        self.dxfz = torch.empty(K, B, 3 * E, device=dev)
-        first = self.mixers[0]
-        for m in self.mixers:
-            m.dx, m.df = self.dxfz[..., :E], self.dxfz[..., E:2 * E]
-            m.dz = self.dxfz[..., 2 * E:]
-            if keep8:  # y is formed again, and wanted no longer than its product
-                m.y = first.y
-                first.y_again = first.y_again if first.y_again is not None else torch.empty_like(first.y)
-                m.y_again = first.y_again
-        if keep8:
-            self.stream = torch.empty(rows, D, device=dev)
-            for n in self.norms:
-                n.y = self.norms[0].y
+
+        def new(*shape):
+            return torch.empty(*shape, device=self.last.device)
+
+        self.xfz = [new(K, B, 3 * E) for _ in range(1 if keep8 else layers)]
+        self.o = new(rows, D)
+        # Gradients on their way back, the same buffers for all layers; a norm's dx takes the place of
+        # the stream's gradient that it is added to.
+        self.dy, self.dn, self.dxfz = new(K, B, E), new(rows, D), new(K, B, 3 * E)
+        norm, mix = dict(dx=new(rows, D)), {
+            k: self.dxfz[..., n * E:(n + 1) * E] for n, k in enumerate(("dx", "df", "dz"))}
+        if keep8:  # y is formed again, and wanted no longer than its product; the sum is in place
+            self.stream = new(rows, D)
+            norm.update(y=new(rows, D), y_again=new(rows, D), s=self.stream)
+            mix.update(y=new(K, B, E), y_again=new(K, B, E))
+        self.norms = [RMSNormStep(rows, D, keep8=keep8, into=norm) for _ in range(layers)]
+        self.mixers = [GatedStep(K, B, E, train=True, keep8=keep8, into=mix) for _ in range(layers)]
 
     def forward(self, s, h0, ts, lengths=None) -> torch.Tensor:
         """H [K, B, C] from the stream s [K, B, D], the cell's h0 [B, C] and time scales ts [K, B]."""
         P, K, B, E, rows = self.params, self.K, self.B, self.E, self.K * self.B
         stream, o = s.reshape(rows, self.D), None
         for i, (p, norm, mix) in enumerate(zip(P["layers"], self.norms, self.mixers)):
-            if self.keep8 and o is not None:
-                norm.s = self.stream  # the sum in place, but for the caller's s
             norm.bind(stream, p["w"], o).forward()
             stream = stream if o is None else norm.s
             xfz = self.xfz[0 if self.keep8 else i]

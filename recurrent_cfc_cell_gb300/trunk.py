@@ -33,12 +33,16 @@ def _expect(t, name: str, shape, dtype):
 class _Step:
     """Prepared calls, run in order."""
 
-    def __init__(self, device):
-        self.device = _device(device)
+    def __init__(self, device, into: dict | None = None):
+        self.device, self.into = _device(device), into or {}
         self._unbind()
 
     def _act(self, *shape):
         return torch.empty(shape, dtype=self.dtype, device=self.device)
+
+    def _out(self, name: str, *shape):
+        """The output `name`: the tensor that the step was given for it, or one of its own."""
+        return self.into[name] if name in self.into else self._act(*shape)
 
     def _f32(self, *shape):
         return torch.empty(shape, dtype=torch.float32, device=self.device)
@@ -325,14 +329,16 @@ class RMSNormStep(_Step):
     """s = x + residual (without one s is x) and its root-mean-square norm y over `rows` rows of n
     columns; with dy (and the stream's gradient ds) bound also dx (of x and of the residual) and dw.
     With ``out8`` y is held in 8 bits (``y8``, a Held8).  With ``keep8`` the stream is kept in 8 bits
-    (``s8``) and the backward pass reads that in its place and forms y again (``y_again``)."""
+    (``s8``) and the backward pass reads that in its place and forms y again (``y_again``).  ``into``
+    gives tensors for y, s, dx and y_again, by these names, which steps that take turns may share; dx
+    may be ds."""
 
     def __init__(self, rows: int, n: int, dtype=torch.float32, eps: float = 1e-5,
-                 out8: bool = False, keep8: bool = False, device=None):
-        super().__init__(device)
+                 out8: bool = False, keep8: bool = False, device=None, into: dict | None = None):
+        super().__init__(device, into)
         self.rows, self.n, self.dtype, self.eps = rows, n, dtype, eps
         self.out8, self.keep8 = out8, keep8
-        self.y = None if out8 else self._act(rows, n)
+        self.y = None if out8 else self._out("y", rows, n)
         self.y8 = _lib.Held8((rows, n), self.device) if out8 else None
         self.s8 = _lib.Held8((rows, n), self.device) if keep8 else None
         self.rstd = self._f32(rows)
@@ -340,15 +346,15 @@ class RMSNormStep(_Step):
 
     def _alloc_grads(self):
         if self.dx is None:
-            self.dx, self.dw = self._act(self.rows, self.n), self._f32(self.n)
-            self.y_again = self._act(self.rows, self.n) if self.keep8 else None
+            self.dx, self.dw = self._out("dx", self.rows, self.n), self._f32(self.n)
+            self.y_again = self._out("y_again", self.rows, self.n) if self.keep8 else None
             self.ws = _workspace(_lib.rmsnorm_workspace_bytes(self.rows, self.n), self.device)
 
     def bind(self, x, w, residual=None, dy=None, ds=None) -> "RMSNormStep":
         self._unbind()
         _expect(x, "x", (self.rows, self.n), self.dtype)
         if residual is not None and self.s is None:
-            self.s = self._act(self.rows, self.n)
+            self.s = self._out("s", self.rows, self.n)
         s = None if residual is None else self.s
         forward = (_lib.cfc_rmsnorm_forward.prepare(
             x, w, residual, s, self.y, self.s8, self.y8, self.rstd, self.eps),)
@@ -377,23 +383,25 @@ class GatedStep(_Step):
     """Gated linear recurrence over [K, B, D]: y and the last state h.  With ``train`` it keeps the
     states that the backward pass starts from, and a bound dy (and dh_last) gives every gradient.
     With ``keep8`` it keeps x, f and z in 8 bits (``kept``), and the backward pass reads those in
-    their place, so that the inputs may be gone by then, and forms y again (``y_again``)."""
+    their place, so that the inputs may be gone by then, and forms y again (``y_again``).  ``into``
+    gives tensors for y, dx, df, dz and y_again, by these names, which steps that take turns may
+    share."""
 
     def __init__(self, K: int, B: int, D: int, dtype=torch.float32, train: bool = False,
-                 keep8: bool = False, device=None):
-        super().__init__(device)
+                 keep8: bool = False, device=None, into: dict | None = None):
+        super().__init__(device, into)
         if keep8 and not train:
             raise ValueError("a GatedStep made without train keeps nothing")
         self.K, self.B, self.D, self.dtype = K, B, D, dtype
         self.train, self.keep8 = train, keep8
-        self.y, self.h = self._act(K, B, D), self._f32(B, D)
+        self.y, self.h = self._out("y", K, B, D), self._f32(B, D)
         self.states = self.kept = self.y_again = None
         # One workspace for both passes, which follow one another.
         self.ws = _workspace(max(_lib.gated_workspace_bytes(K, B, D, back)
                                 for back in (False, train)), self.device)
         if train:
             self.states = self._f32(-(-K // _lib.GATED_PERIOD), B, D)
-            self.dx, self.df = self._act(K, B, D), self._act(K, B, D)
+            self.dx, self.df = self._out("dx", K, B, D), self._out("df", K, B, D)
             self.dz = None
             self.dbias, self.dh0 = self._f32(D), self._f32(B, D)
 
@@ -419,9 +427,9 @@ class GatedStep(_Step):
             if not self.train:
                 raise ValueError("a GatedStep made without train keeps no states to go back from")
             if z is not None and self.dz is None:
-                self.dz = self._act(self.K, self.B, self.D)
+                self.dz = self._out("dz", self.K, self.B, self.D)
             if self.keep8 and self.y_again is None:
-                self.y_again = self._act(self.K, self.B, self.D)
+                self.y_again = self._out("y_again", self.K, self.B, self.D)
             read = (None, None) if kept else (x, f)
             backward = (_lib.cfc_gated_backward.prepare(
                 dy, *read, self.states, self.dx, self.df, bias, None if kept else z, lengths, dh_last,
