@@ -49,6 +49,7 @@ CFC_F32, CFC_BF16 = 0, 1          # activation types of the trunk operators
 SCAN_PERIOD = 8                   # steps between the states a training scan keeps
 GATED_PERIOD = 8                  # and a training gated recurrence
 HELD8_BLOCK = 32                  # columns that share a scale in 8 bits
+MATVEC4_ROWS = 1 << 19            # most rows of one call of cfc_matvec4
 CFC_ERR_SCRATCH_LIMIT = -10
 NOALLOC_SCRATCH_BYTES = 32 << 20  # size of cfc_backward_noalloc's built-in device scratch
 

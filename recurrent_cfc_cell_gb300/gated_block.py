@@ -123,8 +123,9 @@ class GatedTrunk:
 
 
 class GatedServe:
-    """The trunk up to the last norm for serving, its products on 4-bit weights: a prompt of any
-    length, then single tokens, with the recurrences' states carried in place."""
+    """The trunk up to the last norm for serving, its products on 4-bit weights: a prompt (of at most
+    2^24 steps, the recurrence's limit, and 2^31 - 1 rows), then single tokens, with the recurrences'
+    states carried in place."""
 
     def __init__(self, B: int, params: dict, group: int = 128):
         self.B, self.params = B, params

@@ -499,7 +499,8 @@ class Weights4:
 
 
 class MatvecStep(_Step):
-    """y [M, N] = x W^T for M rows and a matrix of 4-bit weights."""
+    """y [M, N] = x W^T for M rows and a matrix of 4-bit weights; more rows than a call of the product
+    takes go in several."""
 
     def __init__(self, M: int, weights: Weights4, dtype=torch.float32, device=None):
         super().__init__(device)
@@ -510,7 +511,10 @@ class MatvecStep(_Step):
         self._unbind()
         w = self.weights
         _expect(x, "x", (self.M, w.K), self.dtype)
-        self._forward = (_lib.cfc_matvec4.prepare(x, w.data, w.N, w.group, self.y),)
+        most = _lib.MATVEC4_ROWS
+        self._forward = tuple(_lib.cfc_matvec4.prepare(x[m:m + most], w.data, w.N, w.group,
+                                                       self.y[m:m + most])
+                              for m in range(0, max(self.M, 1), most))
         self.inputs = dict(x=x)
         return self
 
