@@ -418,11 +418,10 @@ inline GatedShape gated_shape(int B, int K, int tiles, int slots) {
   return s;
 }
 constexpr int kFwdSlots = 3 * 152, kBwdSlots = 2 * 152;
-template <typename F>
-cudaError_t gated_smem(F* kern, size_t smem) {
-  return smem > 16 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem))
-                          : cudaSuccess;
+// Dynamic shared memory of a CTA: `ring` bytes a warp (0: without one) and the exchange.
+template <int V>
+size_t gated_smem(int warps, size_t ring) {
+  return Exchange<V>::bytes(warps) + warps * ring;
 }
 
 }  // namespace cfc

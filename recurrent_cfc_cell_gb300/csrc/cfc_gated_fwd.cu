@@ -415,9 +415,9 @@ cudaError_t fwd_mode(const GatedCall& q, const GatedShape& sh, int tiles, cudaSt
   c.block = dim3(32 * sh.warps);
   c.stream = s;
   c.pdl = MODE == kSegments;
-  c.smem = Exchange<path_v(PATH)>::bytes(sh.warps);
-  if (PATH != kSingles) c.smem += static_cast<size_t>(sh.warps) * Ring<T, Z, PATH>::kWarp;
-  const cudaError_t e = gated_smem(kern, c.smem);
+  constexpr size_t ring = PATH == kSingles ? 0 : Ring<T, Z, PATH>::kWarp;
+  c.smem = gated_smem<path_v(PATH)>(sh.warps, ring);
+  const cudaError_t e = allow_smem(kern, gated_smem<path_v(PATH)>(kGatedWarps, ring));
   return e == cudaSuccess ? launch(c, kern, q, sh) : e;
 }
 template <typename T, bool Z, bool KEEP, GatedPath PATH>

@@ -49,4 +49,15 @@ cudaError_t launch(const LaunchCfg& c, void (*kern)(KArgs...), Args&&... args) {
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Lets a kernel be launched with up to `most` bytes of dynamic shared memory.  The limit is the
+// kernel's, not the call's: `most` is what its largest launch takes, whatever this one needs, so that a
+// call in another thread never finds it lowered.  48 KB, with up to 8 KB that the kernel declares, need no
+// leave.
+template <typename F>
+cudaError_t allow_smem(F* kern, size_t most) {
+  return most > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(most))
+                          : cudaSuccess;
+}
+
 }  // namespace cfc

@@ -1062,11 +1062,9 @@ cudaError_t launch_rows(void (*kern)(const NormArgs), LaunchCfg c, const NormArg
   if constexpr (RING) {
     using Rg = Ring<T, TM, LY, NT>;
     c.smem = 16 * static_cast<size_t>(c.block.x) * (Rg::kDepth * Rg::kRow + params * Rg::kParam);
-    if (c.smem > 40 * 1024) {  // 48 KB, with what the kernel declares, need no leave
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(c.smem));
-      if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(kern, 16 * static_cast<size_t>(TM::kMaxThreads) *
+                                               (Rg::kDepth * Rg::kRow + params * Rg::kParam));
+    if (e != cudaSuccess) return e;
   }
   return launch(c, kern, a);
 }

@@ -33,6 +33,9 @@ constexpr int kTileN = 16, kTileK = 128, kTileBytes = kTileN * kTileK / 2;
 // one row of bf16: 12.5 us; four tiles and three CTAs 13.9, four and four 15.5, which spills).
 constexpr int kAhead = 2;
 
+// Shared memory for a chunk of x.  The warps' sums, at most 512 threads x 4 of 16 bytes, fit it too.
+constexpr int kChunkBytes = 64 * 1024;
+
 struct Shape4 {
   int tn, tk, groups;   // tiles along N and K, groups of a row (padded to whole tiles)
   size_t codes_bytes;
@@ -376,7 +379,7 @@ cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
   if (sh.tk < sp.deep) sp.deep = sh.tk;
   const int bytes = 256 * sp.m * kTerms;  // of x for a tile along K; at most 8 KB,
                                               // so a chunk has eight tiles, and deep is at most 8
-  sp.chunk = 64 * 1024 / bytes / sp.deep * sp.deep;
+  sp.chunk = kChunkBytes / bytes / sp.deep * sp.deep;
   if (sp.chunk > sh.tk) sp.chunk = sh.tk;
   LaunchCfg c;
   c.grid = dim3((sh.tn - 1 >> sp.rows) + 1, (q.M - 1) / sp.m + 1);
@@ -385,12 +388,8 @@ cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
   c.smem = sums > xs ? sums : xs;
   c.stream = s;
   auto run = [&](auto* kern) {
-    if (c.smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(c.smem));
-      if (e != cudaSuccess) return e;
-    }
-    return launch(c, kern, q, sp);
+    const cudaError_t e = allow_smem(kern, kChunkBytes);
+    return e == cudaSuccess ? launch(c, kern, q, sp) : e;
   };
   if (nt == 1) return run(matvec4_kernel<T, GROUP, 1>);
   if (nt == 2) return run(matvec4_kernel<T, GROUP, 2>);
