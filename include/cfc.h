@@ -639,7 +639,8 @@ int cfc_unpack8(const cfc_held8* held, int rows, int n, int dtype, void* y, long
 /*
  * Root-mean-square norm: s = x + residual, rounded to dtype (residual NULL: s = x);
  * rstd = (sum s^2 / n + eps)^-1/2;  y = s rstd w.  The norm reads s as rounded.  (A row of zeros with
- * eps = 0 gives NaN; squares beyond fp32, from magnitudes of 1.8e19, make rstd 0.)
+ * eps = 0 gives NaN; a sum of squares beyond fp32, from magnitudes of 1.8e19 / n^1/2, makes rstd 0, and y with
+ * it but for infinities, which become NaN.)
  */
 typedef struct cfc_rmsnorm_args {
   int rows, n;             /* n <= 2^24                                                          */

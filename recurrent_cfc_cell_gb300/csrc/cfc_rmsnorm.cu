@@ -286,11 +286,12 @@ __device__ __forceinline__ float rstd_of(float sum, int n, float eps) {
   return r > 0.f && r < 1e18f && m < 1e38f ? better : r;
 }
 
-// s w rstd rounded once: the product s w is kept in two parts.
+// s rstd w rounded once: the product s rstd, n^1/2 at most, is kept in two parts.  (s w could be beyond
+// fp32 where y is not.)
 __device__ __forceinline__ float normed(float s, float w, float rstd) {
-  const float p = s * w;
-  const float low = fmaf(s, w, -p);
-  return fmaf(p, rstd, low * rstd);
+  const float p = s * rstd;
+  const float low = fmaf(s, rstd, -p);
+  return fmaf(p, w, low * w);
 }
 
 // ---- y to 8 bits ----
@@ -346,12 +347,12 @@ __device__ __forceinline__ Two rstd_two(Two sum, float nf, float over_n, float e
   const float low = r * e * fmaf(0.375f, e, -0.5f);
   return r > 0.f && r < 1e18f && m.hi < 1e38f ? fast_two(r, low) : Two{r, 0.f};
 }
-// s w rstd in two parts.
+// s rstd w in two parts.
 __device__ __forceinline__ Pair normed_two(float2 s, float2 w, Two rstd) {
   const float2 hi = make_float2(rstd.hi, rstd.hi), lo = make_float2(rstd.lo, rstd.lo);
-  const float2 p = __fmul2_rn(s, w), p_low = fma2(s, w, neg2(p));
-  const float2 y = __fmul2_rn(p, hi);
-  const float2 low = __fadd2_rn(fma2(p, hi, neg2(y)), fma2(p, lo, __fmul2_rn(p_low, hi)));
+  const float2 p = __fmul2_rn(s, hi), p_low = fma2(s, lo, fma2(s, hi, neg2(p)));
+  const float2 y = __fmul2_rn(p, w);
+  const float2 low = fma2(p_low, w, fma2(p, w, neg2(y)));
   const float2 sum = __fadd2_rn(y, low);
   return {sum, __fadd2_rn(low, neg2(__fadd2_rn(sum, neg2(y))))};
 }

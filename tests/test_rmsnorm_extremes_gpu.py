@@ -15,6 +15,70 @@ DTYPES = ["f32", "bf16"]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [8, 40, 37, 256, 1000, 1537, 5000, 8193])
+def test_rows_that_are_not_numbers(n, dtype):
+    """A NaN makes its row NaN; an infinity and squares beyond fp32 make rstd 0, so that y is 0 but for the
+    infinity, which is NaN; other rows are as they were, also to 8 bits."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import trunk
+
+    x = torch.randn(12, n, device="cuda").to(act(dtype))
+    w = torch.rand(n, device="cuda") + 0.5
+    w[n // 2] = 1e30  # s w is beyond fp32 where s is 1e19
+    clean = x.clone()
+    x[2, n - 1] = float("nan")
+    x[5, n // 3] = float("inf")
+    x[7, 0] = -float("inf")
+    x[9] = 3e19
+    x[9, n // 2] = -2e38
+    ok = [r for r in range(12) if r not in (2, 5, 7, 9)]
+    for out8 in (False, True):
+        a = trunk.RMSNormStep(12, n, act(dtype), out8=out8).bind(x, w)
+        b = trunk.RMSNormStep(12, n, act(dtype), out8=out8).bind(clean, w)
+        ys = []
+        for st in (a, b):
+            st.run()
+            ys.append(trunk.Unpack8Step(12, n).bind(st.y8).run().clone() if out8 else st.y)
+        y = ys[0]
+        assert torch.equal(y[ok], ys[1][ok])
+        assert torch.isnan(y[2]).all() and torch.isnan(a.rstd[2])
+        assert not a.rstd[[5, 7, 9]].any()
+        for r, c in ((5, n // 3), (7, 0)):
+            bad = torch.isnan(y[r])
+            block = torch.zeros(n, dtype=torch.bool, device="cuda")
+            if out8:  # its whole block
+                block[c // 32 * 32:c // 32 * 32 + 32] = True
+            else:
+                block[c] = True
+            assert torch.equal(bad, block) and not y[r][~bad].any()
+        assert not y[9].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [64, 1537])
+def test_products_beyond_fp32_on_the_way(n, dtype):
+    """s w alone is beyond fp32, or below it, and y is neither."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import trunk
+
+    big, small = torch.randn(6, n, device="cuda") * 1e17, torch.randn(6, n, device="cuda") * 1e-17
+    for x, w in ((big, 1e25), (small, 1e-25)):
+        x, w = x.to(act(dtype)), torch.full((n,), w, device="cuda")
+        dy = torch.randn(6, n, device="cuda").to(act(dtype))
+        st = trunk.RMSNormStep(6, n, act(dtype), eps=0.0).bind(x, w, dy=dy)
+        st.run()
+        v = x.double()
+        want = (v / torch.sqrt((v * v).mean(1, keepdim=True)) * w.double()).cpu().numpy()
+        check(st.y, want, EL, "y")
+        st8 = trunk.RMSNormStep(6, n, act(dtype), eps=0.0, out8=True).bind(x, w)
+        st8.run()
+        got = trunk.Unpack8Step(6, n).bind(st8.y8).run().double().cpu().numpy()
+        assert np.array_equal(got, og.held8(want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_long_rows_in_many_turns(dtype):
     """More rows of more than 8192 columns than the GPU holds CTAs for, the sum in the residual's place."""
     import torch
