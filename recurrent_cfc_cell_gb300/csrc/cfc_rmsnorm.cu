@@ -289,7 +289,7 @@ __device__ __forceinline__ float rstd_of(float sum, int n, float eps) {
 // s rstd w rounded once: the product s rstd, n^1/2 at most, is kept in two parts.  (s w could be beyond
 // fp32 where y is not.)
 __device__ __forceinline__ float normed(float s, float w, float rstd) {
-  const float p = s * rstd;
+  const float p = __fmul_rn(s, rstd);
   const float low = fmaf(s, rstd, -p);
   return fmaf(p, w, low * w);
 }
@@ -336,13 +336,15 @@ __device__ __forceinline__ Pair plus_square(Pair v, float2 a) {
 __device__ __forceinline__ Two both(Pair v) {
   return plus(Two{v.hi.x, v.lo.x}, Two{v.hi.y, v.lo.y});
 }
-// (sum / n + eps)^-1/2 in two parts.  r = m^-1/2 (1 - e / 2 + ...) with e = m r^2 - 1.
+// (sum / n + eps)^-1/2 in two parts.  r = m^-1/2 (1 - e / 2 + ...) with e = m r^2 - 1.  Products whose
+// rests are formed are rounded by their own (__fmul_rn): with one of them inside a multiply-add its rest
+// would count twice.
 __device__ __forceinline__ Two rstd_two(Two sum, float nf, float over_n, float eps) {
-  const float q = sum.hi * over_n;  // within a place of the quotient, so that its rest is exact
+  const float q = __fmul_rn(sum.hi, over_n);  // within a place of the quotient: its rest is exact
   const Two m = plus(Two{q, (fmaf(-q, nf, sum.hi) + sum.lo) * over_n}, Two{eps, 0.f});
   const float r = rsqrtf(m.hi);
-  const float rr = r * r, rr_low = fmaf(r, r, -rr);
-  const float p = m.hi * rr;  // near 1
+  const float rr = __fmul_rn(r, r), rr_low = fmaf(r, r, -rr);
+  const float p = __fmul_rn(m.hi, rr);  // near 1
   const float e = (p - 1.f) + (fmaf(m.hi, rr, -p) + (m.hi * rr_low + m.lo * rr));
   const float low = r * e * fmaf(0.375f, e, -0.5f);
   return r > 0.f && r < 1e18f && m.hi < 1e38f ? fast_two(r, low) : Two{r, 0.f};

@@ -79,6 +79,36 @@ def test_products_beyond_fp32_on_the_way(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [96, 1024, 2501, 8192, 9000])
+def test_codes_as_near_to_borders_as_weights_bring_them(n, dtype):
+    """Weights that bring every y of a row to within half a place of a border between two codes: an error
+    of 3e-8 anywhere in rstd or in the products takes the wrong code for about half of them.  What is
+    within 2^-39 of a border, relative to y, is not looked at: the sums of squares keep 48 bits of each
+    term, up to 2^4 roundings of 2^-48 a thread, whose parts may be 2^4 times as large."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import trunk
+
+    for seed in range(6):
+        r = np.random.default_rng(100 * n + seed)
+        s = rounded(r.normal(size=(1, n)), dtype)
+        s = np.where(np.abs(s) < 0.05, 0.5, s)
+        rstd = 1.0 / np.sqrt((s * s).mean() + float(np.float32(1e-5)))
+        ties = (og.E4M3[9:] + og.E4M3[8:-1]) / 2
+        u = r.choice(ties[ties < 440], size=n)
+        u[::32] = 448.0 * (1 - 2.0 ** -20)  # holds the block's scale at 1, off a border
+        w = (u / (s[0] * rstd)).astype(np.float32)
+        y = s[0] * rstd * w.astype(np.float64)
+        st = trunk.RMSNormStep(1, n, act(dtype), out8=True).bind(cuda(s, dtype), torch.from_numpy(w).cuda())
+        st.run()
+        got = trunk.Unpack8Step(1, n).bind(st.y8).run().double().cpu().numpy()[0]
+        want = og.held8(y[None])[0]
+        sure = np.abs(y / u - 1) > 2.0 ** -39
+        assert np.all((got == want) | ~sure)
+        assert sure.mean() > 0.99 and np.all(np.abs(y / u - 1) <= 2.0 ** -24 * 1.000001)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_long_rows_in_many_turns(dtype):
     """More rows of more than 8192 columns than the GPU holds CTAs for, the sum in the residual's place."""
     import torch
