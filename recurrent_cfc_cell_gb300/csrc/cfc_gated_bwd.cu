@@ -317,7 +317,9 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
 #pragma unroll
       for (int k = kGS - 1; k >= 0; --k, to_x -= q.dx_t, to_f -= q.df_t) {
         g = g + dh[k];
-        const Fv<V> dx = g * i[k], df = g * u[k];
+        Fv<V> dx = g * i[k], df = g * u[k];
+        // Behind the end g may be an infinity or a NaN that dh_last brought.
+        if (!decltype(whole)::value && t0 + k >= len) dx = df = Fv<V>(0.f);
         dsum = dsum + df;
         g = g * a[k];
         if ((decltype(whole)::value || t0 + k < K) && ch.in) {

@@ -1,0 +1,36 @@
+"""Variants of the gated block's operators that only some sizes reach, and values that are not numbers
+in the recurrence's gradients and among 4-bit weights.
+
+Tolerances are those of the operators' tests (1e-5 max|y| per element, 1e-4 max|y| for sums over steps, a
+product's K terms each off by 2^-24 of the sum of magnitudes)."""
+import numpy as np
+import pytest
+
+import oracle.gated as og
+from gated_cases import gated_inputs, weights4_inputs
+from test_gated_gpu import SUM, act, built, check, cuda, gated_check, gated_step  # noqa: F401 (built: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("K,D", [(45, 64), (45, 33), (45, 50), (900, 64), (900, 33)])
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_gradients_behind_a_length_are_0_whatever_comes_back(bad, keep8, K, D):
+    """An infinite gradient of the last state reaches a sequence's steps, and none behind them."""
+    i = gated_inputs(K, 3, D, "f32", K + D, [K - 2, 13, 0])
+    i["dh_last"][1, D // 2] = bad
+    st = gated_step(i, K, 3, D, "f32", keep8=keep8, dh_last=True)
+    for b, e in enumerate(i["ends"]):
+        for v in (st.y, st.dx, st.df, st.dz):
+            assert not v[e:, b].any()
+    i["dh_last"][1, D // 2] = 0
+    fine = gated_step(i, K, 3, D, "f32", keep8=keep8, dh_last=True)
+    import torch
+
+    for name in ("dx", "df", "dz"):
+        a, b = getattr(st, name).clone(), getattr(fine, name).clone()
+        if name != "dz":
+            assert not torch.isfinite(a[12, 1, D // 2])
+            a[:, 1, D // 2] = b[:, 1, D // 2] = 0
+        assert torch.equal(a, b)
