@@ -748,7 +748,8 @@ int cfc_gated_step(const cfc_gated_args* a, void* y, long long y_b, float* new_s
  * shorter).  1 <= N, K <= 2^24, N K <= 2^36, M <= 2^19.
  *
  * cfc_weights4_quantize -- codes, scales <- W [N][K] (rows ldw; fp32 or bf16): a group's scale is its
- * largest magnitude / 7, rounded to bf16, and its codes the nearest ones.
+ * largest magnitude / 7, rounded to bf16, and its codes the nearest ones.  A group with an infinity or a NaN
+ * is NaN throughout.
  * cfc_weights4_bytes -- size of the laid-out weights.
  * cfc_weights4_lay_out -- weights (16-byte aligned) <- codes and scales in the order in which
  * cfc_matvec4 reads them; done once for a matrix.

@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(256) quantize4_kernel(const Weights4Call q, in
   for (int k = k0 + lane; k < min(q.K, k0 + q.group); k += 32)
     most = max(most, __float_as_uint(to_f32(row[k])) & 0x7fffffffu);
   most = __reduce_max_sync(0xffffffffu, most);
-  // The largest magnitude becomes 7 steps, up to the scale's rounding.
+  // The largest magnitude becomes 7 steps, up to the scale's rounding; of an infinity NaN, as of a NaN.
+  if (most == 0x7f800000u) most = 0x7fffffffu;
   const __nv_bfloat16 held = __float2bfloat16_rn(__uint_as_float(most) / 7.f);
   const float scale = __bfloat162float(held);
   if (lane == 0) q.scales_out[at] = __bfloat16_as_ushort(held);

@@ -34,3 +34,26 @@ def test_gradients_behind_a_length_are_0_whatever_comes_back(bad, keep8, K, D):
             assert not torch.isfinite(a[12, 1, D // 2])
             a[:, 1, D // 2] = b[:, 1, D // 2] = 0
         assert torch.equal(a, b)
+
+
+def test_groups_with_an_infinity_are_not_numbers():
+    """As a block in 8 bits: a group of weights with an infinity or a NaN is NaN throughout, and others are
+    as they were."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import trunk
+
+    W = torch.randn(5, 130, device="cuda")
+    clean = trunk.Weights4.quantized(W, 64)
+    W[1, 70], W[2, 3], W[3, 129] = float("inf"), -float("inf"), float("nan")
+    codes, scales = trunk.Weights4.quantized(W, 64)
+    bad = torch.zeros(5, 3, dtype=torch.bool, device="cuda")
+    bad[1, 1] = bad[2, 0] = bad[3, 2] = True
+    assert torch.equal(torch.isnan(scales), bad)
+    assert torch.equal(scales[~bad], clean[1][~bad])
+    rows = [0, 4]
+    assert torch.equal(codes[rows], clean[0][rows])
+    x = torch.ones(1, 130, device="cuda")
+    st = trunk.MatvecStep(1, trunk.Weights4(codes, scales, 130, 64)).bind(x)
+    st.run()
+    assert torch.equal(torch.isnan(st.y[0]), torch.tensor([0, 1, 1, 1, 0], device="cuda").bool())
