@@ -73,6 +73,7 @@ class GatedTrunk:
     def forward(self, s, h0, ts, lengths=None) -> torch.Tensor:
         """H [K, B, C] from the stream s [K, B, D], the cell's h0 [B, C] and time scales ts [K, B]."""
         P, K, B, E, rows = self.params, self.K, self.B, self.E, self.K * self.B
+        _expect(s, "s", (K, B, self.D), torch.float32)  # as many elements in another order would do
         stream, o = s.reshape(rows, self.D), None
         for i, (p, norm, mix) in enumerate(zip(P["layers"], self.norms, self.mixers)):
             norm.bind(stream, p["w"], o).forward()
@@ -153,6 +154,7 @@ class GatedServe:
     def prompt(self, s, lengths=None) -> torch.Tensor:
         """The last norm's output [K, B, D] of a prompt s [K, B, D], continuing from the carried
         states."""
+        _expect(s, "s", (*s.shape[:1], self.B, self.D), torch.float32)
         K, B, E = s.shape[0], self.B, self.E
 
         def mixer(state):

@@ -50,3 +50,24 @@ def test_a_prompt_of_any_length():
         assert (whole - parts).abs().max() <= 1e-4 * parts.abs().max()
         a, b = one.states[0], two.states[0]
         assert (a - b).abs().max() <= 1e-4 * b.abs().max()
+
+
+def test_shapes_of_as_many_elements_are_refused():
+    import torch
+
+    from recurrent_cfc_cell_gb300.gated_block import GatedServe, GatedTrunk, make_gated_params
+
+    K, B, D, C = 6, 4, 32, 32
+    P = make_gated_params(1, D, 64, C)
+    z = lambda *n: torch.zeros(*n, device="cuda")  # noqa: E731
+    serve, trunk = GatedServe(B, P, group=32), GatedTrunk(K, B, P)
+    for shape in ((K, D, B), (K, B * D), (K * B, D), (K, 2 * B, D // 2)):
+        with pytest.raises(ValueError):
+            serve.prompt(z(*shape))
+        with pytest.raises(ValueError):
+            trunk.forward(z(*shape), z(B, C), z(K, B))
+    with pytest.raises(ValueError):
+        trunk.forward(z(B, K, D), z(B, C), z(K, B))
+    with pytest.raises(ValueError):
+        serve.prompt(z(K, B, D).bfloat16())
+    assert serve.prompt(z(K, B, D)).shape == (K, B, D)
