@@ -186,15 +186,17 @@ class GatedServe:
             calls, self.y = self._calls(self.s, [mixer(t) for t in self.states], B)
             before = [t.clone() for t in self.states]
             self.s.copy_(s)
-            for c in calls:  # eagerly once, before the capture
-                c.run()
-            torch.cuda.synchronize()
-            graph = torch.cuda.CUDAGraph()
-            with torch.cuda.graph(graph):
-                for c in calls:
+            try:
+                for c in calls:  # eagerly once, before the capture
                     c.run()
-            for t, b in zip(self.states, before):
-                t.copy_(b)
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    for c in calls:
+                        c.run()
+            finally:  # the states move on with the replay, and not where the capture fails
+                for t, b in zip(self.states, before):
+                    t.copy_(b)
             self._token = (graph, calls)
         self.s.copy_(s)
         self._token[0].replay()

@@ -71,3 +71,25 @@ def test_shapes_of_as_many_elements_are_refused():
     with pytest.raises(ValueError):
         serve.prompt(z(K, B, D).bfloat16())
     assert serve.prompt(z(K, B, D)).shape == (K, B, D)
+
+
+def test_a_token_whose_capture_fails_leaves_the_states(monkeypatch):
+    import torch
+
+    from recurrent_cfc_cell_gb300.gated_block import GatedServe, make_gated_params
+
+    P = make_gated_params(2, 32, 64, 32)
+    s = torch.randn(5, 3, 32, device="cuda")
+    serve, other = GatedServe(3, P, group=32), GatedServe(3, P, group=32)
+    serve.prompt(s[:4])
+    other.prompt(s[:4])
+
+    def fails(*a, **k):
+        raise RuntimeError("no capture")
+
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "graph", fails)
+        with pytest.raises(RuntimeError):
+            serve.token(s[4])
+    assert all(torch.equal(a, b) for a, b in zip(serve.states, other.states))
+    assert torch.equal(serve.token(s[4]), other.token(s[4]))
