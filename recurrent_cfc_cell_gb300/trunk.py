@@ -87,6 +87,17 @@ class _Step:
         self.graph.replay()
 
 
+class _Call:
+    """One prepared call.  A bind that is refused leaves the one before as it was."""
+
+    _call = None
+
+    def _enqueue(self, stream) -> None:
+        if self._call is None:
+            raise ValueError("no inputs are bound")
+        self._call(stream)
+
+
 class LayerNormStep(_Step):
     """Layer norm over `rows` rows of n columns: y; with dy bound also dx, dw, db."""
 
@@ -252,7 +263,7 @@ class ScanStep(_Step):
         return out
 
 
-class ConvToken:
+class ConvToken(_Call):
     """One token per sequence of the causal convolution: u [B, D] and the moved-on state."""
 
     def __init__(self, B: int, D: int, W: int, dtype=torch.float32, silu: bool = True, device=None):
@@ -267,11 +278,11 @@ class ConvToken:
         return self
 
     def run(self, stream=None):
-        self._call(stream)
+        self._enqueue(stream)
         return self.u, self.state
 
 
-class ScanToken:
+class ScanToken(_Call):
     """One token per sequence of the selective scan: y [B, D] and the new state [B, D, N]."""
 
     def __init__(self, B: int, D: int, N: int, G: int = 1, dtype=torch.float32,
@@ -289,11 +300,11 @@ class ScanToken:
         return self
 
     def run(self, stream=None):
-        self._call(stream)
+        self._enqueue(stream)
         return self.y, self.state
 
 
-class Pack8Step:
+class Pack8Step(_Call):
     """The rows of x [rows, n] in 8 bits: `held`, a Held8."""
 
     def __init__(self, rows: int, n: int, dtype=torch.float32, device=None):
@@ -306,11 +317,11 @@ class Pack8Step:
         return self
 
     def run(self, stream=None):
-        self._call(stream)
+        self._enqueue(stream)
         return self.held
 
 
-class Unpack8Step:
+class Unpack8Step(_Call):
     """What rows in 8 bits stand for: y [rows, n]."""
 
     def __init__(self, rows: int, n: int, dtype=torch.float32, device=None):
@@ -321,7 +332,7 @@ class Unpack8Step:
         return self
 
     def run(self, stream=None):
-        self._call(stream)
+        self._enqueue(stream)
         return self.y
 
 
@@ -454,7 +465,7 @@ class GatedStep(_Step):
         return out
 
 
-class GatedToken:
+class GatedToken(_Call):
     """One token per sequence of the gated linear recurrence: y [B, D] and the new state [B, D]."""
 
     def __init__(self, B: int, D: int, dtype=torch.float32, device=None):
@@ -468,7 +479,7 @@ class GatedToken:
         return self
 
     def run(self, stream=None):
-        self._call(stream)
+        self._enqueue(stream)
         return self.y, self.state
 
 

@@ -57,3 +57,27 @@ def test_groups_with_an_infinity_are_not_numbers():
     st = trunk.MatvecStep(1, trunk.Weights4(codes, scales, 130, 64)).bind(x)
     st.run()
     assert torch.equal(torch.isnan(st.y[0]), torch.tensor([0, 1, 1, 1, 0], device="cuda").bool())
+
+
+def test_nothing_bound_is_refused():
+    """Tokens and conversions as the other steps; a bind that is refused leaves the call before it."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import _lib, trunk
+
+    z = lambda *n: torch.zeros(*n, device="cuda")  # noqa: E731
+    held = trunk.Pack8Step(4, 8).bind(z(4, 8)).run()
+    for step, good, bad in (
+            (trunk.Pack8Step(4, 8), (z(4, 8),), (z(4, 9),)),
+            (trunk.Unpack8Step(4, 8), (held,), (_lib.Held8((4, 9)),)),
+            (trunk.GatedToken(4, 8), (z(4, 8), z(4, 8), z(4, 8)), (z(4, 8), z(4, 9), z(4, 8))),
+            (trunk.ConvToken(4, 8, 3), (z(4, 8), z(8, 3), z(4, 2, 8)), (z(4, 8), z(8, 3), z(4, 2, 9))),
+            (trunk.ScanToken(4, 8, 4), (z(4, 8), z(4, 8), z(8, 4), z(4, 1, 4), z(4, 1, 4), z(4, 8, 4)),
+             (z(4, 8), z(4, 9), z(8, 4), z(4, 1, 4), z(4, 1, 4), z(4, 8, 4)))):
+        with pytest.raises(ValueError, match="bound"):
+            step.run()
+        step.bind(*good).run()
+        call = step._call
+        with pytest.raises(ValueError):
+            step.bind(*bad)
+        assert step._call is call
