@@ -161,13 +161,17 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   return r;
 }
 
-// Codes j and j + 4 of a word, minus 8, as a pair of bf16: 0x4300 is 128, whose last place is 1.
+// Codes j and j + 4 of a word, minus 8, as a pair of bf16.  A bf16 number from 128 to 256 has seven bits
+// behind the leading one, worth 64 to 1: with a code in the last four of 128's it is 128 + code, and the
+// difference from 136 is exact.
 template <int J>
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t word) {
-  uint32_t v;  // (word >> 4 J & 0x000f000f) | 0x43004300, in one instruction behind the shift
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * J)), "r"(0x000f000fu), "r"(0x43004300u));
-  uint32_t r;  // v * 1 - 136
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3f803f80u), "r"(0xc308c308u));
+  constexpr uint32_t kTwo = 0x00010001u;  // in both halves
+  constexpr uint32_t kCode = 15u * kTwo, k128 = 0x4300u * kTwo, k136 = 0x4308u * kTwo;
+  uint32_t v, r;
+  // (word >> 4 J & kCode) | k128 in one instruction behind the shift.
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * J)), "r"(kCode), "r"(k128));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(k136));
   return r;
 }
 
