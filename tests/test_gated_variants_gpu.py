@@ -13,6 +13,43 @@ from test_gated_gpu import SUM, act, built, check, cuda, gated_check, gated_step
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("D", [6, 8])
+def test_bias_gradient_of_many_sequences(D):
+    """More partial sums than one CTA's merge takes, with and without four columns at a time."""
+    K, B = 9, 2100
+    ends = np.random.default_rng(D).integers(0, K + 1, size=B)
+    i = gated_inputs(K, B, D, "f32", D, ends)
+    st = gated_step(i, K, B, D, "f32", dh_last=True)
+    gated_check(st, i, dh_last=True)
+    first = st.dbias.clone()
+    st.dbias.fill_(float("nan"))
+    st.run()
+    assert (st.dbias == first).all()
+
+
+@pytest.mark.parametrize("M,N,K,group,dtype", [(1, 40, 12000, 128, "f32"), (2, 40, 12000, 64, "f32"),
+                                               (1, 40, 40000, 128, "bf16"), (2, 40, 17000, 32, "bf16"),
+                                               (1, 16000, 11000, 128, "f32"), (1, 40000, 11000, 128, "f32")])
+def test_matvec4_in_several_chunks_of_one_row(M, N, K, group, dtype):
+    """x beyond what shared memory holds, for tiles of rows that eight, four and two warps go along."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import trunk
+
+    i = weights4_inputs(M, N, K, group, dtype, N + K)
+    codes, scales = torch.from_numpy(i["codes"]).cuda(), cuda(i["scales"], "bf16")
+    st = trunk.MatvecStep(M, trunk.Weights4(codes, scales, K, group), act(dtype)).bind(cuda(i["x"], dtype))
+    st.run()
+    c = torch.stack([codes & 15, codes >> 4], -1).view(N, -1)[:, :K].double() - 8
+    W = c * scales.double().repeat_interleave(group, 1)[:, :K]
+    x = st.inputs["x"].double()
+    want = x @ W.T
+    bound = (K + 8) * 2.0 ** -24 * (x.abs() @ W.abs().T) * (1 + 2.0 ** -7)
+    if dtype == "bf16":
+        bound += 2.0 ** -8 * want.abs()
+    assert ((st.y.double() - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("K,D", [(45, 64), (45, 33), (45, 50), (900, 64), (900, 33)])
 @pytest.mark.parametrize("keep8", [False, True])
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])

@@ -109,6 +109,44 @@ def test_codes_as_near_to_borders_as_weights_bring_them(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n,pad,off", [(9, 64, 3, 0), (9, 64, 8, 0), (9, 64, 0, 1), (9, 256, 8, 4),
+                                            (5, 300, 5, 0), (33, 96, 0, 3), (5, 1024, 1, 0), (3, 8200, 3, 1)])
+def test_to_and_from_8_bits_anywhere(rows, n, pad, off, dtype):
+    """Strided inputs, codes that start off an 8-byte border, the sum in the residual's memory."""
+    import torch
+
+    from recurrent_cfc_cell_gb300 import _lib
+
+    i = rms_inputs(rows, n, dtype, rows * 41 + n + pad)
+
+    def held():
+        codes = torch.zeros(rows * n + off, dtype=torch.uint8, device="cuda")[off:].view(rows, n)
+        return _lib.Held8((rows, n), codes=codes)
+
+    s8, y8 = held(), held()
+    x, res = wide(cuda(i["x"], dtype), pad), wide(cuda(i["residual"], dtype), pad, 7.0)
+    w, rstd = cuda(i["w"]), cuda(np.zeros(rows))
+    _lib.cfc_rmsnorm_forward(x, w, res, res, None, s8, y8, rstd)
+    assert np.array_equal(res.double().cpu().numpy(), i["s"])
+    if pad:
+        assert (res._base[..., 0] == 7.0).all() and (res._base[..., 1 + n:] == 7.0).all()
+    want = [og.pack8(row) for row in i["s"]]
+    codes, scales = held_bits(s8)
+    assert np.array_equal(scales, np.stack([s for _, s in want]))
+    assert np.array_equal(codes, np.stack([c for c, _ in want]))
+    y = og.rmsnorm(i["s"], i["w"], float(np.float32(1e-5)))
+    assert np.array_equal(np.stack([og.unpack8(c, s) for c, s in zip(*held_bits(y8))]), og.held8(y))
+    dy, ds = wide(cuda(i["dy"], dtype), pad), wide(cuda(i["ds"], dtype), pad)
+    dw, again = cuda(np.zeros(n)), wide(cuda(np.zeros((rows, n)), dtype), pad)
+    ws = torch.empty(max(_lib.rmsnorm_workspace_bytes(rows, n), 16), dtype=torch.uint8, device="cuda")
+    _lib.cfc_rmsnorm_backward(dy, s8, w, rstd, ds, dw, ds, again, ws)  # dx in ds's place
+    dx, want_dw, want_y = og.rmsnorm_backward(i["dy"], i["s"], i["w"], 1e-5, og.held8(i["s"]), i["ds"])
+    check(ds, dx, SUM, "dx")
+    check(dw, want_dw, SUM, "dw")
+    check(again, want_y, EL, "y_again")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_long_rows_in_many_turns(dtype):
     """More rows of more than 8192 columns than the GPU holds CTAs for, the sum in the residual's place."""
     import torch
