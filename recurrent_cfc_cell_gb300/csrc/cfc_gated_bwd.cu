@@ -387,7 +387,7 @@ cudaError_t bwd_mode(const GatedCall& q, const GatedShape& sh, int tiles, float*
   c.pdl = MODE == kSegments;
   constexpr size_t ring = PATH == kSingles ? 0 : Ring<T, Z, KEEP, PATH>::kWarp;
   c.smem = gated_smem<path_v(PATH)>(sh.warps, ring);
-  const cudaError_t e = allow_smem(kern, gated_smem<path_v(PATH)>(kGatedWarps, ring));
+  const cudaError_t e = allow_smem(kern, c.smem, gated_smem<path_v(PATH)>(kGatedWarps, ring));
   return e == cudaSuccess ? launch(c, kern, q, sh, dbias) : e;
 }
 template <typename T, bool Z, bool KEEP, GatedPath PATH>

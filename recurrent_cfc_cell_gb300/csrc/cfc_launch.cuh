@@ -49,13 +49,13 @@ cudaError_t launch(const LaunchCfg& c, void (*kern)(KArgs...), Args&&... args) {
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// Lets a kernel be launched with up to `most` bytes of dynamic shared memory.  The limit is the
-// kernel's, not the call's: `most` is what its largest launch takes, whatever this one needs, so that a
+// Leave for a launch with `need` bytes of dynamic shared memory.  The limit is the kernel's, not the
+// call's: it is set to `most`, what the kernel's largest launch takes, whatever this one needs, so that a
 // call in another thread never finds it lowered.  48 KB, with up to 8 KB that the kernel declares, need no
 // leave.
 template <typename F>
-cudaError_t allow_smem(F* kern, size_t most) {
-  return most > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+cudaError_t allow_smem(F* kern, size_t need, size_t most) {
+  return need > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(most))
                           : cudaSuccess;
 }

@@ -1062,8 +1062,8 @@ cudaError_t launch_rows(void (*kern)(const NormArgs), LaunchCfg c, const NormArg
   if constexpr (RING) {
     using Rg = Ring<T, TM, LY, NT>;
     c.smem = 16 * static_cast<size_t>(c.block.x) * (Rg::kDepth * Rg::kRow + params * Rg::kParam);
-    const cudaError_t e = allow_smem(kern, 16 * static_cast<size_t>(TM::kMaxThreads) *
-                                               (Rg::kDepth * Rg::kRow + params * Rg::kParam));
+    const cudaError_t e = allow_smem(kern, c.smem, 16 * static_cast<size_t>(TM::kMaxThreads) *
+                                                       (Rg::kDepth * Rg::kRow + params * Rg::kParam));
     if (e != cudaSuccess) return e;
   }
   return launch(c, kern, a);

@@ -358,6 +358,12 @@ __device__ __forceinline__ Pair normed_two(float2 s, float2 w, Two rstd) {
   const float2 sum = __fadd2_rn(y, low);
   return {sum, __fadd2_rn(low, neg2(__fadd2_rn(sum, neg2(y))))};
 }
+// The same of one column.
+__device__ __forceinline__ Two normed_two(float s, float w, Two rstd) {
+  const float p = __fmul_rn(s, rstd.hi), p_low = fmaf(s, rstd.lo, fmaf(s, rstd.hi, -p));
+  const float y = __fmul_rn(p, w);
+  return fast_two(y, fmaf(p_low, w, fmaf(p, w, -y)));
+}
 // To odd: a last place of 0 becomes 1, upwards or downwards to where the rest lies.
 __device__ __forceinline__ float to_odd(float hi, float lo) {
   const uint32_t bits = __float_as_uint(hi), some = fabsf(lo) > 0.f ? 1u : 0u;
@@ -429,15 +435,16 @@ __global__ void __launch_bounds__(TM::kThreads) rms_fwd_kernel(const RmsCall q) 
       if (ok && q.rstd && threadIdx.x % TM::TPR == 0) q.rstd[row] = rstd.hi;
       if (q.s8.codes) store_held<TM>(at, q.s8, row, s, ok);
       float y[TM::E];
+      if constexpr (TM::E == 1) {
+        const Two v = normed_two(s[0], w[0], rstd);
+        y[0] = v.hi;
+        s[0] = to_odd(v.hi, v.lo);
+      } else {
 #pragma unroll
-      for (int i = 0; i < TM::E; i += 2) {
-        const bool two = i + 1 < TM::E;
-        const Pair v = normed_two(make_float2(s[i], two ? s[i + 1] : 0.f),
-                                  make_float2(w[i], two ? w[i + 1] : 0.f), rstd);
-        y[i] = v.hi.x;
-        s[i] = to_odd(v.hi.x, v.lo.x);
-        if (two) {
-          y[i + 1] = v.hi.y;
+        for (int i = 0; i < TM::E; i += 2) {
+          const Pair v = normed_two(make_float2(s[i], s[i + 1]), make_float2(w[i], w[i + 1]), rstd);
+          y[i] = v.hi.x, y[i + 1] = v.hi.y;
+          s[i] = to_odd(v.hi.x, v.lo.x);
           s[i + 1] = to_odd(v.hi.y, v.lo.y);
         }
       }
@@ -603,10 +610,8 @@ __global__ void __launch_bounds__(kLongThreads) rms_long_fwd_kernel(const RmsCal
         // s where it was written: x and the residual may have been in its place.
         float v = to_f32(so ? so[c] : x[c]);
         if (res && !so) v = to_f32(from_f32<T>(v + to_f32(res[c])));
-        if constexpr (OUT8) {
-          const Pair p = normed_two(make_float2(v, 0.f), make_float2(__ldg(q.w + c), 0.f), rstd);
-          y = {p.hi.x, p.lo.x};
-        } else y.hi = normed(v, __ldg(q.w + c), rstd.hi);
+        if constexpr (OUT8) y = normed_two(v, __ldg(q.w + c), rstd);
+        else y.hi = normed(v, __ldg(q.w + c), rstd.hi);
         if (q.y) static_cast<T*>(q.y)[row * q.ldy + c] = from_f32<T>(y.hi);
       }
       if constexpr (OUT8) hold(q.y8, row, c, to_odd(y.hi, y.lo));

@@ -393,7 +393,7 @@ cudaError_t matvec(const Weights4Call& q, cudaStream_t s) {
   c.smem = sums > xs ? sums : xs;
   c.stream = s;
   auto run = [&](auto* kern) {
-    const cudaError_t e = allow_smem(kern, kChunkBytes);
+    const cudaError_t e = allow_smem(kern, c.smem, kChunkBytes);
     return e == cudaSuccess ? launch(c, kern, q, sp) : e;
   };
   if (nt == 1) return run(matvec4_kernel<T, GROUP, 1>);

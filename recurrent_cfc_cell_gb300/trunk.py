@@ -33,8 +33,12 @@ def _expect(t, name: str, shape, dtype):
 class _Step:
     """Prepared calls, run in order."""
 
+    _into = ()  # names of the outputs for which a step takes tensors
+
     def __init__(self, device, into: dict | None = None):
         self.device, self.into = _device(device), into or {}
+        if not set(self.into) <= set(self._into):
+            raise ValueError(f"into names {sorted(self.into)}, but the step takes {self._into}")
         self._unbind()
 
     def _act(self, *shape):
@@ -344,6 +348,8 @@ class RMSNormStep(_Step):
     gives tensors for y, s, dx and y_again, by these names, which steps that take turns may share; dx
     may be ds."""
 
+    _into = ("y", "s", "dx", "y_again")
+
     def __init__(self, rows: int, n: int, dtype=torch.float32, eps: float = 1e-5,
                  out8: bool = False, keep8: bool = False, device=None, into: dict | None = None):
         super().__init__(device, into)
@@ -397,6 +403,8 @@ class GatedStep(_Step):
     their place, so that the inputs may be gone by then, and forms y again (``y_again``).  ``into``
     gives tensors for y, dx, df, dz and y_again, by these names, which steps that take turns may
     share."""
+
+    _into = ("y", "dx", "df", "dz", "y_again")
 
     def __init__(self, K: int, B: int, D: int, dtype=torch.float32, train: bool = False,
                  keep8: bool = False, device=None, into: dict | None = None):
