@@ -68,9 +68,10 @@ __device__ __forceinline__ Fv<2> fma(Fv<2> a, Fv<2> b, Fv<2> c) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// f = sigmoid(logit + bias) and i = 1 - f, both to full relative precision, from t = (logit + bias)
-// log2 e: i = 1 / (1 + 2^t), and f = 2^t i where that is the smaller one, else 1 - i, which is
-// rounded to nearest, so that a long product of f does not drift with an error of the reciprocal.
+// f = sigmoid(logit + bias) and i = 1 - f from t = (logit + bias) log2 e: i = 1 / (1 + 2^t), and
+// f = 2^t i where that is the smaller one, else 1 - i, which is rounded to nearest, so that a long
+// product of f does not drift with an error of the reciprocal.  Both have fp32's relative precision
+// for their t, which is off by 2^-24 of itself and of bias log2 e (a bias is a few units).
 // `bias2` is bias log2 e.  2^t may be infinite: i is 0 then and f 1.
 template <int V>
 __device__ __forceinline__ void gates(Fv<V> logit, Fv<V> bias2, Fv<V>& f, Fv<V>& i) {
