@@ -9,9 +9,9 @@
 //
 // Rounds are bound by memory: 64 x 1024 steps x 1536 channels bf16 249 us (5.9 TB/s), 64 x 512 x 1024
 // fp32 151 us (6.3 TB/s).  What is kept in 8 bits is bound by the instructions and their latency (131 a
-// warp for a step of 64 channels, 107 for inputs as they are; 2.5 of 4 a cycle from 3.3 warps a scheduler): 16
-// x 2048 x 2048 bf16 203 us with y formed again.  128 registers hold a run's
-// factors between the two ways through it (gather, finish), so that nothing is computed twice.
+// warp for a step of 64 channels, 107 for inputs as they are; 2.5 of 4 a cycle from 3.3 warps a
+// scheduler): 16 x 2048 x 2048 bf16 203 us with y formed again.  128 registers hold a run's factors
+// between the two ways through it (gather, finish), so that nothing is computed twice.
 #include "cfc_gated.cuh"
 
 namespace cfc {

@@ -3,10 +3,10 @@
 //
 // Rounds are bound by memory, segments and what is kept in 8 bits by the instructions and their latency
 // (65 a warp for a step of 64 channels with z, 115 with all three inputs kept, four a channel of them
-// exponentials and reciprocals; 2.4 and 2.8 of 4 a cycle).  64 x 1024 steps x 1536 channels bf16 with states: 135 us (6.3 TB/s);
-// 64 x 512 x 1024 fp32 82 us (6.7 TB/s); 32768 steps of one sequence of 1024 channels bf16 70 us in
-// segments, of which the summary, that reads x and f once more, is a third; 16 x 2048 x 2048 bf16 in
-// 8 bits 169 us.  A token of 1024 sequences of 2048 channels in bf16 8 us.
+// exponentials and reciprocals; 2.4 and 2.8 of 4 a cycle).  64 x 1024 steps x 1536 channels bf16 with
+// states: 135 us (6.3 TB/s); 64 x 512 x 1024 fp32 82 us (6.7 TB/s); 32768 steps of one sequence of 1024
+// channels bf16 70 us in segments, of which the summary, that reads x and f once more, is a third; 16 x
+// 2048 x 2048 bf16 in 8 bits 169 us.  A token of 1024 sequences of 2048 channels in bf16 8 us.
 #include "cfc_gated.cuh"
 
 namespace cfc {
